@@ -388,6 +388,154 @@ SL8_API int sl8_attn_decode_combine(const float* o_partial, const float* lse_par
                             float* lse_out, void* stream);
 
 /*
+ * ---- Serving from the paged int8 cache ("Engine" table, "Paged KV cache" row; the pages
+ * name the cache, not how it is filled or pruned: the four operators below are readings).
+ * The pages are those of sl8_attn_int8_paged_decode_splitkv; a slot is page * page_size +
+ * row.  A contiguous cache [B][Hkv][Lmax][d] is the case page_size = Lmax, num_pages = B,
+ * slot = b * Lmax + position.
+ *
+ * The page plan of one step: block tables, slot map and free list from request lengths.
+ *   ctx_lens, new_lens  device, [B] int32: tokens already in the cache and tokens to append.
+ *   release             device, nullable, [B] int32: nonzero, the slot's request has ended.
+ *                       Its ceil(ctx / page_size) pages go back to the free list and its
+ *                       length becomes 0 before anything is granted (a new request may
+ *                       start in the slot in the same step).  A released page must belong
+ *                       to no other request.
+ *   block_table         device, [B][max_blocks] int32, updated: entries of the blocks that
+ *                       the granted tokens open are written, all others are left.
+ *   free_pages          device, [free_capacity] int32, updated: a stack of free pages whose
+ *                       first free_count entries count; released pages are pushed (slot
+ *                       order, block order), granted ones are taken from its end.
+ *   free_count          device, [1] int32;  free_count_out: what it is after the step (may
+ *                       be the same word).
+ *   max_tokens          length of slot_map and token_pos (fixed for a captured step).
+ *   seqlens, granted    device, [B] int32: length after the step, and tokens granted: new_lens
+ *                       or 0.  A request is granted all of its tokens or none: none if it
+ *                       would pass max_blocks * page_size or if the new tokens up to and
+ *                       including its own pass max_tokens; of the others, one that needs
+ *                       pages is granted iff the pages that they ask for up to and including
+ *                       its own are there.  These may be the same buffers as ctx_lens and
+ *                       new_lens.
+ *   cu_new              device, [B + 1] int32: new tokens before each request, refused ones
+ *                       included (the caller's packed order).
+ *   slot_map            device, [max_tokens] int32: slot of each new token, -1 for tokens of
+ *                       refused requests and past the last token.
+ *   token_pos           device, nullable, [max_tokens] int32: its position in its sequence, 0
+ *                       past the last token.
+ * A negative length, ctx_lens above max_blocks * page_size or a free_count outside [0,
+ * free_capacity] is recorded (SL8_ERR_DEVICE_ARG) and its request refused, its pages not
+ * released, the count clamped; pushes past free_capacity are recorded and dropped.
+ * page_size * max_blocks must stay below 2^31.
+ */
+SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
+                             int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,
+                             int32_t free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                             int32_t max_tokens, int32_t* seqlens, int32_t* granted, int32_t* cu_new,
+                             int32_t* slot_map, int32_t* token_pos, void* stream);
+
+/*
+ * Rotary positions and the int8 append in one pass: rotate q and k, quantise k and v per
+ * row as sl8_quant_rowwise and store them in their slots.
+ *   q, k, v       device, [T][Hq or Hkv][d] of dtype (F16, BF16 or F32; one for all three);
+ *                 a token's heads are contiguous, tokens are *_stride elements apart (a
+ *                 multiple of 16 bytes: slices of a fused projection).  Hq = 0: k, v only.
+ *   positions     device, [axes][T] int32 (time, height, width, ...), 1 <= axes <= 4.
+ *   rot_dim       rotated channels of each head, a multiple of 8 up to d; the others pass
+ *                 through.  0: no rotation (positions, inv_freq and axes are not used).
+ *   inv_freq      device, [rot_dim / 2] fp32: radians per position of each pair.
+ *   pair_axis     HOST, [rot_dim / 2] uint8: axis of each pair (nullable when axes is 1).
+ *   adjacent      0: pair p is channels (p, rot_dim / 2 + p); nonzero: (2 p, 2 p + 1).  Pair
+ *                 (x, y) becomes (x cos - y sin, y cos + x sin) in fp32, the angle exact to
+ *                 about 1e-6 rad at any int32 position.
+ *   q_out         device, [T][Hq][d] of dtype, tokens q_out_stride elements apart; may be q.
+ *   slot_map      device, [T] int32: slot of each token; negative: the token is not stored
+ *                 (its q is rotated all the same).  Slots must differ.  A slot of num_pages *
+ *                 page_size or more is recorded (SL8_ERR_DEVICE_ARG) and not stored.
+ *   k_pages, k_scale_pages, v_pages, v_scale_pages   device, updated rows only: int8 codes
+ *                 [num_pages][Hkv][page_size][d] and fp32 scales [num_pages][Hkv][page_size].
+ * The rotated k is quantised from its fp32 values.  num_pages * page_size < 2^31.
+ */
+SL8_API int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
+                            int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis,
+                            int adjacent, void* q_out, int64_t q_out_stride, const int32_t* slot_map, int8_t* k_pages,
+                            float* k_scale_pages, int8_t* v_pages, float* v_scale_pages, int32_t num_pages,
+                            int32_t page_size, void* stream);
+
+/*
+ * Per-channel bounds of each page's keys, the summary that sl8_page_select scores.  With S
+ * the largest scale s_t among the page's rows that hold tokens, row t's keys are
+ * y = code * (s_t / S) in steps of S (fp32 division and product):
+ *   bounds       device, [num_pages][Hkv][2][d] int8: floor(min y), ceil(max y);
+ *   bound_scale  device, [num_pages][Hkv] fp32: S (zero: the codes are zero too).
+ * Written for the pages that the last new_lens[b] (<= max_new, a host bound) tokens of each
+ * sequence lie in, over all tokens of those pages; new_lens NULL: for every page of the
+ * sequences.  seqlens [B] counts the new tokens.  Sequences must not share pages that take
+ * new tokens.  Scales are >= 0.  A length or page out of range is recorded
+ * (SL8_ERR_DEVICE_ARG) and clamped or skipped.
+ */
+SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,
+                            const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
+                            const int32_t* new_lens, int32_t max_new, int32_t B, int32_t Hkv, int32_t d,
+                            int8_t* bounds, float* bound_scale, void* stream);
+
+/*
+ * Page selection: for every query and kv head the max_sel pages whose keys can reach the
+ * largest logits.  Query t of T in sequence b is position seqlens[b] - T + t and sees the
+ * tokens up to itself (T = 1: the decode's query; more: drafts or a prompt chunk).
+ *   q            device, [B][T][Hq][d] (F16, BF16 or F32), quantised per row to codes c and
+ *                scale s_q as the decode does.
+ *   bounds, bound_scale  as sl8_page_bounds leaves them for every page of the sequences.
+ *   score        of a page: the maximum over the kv head's query heads of
+ *                (float(sum_i max(c_i lo_i, c_i hi_i)) * S) * s_q, fp32 products in this
+ *                order: an upper bound of every q . k of the page (before 1 / sqrt(d)).
+ *   first, last  the first `first` and last `last` pages of a query's range are always kept,
+ *                first + last <= max_sel.  The others are kept in the order of their scores,
+ *                ties to the lowest block.  A range of at most max_sel pages is kept whole.
+ *   sel_blocks   device, [B][T][Hkv][max_sel] int32: the kept blocks, ascending, -1 after;
+ *   sel_pages    device, the same of their pages (block_table entries), -1 after;
+ *   sel_lens     device, [B][T][Hkv] int32: the tokens that the list holds for the query:
+ *                its pages are full but the query's own last one.
+ *   scores       device, nullable, [B][T][Hkv][max_blocks] fp32: the scores of the query's
+ *                blocks (entries past them are left).
+ * The same selection on every run.  Hq / Hkv <= 64; about 400,000 blocks a sequence at most
+ * (SL8_ERR_UNSUPPORTED).  A length or page out of range is recorded (SL8_ERR_DEVICE_ARG)
+ * and clamped, or read as page 0.
+ */
+SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const float* bound_scale,
+                            int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seqlens, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                            int32_t max_sel, int32_t first, int32_t last, int32_t* sel_blocks, int32_t* sel_pages,
+                            int32_t* sel_lens, float* scores, void* stream);
+
+/*
+ * Sparse decode: attention of each query row over a page list of its own per kv head, split
+ * over the list and combined (partials in the workspace).
+ *   q            device, [rows][Hq][d] of q_dtype (F16, BF16 or F32), quantised per row.
+ *   page_list    device, [rows][Hkv][max_sel] int32 pages, as sl8_page_select's sel_pages or
+ *                from any other policy; list_lens device, [rows][Hkv] int32: the tokens that
+ *                the list holds, 0 .. max_sel * page_size: every page of the list is full
+ *                but the last one.  Entries past the list are not read.
+ *   pages        as sl8_attn_int8_paged_decode_splitkv (page_size a multiple of 16).
+ *   num_splits   requested splits of each list (0 = automatic).
+ *   out          device, [rows][Hq][d] of out_dtype; a row whose list is empty gets 0.
+ *   lse_out      device, nullable, [rows][Hq] fp32 (natural log; -inf for an empty list).
+ *   workspace    at least sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
+ *                unsupported shape); launches that run at the same time need their own.
+ * Any Hq that is a multiple of Hkv (above 8 heads a group, each 8 read the list again).  A
+ * page outside [0, num_pages) or a length out of range is recorded (SL8_ERR_DEVICE_ARG), and
+ * page 0 read or the length clamped.
+ */
+SL8_API size_t sl8_attn_int8_sparse_decode_workspace_size(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel,
+                                                          int32_t page_size, int32_t d, int32_t num_splits);
+SL8_API int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_pages, const float* k_scale_pages,
+                                        const int8_t* v_pages, const float* v_scale_pages, int32_t num_pages,
+                                        int32_t page_size, const int32_t* page_list, const int32_t* list_lens,
+                                        int32_t max_sel, int32_t rows, int32_t Hq, int32_t Hkv, int32_t d,
+                                        int32_t num_splits, void* out, int out_dtype, float* lse_out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
  * Debug view of the decode's q quantisation and int32 logits (same kernel as the
  * split call, with num_splits automatic: o_partial/lse_partial sized for
  * S = sl8_attn_decode_num_splits(B, Hkv, Lmax, d, 0)).

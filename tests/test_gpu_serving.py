@@ -1,0 +1,582 @@
+"""Serving from the paged int8 cache on the GPU, against the CPU definitions: the page plan,
+the rotary append, page bounds, page selection and sparse decode, alone and as one step.
+
+Tolerances.  Page plans, bounds, scores and selections are fixed bit for bit.  Rotations:
+the angle is good to 2^-23 turns (7.5e-7 rad) or better, sincospif to 2 ulp, and each output takes
+three fp32 roundings, so a rotated value is within 2e-6 of its pair's length, then half a
+step of its type.  Codes: half a scale plus that.  Attention: each probability is rounded
+to fp16 (2^-11 of itself, or 2^-25 of the range of P' = p s_v 2^-E at the bottom of fp16,
+at most 2^-24 max|v| a token), then the output's type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_flashattention_gb300 as sl8
+from oracle import serving as S
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+DEV = "cuda"
+NP = {torch.float16: np.float16, torch.float32: np.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from w8a8_int8_flashattention_gb300 import build
+    build.build()
+    sl8.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    st, site = sl8.last_device_status()
+    assert st == sl8.SL8_OK, (st, site)
+
+
+def i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device=DEV)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ page plan
+
+def _plan_case(rng, B, nb, page, releases, spare):
+    ctx = rng.integers(0, nb * page + 1, B)
+    ctx[rng.random(B) < 0.2] = 0
+    held = -(-ctx // page)
+    total = int(held.sum()) + spare
+    perm = rng.permutation(total)
+    table, at = np.full((B, nb), -1), 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    free = np.full(total + 1, -1)
+    free[:spare] = perm[at:]
+    return ctx, table, free, spare, (rng.integers(0, 2, B) if releases else None)
+
+
+def _check_plan(got, want, table, free, tag):
+    for name in ("seqlens", "granted", "cu_new", "slot_map", "token_pos"):
+        np.testing.assert_array_equal(got[name].cpu().numpy(), want[name], err_msg=f"{tag} {name}")
+    assert got["free_count"].item() == want["free_count"], tag
+    np.testing.assert_array_equal(table.cpu().numpy(), want["block_table"], err_msg=tag)
+    np.testing.assert_array_equal(free.cpu().numpy(), want["free_pages"], err_msg=tag)
+
+
+@pytest.mark.parametrize("B,nb,page,max_new,max_tokens,releases", [
+    (1, 4, 16, 1, 1, False), (3, 3, 1, 2, 5, True), (8, 7, 16, 40, 300, True), (33, 5, 3, 9, 200, True),
+    (256, 40, 16, 700, 60000, True), (1025, 4, 8, 20, 9000, True), (2500, 3, 16, 30, 50000, False)])
+def test_paged_assign(B, nb, page, max_new, max_tokens, releases):
+    rng = np.random.default_rng(B * 7 + page)
+    for spare in (0, B // 2, 4 * B):
+        ctx, table, free, count, release = _plan_case(rng, B, nb, page, releases, spare)
+        new = rng.integers(0, max_new + 1, B)
+        want = S.paged_assign(ctx, new, release, table, free, count, page, max_tokens)
+        tab, fr = i32(table), i32(free)
+        got = sl8.paged_assign(i32(ctx), i32(new), tab, fr, i32([count]), page, max_tokens,
+                               release=None if release is None else i32(release))
+        _check_plan(got, want, tab, fr, f"spare {spare}")
+
+
+def test_paged_assign_in_place_and_steps():
+    """Lengths and the count kept in place over many steps, slots released and refilled."""
+    rng = np.random.default_rng(11)
+    B, nb, page, T = 1300, 6, 4, 3000
+    seqlens, table, count = np.zeros(B, np.int64), np.full((B, nb), -1), 900
+    free = rng.permutation(900)
+    d = dict(seq=i32(seqlens), table=i32(table), free=i32(free), count=i32([count]))
+    out = None
+    for step in range(8):
+        new, release = rng.integers(0, 5, B), (rng.random(B) < 0.1).astype(np.int64)
+        want = S.paged_assign(seqlens, new, release, table, free, count, page, T)
+        if out is None:
+            out = sl8.paged_assign(d["seq"], i32(new), d["table"].clone(), d["free"].clone(), d["count"], page, T,
+                                   release=i32(release))
+            out.update(seqlens=d["seq"], free_count=d["count"])
+        out["granted"].copy_(i32(new))  # new lengths in, granted tokens out
+        got = sl8.paged_assign(d["seq"], out["granted"], d["table"], d["free"], d["count"], page, T, release=i32(release),
+                               out=out)
+        _check_plan(got, want, d["table"], d["free"], f"step {step}")
+        seqlens, table, free, count = want["seqlens"], want["block_table"], want["free_pages"], want["free_count"]
+
+
+def test_paged_assign_no_requests_and_bad_lengths():
+    z = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = sl8.paged_assign(z, z, z.view(0, 4), i32([1, 2]), i32([2]), 16, 3)
+    assert out["slot_map"].tolist() == [-1] * 3 and out["token_pos"].tolist() == [0] * 3
+    assert out["cu_new"].tolist() == [0] and out["free_count"].item() == 2
+    # a negative length, a context above the table and a count above the list: recorded,
+    # refused, and nothing else is touched
+    table = i32([[3, -1], [4, 5], [6, -1]])
+    free = i32([7, 8, -1])
+    out = sl8.paged_assign(i32([4, 99, 2]), i32([-1, 1, 3]), table, free, i32([2]), 4, 8)
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["granted"].tolist() == [0, 0, 3] and out["seqlens"].tolist() == [4, 8, 5]
+    assert out["cu_new"].tolist() == [0, 0, 0, 3] and out["slot_map"].tolist() == [26, 27, 32] + [-1] * 5
+    assert table.tolist() == [[3, -1], [4, 5], [6, 8]] and out["free_count"].item() == 1
+    out = sl8.paged_assign(i32([0]), i32([1]), i32([[-1]]), free, i32([9]), 4, 1)
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    # a released slot whose pages would pass the list's end
+    out = sl8.paged_assign(i32([8]), i32([0]), i32([[1, 2]]), i32([0]), i32([0]), 4, 1, release=i32([1]))
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["free_count"].item() == 1 and out["seqlens"].tolist() == [0]
+
+
+# ------------------------------------------------------------------ rotary append
+
+def _rotation_tol(x, rot, adjacent):
+    """2e-6 of each rotated channel's pair length; 0 for the others."""
+    t = np.zeros_like(x)
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if adjacent else (slice(0, rot // 2), slice(rot // 2, rot))
+    t[..., a] = t[..., b] = 2e-6 * np.hypot(x[..., a], x[..., b])
+    return t
+
+
+@pytest.mark.parametrize("d,rot,axes,adjacent,hq,hkv,dtype,T,page", [
+    (128, 128, 1, False, 32, 8, torch.bfloat16, 1, 16), (128, 96, 3, False, 5, 1, torch.float16, 37, 16),
+    (64, 64, 1, True, 7, 3, torch.bfloat16, 130, 7), (32, 8, 2, False, 3, 3, torch.float32, 65, 32),
+    (256, 256, 4, True, 2, 2, torch.float32, 9, 16), (256, 64, 1, False, 16, 8, torch.float16, 700, 64),
+    (32, 32, 1, True, 1, 1, torch.float16, 3000, 1000), (64, 0, 0, False, 2, 2, torch.bfloat16, 20, 16),
+    (128, 128, 1, False, 0, 2, torch.bfloat16, 20, 16)])
+def test_rope_append(d, rot, axes, adjacent, hq, hkv, dtype, T, page):
+    g = torch.Generator().manual_seed(T + d)
+    rng = np.random.default_rng(T)
+    qkv = torch.randn((T, (hq + 2 * hkv) * d + 16), generator=g).to(dtype)
+    qkv[T // 2, -1 - 16 - d:-16] = 0  # part of a row of zeros
+    qkv[:, hq * d:(hq + 1) * d] *= 30
+    dq = qkv.to(DEV)
+    view = lambda x, a, n: x[:, a * d:(a + n) * d].unflatten(1, (n, d)) if n else None  # noqa: E731
+    q, k, v = view(dq, 0, hq), view(dq, hq, hkv), view(dq, hq + hkv, hkv)
+    pos = rng.integers(0, 1 << 20, (max(axes, 1), T))
+    pos[:, -1] = (1 << 31) - 1 - np.arange(max(axes, 1))
+    pos[:, 0] = -5 if T > 1 else 3
+    inv = (10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))).astype(np.float32)
+    axis = rng.integers(0, max(axes, 1), rot // 2).tolist()
+    num_pages = -(-T // page) + 1
+    slots = rng.permutation(num_pages * page)[:T]
+    if T > 4:
+        slots[[1, 3]] = -1
+    pages = torch.full((2, num_pages, hkv, page, d), 77, dtype=torch.int8, device=DEV)
+    scales = torch.full((2, num_pages, hkv, page), -7.0, dtype=torch.float32, device=DEV)
+    out = sl8.rope_append(q, k, v, i32(pos if axes > 1 else pos[0]) if rot else None,
+                          torch.from_numpy(inv).to(DEV) if rot else None, i32(slots), pages[0], scales[0], pages[1],
+                          scales[1], pair_axis=axis if axes > 1 else None, adjacent=adjacent)
+    host = qkv.double().numpy()
+    eps = torch.finfo(dtype).eps / 2
+    used = axis if axes > 1 else None
+    if hq:
+        x = host[:, :hq * d].reshape(T, hq, d)
+        want = S.rope(x, pos, inv, used, adjacent)
+        err = np.abs(np64(out) - want)
+        # a value rounds from within the rotation's error; tiny fp16 results round to 2^-25
+        assert np.all(err <= _rotation_tol(x, rot, adjacent) * (1 + eps) + eps * np.abs(want) + 2.0 ** -25)
+    kx = host[:, hq * d:(hq + hkv) * d].reshape(T, hkv, d)
+    want, tol = S.rope(kx, pos, inv, used, adjacent), _rotation_tol(kx, rot, adjacent)
+    vc, vs = S._quant(host[:, (hq + hkv) * d:(hq + 2 * hkv) * d].reshape(T, hkv, d).astype(np.float32))
+    gk, gs = pages.cpu().numpy(), scales.cpu().numpy()
+    touched = np.zeros((num_pages, page), bool)
+    for t in range(T):
+        if slots[t] < 0:
+            continue
+        at = slots[t] // page, slice(None), slots[t] % page
+        touched[at[0], at[2]] = True
+        np.testing.assert_array_equal(gk[1][at], vc[t])
+        np.testing.assert_array_equal(gs[1][at], vs[t])
+        amax = np.abs(want[t]).max(-1)
+        assert np.all(np.abs(gs[0][at] * 127.0 - amax) <= tol[t].max(-1) + 2.0 ** -23 * amax)
+        near = gk[0][at].astype(np.float64) * gs[0][at][:, None].astype(np.float64)
+        step = gs[0][at][:, None].astype(np.float64)
+        assert np.all(np.abs(near - want[t]) <= step * (0.5 + 127 * 2.0 ** -23) + tol[t])
+    # rows without a slot stay as they were
+    assert np.all(gk.transpose(0, 1, 3, 2, 4)[:, ~touched] == 77) and np.all(gs.transpose(0, 1, 3, 2)[:, ~touched] == -7.0)
+
+
+def test_rope_append_in_place_and_bad_slot():
+    T, hq, hkv, d = 6, 4, 2, 64
+    qkv = torch.randn((T, (hq + 2 * hkv) * d), device=DEV).half()
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hkv * d, hkv * d], 1))
+    pos, inv = torch.arange(T, dtype=torch.int32, device=DEV), torch.rand(d // 2, device=DEV)
+    pages, scales = torch.zeros((2, 2, hkv, 4, d), dtype=torch.int8, device=DEV), torch.zeros((2, 2, hkv, 4), device=DEV)
+    slots = i32([0, 1, 2, 8, -3, 5])  # slot 8 lies past the two pages
+    want = sl8.rope_append(q, k, v, pos, inv, slots, pages[0], scales[0], pages[1], scales[1])
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    kept = k.clone()
+    got = sl8.rope_append(q, k, v, pos, inv, i32([0, 1, 2, -1, -3, 5]), pages[0], scales[0], pages[1], scales[1], q_out=q)
+    assert got.data_ptr() == qkv.data_ptr() and torch.equal(got, want) and torch.equal(k, kept)
+    assert int((scales[0] != 0).sum()) == 4 * hkv
+
+
+def test_rope_append_to_a_contiguous_cache():
+    """page_size = Lmax: the contiguous cache of attn_int8_decode."""
+    B, hq, hkv, d, L = 3, 8, 2, 128, 50
+    lens = [50, 1, 33]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    kc, vc = (torch.zeros((B, hkv, 64, d), dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((B, hkv, 64), device=DEV) for _ in range(2))
+    k, v = (torch.randn((B * L, hkv, d), generator=g, device=DEV).bfloat16() for _ in range(2))
+    slots = torch.cat([torch.where(torch.arange(L) < n, torch.arange(L) + 64 * b, -1) for b, n in enumerate(lens)])
+    sl8.rope_append(None, k, v, None, None, i32(slots), kc, ks, vc, vs)
+    want, wants = sl8.quant_rowwise(k.view(B, L, hkv, d).transpose(1, 2).contiguous())
+    for b, n in enumerate(lens):
+        assert torch.equal(kc[b, :, :n], want[b, :, :n]) and torch.equal(ks[b, :, :n], wants[b, :, :n])
+    q = torch.randn((B, hq, d), generator=g, device=DEV).bfloat16()
+    out = sl8.attn_int8_decode(q, kc, ks, vc, vs, i32(lens))
+    assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------------ page bounds
+
+def _pool(rng, num_pages, hkv, page, d):
+    """A page pool with rows of very different scales (some zero) and its tensors."""
+    codes = [rng.integers(-127, 128, (num_pages, hkv, page, d)).astype(np.int8) for _ in range(2)]
+    scales = [(rng.random((num_pages, hkv, page)) * 10.0 ** rng.integers(-3, 1, (num_pages, hkv, page)) * 0.03).astype(np.float32)
+              for _ in range(2)]
+    scales[0][rng.random(scales[0].shape) < 0.05] = 0
+    return codes, scales, [torch.from_numpy(x).to(DEV) for x in codes], [torch.from_numpy(x).to(DEV) for x in scales]
+
+
+def _tables(rng, lens, nb, page, spare=2):
+    need = -(-np.asarray(lens) // page)
+    perm = rng.permutation(int(need.sum()) + spare)
+    table, at = np.full((len(lens), nb), -1), 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, int(need.sum()) + spare
+
+
+@pytest.mark.parametrize("d,hkv,page", [(32, 1, 16), (64, 3, 7), (128, 2, 64), (256, 8, 16), (128, 1, 300)])
+def test_page_bounds(d, hkv, page):
+    rng = np.random.default_rng(d + page)
+    lens = [1, page, page + 1, 3 * page - 1, 4 * page, 0]
+    new = [1, 1, 2, 2 * page, 0, 0]
+    table, num_pages = _tables(rng, lens, 5, page)
+    codes, scales, dk, ds = _pool(rng, num_pages, hkv, page, d)
+    for some in (True, False):
+        bounds = torch.full((num_pages, hkv, 2, d), 99, dtype=torch.int8, device=DEV)
+        bs = torch.full((num_pages, hkv), -3.0, device=DEV)
+        sl8.page_bounds(dk[0], ds[0], i32(table), i32(lens), bounds, bs, new_lens=i32(new) if some else None,
+                        max_new=2 * page if some else None)
+        gb, gs = bounds.cpu().numpy(), bs.cpu().numpy()
+        seen = set()
+        for b, L in enumerate(lens):
+            n = new[b] if some else L
+            for j in range((L - n) // page, -(-L // page)) if n else []:
+                p, rows = table[b, j], min(page, L - j * page)
+                seen.add(p)
+                for h in range(hkv):
+                    lo, hi, s = S.page_bounds(codes[0][p, h, :rows], scales[0][p, h, :rows])
+                    np.testing.assert_array_equal(gb[p, h, 0], lo)
+                    np.testing.assert_array_equal(gb[p, h, 1], hi)
+                    assert gs[p, h] == s
+        rest = [p for p in range(num_pages) if p not in seen]
+        assert np.all(gb[rest] == 99) and np.all(gs[rest] == -3.0)
+
+
+def test_page_bounds_reports_bad_lengths_and_pages():
+    k, ks = torch.ones((2, 1, 16, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1, 16), device=DEV)
+    b, bs = torch.zeros((2, 1, 2, 64), dtype=torch.int8, device=DEV), torch.zeros((2, 1), device=DEV)
+    for table, lens, new in (([[0], [5]], [16, 16], [1, 1]), ([[0], [1]], [16, 17], [1, 1]), ([[0], [1]], [16, 16], [1, 3])):
+        sl8.page_bounds(k, ks, i32(table), i32(lens), b, bs, new_lens=i32(new), max_new=2)
+        assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+        assert bs[0, 0] == 1.0
+
+
+# ------------------------------------------------------------------ page selection
+
+def _bounds_pool(rng, num_pages, hkv, d, coarse=False):
+    lo = rng.integers(-127, 100, (num_pages, hkv, d))
+    hi = np.minimum(127, lo + rng.integers(0, 60, lo.shape))
+    s = rng.random((num_pages, hkv)).astype(np.float32) * 0.02 + 0.01
+    if coarse:  # many equal pages: the scores tie
+        lo, hi, s = lo[rng.integers(0, 3, num_pages)], hi[rng.integers(0, 3, num_pages)], np.full_like(s, 0.5)
+        hi = np.maximum(lo, hi)
+    b = np.stack([lo, hi], 2).astype(np.int8)
+    return b, s, torch.from_numpy(b).to(DEV), torch.from_numpy(s).to(DEV)
+
+
+@pytest.mark.parametrize("B,T,hq,hkv,d,page,nb,max_sel,first,last,dtype,coarse", [
+    (1, 1, 4, 1, 64, 16, 1, 1, 1, 0, torch.bfloat16, False), (3, 1, 32, 8, 128, 64, 40, 8, 1, 2, torch.bfloat16, False),
+    (2, 3, 6, 2, 64, 16, 300, 33, 2, 1, torch.float16, True), (1, 1, 8, 8, 32, 16, 3000, 200, 0, 0, torch.float32, False),
+    (1, 1, 16, 1, 256, 16, 2100, 100, 1, 1, torch.bfloat16, False), (2, 2, 40, 1, 128, 32, 600, 64, 4, 4, torch.float16, False),
+    (1, 1, 2, 1, 64, 16, 9000, 8990, 1, 2, torch.bfloat16, True), (5, 4, 12, 4, 128, 16, 70, 16, 8, 8, torch.bfloat16, False),
+    (2, 1, 64, 1, 32, 16, 520, 1, 0, 1, torch.bfloat16, True), (60, 1, 8, 4, 64, 16, 90, 20, 1, 2, torch.bfloat16, True)])
+def test_page_select(B, T, hq, hkv, d, page, nb, max_sel, first, last, dtype, coarse):
+    rng = np.random.default_rng(B * 1000 + nb)
+    lens = rng.integers(1, nb * page + 1, B)
+    lens[0] = nb * page
+    if B > 1:
+        lens[1] = min(2, nb * page)  # with drafts: fewer tokens than queries
+    if B > 2:
+        lens[2] = 0
+    table, num_pages = _tables(rng, lens, nb, page)
+    b, s, db, ds = _bounds_pool(rng, num_pages, hkv, d, coarse)
+    q = torch.randn((B, T, hq, d), generator=torch.Generator().manual_seed(nb)).to(dtype)
+    q[0, 0, 0] = 0  # a head without a direction scores every page 0
+    scores = torch.full((B, T, hkv, nb), -9.0, device=DEV)
+    out = sl8.page_select(q.to(DEV) if T > 1 else q[:, 0].to(DEV), db, ds, i32(table), i32(lens), page, max_sel, first, last,
+                          scores=scores)
+    plain = sl8.page_select(q.to(DEV), db, ds, i32(table), i32(lens), page, max_sel, first, last)
+    for name in plain:
+        assert torch.equal(out[name], plain[name])
+    blocks, pages, got_lens, sc = (x.cpu().numpy() for x in (out["blocks"], out["pages"], out["lens"], scores))
+    qf, G = q.float().numpy(), hq // hkv
+    for i in range(B):
+        for t in range(T):
+            L = max(0, int(lens[i]) - T + 1 + t)
+            n = -(-L // page)
+            ids = table[i, :n]
+            for h in range(hkv):
+                want = S.page_scores(qf[i, t, h * G:(h + 1) * G], b[ids, h, 0].astype(np.int64), b[ids, h, 1].astype(np.int64),
+                                     s[ids, h]) if n else np.zeros(0, np.float32)
+                np.testing.assert_array_equal(sc[i, t, h, :n], want)
+                assert np.all(sc[i, t, h, n:] == -9.0)
+                kept = S.select(want, max_sel, first, last)
+                np.testing.assert_array_equal(blocks[i, t, h], kept + [-1] * (max_sel - len(kept)))
+                np.testing.assert_array_equal(pages[i, t, h], [*ids[kept]] + [-1] * (max_sel - len(kept)))
+                tokens = sum(page if j < n - 1 else L - (n - 1) * page for j in kept)
+                assert got_lens[i, t, h] == tokens
+
+
+def test_page_select_long_table():
+    """Contexts past what one CTA's shared memory holds, and far more pages than are kept."""
+    nb, page, d = 120000, 16, 32
+    rng = np.random.default_rng(8)
+    b, s, db, ds = _bounds_pool(rng, 1000, 1, d)
+    table = rng.integers(0, 1000, (1, nb))
+    q = torch.randn((1, 2, d), generator=torch.Generator().manual_seed(1))
+    out = sl8.page_select(q.to(DEV), db, ds, i32(table), i32([nb * page - 3]), page, 512, 1, 1)
+    ids = table[0]
+    want = S.page_scores(q[0].numpy(), b[ids, 0, 0].astype(np.int64), b[ids, 0, 1].astype(np.int64), s[ids, 0])
+    kept = S.select(want, 512, 1, 1)
+    np.testing.assert_array_equal(out["blocks"].cpu().numpy()[0, 0, 0], kept)
+    assert out["lens"].item() == 512 * page - 3
+
+
+def test_page_select_reports_bad_lengths_and_pages():
+    b, s = torch.ones((2, 1, 2, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1), device=DEV)
+    q = torch.ones((1, 1, 64), device=DEV)
+    out = sl8.page_select(q, b, s, i32([[0, 1, 7]]), i32([48]), 16, 2, 1, 0)
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["blocks"].tolist() == [[[[0, 1]]]] and out["lens"].item() == 32
+    for L, want in ((49, 48), (-1, 0)):
+        out = sl8.page_select(q, b, s, i32([[0, 1, 0]]), i32([L]), 16, 4, 1, 0)
+        assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+        assert out["lens"].item() == want
+
+
+# ------------------------------------------------------------------ sparse decode
+
+def _check_attention(out, lse, want, wlse, vmax, n):
+    eps = 0 if out.dtype == torch.float32 else torch.finfo(out.dtype).eps / 2
+    err = np.abs(np64(out).reshape(want.shape) - want)
+    tol = (2.0 ** -11 + 2.0 ** -24 * n) * vmax * (1 + eps) + eps * np.abs(want) + 2.0 ** -25
+    assert np.all(err <= tol), (err.max(), np.max(tol))
+    got = np64(lse).reshape(wlse.shape)
+    dead = np.isinf(wlse)
+    assert np.array_equal(got == -np.inf, dead)
+    # logits: an exact integer times three fp32 factors; the sum: ex2.approx (2^-22) of each
+    assert np.all(np.abs(got - wlse)[~dead] <= 1e-5 + 1e-6 * np.abs(wlse[~dead]))
+    assert np.all(np64(out).reshape(want.shape)[dead] == 0)
+
+
+@pytest.mark.parametrize("R,hq,hkv,d,page,max_sel,splits,dtype,odt", [
+    (1, 4, 1, 64, 16, 1, 0, torch.bfloat16, torch.float32), (3, 32, 8, 128, 16, 20, 0, torch.bfloat16, torch.bfloat16),
+    (5, 6, 2, 64, 48, 7, 1, torch.float16, torch.float16), (2, 16, 1, 128, 64, 9, 3, torch.float32, torch.float32),
+    (4, 12, 1, 256, 16, 33, 0, torch.bfloat16, torch.float32), (2, 3, 3, 32, 32, 5, 2, torch.float16, torch.bfloat16),
+    (70, 16, 8, 128, 16, 12, 0, torch.bfloat16, torch.bfloat16), (2, 64, 2, 64, 16, 40, 5, torch.bfloat16, torch.float32),
+    (300, 2, 2, 64, 16, 3, 0, torch.float16, torch.float16)])
+def test_sparse_decode(R, hq, hkv, d, page, max_sel, splits, dtype, odt):
+    rng = np.random.default_rng(R * 31 + d)
+    num_pages = max_sel * 2 + 3
+    codes, scales, dc, ds = _pool(rng, num_pages, hkv, page, d)
+    pages = np.stack([np.stack([rng.permutation(num_pages)[:max_sel] for _ in range(hkv)]) for _ in range(R)])
+    lens = rng.integers(0, max_sel * page + 1, (R, hkv))
+    lens[0] = max_sel * page
+    if R > 1:
+        lens[1] = 0
+        lens[1, 0] = 1
+    # entries past a list are never read
+    for r in range(R):
+        for h in range(hkv):
+            pages[r, h, -(-lens[r, h] // page):] = -1
+    q = torch.randn((R, hq, d), generator=torch.Generator().manual_seed(R)).to(dtype)
+    q[-1, -1] = 0
+    out, lse = sl8.attn_int8_sparse_decode(q.to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens), num_splits=splits,
+                                           out_dtype=odt, return_lse=True)
+    want, wlse = S.sparse_attention(q.float().numpy(), codes[0], scales[0], codes[1], scales[1], pages, lens)
+    vmax = np.abs(codes[1].astype(np.float64) * scales[1][..., None]).max()
+    _check_attention(out, lse, want, wlse, vmax, max_sel * page)
+    again = sl8.attn_int8_sparse_decode(q.to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens), num_splits=splits,
+                                        out_dtype=odt)
+    assert torch.equal(out, again)
+
+
+def test_sparse_decode_of_every_page_is_the_paged_decode():
+    rng = np.random.default_rng(6)
+    B, hq, hkv, d, page, nb = 4, 16, 4, 128, 16, 30
+    lens = [nb * page, 5, 0, 333]
+    table, num_pages = _tables(rng, lens, nb, page)
+    codes, scales, dc, ds = _pool(rng, num_pages, hkv, page, d)
+    q = torch.randn((B, hq, d), generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    out, lse = sl8.attn_int8_sparse_decode(q, dc[0], ds[0], dc[1], ds[1], i32(np.repeat(table[:, None], hkv, 1)),
+                                           i32(np.repeat(np.array(lens)[:, None], hkv, 1)), return_lse=True)
+    want, wl = sl8.attn_int8_paged_decode(q, dc[0], ds[0], dc[1], ds[1], i32(table), i32(lens), return_lse=True)
+    vmax = np.abs(codes[1].astype(np.float64) * scales[1][..., None]).max()
+    # two roundings of the probabilities and of the output apart
+    assert (out.float() - want.float()).abs().max() <= vmax * (2.0 ** -10 + 2.0 ** -8)
+    assert torch.equal(torch.isinf(lse), torch.isinf(wl))
+    live = ~torch.isinf(lse)
+    assert (lse - wl)[live].abs().max() <= 1e-5
+
+
+def test_sparse_decode_reports_bad_pages_and_lengths():
+    k, s = torch.ones((2, 1, 16, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1, 16), device=DEV)
+    q = torch.ones((1, 1, 64), device=DEV)
+    for pages, n in (([[[0, 9]]], 32), ([[[0, 1]]], 33), ([[[0, 1]]], -4)):
+        out = sl8.attn_int8_sparse_decode(q, k, s, k, s, i32(pages), i32([[n]]))
+        assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+        assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------------ one step
+
+def _serving_state(B, hq, hkv, d, page, nb, num_pages, T):
+    z = lambda *n, t=torch.int32: torch.zeros(n, dtype=t, device=DEV)  # noqa: E731
+    return dict(seq=z(B), new=z(B), release=z(B), table=z(B, nb) - 1, free=torch.arange(num_pages, dtype=torch.int32, device=DEV),
+                count=i32([num_pages]), k=z(num_pages, hkv, page, d, t=torch.int8), v=z(num_pages, hkv, page, d, t=torch.int8),
+                ks=z(num_pages, hkv, page, t=torch.float32), vs=z(num_pages, hkv, page, t=torch.float32),
+                bounds=z(num_pages, hkv, 2, d, t=torch.int8), bs=z(num_pages, hkv, t=torch.float32),
+                qkv=z(T, (hq + 2 * hkv) * d, t=torch.bfloat16), dims=(B, hq, hkv, d, page, T))
+
+
+def _serving_step(s, inv, max_sel, plan=None, sel=None, out=None):
+    """One step of one layer: plan, rotary append, bounds, selection and attention of the
+    step's last token of every sequence."""
+    B, hq, hkv, d, page, T = s["dims"]
+    plan = sl8.paged_assign(s["seq"], s["new"], s["table"], s["free"], s["count"], page, T, release=s["release"], out=plan)
+    s["seq"].copy_(plan["seqlens"])
+    s["count"].copy_(plan["free_count"])
+    q, k, v = (x.unflatten(1, (-1, d)) for x in s["qkv"].split([hq * d, hkv * d, hkv * d], 1))
+    q = sl8.rope_append(q, k, v, plan["token_pos"], inv, plan["slot_map"], s["k"], s["ks"], s["v"], s["vs"])
+    sl8.page_bounds(s["k"], s["ks"], s["table"], s["seq"], s["bounds"], s["bs"], new_lens=plan["granted"], max_new=T)
+    last = (plan["cu_new"][1:] - 1).clamp(min=0).long()
+    sel = sl8.page_select(q[last], s["bounds"], s["bs"], s["table"], s["seq"], page, max_sel, out=sel)
+    out = sl8.attn_int8_sparse_decode(q[last], s["k"], s["ks"], s["v"], s["vs"], sel["pages"], sel["lens"], out=out)
+    return plan, sel, out, q
+
+
+def test_a_serving_loop():
+    """Prompts, decode steps, a release and a new request in its slot, against attention in
+    64 bits over the cache's own keys and values; the budget holds every page, then not."""
+    B, hq, hkv, d, page, nb, T = 5, 8, 2, 64, 16, 12, 256
+    for max_sel in (nb, 4):
+        s = _serving_state(B, hq, hkv, d, page, nb, 40, T)
+        inv = (10000.0 ** (-torch.arange(0, d, 2, device=DEV) / d)).float()
+        g = torch.Generator(device=DEV).manual_seed(max_sel)
+        steps = [([60, 33, 1, 100, 0], [0] * 5)] + [([1, 1, 1, 1, 0], [0] * 5)] * 18 + [([1, 20, 1, 1, 16], [0, 1, 0, 0, 0])] + \
+                [([1] * 5, [0] * 5)] * 3
+        for new, release in steps:
+            s["new"].copy_(i32(new))
+            s["release"].copy_(i32(release))
+            s["qkv"].copy_(torch.randn(s["qkv"].shape, generator=g, device=DEV))
+            plan, sel, out, q = _serving_step(s, inv, max_sel)
+        lens = s["seq"].cpu().numpy()
+        assert list(lens) == [82, 23, 23, 122, 19]
+        kn, vn, ksn, vsn = (s[x].cpu().numpy() for x in ("k", "v", "ks", "vs"))
+        last = (plan["cu_new"][1:] - 1).long()
+        pages, n = sel["pages"].cpu().numpy()[:, 0], sel["lens"].cpu().numpy()[:, 0]
+        want, _ = S.sparse_attention(q[last].float().cpu().numpy(), kn, ksn, vn, vsn, pages, n)
+        tol = (2.0 ** -11 + 2.0 ** -24 * nb * page) * 5.0 + 2.0 ** -8 * np.abs(want)
+        assert np.all(np.abs(np64(out) - want) <= tol)
+        # the selection is the definition's over the cache as it stands
+        table = s["table"].cpu().numpy()
+        for b in range(B):
+            nblk = -(-lens[b] // page)
+            for h in range(hkv):
+                box = [S.page_bounds(kn[table[b, j], h, :lens[b] - j * page], ksn[table[b, j], h, :lens[b] - j * page])
+                       for j in range(nblk)]
+                score = S.page_scores(q[last][b].float().cpu().numpy()[h * 4:h * 4 + 4], np.stack([x[0] for x in box]),
+                                      np.stack([x[1] for x in box]), np.array([x[2] for x in box]))
+                kept = S.select(score, max_sel, 1, 2)
+                assert sel["blocks"][b, 0, h].tolist() == kept + [-1] * (max_sel - len(kept))
+
+
+def test_two_captured_steps_and_an_eager_one():
+    """Two graphs of a step over the same buffers, replayed in turn on a side stream, do what
+    eager calls do; graphs of different steps replayed at the same time share nothing."""
+    B, hq, hkv, d, page, nb, T = 3, 8, 2, 64, 16, 20, 8
+    inv = (10000.0 ** (-torch.arange(0, d, 2, device=DEV) / d)).float()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for seed in (1, 2, 3):
+        s = _serving_state(B, hq, hkv, d, page, nb, 60, T)
+        s["new"].fill_(2)
+        _serving_step(s, inv, 3)  # warms up what a capture may not do
+        torch.cuda.synchronize()
+        s["seq"].zero_(), s["table"].fill_(-1), s["count"].fill_(60)
+        s["free"].copy_(torch.arange(60)), s["k"].zero_(), s["v"].zero_(), s["ks"].zero_(), s["vs"].zero_()
+        s["bounds"].zero_(), s["bs"].zero_()
+        g = torch.cuda.CUDAGraph()
+        if seed < 3:
+            with torch.cuda.graph(g):
+                res = _serving_step(s, inv, 3)
+        else:
+            res = None
+        runs.append([s, g, res])
+    for step in range(40):
+        x = torch.randn(runs[0][0]["qkv"].shape, generator=torch.Generator(device=DEV).manual_seed(step), device=DEV)
+        for s, _, _ in runs:
+            s["qkv"].copy_(x)
+        for st in (side, other):
+            st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            runs[0][1].replay()
+        with torch.cuda.stream(other):
+            runs[1][1].replay()
+        runs[2][2] = _serving_step(runs[2][0], inv, 3)
+        for st in (side, other):
+            torch.cuda.current_stream().wait_stream(st)
+        for s, _, res in runs[:2]:
+            for a, b in zip(res[1].values(), runs[2][2][1].values()):
+                assert torch.equal(a, b), step
+            assert torch.equal(res[2], runs[2][2][2]) and torch.equal(s["k"], runs[2][0]["k"]), step
+    assert runs[0][0]["seq"].tolist() == [80] * 3
+
+
+def test_side_stream_and_refusals():
+    q = torch.randn((2, 4, 64), device=DEV).half()
+    pages, scales = torch.ones((2, 3, 2, 16, 64), dtype=torch.int8, device=DEV), torch.ones((2, 3, 2, 16), device=DEV)
+    lists, lens = i32(np.zeros((2, 2, 2))), i32(np.full((2, 2), 20))
+    args = (pages[0], scales[0], pages[1], scales[1], lists, lens)
+    want = sl8.attn_int8_sparse_decode(q, *args)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        got = sl8.attn_int8_sparse_decode(q, *args)
+    st.synchronize()
+    assert torch.equal(got, want)
+    with pytest.raises(ValueError):
+        sl8.attn_int8_sparse_decode(q.transpose(0, 1), *args)
+    with pytest.raises(TypeError):
+        sl8.attn_int8_sparse_decode(q, *args[:4], lists.long(), lens)
+    with pytest.raises(ValueError):
+        sl8.attn_int8_sparse_decode(q, *args[:4], lists, lens[:1])
+    with pytest.raises(sl8.SL8Error):
+        sl8.attn_int8_sparse_decode(q, *args, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    k = torch.randn((4, 2, 64), device=DEV).half()
+    slots = i32([0, 1, 2, 3])
+    with pytest.raises(ValueError):
+        sl8.rope_append(None, k[..., ::2], k[..., ::2], None, None, slots, *args[:4])
+    with pytest.raises(TypeError):
+        sl8.rope_append(None, k, k.float(), None, None, slots, *args[:4])
+    with pytest.raises(ValueError):
+        sl8.rope_append(None, k, k, slots, None, slots, *args[:4])
+    with pytest.raises(ValueError):
+        sl8.rope_append(k, k, k, i32([0, 1, 2]), torch.ones(32, device=DEV), slots, *args[:4])

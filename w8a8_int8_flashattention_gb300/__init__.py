@@ -96,6 +96,15 @@ _SIGNATURES = {
                                                  _P, _P, _P, _P]),
     "sl8_attn_int8_decode_noalloc": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _INT,
                                             _P]),
+    "sl8_paged_assign": (_INT, [_P, _P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _P, _P, _P]),
+    "sl8_rope_append": (_INT, [_P, _P, _P, _INT, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32, _P,
+                               ctypes.c_char_p, _INT, _P, _I64, _P, _P, _P, _P, _P, _I32, _I32, _P]),
+    "sl8_page_bounds": (_INT, [_P, _P, _I32, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "sl8_page_select": (_INT, [_P, _INT, _P, _P, _I32, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                               _I32, _P, _P, _P, _P, _P]),
+    "sl8_attn_int8_sparse_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "sl8_attn_int8_sparse_decode": (_INT, [_P, _INT, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32,
+                                           _I32, _P, _INT, _P, _P, _SZ, _P]),
     "sl8_last_device_status": (_INT, [_P, ctypes.POINTER(_INT)]),
     "sl8_set_spin_limit_ns": (None, [_U64]),
     "sl8_get_spin_limit_ns": (_U64, []),
@@ -522,6 +531,258 @@ def attn_int8_decode_logits_debug(q, k_cache, k_scale, v_cache, v_scale, seqlens
                                                    _ptr(q_codes), _ptr(q_scales), _ptr(o_p), _ptr(l_p),
                                                    _stream(dev)), "sl8_attn_int8_decode_logits_debug")
     return dict(logits=logits, q_codes=q_codes, q_scales=q_scales)
+
+
+# ------------------------------------------------------------------ serving from the paged cache
+
+def _device(*ts) -> torch.device:
+    """The one CUDA device that every given tensor (None aside) lives on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("sl8 takes CUDA tensors only (no CPU fallback)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("sl8 takes tensors of one device")
+    return dev
+
+
+def _typed(dtype, **ts) -> None:
+    """Every given tensor (None aside) is contiguous and of this dtype."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _shaped(t, shape, name) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Call an entry point on the device's current stream, with that device current."""
+    if dev.index == torch.cuda.current_device():
+        _check(getattr(lib(), fn)(*args, _stream(dev)), fn)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(lib(), fn)(*args, _stream(dev)), fn)
+
+
+def paged_assign(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, max_tokens, release=None,
+                 out=None):
+    """The page plan of one serving step: block tables, slot map and free list from request
+    lengths.  ctx_lens, new_lens [B] int32; release [B] int32 (nonzero: the slot's request
+    has ended, its pages go back first); block_table [B, max_blocks] and free_pages
+    [capacity] are updated, free_count [1] int32 is read.  Returns a dict of int32 tensors:
+    seqlens, granted [B], cu_new [B + 1], slot_map, token_pos [max_tokens], free_count [1]
+    (out: a dict returned earlier, whose tensors are written again)."""
+    dev = _device(ctx_lens, new_lens, block_table, free_pages, free_count, release)
+    _typed(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages,
+           free_count=free_count, release=release)
+    B, max_blocks = block_table.shape
+    max_tokens = int(max_tokens)
+    if ctx_lens.numel() != B or new_lens.numel() != B or (release is not None and release.numel() != B):
+        raise ValueError("ctx_lens, new_lens and release need one entry per row of block_table")
+    if out is None:
+        sizes = dict(seqlens=B, granted=B, cu_new=B + 1, slot_map=max_tokens, token_pos=max_tokens, free_count=1)
+        out = {n: torch.empty(size, dtype=torch.int32, device=dev) for n, size in sizes.items()}
+    else:
+        _device(ctx_lens, *out.values())
+        _typed(torch.int32, **out)
+        if (out["seqlens"].numel() != B or out["granted"].numel() != B or out["cu_new"].numel() != B + 1 or
+                out["slot_map"].numel() != max_tokens or out["token_pos"].numel() != max_tokens):
+            raise ValueError("out holds tensors of another batch or max_tokens")
+    _call("sl8_paged_assign", dev, _ptr(ctx_lens), _ptr(new_lens), _ptr(release), B, int(page_size), max_blocks,
+          _ptr(block_table), _ptr(free_pages), free_pages.numel(), _ptr(free_count), _ptr(out["free_count"]),
+          max_tokens, _ptr(out["seqlens"]), _ptr(out["granted"]), _ptr(out["cu_new"]), _ptr(out["slot_map"]),
+          _ptr(out["token_pos"]))
+    return out
+
+
+def _tokens(x, name, d=None):
+    """(heads, d, stride in elements) of [T, H, d] whose tokens may be strided."""
+    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError(f"{name} must be [T, heads, d] with each token's heads contiguous")
+    if d is not None and x.shape[2] != d:
+        raise ValueError(f"{name} has head dim {x.shape[2]}, not {d}")
+    return x.shape[1], x.shape[2], (x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2])
+
+
+def _pages_of(k_pages, k_scale_pages, v_pages=None, v_scale_pages=None):
+    _typed(torch.int8, k_pages=k_pages, v_pages=v_pages)
+    _typed(torch.float32, k_scale_pages=k_scale_pages, v_scale_pages=v_scale_pages)
+    num_pages, hkv, page_size, d = k_pages.shape
+    _shaped(k_scale_pages, (num_pages, hkv, page_size), "k_scale_pages")
+    if v_pages is not None:
+        _shaped(v_pages, (num_pages, hkv, page_size, d), "v_pages")
+        _shaped(v_scale_pages, (num_pages, hkv, page_size), "v_scale_pages")
+    return num_pages, hkv, page_size, d
+
+
+def rope_pair_axis(sections, interleaved=False) -> bytes:
+    """The axis of each rotary pair for rope_append: sections[a] pairs turn with axis a, in
+    that order, or (interleaved) dealt out in turn until an axis has all of its pairs."""
+    if not interleaved:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    left, pairs = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                pairs.append(a)
+                left[a] -= 1
+    return bytes(pairs)
+
+
+def rope_append(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, v_pages, v_scale_pages,
+                pair_axis=None, adjacent=False, q_out=None):
+    """Rotary positions and the int8 append: q [T,Hq,d] and k [T,Hkv,d] are rotated, k and v
+    quantised per row and stored at slot_map [T] int32 (negative: not stored) of the pages
+    [num_pages,Hkv,page_size,d] int8 with scales [num_pages,Hkv,page_size].  positions int32
+    [T] or [axes,T]; inv_freq fp32 [rot_dim / 2]; pair_axis (bytes or ints, one per pair;
+    see rope_pair_axis) for several axes; adjacent: pairs (2p, 2p+1) instead of halves.
+    positions = inv_freq = None: no rotation.  q may be None.  Returns the rotated q (q_out,
+    which may be q itself)."""
+    dev = _device(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, v_pages, v_scale_pages, q_out)
+    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages, v_pages, v_scale_pages)
+    _typed(torch.int32, positions=positions, slot_map=slot_map)
+    _typed(torch.float32, inv_freq=inv_freq)
+    T = k.shape[0]
+    if _tokens(k, "k", d)[0] != hkv or _tokens(v, "v", d)[0] != hkv or v.shape[0] != T or slot_map.numel() != T:
+        raise ValueError("k, v and slot_map must hold the same tokens, with the pages' kv heads")
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have one dtype")
+    hq = q_stride = out_stride = 0
+    if q is not None:
+        hq, _, q_stride = _tokens(q, "q", d)
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
+        if q.shape[0] != T or q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("q and q_out must be alike and hold k's tokens")
+        out_stride = _tokens(q_out, "q_out", d)[2]
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if positions is not None and positions.numel() != axes * T:
+        raise ValueError("positions must be [T] or [axes, T]")
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != rot // 2:
+            raise ValueError("pair_axis needs one entry per rotary pair")
+    _call("sl8_rope_append", dev, _ptr(q), _ptr(k), _ptr(v), _dt(k), q_stride, _tokens(k, "k")[2], _tokens(v, "v")[2], T,
+          hq, hkv, d, _ptr(positions), axes, rot, _ptr(inv_freq), pair_axis, int(bool(adjacent)), _ptr(q_out), out_stride,
+          _ptr(slot_map), _ptr(k_pages), _ptr(k_scale_pages), _ptr(v_pages), _ptr(v_scale_pages), num_pages, page_size)
+    return q_out
+
+
+def _bounds_of(bounds, bound_scale, num_pages, hkv, d):
+    _typed(torch.int8, bounds=bounds)
+    _typed(torch.float32, bound_scale=bound_scale)
+    _shaped(bounds, (num_pages, hkv, 2, d), "bounds")
+    _shaped(bound_scale, (num_pages, hkv), "bound_scale")
+
+
+def page_bounds(k_pages, k_scale_pages, block_table, seqlens, bounds, bound_scale, new_lens=None, max_new=None):
+    """Per-channel key bounds (bounds [num_pages,Hkv,2,d] int8, bound_scale [num_pages,Hkv]
+    fp32, updated) of the pages that the last new_lens [B] int32 tokens of each sequence lie
+    in (max_new: a host int >= every entry), or of every page without new_lens.
+    seqlens [B] int32 counts the new tokens."""
+    dev = _device(k_pages, k_scale_pages, block_table, seqlens, bounds, bound_scale, new_lens)
+    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages)
+    _bounds_of(bounds, bound_scale, num_pages, hkv, d)
+    _typed(torch.int32, block_table=block_table, seqlens=seqlens, new_lens=new_lens)
+    B, max_blocks = block_table.shape
+    if seqlens.numel() != B or (new_lens is not None and new_lens.numel() != B):
+        raise ValueError("seqlens and new_lens need one entry per row of block_table")
+    if (new_lens is None) != (max_new is None):
+        raise ValueError("new_lens and max_new go together")
+    _call("sl8_page_bounds", dev, _ptr(k_pages), _ptr(k_scale_pages), num_pages, page_size, _ptr(block_table), max_blocks,
+          _ptr(seqlens), _ptr(new_lens), 0 if max_new is None else int(max_new), B, hkv, d, _ptr(bounds),
+          _ptr(bound_scale))
+
+
+def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel, first=1, last=2, out=None,
+                scores=None):
+    """The max_sel pages of each query and kv head whose keys can reach the largest logits,
+    the first `first` and last `last` ones always among them.  q [B,Hq,d] (the decode's
+    queries) or [B,T,Hq,d] (query t at position seqlens - T + t); bounds as page_bounds leaves
+    them.  Returns a dict of int32 tensors: blocks and pages [B,T,Hkv,max_sel] (ascending
+    blocks; -1 past the list) and lens [B,T,Hkv], the tokens listed (out: a dict returned
+    earlier, written again).  scores fp32 [B,T,Hkv,max_blocks] receives the pages' scores."""
+    dev = _device(q, bounds, bound_scale, block_table, seqlens, scores)
+    _need_cuda(q)
+    num_pages, hkv, _, d = bounds.shape
+    _bounds_of(bounds, bound_scale, num_pages, hkv, d)
+    _typed(torch.int32, block_table=block_table, seqlens=seqlens)
+    _typed(torch.float32, scores=scores)
+    B, max_blocks = block_table.shape
+    T, hq = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
+    if q.shape[0] != B or q.shape[-1] != d or seqlens.numel() != B:
+        raise ValueError("q, block_table, seqlens and bounds do not belong together")
+    max_sel = int(max_sel)
+    if out is None:
+        out = {"blocks": torch.empty((B, T, hkv, max_sel), dtype=torch.int32, device=dev),
+               "pages": torch.empty((B, T, hkv, max_sel), dtype=torch.int32, device=dev),
+               "lens": torch.empty((B, T, hkv), dtype=torch.int32, device=dev)}
+    else:
+        _device(q, *out.values())
+        _typed(torch.int32, **out)
+        if out["blocks"].numel() != B * T * hkv * max_sel or out["pages"].numel() != B * T * hkv * max_sel or \
+                out["lens"].numel() != B * T * hkv:
+            raise ValueError("out holds tensors of another shape")
+    if scores is not None:
+        _shaped(scores, (B, T, hkv, max_blocks), "scores")
+    _call("sl8_page_select", dev, _ptr(q), _dt(q), _ptr(bounds), _ptr(bound_scale), num_pages, int(page_size),
+          _ptr(block_table), max_blocks, _ptr(seqlens), B, T, hq, hkv, d, max_sel, int(first), int(last),
+          _ptr(out["blocks"]), _ptr(out["pages"]), _ptr(out["lens"]), _ptr(scores))
+    return out
+
+
+def sparse_decode_workspace_bytes(rows: int, Hq: int, Hkv: int, max_sel: int, page_size: int, d: int,
+                                  num_splits: int = 0) -> int:
+    return int(lib().sl8_attn_int8_sparse_decode_workspace_size(rows, Hq, Hkv, max_sel, page_size, d, num_splits))
+
+
+def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, pages, lens, num_splits=0,
+                            out_dtype=None, return_lse=False, workspace=None, out=None, lse=None):
+    """Decode attention of each query over a page list of its own per kv head: q [B,Hq,d] or
+    [B,T,Hq,d], pages [B(,T),Hkv,max_sel] int32 and lens [B(,T),Hkv] int32 as page_select
+    returns them (or from any other policy: full pages, the last one up to the length).
+    Returns out like q (dtype q.dtype unless given) and, with return_lse, the fp32 LSE.
+    workspace: uint8, at least sparse_decode_workspace_bytes."""
+    dev = _device(q, k_pages, k_scale_pages, v_pages, v_scale_pages, pages, lens, workspace, out, lse)
+    _need_cuda(q, workspace, out, lse)
+    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages, v_pages, v_scale_pages)
+    _typed(torch.int32, pages=pages, lens=lens)
+    _typed(torch.float32, lse=lse)
+    hq, max_sel = q.shape[-2], pages.shape[-1]
+    rows = q.numel() // (hq * d) if hq * d else 0
+    if q.shape[-1] != d or lens.numel() != rows * hkv or pages.numel() != rows * hkv * max_sel:
+        raise ValueError("q, pages and lens do not belong together")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if return_lse:
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        elif lse.shape != q.shape[:-1]:
+            raise ValueError("lse must have one entry per query head")
+    if workspace is None:
+        workspace = torch.empty(max(sparse_decode_workspace_bytes(rows, hq, hkv, max_sel, page_size, d, num_splits), 16),
+                                dtype=torch.uint8, device=dev)
+    _call("sl8_attn_int8_sparse_decode", dev, _ptr(q), _dt(q), _ptr(k_pages), _ptr(k_scale_pages), _ptr(v_pages),
+          _ptr(v_scale_pages), num_pages, page_size, _ptr(pages), _ptr(lens), max_sel, rows, hq, hkv, d, num_splits,
+          _ptr(out), _dt(out), _ptr(lse) if return_lse else None, _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+    return (out, lse) if return_lse else out
 
 
 # ------------------------------------------------------------------ status / tracing

@@ -894,6 +894,202 @@ int sl8_attn_int8_decode_logits_debug(const void* q, int q_dtype, const int8_t* 
                        lse_partial, logits_out, q_codes, q_scales, stream);
 }
 
+// ---------------------------------------------------------------- paged cache: plan, append, bounds, selection
+int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
+                     int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,
+                     int32_t free_capacity, const int32_t* free_count, int32_t* free_count_out, int32_t max_tokens,
+                     int32_t* seqlens, int32_t* granted, int32_t* cu_new, int32_t* slot_map, int32_t* token_pos,
+                     void* stream) {
+  SL8_CHECK(B >= 0 && page_size > 0 && max_blocks > 0 && free_capacity >= 0 && max_tokens >= 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(free_count && free_count_out && cu_new, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(B == 0 || (ctx_lens && new_lens && block_table && seqlens && granted), SL8_ERR_INVALID_ARG);
+  SL8_CHECK((free_capacity == 0 || free_pages) && (max_tokens == 0 || slot_map), SL8_ERR_INVALID_ARG);
+  SL8_LAUNCH(launch_paged_assign(ctx_lens, new_lens, release, B, page_size, max_blocks, block_table, free_pages,
+                                 free_capacity, free_count, free_count_out, max_tokens, seqlens, granted, cu_new,
+                                 slot_map, token_pos, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
+                    int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
+                    int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis, int adjacent,
+                    void* q_out, int64_t q_out_stride, const int32_t* slot_map, int8_t* k_pages, float* k_scale_pages,
+                    int8_t* v_pages, float* v_scale_pages, int32_t num_pages, int32_t page_size, void* stream) {
+  SL8_CHECK(dtype == SL8_F16 || dtype == SL8_BF16 || dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(T >= 0 && Hq >= 0 && Hkv > 0 && d > 0 && num_pages > 0 && page_size > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(rot_dim >= 0 && rot_dim <= d, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(rot_dim % 8 == 0 && axes <= 4, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(Hq <= (1 << 16) && Hkv <= (1 << 16), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(rot_dim == 0 || axes >= 1, SL8_ERR_INVALID_ARG);
+  // several axes need to know whose each pair is
+  SL8_CHECK(rot_dim == 0 || axes == 1 || pair_axis, SL8_ERR_INVALID_ARG);
+  if (pair_axis)
+    for (int i = 0; i < rot_dim / 2; ++i) SL8_CHECK(pair_axis[i] < axes, SL8_ERR_INVALID_ARG);
+  if (T == 0) return SL8_OK;
+  SL8_CHECK(k && v && slot_map && k_pages && v_pages && k_scale_pages && v_scale_pages, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(Hq == 0 || (q && q_out), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(rot_dim == 0 || (positions && inv_freq), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(q_out) && aligned16(k_pages) && aligned16(v_pages),
+            SL8_ERR_INVALID_ARG);
+  // rows are read and written in 16-byte steps
+  const int64_t step = dtype == SL8_F32 ? 4 : 8;
+  SL8_CHECK(k_stride >= static_cast<int64_t>(Hkv) * d && v_stride >= static_cast<int64_t>(Hkv) * d, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(k_stride % step == 0 && v_stride % step == 0, SL8_ERR_INVALID_ARG);
+  if (Hq > 0) {
+    SL8_CHECK(q_stride >= static_cast<int64_t>(Hq) * d && q_out_stride >= static_cast<int64_t>(Hq) * d,
+              SL8_ERR_INVALID_ARG);
+    SL8_CHECK(q_stride % step == 0 && q_out_stride % step == 0, SL8_ERR_INVALID_ARG);
+  }
+  // one warp per part of a token, at most one part per row group
+  SL8_CHECK(static_cast<int64_t>(T) * (Hq + 2 * static_cast<int64_t>(Hkv)) < (int64_t(1) << 33), SL8_ERR_UNSUPPORTED);
+  RopeAppendArgs r{};
+  r.q = q;
+  r.k = k;
+  r.v = v;
+  r.dtype = static_cast<sl8_dtype>(dtype);
+  r.q_stride = q_stride;
+  r.k_stride = k_stride;
+  r.v_stride = v_stride;
+  r.T = T;
+  r.Hq = Hq;
+  r.Hkv = Hkv;
+  r.d = d;
+  r.positions = positions;
+  r.axes = axes;
+  r.rot_dim = rot_dim;
+  r.inv_freq = inv_freq;
+  r.pair_axis = rot_dim ? pair_axis : nullptr;
+  r.adjacent = adjacent != 0;
+  r.q_out = q_out;
+  r.q_out_stride = q_out_stride;
+  r.slot_map = slot_map;
+  r.k_pages = k_pages;
+  r.k_scale = k_scale_pages;
+  r.v_pages = v_pages;
+  r.v_scale = v_scale_pages;
+  r.num_pages = num_pages;
+  r.page_size = page_size;
+  SL8_LAUNCH(launch_rope_append(r, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,
+                    const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens, const int32_t* new_lens,
+                    int32_t max_new, int32_t B, int32_t Hkv, int32_t d, int8_t* bounds, float* bound_scale,
+                    void* stream) {
+  SL8_CHECK(B >= 0 && Hkv > 0 && d > 0 && num_pages > 0 && page_size > 0 && max_blocks > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(!new_lens || max_new >= 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(B) * max_blocks <= (int64_t(1) << 33) / Hkv, SL8_ERR_UNSUPPORTED);
+  if (B == 0 || (new_lens && max_new == 0)) return SL8_OK;
+  SL8_CHECK(k_pages && k_scale_pages && block_table && seqlens && bounds && bound_scale, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(k_pages) && aligned16(bounds), SL8_ERR_INVALID_ARG);
+  SL8_LAUNCH(launch_page_bounds(k_pages, k_scale_pages, num_pages, page_size, block_table, max_blocks, seqlens, new_lens,
+                                max_new, B, Hkv, d, bounds, bound_scale, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const float* bound_scale, int32_t num_pages,
+                    int32_t page_size, const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens, int32_t B,
+                    int32_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_sel, int32_t first, int32_t last,
+                    int32_t* sel_blocks, int32_t* sel_pages, int32_t* sel_lens, float* scores, void* stream) {
+  SL8_CHECK(q_dtype == SL8_F16 || q_dtype == SL8_BF16 || q_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(B >= 0 && T >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && d > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(num_pages > 0 && page_size > 0 && max_blocks > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(first >= 0 && last >= 0 && max_sel > 0 && first <= max_sel && last <= max_sel - first, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(Hq / Hkv <= 64, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31) &&
+                static_cast<int64_t>(page_size) * max_sel < (int64_t(1) << 31),
+            SL8_ERR_UNSUPPORTED);
+  if (B == 0 || T == 0) return SL8_OK;
+  SL8_CHECK(static_cast<int64_t>(B) * T <= (int64_t(1) << 27) / Hkv, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(q && bounds && bound_scale && block_table && seqlens && sel_blocks && sel_pages && sel_lens,
+            SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(q) && aligned16(bounds), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(page_select_fits(static_cast<int64_t>(B) * T * Hkv, max_blocks, d, Hq / Hkv), SL8_ERR_UNSUPPORTED);
+  SL8_LAUNCH(launch_page_select(q, static_cast<sl8_dtype>(q_dtype), bounds, bound_scale, num_pages, page_size,
+                                block_table, max_blocks, seqlens, B, T, Hq, Hkv, d, max_sel, first, last, sel_blocks,
+                                sel_pages, sel_lens, scores, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+// Split count of the decode over page lists: the plan of rows * Hkv sequences of one kv
+// head; 0 for an invalid or unsupported shape.
+static int32_t list_splits(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel, int32_t page_size, int32_t d,
+                           int32_t num_splits) {
+  if (rows <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_sel <= 0 || page_size <= 0) return 0;
+  if (static_cast<int64_t>(max_sel) * page_size >= (int64_t(1) << 31) || page_size % 16) return 0;
+  if (static_cast<int64_t>(rows) > (int64_t(1) << 27) / Hq) return 0;
+  return sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, num_splits);
+}
+
+static size_t list_lse_offset(int32_t rows, int32_t Hq, int32_t d, int32_t S) {
+  return align_up(static_cast<size_t>(rows) * Hq * S * d * sizeof(float), 256);
+}
+
+size_t sl8_attn_int8_sparse_decode_workspace_size(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel,
+                                                  int32_t page_size, int32_t d, int32_t num_splits) {
+  const int32_t S = list_splits(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
+  return S > 0 ? list_lse_offset(rows, Hq, d, S) + static_cast<size_t>(rows) * Hq * S * sizeof(float) : 0;
+}
+
+int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_pages, const float* k_scale_pages,
+                                const int8_t* v_pages, const float* v_scale_pages, int32_t num_pages, int32_t page_size,
+                                const int32_t* page_list, const int32_t* list_lens, int32_t max_sel, int32_t rows,
+                                int32_t Hq, int32_t Hkv, int32_t d, int32_t num_splits, void* out, int out_dtype,
+                                float* lse_out, void* workspace, size_t workspace_bytes, void* stream) {
+  SL8_CHECK(q_dtype == SL8_F16 || q_dtype == SL8_BF16 || q_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(out_dtype == SL8_F16 || out_dtype == SL8_BF16 || out_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(rows >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && d > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(num_pages > 0 && page_size > 0 && max_sel > 0 && num_splits >= 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(decode_head_dim_ok(d) && page_size % 16 == 0, SL8_ERR_UNSUPPORTED);
+  if (rows == 0) return SL8_OK;
+  SL8_CHECK(q && k_pages && k_scale_pages && v_pages && v_scale_pages && page_list && list_lens && out,
+            SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(q) && aligned16(k_pages) && aligned16(v_pages) && aligned16(k_scale_pages) &&
+                aligned16(v_scale_pages),
+            SL8_ERR_INVALID_ARG);
+  SL8_CHECK(static_cast<int64_t>(num_pages) * Hkv < (int64_t(1) << 31) / page_size, SL8_ERR_UNSUPPORTED);
+  const int32_t S = list_splits(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
+  SL8_CHECK(S > 0, SL8_ERR_UNSUPPORTED);
+  const size_t need = sl8_attn_int8_sparse_decode_workspace_size(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
+  SL8_CHECK(workspace && workspace_bytes >= need && aligned16(workspace), SL8_ERR_WORKSPACE);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DecodeArgs a{};
+  a.q = q;
+  a.q_dtype = static_cast<sl8_dtype>(q_dtype);
+  a.k_cache = k_pages;
+  a.k_scale = k_scale_pages;
+  a.v_cache = v_pages;
+  a.v_scale = v_scale_pages;
+  a.seqlens = list_lens;
+  a.B = rows * Hkv;
+  a.Hq = Hq / Hkv;
+  a.kv_groups = decode_kv_groups(a.Hq, 1);
+  a.Hkv = a.kv_groups;
+  a.Lmax = max_sel * page_size;
+  a.d = d;
+  a.num_splits = S;
+  a.split_size = split_size_for(a.Lmax, S, d);
+  a.o_partial = static_cast<float*>(workspace);
+  a.lse_partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + list_lse_offset(rows, Hq, d, S));
+  a.verify_dps = a.verify_ng = 1;
+  a.block_table = page_list;
+  a.page_size = page_size;
+  a.max_blocks = max_sel;
+  a.num_pages = num_pages;
+  a.list_heads = Hkv;
+  SL8_LAUNCH(launch_decode_split(a, s));
+  SL8_LAUNCH(launch_decode_combine(a.o_partial, a.lse_partial, list_lens, a.B, a.Hq, d, S, a.split_size, out,
+                                   static_cast<sl8_dtype>(out_dtype), lse_out, s));
+  return SL8_OK;
+}
+
 int sl8_last_device_status(void* stream, int* site) {
   if (site) *site = 0;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SL8_ERR_CUDA;

@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     uint32_t k = 0, n = 0;  // stages issued, current slot
     bool ok = true, sorted = !balanced;
     // the next entry of the slot list for this CTA: entry blockIdx.x first, then claims
-    int64_t first = blockIdx.x;
+    // (page lists: entries blockIdx.x + i * gridDim.x, no claims)
+    int64_t first = blockIdx.x, last = 0;
     uint32_t pending = 0;  // claim in flight (valid when claiming)
     bool claiming = false, exhausted = static_cast<int64_t>(blockIdx.x) >= total;
     auto next_entry = [&](Slot& x) {
@@ -447,6 +448,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         if (first >= 0) {
           j = first;
           first = -1;
+        } else if (a.list_heads) {
+          j = last + gridDim.x;
         } else {
           if (!claiming) {
             if (lane == 0) pending = atomicAdd(counter, 1u);
@@ -459,9 +462,12 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
           exhausted = true;
           break;
         }
+        last = j;
         // start the following claim now; its result is read at the next call
-        if (lane == 0) pending = atomicAdd(counter, 1u);
-        claiming = true;
+        if (!a.list_heads) {
+          if (lane == 0) pending = atomicAdd(counter, 1u);
+          claiming = true;
+        }
         if (balanced && j >= sc->n_full && !sorted) {
           sorted = warp_wait(sched_sorted, 0, limit_ns, st, 48);
           if (!sorted) {
@@ -539,8 +545,10 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
               record_status(st, kStatusBadArg, 49);
               pg = 0;
             }
-            const int64_t prow = (static_cast<int64_t>(pg) * (a.Hkv / a.kv_groups) + cur.hkv / a.kv_groups) * a.page_size +
-                                 t % a.page_size;
+            const int64_t prow =
+                (a.list_heads ? static_cast<int64_t>(pg) * a.list_heads + cur.b % a.list_heads
+                              : static_cast<int64_t>(pg) * (a.Hkv / a.kv_groups) + cur.hkv / a.kv_groups) * a.page_size +
+                t % a.page_size;
             for (int r = 0; r < rows;) {
               const int left = rows - r;
               const int i = left >= 128 ? 3 : left >= 64 ? 2 : left >= 32 ? 1 : 0;
@@ -587,7 +595,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     }
     // This CTA claims no more; a claim still in flight is part of the count.  The last
     // CTA of the launch resets the ticket's counters.
-    if (lane == 0) {
+    if (lane == 0 && !a.list_heads) {
       if (claiming) {
         volatile uint32_t settled = pending;  // the claim in flight has completed
         (void)settled;
@@ -1228,7 +1236,8 @@ cudaError_t launch_split_d(const DecodeArgs& a, cudaStream_t s) {
   // C::kChunk rows x kBW bytes; a paged cache as [num_pages * Hkv * page_size rows][d],
   // loaded in boxes of one 16-token unit
   const bool paged = a.block_table != nullptr;
-  const uint64_t hkv_cache = static_cast<uint64_t>(a.Hkv / a.kv_groups);  // kv heads the cache holds
+  // kv heads the cache holds
+  const uint64_t hkv_cache = static_cast<uint64_t>(a.list_heads ? a.list_heads : a.Hkv / a.kv_groups);
   const uint64_t rows = paged ? static_cast<uint64_t>(a.num_pages) * hkv_cache * a.page_size
                               : static_cast<uint64_t>(a.B) * hkv_cache * a.Lmax;
   bool ok = true;

@@ -149,6 +149,45 @@ cudaError_t launch_export_codes(const uint16_t* codes, const float* scales, bool
                                 int32_t N, int32_t d, const SeqTable& t, int64_t t_pad_max, int8_t* codes_out,
                                 float* scales_out, cudaStream_t s, int32_t d_io = 0);
 
+// ---- the paged cache's bookkeeping, writes and page selection (paged.cu, select.cu);
+// arguments as the entry points of sl8.h
+cudaError_t launch_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
+                                int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,
+                                int32_t free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                                int32_t max_tokens, int32_t* seqlens, int32_t* granted, int32_t* cu_new,
+                                int32_t* slot_map, int32_t* token_pos, cudaStream_t s);
+struct RopeAppendArgs {
+  const void *q, *k, *v;
+  sl8_dtype dtype;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t T, Hq, Hkv, d;
+  const int32_t* positions;
+  int32_t axes, rot_dim;
+  const float* inv_freq;
+  const uint8_t* pair_axis;  // host, nullable
+  bool adjacent;
+  void* q_out;
+  int64_t q_out_stride;
+  const int32_t* slot_map;
+  int8_t* k_pages;
+  float* k_scale;
+  int8_t* v_pages;
+  float* v_scale;
+  int32_t num_pages, page_size;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s);
+cudaError_t launch_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,
+                               const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
+                               const int32_t* new_lens, int32_t max_new, int32_t B, int32_t Hkv, int32_t d,
+                               int8_t* bounds, float* bound_scale, cudaStream_t s);
+// Whether the keys of a row's pages fit the shared memory of the largest cluster.
+bool page_select_fits(int64_t rows, int32_t max_blocks, int32_t d, int32_t group);
+cudaError_t launch_page_select(const void* q, sl8_dtype q_dtype, const int8_t* bounds, const float* bound_scale,
+                               int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seqlens, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                               int32_t max_sel, int32_t first, int32_t last, int32_t* sel_blocks, int32_t* sel_pages,
+                               int32_t* sel_lens, float* scores, cudaStream_t s);
+
 struct PrefillArgs {
   const uint16_t* q_codes;  // [Hq][t_pad][d] bf16 codes
   const float* q_scales;    // [Hq][t_pad]
@@ -228,6 +267,13 @@ struct DecodeArgs {
   // its query columns are heads hv * (Hq / Hkv) + c, i.e. consecutive groups of the cache
   // head's query heads.  1 otherwise.
   int32_t kv_groups;
+  // page lists per kv head (list_heads > 0, paged only): the pages hold list_heads kv heads
+  // and B counts the virtual sequences v = row * list_heads + kv head, each with one kv
+  // head of its own (Hq = the group's query heads, Hkv = kv_groups): block_table row v
+  // lists the pages that v reads and seqlens[v] the tokens they hold, the pages all full
+  // but the last one listed.  The work slots are dealt out in turn instead of claimed, so
+  // that launches replayed from several graphs share no counter.
+  int32_t list_heads;
 };
 cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_combine(const float* o_partial, const float* lse_partial, const int32_t* seqlens,
