@@ -496,11 +496,12 @@ SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, i
  *   sel_pages    device, the same of their pages (block_table entries), -1 after;
  *   sel_lens     device, [B][T][Hkv] int32: the tokens that the list holds for the query:
  *                its pages are full but the query's own last one.
- *   scores       device, nullable, [B][T][Hkv][max_blocks] fp32: the scores of the query's
- *                blocks (entries past them are left).
- * The same selection on every run.  Hq / Hkv <= 64; about 400,000 blocks a sequence at most
- * (SL8_ERR_UNSUPPORTED).  A length or page out of range is recorded (SL8_ERR_DEVICE_ARG)
- * and clamped, or read as page 0.
+ *   scores       device, nullable, [B][T][Hkv][max_blocks] fp32: receives the scores of the
+ *                blocks of every range of more than max_sel (all else is left).
+ * The same selection on every run.  Hq / Hkv <= 64, B * T * Hkv <= 2^27 and some 190,000
+ * blocks a sequence at most (SL8_ERR_UNSUPPORTED).  A length out of range, or a page out of
+ * range that is scored, is recorded (SL8_ERR_DEVICE_ARG) and clamped, or scored as page 0
+ * (and listed as that).
  */
 SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const float* bound_scale,
                             int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,
@@ -510,18 +511,22 @@ SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, co
 
 /*
  * Sparse decode: attention of each query row over a page list of its own per kv head, split
- * over the list and combined (partials in the workspace).
+ * over the list and merged.
  *   q            device, [rows][Hq][d] of q_dtype (F16, BF16 or F32), quantised per row.
  *   page_list    device, [rows][Hkv][max_sel] int32 pages, as sl8_page_select's sel_pages or
  *                from any other policy; list_lens device, [rows][Hkv] int32: the tokens that
  *                the list holds, 0 .. max_sel * page_size: every page of the list is full
  *                but the last one.  Entries past the list are not read.
  *   pages        as sl8_attn_int8_paged_decode_splitkv (page_size a multiple of 16).
- *   num_splits   requested splits of each list (0 = automatic).
+ *   num_splits   requested splits of each list (0 = automatic).  Up to 8 run as one launch,
+ *                a cluster of CTAs per list that merges its parts itself; more, which pays
+ *                for a few long lists, as the split kernel and the combine.
  *   out          device, [rows][Hq][d] of out_dtype; a row whose list is empty gets 0.
  *   lse_out      device, nullable, [rows][Hq] fp32 (natural log; -inf for an empty list).
- *   workspace    at least sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
- *                unsupported shape); launches that run at the same time need their own.
+ *   workspace    for more than 8 splits, at least
+ *                sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
+ *                unsupported shape; 16: none is used and it may be null); launches that run
+ *                at the same time need their own.
  * Any Hq that is a multiple of Hkv (above 8 heads a group, each 8 read the list again).  A
  * page outside [0, num_pages) or a length out of range is recorded (SL8_ERR_DEVICE_ARG), and
  * page 0 read or the length clamped.

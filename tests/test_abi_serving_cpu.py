@@ -98,14 +98,16 @@ def test_sparse_decode(lib, p):
         assert f(*_changed(ok, change)) == INVALID, change
     for change in ({14: 96}, {7: 24}, {6: 1 << 20, 7: 1 << 11}):
         assert f(*_changed(ok, change)) == UNSUPPORTED, change
-    need = sl8.sparse_decode_workspace_bytes(2, 8, 2, 8, 16, 128)
-    assert need >= 2 * 8 * 129 * 4
-    assert f(*_changed(ok, {20: need - 1})) == WORKSPACE and f(*_changed(ok, {19: None})) == WORKSPACE
-    assert f(*_changed(ok, {19: p + 8})) == WORKSPACE
+    assert sl8.sparse_decode_workspace_bytes(2, 8, 2, 8, 16, 128) == 16  # one launch, nothing kept
+    long = _changed(ok, {10: 64, 15: 20})  # 20 splits of 1,024 tokens
+    need = sl8.sparse_decode_workspace_bytes(2, 8, 2, 64, 16, 128, 20)
+    assert need >= 2 * 8 * 129 * 4 * 16
+    for change in ({20: need - 1}, {19: None}, {19: p + 8}):
+        assert f(*_changed(long, change)) == WORKSPACE, change
     size = lib.sl8_attn_int8_sparse_decode_workspace_size
     assert size(2, 8, 2, 8, 24, 128, 0) == 0 and size(0, 8, 2, 8, 16, 128, 0) == 0 and size(2, 7, 2, 8, 16, 128, 0) == 0
     # more splits need more room
-    assert size(1, 8, 1, 512, 64, 128, 64) > size(1, 8, 1, 512, 64, 128, 1)
+    assert size(1, 8, 1, 512, 64, 128, 64) > size(1, 8, 1, 512, 64, 128, 9) > 16
 
 
 def test_binding_refuses_cpu_tensors(lib):

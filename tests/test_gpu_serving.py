@@ -335,8 +335,9 @@ def test_page_select(B, T, hq, hkv, d, page, nb, max_sel, first, last, dtype, co
             for h in range(hkv):
                 want = S.page_scores(qf[i, t, h * G:(h + 1) * G], b[ids, h, 0].astype(np.int64), b[ids, h, 1].astype(np.int64),
                                      s[ids, h]) if n else np.zeros(0, np.float32)
-                np.testing.assert_array_equal(sc[i, t, h, :n], want)
-                assert np.all(sc[i, t, h, n:] == -9.0)
+                if n > max_sel:
+                    np.testing.assert_array_equal(sc[i, t, h, :n], want)
+                assert np.all(sc[i, t, h, n if n > max_sel else 0:] == -9.0)
                 kept = S.select(want, max_sel, first, last)
                 np.testing.assert_array_equal(blocks[i, t, h], kept + [-1] * (max_sel - len(kept)))
                 np.testing.assert_array_equal(pages[i, t, h], [*ids[kept]] + [-1] * (max_sel - len(kept)))
@@ -345,7 +346,7 @@ def test_page_select(B, T, hq, hkv, d, page, nb, max_sel, first, last, dtype, co
 
 
 def test_page_select_long_table():
-    """Contexts past what one CTA's shared memory holds, and far more pages than are kept."""
+    """More pages than a CTA holds in shared memory, and far more than are kept."""
     nb, page, d = 120000, 16, 32
     rng = np.random.default_rng(8)
     b, s, db, ds = _bounds_pool(rng, 1000, 1, d)
@@ -362,9 +363,11 @@ def test_page_select_long_table():
 def test_page_select_reports_bad_lengths_and_pages():
     b, s = torch.ones((2, 1, 2, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1), device=DEV)
     q = torch.ones((1, 1, 64), device=DEV)
+    b[0] = 3
     out = sl8.page_select(q, b, s, i32([[0, 1, 7]]), i32([48]), 16, 2, 1, 0)
     assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
-    assert out["blocks"].tolist() == [[[[0, 1]]]] and out["lens"].item() == 32
+    # page 7 is scored as page 0, above page 1
+    assert out["blocks"].tolist() == [[[[0, 2]]]] and out["lens"].item() == 32
     for L, want in ((49, 48), (-1, 0)):
         out = sl8.page_select(q, b, s, i32([[0, 1, 0]]), i32([L]), 16, 4, 1, 0)
         assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
@@ -569,7 +572,8 @@ def test_side_stream_and_refusals():
     with pytest.raises(ValueError):
         sl8.attn_int8_sparse_decode(q, *args[:4], lists, lens[:1])
     with pytest.raises(sl8.SL8Error):
-        sl8.attn_int8_sparse_decode(q, *args, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        sl8.attn_int8_sparse_decode(q, *args[:4], i32(np.zeros((2, 2, 64))), lens, num_splits=40,
+                                    workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     k = torch.randn((4, 2, 64), device=DEV).half()
     slots = i32([0, 1, 2, 3])
     with pytest.raises(ValueError):

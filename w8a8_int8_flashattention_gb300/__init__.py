@@ -715,7 +715,8 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     queries) or [B,T,Hq,d] (query t at position seqlens - T + t); bounds as page_bounds leaves
     them.  Returns a dict of int32 tensors: blocks and pages [B,T,Hkv,max_sel] (ascending
     blocks; -1 past the list) and lens [B,T,Hkv], the tokens listed (out: a dict returned
-    earlier, written again).  scores fp32 [B,T,Hkv,max_blocks] receives the pages' scores."""
+    earlier, written again).  scores fp32 [B,T,Hkv,max_blocks] receives the scores of
+    the pages of every range longer than max_sel."""
     dev = _device(q, bounds, bound_scale, block_table, seqlens, scores)
     _need_cuda(q)
     num_pages, hkv, _, d = bounds.shape
@@ -756,7 +757,7 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
     [B,T,Hq,d], pages [B(,T),Hkv,max_sel] int32 and lens [B(,T),Hkv] int32 as page_select
     returns them (or from any other policy: full pages, the last one up to the length).
     Returns out like q (dtype q.dtype unless given) and, with return_lse, the fp32 LSE.
-    workspace: uint8, at least sparse_decode_workspace_bytes."""
+    workspace: uint8, at least sparse_decode_workspace_bytes (16: none is used)."""
     dev = _device(q, k_pages, k_scale_pages, v_pages, v_scale_pages, pages, lens, workspace, out, lse)
     _need_cuda(q, workspace, out, lse)
     num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages, v_pages, v_scale_pages)
@@ -776,12 +777,12 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
         elif lse.shape != q.shape[:-1]:
             raise ValueError("lse must have one entry per query head")
     if workspace is None:
-        workspace = torch.empty(max(sparse_decode_workspace_bytes(rows, hq, hkv, max_sel, page_size, d, num_splits), 16),
-                                dtype=torch.uint8, device=dev)
+        need = sparse_decode_workspace_bytes(rows, hq, hkv, max_sel, page_size, d, num_splits)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 16 else None
     _call("sl8_attn_int8_sparse_decode", dev, _ptr(q), _dt(q), _ptr(k_pages), _ptr(k_scale_pages), _ptr(v_pages),
           _ptr(v_scale_pages), num_pages, page_size, _ptr(pages), _ptr(lens), max_sel, rows, hq, hkv, d, num_splits,
           _ptr(out), _dt(out), _ptr(lse) if return_lse else None, _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+          0 if workspace is None else workspace.numel() * workspace.element_size())
     return (out, lse) if return_lse else out
 
 

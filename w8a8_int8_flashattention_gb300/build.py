@@ -18,8 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "sl8")
 LIB = os.path.join(PKG, "libsl8.so")
-SOURCES = ["abi.cu", "quant.cu", "prefill.cu", "decode.cu", "noalloc.cu", "paged.cu", "select.cu"]
-HEADERS = [os.path.join(CSRC, "sl8_internal.h"), os.path.join(CSRC, "sm103_ptx.cuh"),
+SOURCES = ["abi.cu", "quant.cu", "prefill.cu", "decode.cu", "noalloc.cu", "paged.cu", "select.cu", "list_decode.cu"]
+HEADERS = [os.path.join(CSRC, "sl8_internal.h"), os.path.join(CSRC, "sm103_ptx.cuh"), os.path.join(CSRC, "decode_unit.cuh"),
            os.path.join(ROOT, "include", "sl8.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1018,14 +1018,24 @@ int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const floa
   return SL8_OK;
 }
 
-// Split count of the decode over page lists: the plan of rows * Hkv sequences of one kv
-// head; 0 for an invalid or unsupported shape.
+// Parts that a page list is cut into; 0 for an invalid or unsupported shape.  Up to
+// list_decode_max_splits() parts run as one launch of clusters, more as the split kernel and
+// the combine.
 static int32_t list_splits(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel, int32_t page_size, int32_t d,
                            int32_t num_splits) {
-  if (rows <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_sel <= 0 || page_size <= 0) return 0;
+  if (rows <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_sel <= 0 || page_size <= 0 || num_splits < 0) return 0;
   if (static_cast<int64_t>(max_sel) * page_size >= (int64_t(1) << 31) || page_size % 16) return 0;
-  if (static_cast<int64_t>(rows) > (int64_t(1) << 27) / Hq) return 0;
-  return sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, num_splits);
+  if (static_cast<int64_t>(rows) > (int64_t(1) << 27) / Hq || !decode_head_dim_ok(d)) return 0;
+  const int32_t most = list_decode_max_splits();
+  int64_t n = num_splits;
+  if (n == 0) {
+    const int64_t lists = static_cast<int64_t>(rows) * Hkv * decode_kv_groups(Hq, Hkv);
+    const int64_t tokens = static_cast<int64_t>(max_sel) * page_size;
+    n = list_decode_splits(lists, tokens, d);
+    // few long lists: clusters of `most` CTAs would leave SMs without work
+    if (lists * most < num_sms() && tokens / most > 4096) n = most + 1;
+  }
+  return n <= most ? static_cast<int32_t>(n) : sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, num_splits);
 }
 
 static size_t list_lse_offset(int32_t rows, int32_t Hq, int32_t d, int32_t S) {
@@ -1035,7 +1045,9 @@ static size_t list_lse_offset(int32_t rows, int32_t Hq, int32_t d, int32_t S) {
 size_t sl8_attn_int8_sparse_decode_workspace_size(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel,
                                                   int32_t page_size, int32_t d, int32_t num_splits) {
   const int32_t S = list_splits(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
-  return S > 0 ? list_lse_offset(rows, Hq, d, S) + static_cast<size_t>(rows) * Hq * S * sizeof(float) : 0;
+  if (S <= 0) return 0;
+  if (S <= list_decode_max_splits()) return 16;  // none is used
+  return list_lse_offset(rows, Hq, d, S) + static_cast<size_t>(rows) * Hq * S * sizeof(float);
 }
 
 int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_pages, const float* k_scale_pages,
@@ -1057,9 +1069,33 @@ int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_page
   SL8_CHECK(static_cast<int64_t>(num_pages) * Hkv < (int64_t(1) << 31) / page_size, SL8_ERR_UNSUPPORTED);
   const int32_t S = list_splits(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
   SL8_CHECK(S > 0, SL8_ERR_UNSUPPORTED);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (S <= list_decode_max_splits()) {
+    ListDecodeArgs l{};
+    l.q = q;
+    l.q_dtype = static_cast<sl8_dtype>(q_dtype);
+    l.k_pages = k_pages;
+    l.k_scale = k_scale_pages;
+    l.v_pages = v_pages;
+    l.v_scale = v_scale_pages;
+    l.num_pages = num_pages;
+    l.page = page_size;
+    l.list = page_list;
+    l.lens = list_lens;
+    l.max_sel = max_sel;
+    l.rows = rows;
+    l.Hq = Hq;
+    l.Hkv = Hkv;
+    l.groups = decode_kv_groups(Hq, Hkv);
+    l.splits = S;
+    l.out = out;
+    l.out_dtype = static_cast<sl8_dtype>(out_dtype);
+    l.lse = lse_out;
+    SL8_LAUNCH(launch_list_decode(l, d, s));
+    return SL8_OK;
+  }
   const size_t need = sl8_attn_int8_sparse_decode_workspace_size(rows, Hq, Hkv, max_sel, page_size, d, num_splits);
   SL8_CHECK(workspace && workspace_bytes >= need && aligned16(workspace), SL8_ERR_WORKSPACE);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   DecodeArgs a{};
   a.q = q;
   a.q_dtype = static_cast<sl8_dtype>(q_dtype);

@@ -42,6 +42,7 @@
 #include <type_traits>
 #include <cuda_fp16.h>
 
+#include "decode_unit.cuh"
 #include "sl8_internal.h"
 
 namespace sl8 {
@@ -51,7 +52,6 @@ namespace {
 constexpr int kFirstCompute = 2;                // warp 0: loads, warp 1: merges
 constexpr int kUnit = 16;                       // tokens per compute warp per stage
 constexpr int kQSlots = 2;                      // q-row buffers (one per split in flight)
-constexpr float kLazy = 8.0f;                   // log2 headroom of the lazy max
 
 constexpr int kSchedMaxB = 512;
 struct Slot {
@@ -122,61 +122,6 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return static_cast<uint32_t>(b * (C::kChunk * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
 }
 
-__device__ __forceinline__ float bf16_bits(uint32_t b) { return __uint_as_float(b << 16); }
-__device__ __forceinline__ float f16_bits(uint32_t b) {
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-}
-__device__ __forceinline__ float warp_max_f(float a) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  return a;
-}
-// max / sum over the 8 lanes of one thread-in-group column (lanes t, t+4, ..., t+28)
-__device__ __forceinline__ float col_max(float a) {
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-  return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-}
-__device__ __forceinline__ float col_sum(float a) {
-  a += __shfl_xor_sync(0xffffffffu, a, 4);
-  a += __shfl_xor_sync(0xffffffffu, a, 8);
-  return a + __shfl_xor_sync(0xffffffffu, a, 16);
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, DeviceStatus* st,
-                                          int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, st, site));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^n as a float for -126 <= n <= 127, 0 below.
-__device__ __forceinline__ float pow2i(int n) {
-  return n < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
-}
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-// Two int8 codes, already offset by 128 (byte ^ 0x80), picked from ub by sel (0x4140:
-// bytes 0 and 1; 0x4342: bytes 2 and 3) and widened exactly to an fp16 pair: each byte
-// u becomes the mantissa of 1024 + u, and subtracting 1152 leaves u - 128.
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t ub, uint32_t sel) {
-  const uint32_t h = prmt(ub, 0x64646464u, sel);
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-  return r;
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // Four transposed 8x8 fp16 matrices from shared memory: lanes 8i .. 8i+7 give the row
 // addresses of matrix i; register i of thread T holds its rows 2 (T % 4) and 2 (T % 4) + 1
 // in column T / 4.
@@ -185,44 +130,6 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t&
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(addr));
 }
-// Transpose of an 8x8 fp16 matrix held one register per lane (lane l: row l / 4,
-// columns 2 (l % 4) and 2 (l % 4) + 1), into the same layout.
-__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Quantise one q row of D values (f16/bf16/f32) held by a warp, D / 32 per lane.
-template <int D>
-__device__ __forceinline__ float quant_row_warp(const float (&v)[D / 32], int8_t (&code)[D / 32]) {
-  float amax = 0.0f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
-  amax = warp_max_f(amax);
-  const float sc = __fdiv_rn(amax, 127.0f);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    int c = 0;
-    if (sc != 0.0f) {
-      c = __float2int_rn(__fdiv_rn(v[e], sc));
-      c = c > 127 ? 127 : (c < -127 ? -127 : c);
-    }
-    code[e] = static_cast<int8_t>(c);
-  }
-  return sc;
-}
-
-__device__ __forceinline__ float load_q_elem(const void* base, sl8_dtype dt, int64_t idx) {
-  return dt == SL8_BF16 ? bf16_bits(static_cast<const uint16_t*>(base)[idx])
-       : dt == SL8_F16 ? f16_bits(static_cast<const uint16_t*>(base)[idx])
-                       : static_cast<const float*>(base)[idx];
-}
-
 // ---- work schedule
 // A work slot is one (b, kv head, split).  With B <= kSchedMaxB the launch's slot list
 // is: the full splits (split_size tokens), then the sequences' partial last splits,

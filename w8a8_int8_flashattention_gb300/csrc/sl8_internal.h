@@ -280,6 +280,30 @@ cudaError_t launch_decode_combine(const float* o_partial, const float* lse_parti
                                   int32_t B, int32_t Hq, int32_t d, int32_t num_splits, int32_t split_size,
                                   void* out, sl8_dtype out_dtype, float* lse_out, cudaStream_t s,
                                   int32_t seq_div = 1);
+// Decode over page lists in one launch (list_decode.cu): `splits` CTAs (a cluster, at most
+// list_decode_max_splits()) per list and group of at most 8 query heads.
+struct ListDecodeArgs {
+  const void* q;  // [rows][Hq][d]
+  sl8_dtype q_dtype;
+  const int8_t* k_pages;  // [num_pages][Hkv][page][d]
+  const float* k_scale;
+  const int8_t* v_pages;
+  const float* v_scale;
+  int32_t num_pages, page;
+  const int32_t* list;  // [rows][Hkv][max_sel]
+  const int32_t* lens;  // [rows][Hkv]
+  int32_t max_sel, rows, Hq, Hkv;
+  int32_t groups;  // groups of the Hq / Hkv query heads of a kv head, each at most 8
+  int32_t splits;
+  void* out;
+  sl8_dtype out_dtype;
+  float* lse;
+  int32_t box;  // rows per TMA box (set by the launcher)
+};
+int list_decode_max_splits();
+// The splits for `lists` lists (counted per group of query heads) of up to `tokens` tokens.
+int list_decode_splits(int64_t lists, int64_t tokens, int32_t d);
+cudaError_t launch_list_decode(const ListDecodeArgs& a, int32_t d, cudaStream_t s);
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, cudaStream_t s);
 
 // tokens per stage of the decode kernel for head dim d
