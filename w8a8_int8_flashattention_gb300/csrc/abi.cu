@@ -944,7 +944,7 @@ int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int6
     SL8_CHECK(q_stride % step == 0 && q_out_stride % step == 0, SL8_ERR_INVALID_ARG);
   }
   // one warp per part of a token, at most one part per row group
-  SL8_CHECK(static_cast<int64_t>(T) * (Hq + 2 * static_cast<int64_t>(Hkv)) < (int64_t(1) << 33), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(T) * (Hq + 2 * static_cast<int64_t>(Hkv) + 2) < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
   RopeAppendArgs r{};
   r.q = q;
   r.k = k;
@@ -984,7 +984,7 @@ int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t n
   SL8_CHECK(!new_lens || max_new >= 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
   SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
-  SL8_CHECK(static_cast<int64_t>(B) * max_blocks <= (int64_t(1) << 33) / Hkv, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(B) * max_blocks < (int64_t(1) << 31) / Hkv, SL8_ERR_UNSUPPORTED);
   if (B == 0 || (new_lens && max_new == 0)) return SL8_OK;
   SL8_CHECK(k_pages && k_scale_pages && block_table && seqlens && bounds && bound_scale, SL8_ERR_INVALID_ARG);
   SL8_CHECK(aligned16(k_pages) && aligned16(bounds), SL8_ERR_INVALID_ARG);
@@ -1030,12 +1030,10 @@ static int32_t list_splits(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_se
   int64_t n = num_splits;
   if (n == 0) {
     const int64_t lists = static_cast<int64_t>(rows) * Hkv * decode_kv_groups(Hq, Hkv);
-    const int64_t tokens = static_cast<int64_t>(max_sel) * page_size;
-    n = list_decode_splits(lists, tokens, d);
-    // few long lists: clusters of `most` CTAs would leave SMs without work
-    if (lists * most < num_sms() && tokens / most > 4096) n = most + 1;
+    n = list_decode_splits(lists, static_cast<int64_t>(max_sel) * page_size, d);
   }
-  return n <= most ? static_cast<int32_t>(n) : sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, num_splits);
+  return n <= most ? static_cast<int32_t>(n)
+                   : sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, static_cast<int32_t>(n));
 }
 
 static size_t list_lse_offset(int32_t rows, int32_t Hq, int32_t d, int32_t S) {

@@ -6,14 +6,14 @@
 //
 // GB300 design.  A list is short (some thousand tokens) and there are many, so the kernel
 // is not persistent: a cluster of S CTAs serves one list, each CTA a contiguous run of its
-// 64-token stages, and two or three CTAs share an SM, one's start and end hidden behind
+// stages of 16 W tokens, and two or three CTAs share an SM, one's start and end hidden behind
 // the others' streams.  The S partial results meet over distributed shared memory, so one
 // launch does everything and no workspace or counter is shared between launches.
-//  * Warp 4 loads: per stage, one lane per piece of 64, 32 or 16 rows (the largest that
-//    divides the page) issues the piece's K and V tiles (TMA, 128-byte swizzle for
-//    d >= 128) and its two scale rows; page ids are read one stage ahead.
-//  * Warps 0..3 take 16 tokens of every stage each, with an online-softmax state of their
-//    own.  S^T[16 tokens x 8 q] = K Q^T runs as int8 m16n8k32 MMAs, whose A operand is the
+//  * The last warp loads: per stage, one lane per piece of 64, 32 or 16 rows (the largest
+//    that divides the page) issues the piece's K and V tiles (TMA, 128-byte swizzle for
+//    d >= 128) and its two scale rows; page ids are read 32 pieces ahead.
+//  * Warps 0..W-1 take 16 tokens of every stage each, with an online-softmax state of
+//    their own.  S^T[16 tokens x 8 q] = K Q^T runs as int8 m16n8k32 MMAs, whose A operand is the
 //    K rows as they lie in memory (this part's int8 rate is low, but 8 MMAs per 16 tokens
 //    take 29 of the 180 cycles that their bytes need); O^T[d x 8 q] += V^T P'^T as fp16
 //    MMAs on V codes biased by 128 (P' = p * s_v * 2^-E rounded to fp16, 2^-11 relative;
@@ -35,48 +35,50 @@ namespace sl8 {
 
 namespace {
 
-constexpr int kTok = 64;                     // tokens per stage
-constexpr int kCWarps = 4, kCThreads = 32 * kCWarps, kLThreads = kCThreads + 32;
 constexpr int kMaxSplits = 8;                // CTAs per list (portable cluster size)
 
-template <int D>
+// W compute warps.  Four: three CTAs share an SM (two at d = 256).  Eight: two CTAs share an SM,
+// each nearly twice as fast alone.
+template <int D, int W>
 struct LCfg {
+  static constexpr int kWarps = W, kCThreads = 32 * W, kThreads = kCThreads + 32;
+  static constexpr int kTok = 16 * W;            // tokens per stage
   static constexpr int kBW = D < 128 ? D : 128;  // bytes in one row of a TMA box
   static constexpr int kBoxes = D / kBW;
   static constexpr bool kSwz = D >= 128;
   static constexpr int kTile = kTok * D;
   static constexpr int kSK = 0, kSV = kTile, kSKs = 2 * kTile, kSVs = kSKs + kTok * 4;
   static constexpr int kStageBytes = (kSVs + kTok * 4 + 1023) / 1024 * 1024;
-  static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 4 : 8);
-  static constexpr int kCtas = D == 256 ? 2 : 3;  // resident per SM
-  // after the loop the ring holds the warps' O^T [4][D][8] and the CTA's [D][8], fp32
-  static constexpr int kRed = 0, kPart = kCWarps * D * 32;
+  static constexpr int kStages = D == 256 ? 3 : (W == 4 ? (D == 128 ? 4 : 8) : (D == 128 ? 3 : 6));
+  static constexpr int kCtas = W == 8 ? 2 : D == 256 ? 2 : 3;  // resident per SM
+  // after the loop the ring holds the warps' O^T [warp][D][8] and the CTA's [D][8], fp32
+  static constexpr int kRed = 0, kPart = W * D * 32;
   static_assert(kPart + D * 32 <= kStages * kStageBytes, "the merge fits the ring");
   static constexpr int kQc = kStages * kStageBytes;       // [8][D] query codes
   static constexpr int kQs = kQc + 8 * D;                 // [8] scales
-  static constexpr int kStat = kQs + 32;                  // [4 warps][8][2]: max (log2), sum
-  static constexpr int kWt = kStat + kCWarps * 64;        // [4 warps][8] weights of the warps
-  static constexpr int kMl = kWt + kCWarps * 32;          // [8] max, [8] sum of the CTA
+  static constexpr int kStat = kQs + 32;                  // [warp][8][2]: max (log2), sum
+  static constexpr int kWt = kStat + W * 64;        // [warp][8] weights of the warps
+  static constexpr int kMl = kWt + W * 32;          // [8] max, [8] sum of the CTA
   static constexpr int kBar = kMl + 64;
   static constexpr int kBytes = kBar + 2 * kStages * 8 + 1024;  // + alignment slack
   static_assert(kStageBytes % 1024 == 0 && kTile % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 };
 
 // Byte offset of (row r, 16-byte chunk c of the row) in a stage tile of kBoxes boxes.
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ uint32_t ltile_off(int r, int c) {
-  using C = LCfg<D>;
+  using C = LCfg<D, W>;
   constexpr int cpb = C::kBW / 16;
   const int b = c / cpb, cc = c % cpb;
-  return static_cast<uint32_t>(b * (kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
+  return static_cast<uint32_t>(b * (C::kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
+template <int D, int W>
+__global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
     list_decode_kernel(const ListDecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, DeviceStatus* st, uint64_t limit_ns) {
-  using C = LCfg<D>;
-  constexpr int kStages = C::kStages;
+  using C = LCfg<D, W>;
+  constexpr int kStages = C::kStages, kTok = C::kTok, kCThreads = C::kCThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kCWarps);
+      mbar_init(&empty[i], W);
     }
     fence_barrier_init();
   }
@@ -110,23 +112,27 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
   const int t0 = s0 * kTok, t1 = min(L, s1 * kTok), n = s1 - s0;
   __syncthreads();
 
-  if (warp == kCWarps) {
+  if (warp == W) {
     // ------------------------------------------------------------ loader
     const int pieces = kTok / a.box;
     const int head = v % a.Hkv;
     const int32_t* list = a.list + static_cast<int64_t>(v) * a.max_sel;
-    auto page_at = [&](int s) {  // the page of this lane's piece of stage s
-      const int t = t0 + s * kTok + lane * a.box;
-      return lane < pieces && t < t1 ? list[t / a.page] : 0;
-    };
+    // page ids come 32 pieces at a time, read one batch ahead; pieces past t1 are not loaded
+    const int n_pieces = (t1 - t0 + a.box - 1) / a.box;
+    auto ids_at = [&](int j) { return j + lane < n_pieces ? list[(t0 + (j + lane) * a.box) / a.page] : 0; };
+    int32_t ids = n > 0 ? ids_at(0) : 0, next_ids = n > 0 ? ids_at(32) : 0;
     if (lane == 0) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
     }
-    int pg = n > 0 ? page_at(0) : 0;
     int k = 0;
     for (; k < n; ++k) {
-      const int next = k + 1 < n ? page_at(k + 1) : 0;
+      const int j = k * pieces;  // the stage's first piece; pieces divides 32
+      if (k > 0 && j % 32 == 0) {
+        ids = next_ids;
+        next_ids = ids_at(j + 32);
+      }
+      int32_t pg = __shfl_sync(0xffffffffu, ids, (j + lane) & 31);
       const int stg = k % kStages;
       if (k >= kStages && !warp_wait(&empty[stg], ((k / kStages) - 1) & 1, limit_ns, st, 850)) break;
       uint8_t* base = smem + stg * C::kStageBytes;
@@ -149,7 +155,6 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
         bulk_load(base + C::kSKs + lane * a.box * 4, a.k_scale + prow, static_cast<uint32_t>(a.box * 4), &full[stg]);
         bulk_load(base + C::kSVs + lane * a.box * 4, a.v_scale + prow, static_cast<uint32_t>(a.box * 4), &full[stg]);
       }
-      pg = next;
     }
     // after a wait that gave up: the copies in flight land before the CTA may end
     if (k < n)
@@ -206,8 +211,8 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
     } else {
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
-        offk[h][0] = ltile_off<D>(u0 + pi, 4 * h + t);
-        offk[h][1] = ltile_off<D>(u0 + pi + 8, 4 * h + t);
+        offk[h][0] = ltile_off<D, W>(u0 + pi, 4 * h + t);
+        offk[h][1] = ltile_off<D, W>(u0 + pi + 8, 4 * h + t);
       }
     }
     // V rows of the lane: unit tokens tok(2t), tok(2t + 1) and the same + 8, chunk pi
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
         const int row = u0 + tok(2 * t + (c & 1)) + 8 * (c >> 1);
         offv[b][c] = D == 32   ? static_cast<uint32_t>(row * 32 + 4 * pi)
                      : D == 64 ? static_cast<uint32_t>(row * 64 + 8 * pi)
-                               : ltile_off<D>(row, 8 * b + pi);
+                               : ltile_off<D, W>(row, 8 * b + pi);
       }
 
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.0f, l_b = 0.0f;
@@ -383,21 +388,21 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
       *reinterpret_cast<float2*>(r + 8) = make_float2(fmaf(o[j][2], k2p24, ca) * pe, fmaf(o[j][3], k2p24, cb) * pe);
     }
     named_bar_sync(1, kCThreads);
-    if (threadIdx.x < 32) {
-      // lane: warp lane / 8, column lane % 8
-      const int c = lane & 7, w = lane >> 3;
-      float M = -INFINITY;
+    if (threadIdx.x < 8 * W) {  // column c: the weight of warp w's state, and (w = 0) max and sum
+      const int c = threadIdx.x & 7, w = threadIdx.x >> 3;
+      float M = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kCWarps; ++i) M = fmaxf(M, stat[(i * 8 + c) * 2]);
+      for (int i = 0; i < W; ++i) M = fmaxf(M, stat[(i * 8 + c) * 2]);
       const float mw = stat[(w * 8 + c) * 2];
-      const float f = mw == -INFINITY ? 0.0f : ex2(mw - M);
-      wt[w * 8 + c] = f;
-      float l = f == 0.0f ? 0.0f : f * stat[(w * 8 + c) * 2 + 1];
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      wt[w * 8 + c] = mw == -INFINITY ? 0.0f : ex2(mw - M);
       if (w == 0) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float mi = stat[(i * 8 + c) * 2];
+          if (mi != -INFINITY) sum = fmaf(ex2(mi - M), stat[(i * 8 + c) * 2 + 1], sum);
+        }
         ml[c] = M;
-        ml[8 + c] = l;
+        ml[8 + c] = sum;
       }
     }
     named_bar_sync(1, kCThreads);
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
       if (4 * h >= GC) continue;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kCWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float4 r = *reinterpret_cast<const float4*>(red + (w * D + dim) * 8 + 4 * h);
         const float4 f = *reinterpret_cast<const float4*>(wt + w * 8 + 4 * h);
         acc.x = fmaf(r.x, f.x, acc.x);
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
   const uint8_t* peer[kMaxSplits];
 #pragma unroll
   for (int r = 0; r < kMaxSplits; ++r) peer[r] = cluster.map_shared_rank(smem, r < S ? r : 0);
-  for (int u = rank * kLThreads + threadIdx.x; u < 2 * D; u += S * kLThreads) {
+  for (int u = rank * C::kThreads + threadIdx.x; u < 2 * D; u += S * C::kThreads) {
     const int dim = u % D, h = u / D;
     if (4 * h >= GC) continue;
     float4 m[kMaxSplits], l[kMaxSplits], x[kMaxSplits];
@@ -476,10 +481,10 @@ __global__ void __launch_bounds__(kLThreads, LCfg<D>::kCtas)
   cluster.sync();  // no CTA leaves while another reads its part
 }
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
-  using C = LCfg<D>;
-  auto kern = list_decode_kernel<D>;
+  using C = LCfg<D, W>;
+  auto kern = list_decode_kernel<D, W>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
   bool ok = true;
@@ -491,7 +496,7 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.Hkv * a.groups * a.splits);
-  cfg.blockDim = dim3(kLThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -507,8 +512,18 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
 
 int list_decode_max_splits() { return kMaxSplits; }
 
+// Lists that fill the device once, with four warps a CTA and with eight.
+static int64_t list_wave(int32_t d, bool eight) {
+  return static_cast<int64_t>(eight || d == 256 ? 2 : 3) * num_sms();
+}
+
 int list_decode_splits(int64_t lists, int64_t tokens, int32_t d) {
-  const int64_t fit = static_cast<int64_t>(d == 256 ? LCfg<256>::kCtas : LCfg<128>::kCtas) * num_sms();
+  const int64_t fit = list_wave(d, false);
+  // few long lists: clusters of kMaxSplits CTAs would leave SMs without work (8 lists of
+  // 65,536 tokens, d = 128: 81 us with 8 splits, 51 with 32; 1 list: 80 and 26 with 64)
+  if (lists * kMaxSplits < num_sms() && tokens >= 4096 * kMaxSplits)
+    return static_cast<int>(std::max<int64_t>(kMaxSplits + 1, std::min<int64_t>(64, 256 / lists)));
+  // else as many splits as fit one wave, of 128 tokens at least
   int n = 1;
   while (n < kMaxSplits && lists * (n + 1) <= fit && tokens / (n + 1) >= 128) ++n;
   return n;
@@ -520,11 +535,16 @@ cudaError_t launch_list_decode(const ListDecodeArgs& args, int32_t d, cudaStream
   // rows per TMA box: the largest of a stage's 64, 32 or 16 that divides the page, so that
   // no piece straddles two pages
   a.box = a.page % 64 == 0 ? 64 : a.page % 32 == 0 ? 32 : 16;
+  // Eight warps where four would leave a second wave nearly empty while eight nearly fill
+  // theirs: 512 lists of 4,096 tokens (d = 128) take 93 us with eight and 110 with four (104
+  // in two splits); 448 lists 91 and 76, 768 lists of 2,048 tokens 78 and 73.
+  const int64_t lists = static_cast<int64_t>(a.rows) * a.Hkv * a.groups;
+  const bool eight = d != 256 && a.splits == 1 && lists > list_wave(d, false) && lists <= 2 * list_wave(d, true);
   switch (d) {
-    case 32: return launch_list_d<32>(a, s);
-    case 64: return launch_list_d<64>(a, s);
-    case 128: return launch_list_d<128>(a, s);
-    case 256: return launch_list_d<256>(a, s);
+    case 32: return eight ? launch_list_d<32, 8>(a, s) : launch_list_d<32, 4>(a, s);
+    case 64: return eight ? launch_list_d<64, 8>(a, s) : launch_list_d<64, 4>(a, s);
+    case 128: return eight ? launch_list_d<128, 8>(a, s) : launch_list_d<128, 4>(a, s);
+    case 256: return launch_list_d<256, 4>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }

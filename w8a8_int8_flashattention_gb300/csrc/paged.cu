@@ -9,6 +9,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
+#include "decode_unit.cuh"
 #include "sl8_internal.h"
 
 namespace cg = cooperative_groups;
@@ -18,55 +21,38 @@ namespace sl8 {
 namespace {
 
 // ---------------------------------------------------------------- page plan
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;
+constexpr int kMapRequests = 2048;  // requests whose token counts the mapping kernel holds in shared memory
 
-// Exclusive prefix over the block of a pair of 64-bit counts; totals in ta, tb.
-__device__ __forceinline__ void block_prefix2(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb, int64_t* sm) {
+// Exclusive prefix of a 64-bit count over the block; its sum in total.
+template <int kT>
+__device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t& total, int64_t* sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t ia = a, ib = b;
+  int64_t incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
-    if (lane >= o) {
-      ia += xa;
-      ib += xb;
-    }
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  if (lane == 31) {
-    sm[warp] = ia;
-    sm[32 + warp] = ib;
-  }
+  if (lane == 31) sm[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    int64_t wa = sm[lane], wb = sm[32 + lane];
-    const int64_t a0 = wa, b0 = wb;
+  // every warp scans the warp sums for itself
+  constexpr int kW = kT / 32;
+  int64_t w = sm[lane % kW];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t xa = __shfl_up_sync(0xffffffffu, wa, o), xb = __shfl_up_sync(0xffffffffu, wb, o);
-      if (lane >= o) {
-        wa += xa;
-        wb += xb;
-      }
-    }
-    sm[lane] = wa - a0;
-    sm[32 + lane] = wb - b0;
-    if (lane == 31) {
-      sm[64] = wa;
-      sm[65] = wb;
-    }
+  for (int o = 1; o < kW; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
+  total = __shfl_sync(0xffffffffu, w, kW - 1);
+  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   __syncthreads();
-  const int64_t ea = sm[warp] + ia - a, eb = sm[32 + warp] + ib - b;
-  ta = sm[64];
-  tb = sm[65];
-  __syncthreads();
-  a = ea;
-  b = eb;
+  return (warp > 0 ? before : 0) + incl - x;
 }
 
 // Largest i in [0, n) with p[i] <= x (p nondecreasing, p[0] <= x).
-__device__ __forceinline__ int find_owner(const int64_t* p, int n, int64_t x) {
+template <typename P>
+__device__ __forceinline__ int find_owner(const P* p, int n, P x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -88,148 +74,242 @@ struct PlanArgs {
   int32_t* free_count_out;
   int32_t max_tokens;
   int32_t *seqlens, *granted, *cu_new, *slot_map, *token_pos;
+  bool vec;  // slot_map and token_pos take 16-byte stores
+  bool map;  // the plan maps the tokens too
 };
 
+// Slots and positions of the tokens [t0, t1) of a step's packed order, which belong to n
+// requests with cu[i] tokens before the i-th (counted from `base`): four tokens a search,
+// from a multiple of four.  length(i, p) says how many tokens request i had before the step
+// and whether it was granted; row(i) is its table row, with the new pages already entered.
+template <typename P, typename Length, typename Row>
+__device__ __forceinline__ void map_tokens(const PlanArgs& a, int64_t base, int64_t t0, int64_t t1, uint32_t first,
+                                           uint32_t step, const P* cu, int n, Length length, Row row) {
+  const uint32_t page = static_cast<uint32_t>(a.page);
+  for (int64_t t4 = (t0 & ~int64_t(3)) + 4 * static_cast<int64_t>(first); t4 < t1; t4 += 4 * static_cast<int64_t>(step)) {
+    int32_t slot[4], pos[4];
+    int i = find_owner(cu, n, static_cast<P>((t4 > t0 ? t4 : t0) - base));
+    uint32_t blk = 0, off = 0, p = 0;
+    int32_t pg = -1;
+    bool fresh = true, ok = false;  // fresh: the first token of the quad or of a request
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      slot[j] = pos[j] = -1;
+      const int64_t t = t4 + j;
+      if (t < t0 || t >= t1) continue;
+      const P rel = static_cast<P>(t - base);
+      while (i + 1 < n && cu[i + 1] <= rel) {
+        ++i;
+        fresh = true;
+      }
+      if (fresh) {
+        int32_t had;
+        ok = length(i, had);
+        p = static_cast<uint32_t>(had) + static_cast<uint32_t>(rel - cu[i]);
+        blk = p / page;
+        off = p - blk * page;
+      }
+      pos[j] = static_cast<int32_t>(min(p, 0x7fffffffu));
+      if (ok) {
+        if (fresh || off == page) {
+          if (!fresh) {
+            ++blk;
+            off = 0;
+          }
+          pg = row(i)[blk];
+        }
+        slot[j] = pg * a.page + static_cast<int32_t>(off);
+      }
+      ++p;
+      ++off;
+      fresh = false;
+    }
+    if (a.vec && t4 >= t0 && t4 + 4 <= t1) {
+      *reinterpret_cast<int4*>(a.slot_map + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (a.token_pos) *reinterpret_cast<int4*>(a.token_pos + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t t = t4 + j;
+        if (t < t0 || t >= t1) continue;
+        a.slot_map[t] = slot[j];
+        if (a.token_pos) a.token_pos[t] = pos[j];
+      }
+    }
+  }
+}
+// Padding past the last token.
+__device__ __forceinline__ void map_padding(const PlanArgs& a, int64_t t0, uint32_t first, uint32_t step) {
+  for (int64_t t = t0 + first; t < a.max_tokens; t += step) {
+    a.slot_map[t] = -1;
+    if (a.token_pos) a.token_pos[t] = 0;
+  }
+}
+
+template <int kT>
 struct PlanSmem {
-  int64_t cu[kPlanThreads + 1];    // tokens before each request of the block of requests
-  int64_t need[kPlanThreads + 1];  // pages (pushed or taken) before each
-  int32_t ctx[kPlanThreads];       // length that stays (0 for a released slot)
-  int32_t ok[kPlanThreads];
-  int64_t scan[66];
+  // of each request of the block of requests, counted from the block's first (at most 2^31 - 1)
+  uint32_t cu[kT + 1];    // tokens before it
+  uint32_t need[kT + 1];  // pages (pushed or asked for) before it
+  int32_t ctx[kT];        // length that stays (0 for a released slot)
+  int32_t ok[kT];
+  int64_t scan[32];
+  uint32_t got;           // pages granted
 };
+__device__ __forceinline__ uint32_t clamp31(int64_t x) { return static_cast<uint32_t>(x < 0x7fffffff ? x : 0x7fffffff); }
 
-// One cluster plans the step, in two passes over blocks of kPlanThreads requests; every CTA
-// scans each block's counts itself and then takes its share of the block's pages and
-// tokens, found by binary search in the scanned prefixes.  Pass 1 pushes the pages of the
-// released slots; pass 2 grants requests in order, writes the new table entries and maps
-// the tokens.  A token's page is read from the table for a block the request had before
-// and straight from the free list for a new one, so no CTA waits for another's table
-// writes.  The cluster barriers order pass 1's pushes and table reads before pass 2, and
-// each block's length reads before the writes that may alias them (in-place lengths).
-// Latency-bound: the bytes are 8 per token and 8 per moved page.
-__global__ void __launch_bounds__(kPlanThreads, 1) paged_assign_kernel(const PlanArgs a, DeviceStatus* st) {
-  __shared__ PlanSmem sm;
+// One cluster plans the step, in two passes over blocks of kT requests; every CTA scans each
+// block's counts itself and then takes its share of the block's pages, found by binary
+// search in the scanned prefixes.  Pass 1 pushes the pages of the released slots; pass 2
+// grants requests in order, writes the new table entries and maps the tokens (a.map; else
+// map_tokens_kernel does).  The cluster barriers order pass 1's pushes and table reads
+// before pass 2, each block's length reads before the writes that may alias them (in-place
+// lengths), and the table writes before the mapping that reads them.  Latency-bound.
+template <int kT>
+__global__ void __launch_bounds__(kT, 1) paged_assign_kernel(const PlanArgs a, DeviceStatus* st) {
+  __shared__ PlanSmem<kT> sm;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x), tid = threadIdx.x;
-  const int first = rank * kPlanThreads + tid, step = ranks * kPlanThreads;
-  const int64_t cap = static_cast<int64_t>(a.max_blocks) * a.page;
+  const uint32_t ranks = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
+  const uint32_t first = rank * kT + tid, step = ranks * kT;
+  auto sync = [&] {
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
+  };
+  const int32_t cap = a.max_blocks * a.page;  // below 2^31
+  const uint32_t page = static_cast<uint32_t>(a.page);
   int64_t have = *a.free_count;
   if (have < 0 || have > a.free_cap) {
     if (first == 0) record_status(st, kStatusBadArg, 800);
     have = have < 0 ? 0 : a.free_cap;
   }
   if (a.release) {
-    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-      const int n = min(kPlanThreads, a.B - b0);
-      int64_t pages = 0, zero = 0, total, unused;
-      if (tid < n && a.release[b0 + tid] != 0) {
+    for (int b0 = 0; b0 < a.B; b0 += kT) {
+      const int n = min(kT, a.B - b0);
+      int64_t pages = 0, total;
+      if (tid < static_cast<uint32_t>(n) && a.release[b0 + tid] != 0) {
         const int32_t c = a.ctx[b0 + tid];
         if (c < 0 || c > cap) {
           if (rank == 0) record_status(st, kStatusBadArg, 801);
         } else {
-          pages = (static_cast<int64_t>(c) + a.page - 1) / a.page;
+          pages = (static_cast<uint32_t>(c) + page - 1) / page;
         }
       }
-      block_prefix2(pages, zero, total, unused, sm.scan);
-      sm.need[tid] = pages;
+      sm.need[tid] = clamp31(block_prefix<kT>(pages, total, sm.scan));
       __syncthreads();
-      for (int64_t e = first; e < total; e += step) {
+      const int64_t room = a.free_cap - have;
+      const uint32_t count = static_cast<uint32_t>(total < room ? total : room);
+      for (uint32_t e = first; e < count; e += step) {
         const int i = find_owner(sm.need, n, e);
-        const int64_t dst = have + e;
-        if (dst < a.free_cap) a.free_pages[dst] = a.table[static_cast<int64_t>(b0 + i) * a.max_blocks + (e - sm.need[i])];
+        a.free_pages[have + e] = a.table[static_cast<int64_t>(b0 + i) * a.max_blocks + (e - sm.need[i])];
       }
-      have += total;
-      if (have > a.free_cap) {
-        if (first == 0) record_status(st, kStatusBadArg, 802);
-        have = a.free_cap;
-      }
+      if (total > room && first == 0) record_status(st, kStatusBadArg, 802);
+      have += count;
       __syncthreads();
     }
   }
-  if (ranks > 1) cluster.sync();
-  else __syncthreads();
+  sync();
   int64_t cu0 = 0, need0 = 0, taken = 0;  // sums over the blocks of requests before this one
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int n = min(kPlanThreads, a.B - b0);
-    const int b = b0 + tid;
+  for (int b0 = 0; b0 < a.B; b0 += kT) {
+    const int n = min(kT, a.B - b0), b = b0 + static_cast<int>(tid);
+    const bool live = tid < static_cast<uint32_t>(n);
     int32_t c = 0;
     int64_t tokens = 0, own = 0;
     bool valid = false;
-    if (tid < n) {
+    if (live) {
       c = a.release && a.release[b] != 0 ? 0 : a.ctx[b];
       const int32_t add = a.add[b];
       valid = c >= 0 && c <= cap && add >= 0;
       if (!valid && rank == 0) record_status(st, kStatusBadArg, 803);
-      c = c < 0 ? 0 : (c > cap ? static_cast<int32_t>(cap) : c);
+      c = c < 0 ? 0 : (c > cap ? cap : c);
       if (valid) tokens = add;
     }
-    int64_t cu = tokens, zero = 0, cu_total, unused;
-    block_prefix2(cu, zero, cu_total, unused, sm.scan);
+    int64_t cu_total, need_total;
+    const int64_t cu = block_prefix<kT>(tokens, cu_total, sm.scan);
     // a request that cannot fit (its table row, the step's tokens) asks for no page
     bool ok = valid && c + tokens <= cap && cu0 + cu + tokens <= a.max_tokens;
-    const int32_t held = (c + a.page - 1) / a.page;
-    if (ok) own = (c + tokens + a.page - 1) / a.page - held;
-    int64_t before = own, need_total;
-    zero = 0;
-    block_prefix2(before, zero, need_total, unused, sm.scan);
+    const uint32_t held = (static_cast<uint32_t>(c) + page - 1) / page;
+    if (ok) own = (static_cast<uint32_t>(c) + static_cast<uint32_t>(tokens) + page - 1) / page - held;
+    if (tid == 0) sm.got = 0;
+    const int64_t before = block_prefix<kT>(own, need_total, sm.scan);
     ok = ok && (own == 0 || need0 + before + own <= have);
-    sm.cu[tid] = cu0 + cu;
-    sm.need[tid] = need0 + before;
+    // granted requests that need pages are a prefix of those that do
+    if (ok && own > 0) atomicMax(&sm.got, static_cast<uint32_t>(before + own));
+    sm.cu[tid] = clamp31(cu);
+    sm.need[tid] = clamp31(before);
     sm.ctx[tid] = c;
     sm.ok[tid] = ok;
-    const int64_t mine = ok ? own : 0;
-    int64_t got = mine, got_total;
-    zero = 0;
-    block_prefix2(got, zero, got_total, unused, sm.scan);
-    if (tid == 0) {
-      sm.cu[n] = cu0 + cu_total;
-      sm.need[n] = need0 + need_total;
-    }
-    // every CTA has read this block's lengths: the outputs may be the same buffers
-    if (ranks > 1) cluster.sync();
-    else __syncthreads();
-    if (rank == 0 && tid < n) {
+    sync();  // every CTA has read this block's lengths: the outputs may be the same buffers
+    if (rank == 0 && live) {
       a.seqlens[b] = c + (ok ? static_cast<int32_t>(tokens) : 0);
       a.granted[b] = ok ? static_cast<int32_t>(tokens) : 0;
-      const int64_t at = cu0 + cu;
-      a.cu_new[b] = static_cast<int32_t>(at < 0x7fffffff ? at : 0x7fffffff);
+      a.cu_new[b] = static_cast<int32_t>(clamp31(cu0 + cu));
     }
-    // granted requests that need pages are a prefix of those that do, so their pages are
-    // the got_total entries below have - need0
-    for (int64_t e = first; e < got_total; e += step) {
-      const int i = find_owner(sm.need, n, need0 + e);
-      const int64_t blk = (sm.ctx[i] + a.page - 1) / a.page + (need0 + e - sm.need[i]);
-      a.table[static_cast<int64_t>(b0 + i) * a.max_blocks + blk] = a.free_pages[have - 1 - (need0 + e)];
+    // their pages are the `got` entries below `top` in the free list
+    const int32_t* top = a.free_pages + (have - 1 - need0);
+    const uint32_t got = sm.got;
+    for (uint32_t e = first; e < got; e += step) {
+      const int i = find_owner(sm.need, n, e);
+      const uint32_t blk = (static_cast<uint32_t>(sm.ctx[i]) + page - 1) / page + (e - sm.need[i]);
+      a.table[static_cast<int64_t>(b0 + i) * a.max_blocks + blk] = top[-static_cast<int64_t>(e)];
     }
-    const int64_t t1 = min(cu0 + cu_total, static_cast<int64_t>(a.max_tokens));
-    for (int64_t t = cu0 + first; t < t1; t += step) {
-      const int i = find_owner(sm.cu, n, t);
-      const int32_t pos = static_cast<int32_t>(min(sm.ctx[i] + (t - sm.cu[i]), static_cast<int64_t>(0x7fffffff)));
-      int32_t slot = -1;
-      if (sm.ok[i]) {
-        const int32_t blk = pos / a.page, nb = (sm.ctx[i] + a.page - 1) / a.page;
-        const int32_t pg = blk < nb ? a.table[static_cast<int64_t>(b0 + i) * a.max_blocks + blk]
-                                    : a.free_pages[have - 1 - (sm.need[i] + blk - nb)];
-        slot = pg * a.page + (pos - blk * a.page);
-      }
-      a.slot_map[t] = slot;
-      if (a.token_pos) a.token_pos[t] = pos;
+    if (a.map) {
+      sync();
+      map_tokens(
+          a, cu0, cu0, min(cu0 + cu_total, static_cast<int64_t>(a.max_tokens)), first, step, sm.cu, n,
+          [&](int i, int32_t& had) {
+            had = sm.ctx[i];
+            return sm.ok[i] != 0;
+          },
+          [&](int i) { return a.table + static_cast<int64_t>(b0 + i) * a.max_blocks; });
     }
     cu0 += cu_total;
     need0 += need_total;
-    taken += got_total;
+    taken += got;
     __syncthreads();
   }
-  // padding past the last token
-  for (int64_t t = min(cu0, static_cast<int64_t>(a.max_tokens)) + first; t < a.max_tokens; t += step) {
-    a.slot_map[t] = -1;
-    if (a.token_pos) a.token_pos[t] = 0;
-  }
+  if (a.map) map_padding(a, min(cu0, static_cast<int64_t>(a.max_tokens)), first, step);
   // every CTA has read free_count (before the barriers above): it may be free_count_out
   if (first == 0) {
-    a.cu_new[a.B] = static_cast<int32_t>(cu0 < 0x7fffffff ? cu0 : 0x7fffffff);
+    a.cu_new[a.B] = static_cast<int32_t>(clamp31(cu0));
     *a.free_count_out = static_cast<int32_t>(have - taken);
   }
+}
+
+// The slots and positions of a step with many tokens, from what the plan left: a request's
+// length before the step is its length after it less what it was granted.
+__global__ void __launch_bounds__(256) map_tokens_kernel(const PlanArgs a) {
+  __shared__ int32_t held[kMapRequests];
+  grid_dependency_wait();
+  const bool fits = a.B <= kMapRequests;
+  if (fits)
+    for (int i = threadIdx.x; i < a.B; i += 256) held[i] = a.cu_new[i];
+  __syncthreads();
+  const int64_t t1 = min(a.cu_new[a.B], a.max_tokens);
+  const uint32_t first = blockIdx.x * 256 + threadIdx.x, step = gridDim.x * 256;
+  auto length = [&](int i, int32_t& had) {
+    const int32_t got = a.granted[i];
+    had = a.seqlens[i] - got;
+    return got > 0;
+  };
+  auto row = [&](int i) { return a.table + static_cast<int64_t>(i) * a.max_blocks; };
+  if (fits) map_tokens(a, 0, 0, t1, first, step, held, a.B, length, row);
+  else map_tokens(a, 0, 0, t1, first, step, a.cu_new, a.B, length, row);
+  map_padding(a, t1, first, step);
+}
+
+template <int kT>
+cudaError_t launch_plan(const PlanArgs& a, unsigned ranks, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_assign_kernel<kT>, a, device_status_ptr());
 }
 
 // ---------------------------------------------------------------- rotary append
@@ -250,23 +330,26 @@ struct AppendArgs {
   uint8_t axis[128];         // axis of each rotary pair
 };
 
+// Four values as they lie in memory, and widened to fp32.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&x)[4]);
+struct Raw4 {
+  uint2 v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void widen(float (&x)[4]) const;
+};
 template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void widen(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+};
+template <>
+__device__ __forceinline__ void Raw4<__half>::widen(float (&x)[4]) const {
+  x[0] = f16_bits(v.x & 0xffffu), x[1] = f16_bits(v.x >> 16);
+  x[2] = f16_bits(v.y & 0xffffu), x[3] = f16_bits(v.y >> 16);
 }
 template <>
-__device__ __forceinline__ void load4<__half>(const __half* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-}
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void Raw4<__nv_bfloat16>::widen(float (&x)[4]) const {
   x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
   x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
@@ -315,101 +398,114 @@ __device__ __forceinline__ void turn(int32_t pos, uint64_t g, float& c, float& s
 // (4 l, rot / 2 + 4 l) halves, or the eight adjacent values 8 l .. 8 l + 7 when pairs are
 // adjacent, and the lanes past the rotated part hold eight plain values.  So a lane needs
 // the same four angles for every head: it computes them once per token and keeps them in
-// registers, and no lane exchanges values but the row maximum.  HBM-bound: q, k and v are
-// read once, q is written once and k, v as codes.
+// registers, and no lane exchanges values but the row maximum.  A warp takes 256 / D rows of
+// one kind (q, k or v) at a time, a "group", and has kBatch groups of loads in flight.
+// HBM-bound: q, k and v are read once, q is written once and k, v as codes.
 template <typename T, int D, bool kAdjacent>
 __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a, DeviceStatus* st) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = sizeof(T) == 4 ? 2 : 4;
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t tok = w / a.parts;
-  if (tok >= a.T) return;
+  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t tok = a.parts == 1 ? w : w / static_cast<uint32_t>(a.parts);
+  if (tok >= static_cast<uint32_t>(a.T)) return;
   const int part = static_cast<int>(w - tok * a.parts);
   const int l = lane % kLanes, sub = lane / kLanes;
   const bool turned = 8 * l < a.rot;
   const int ea = !kAdjacent && turned ? 4 * l : 8 * l;
   const int eb = !kAdjacent && turned ? a.rot / 2 + 4 * l : 8 * l + 4;
+  // groups: gq of q rows, then gk of k rows, then gk of v rows
+  const int gq = (a.Hq + kRows - 1) / kRows, gk = (a.Hkv + kRows - 1) / kRows;
+  const int g_begin = part * a.iters, g_end = min(gq + 2 * gk, g_begin + a.iters);
+  const T* const qt = static_cast<const T*>(a.q) + tok * a.q_stride;
+  const T* const kt = static_cast<const T*>(a.k) + tok * a.k_stride;
+  const T* const vt = static_cast<const T*>(a.v) + tok * a.v_stride;
+  const int32_t slot = a.slot_map[tok];
+  Raw4<T> ra[kBatch], rb[kBatch];
+  auto fetch = [&](int g, Raw4<T>& x, Raw4<T>& y) {
+    const bool is_q = g < gq;
+    const int h = (is_q ? g : g < gq + gk ? g - gq : g - gq - gk) * kRows + sub;
+    // the last head stands in for lanes past it, whose results are not stored
+    const T* src = (is_q ? qt : g < gq + gk ? kt : vt) + static_cast<int64_t>(min(h, (is_q ? a.Hq : a.Hkv) - 1)) * D;
+    x.load(src + ea);
+    y.load(src + eb);
+  };
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (g_begin + i < g_end) fetch(g_begin + i, ra[i], rb[i]);
   float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int rows = a.Hq + 2 * a.Hkv;
-  const int r_begin = part * a.iters * kRows, r_end = min(rows, r_begin + a.iters * kRows);
-  if (turned && r_begin < a.Hq + a.Hkv) {
+  if (turned && g_begin < gq + gk) {
+    float f[4];
+    int32_t pos[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int p = 4 * l + i;
-      turn(a.positions[static_cast<int64_t>(a.axis[p]) * a.T + tok], turns_of(a.inv_freq[p]), c[i], s[i]);
+      f[i] = a.inv_freq[4 * l + i];
+      pos[i] = a.positions[static_cast<int64_t>(a.axis[4 * l + i]) * a.T + tok];
     }
-  }
-  const int32_t slot = a.slot_map[tok];
-  bool keep = slot >= 0;
-  int64_t row0 = 0;  // the slot's row in the first head of its page
-  if (keep) {
-    const int32_t pg = slot / a.page;
-    if (pg >= a.num_pages) {
-      if (lane == 0 && part == 0) record_status(st, kStatusBadArg, 810);
-      keep = false;
-    } else {
-      row0 = static_cast<int64_t>(pg) * a.Hkv * a.page + slot % a.page;
-    }
-  }
-  for (int r0 = r_begin; r0 < r_end; r0 += kRows) {
-    const int r = r0 + sub;
-    const bool live = r < r_end;
-    const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-    const int h = is_q ? r : (is_k ? r - a.Hq : r - a.Hq - a.Hkv);
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live && (is_q || keep)) {
-      const T* src = static_cast<const T*>(is_q ? a.q : (is_k ? a.k : a.v)) +
-                     tok * (is_q ? a.q_stride : (is_k ? a.k_stride : a.v_stride)) + static_cast<int64_t>(h) * D;
-      load4<T>(src + ea, x);
-      load4<T>(src + eb, y);
-    }
-    if (turned && (is_q || is_k)) {
-      if constexpr (kAdjacent) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-          x[2 * i] = fmaf(x0, c[i], -(x1 * s[i]));
-          x[2 * i + 1] = fmaf(x1, c[i], x0 * s[i]);
-          y[2 * i] = fmaf(y0, c[i + 2], -(y1 * s[i + 2]));
-          y[2 * i + 1] = fmaf(y1, c[i + 2], y0 * s[i + 2]);
+    for (int i = 0; i < 4; ++i) turn(pos[i], turns_of(f[i]), c[i], s[i]);
+  }
+  int64_t row0 = -1;  // the slot's row in the first head of its page
+  if (slot >= 0) {
+    const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);
+    if (pg < static_cast<uint32_t>(a.num_pages))
+      row0 = static_cast<int64_t>(pg) * a.Hkv * a.page + (static_cast<uint32_t>(slot) - pg * a.page);
+    else if (lane == 0 && part == 0)
+      record_status(st, kStatusBadArg, 810);
+  }
+  T* const ot = static_cast<T*>(a.q_out) + tok * a.q_out_stride;
+  for (int g0 = g_begin; g0 < g_end; g0 += kBatch) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int g = g0 + i;
+      if (g >= g_end) break;
+      float x[4], y[4];
+      ra[i].widen(x);
+      rb[i].widen(y);
+      if (g + kBatch < g_end) fetch(g + kBatch, ra[i], rb[i]);
+      if (g < gq + gk && turned) {
+        if constexpr (kAdjacent) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+            x[2 * j] = fmaf(x0, c[j], -(x1 * s[j]));
+            x[2 * j + 1] = fmaf(x1, c[j], x0 * s[j]);
+            y[2 * j] = fmaf(y0, c[j + 2], -(y1 * s[j + 2]));
+            y[2 * j + 1] = fmaf(y1, c[j + 2], y0 * s[j + 2]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x0 = x[j], y0 = y[j];
+            x[j] = fmaf(x0, c[j], -(y0 * s[j]));
+            y[j] = fmaf(y0, c[j], x0 * s[j]);
+          }
         }
-      } else {
+      }
+      if (g < gq) {
+        const int h = g * kRows + sub;
+        if (h < a.Hq) {
+          store4<T>(ot + static_cast<int64_t>(h) * D + ea, x);
+          store4<T>(ot + static_cast<int64_t>(h) * D + eb, y);
+        }
+      } else if (row0 >= 0) {
+        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = x[i], y0 = y[i];
-          x[i] = fmaf(x0, c[i], -(y0 * s[i]));
-          y[i] = fmaf(y0, c[i], x0 * s[i]);
+        for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(x[j]), fabsf(y[j])));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const RowScale rs = row_scale(m);
+        const uint32_t ca = quant4(x, rs), cb = quant4(y, rs);
+        const bool is_k = g < gq + gk;
+        const int h = (is_k ? g - gq : g - gq - gk) * kRows + sub;
+        if (h < a.Hkv) {
+          const int64_t row = row0 + static_cast<int64_t>(h) * a.page;
+          int8_t* dst = (is_k ? a.k_pages : a.v_pages) + row * D;
+          *reinterpret_cast<uint32_t*>(dst + ea) = ca;
+          *reinterpret_cast<uint32_t*>(dst + eb) = cb;
+          if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = rs.s;
         }
       }
     }
-    if (live && is_q) {
-      T* dst = static_cast<T*>(a.q_out) + tok * a.q_out_stride + static_cast<int64_t>(h) * D;
-      store4<T>(dst + ea, x);
-      store4<T>(dst + eb, y);
-    }
-    if (r0 + kRows <= a.Hq || !keep) continue;  // uniform: the warp's rows are all q rows, or nothing is stored
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float sc = __fdiv_rn(m, 127.0f);
-    if (!live || is_q) continue;
-    uint32_t ca = 0, cb = 0;
-    if (sc != 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p = max(-127, min(127, __float2int_rn(__fdiv_rn(x[i], sc))));
-        const int q = max(-127, min(127, __float2int_rn(__fdiv_rn(y[i], sc))));
-        ca |= static_cast<uint32_t>(p & 0xff) << (8 * i);
-        cb |= static_cast<uint32_t>(q & 0xff) << (8 * i);
-      }
-    }
-    const int64_t row = row0 + static_cast<int64_t>(h) * a.page;
-    int8_t* dst = (is_k ? a.k_pages : a.v_pages) + row * D;
-    *reinterpret_cast<uint32_t*>(dst + ea) = ca;
-    *reinterpret_cast<uint32_t*>(dst + eb) = cb;
-    if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = sc;
   }
 }
 
@@ -437,16 +533,15 @@ template <int D>
 __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, DeviceStatus* st) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int h = static_cast<int>(w % a.Hkv);
-  const int64_t u = w / a.Hkv;
-  const int b = static_cast<int>(u / a.per_seq), i = static_cast<int>(u - static_cast<int64_t>(b) * a.per_seq);
-  if (b >= a.B) return;
-  const int64_t cap = static_cast<int64_t>(a.max_blocks) * a.page;
-  int64_t L = a.seqlens[b];
+  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t u = w / static_cast<uint32_t>(a.Hkv), h = w - u * a.Hkv;
+  const uint32_t b = u / static_cast<uint32_t>(a.per_seq), i = u - b * a.per_seq;
+  if (b >= static_cast<uint32_t>(a.B)) return;
+  const int32_t cap = a.max_blocks * a.page;  // below 2^31
+  int32_t L = a.seqlens[b];
   bool bad = L < 0 || L > cap;
   L = L < 0 ? 0 : (L > cap ? cap : L);
-  int64_t add = L;
+  int32_t add = L;
   if (a.add) {
     add = a.add[b];
     bad = bad || add < 0 || add > L || add > a.max_new;
@@ -454,9 +549,9 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
     if (add > a.max_new) add = a.max_new;
   }
   if (bad && i == 0 && h == 0 && lane == 0) record_status(st, kStatusBadArg, 820);
-  const int64_t blk = (L - add) / a.page + i;
-  if (add == 0 || blk * a.page >= L) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(a.page), L - blk * a.page));
+  const uint32_t blk = static_cast<uint32_t>(L - add) / static_cast<uint32_t>(a.page) + i;
+  if (add == 0 || blk * static_cast<uint64_t>(a.page) >= static_cast<uint32_t>(L)) return;
+  const int n = min(a.page, L - static_cast<int32_t>(blk) * a.page);
   int32_t pg = a.table[static_cast<int64_t>(b) * a.max_blocks + blk];
   if (pg < 0 || pg >= a.num_pages) {
     if (lane == 0) record_status(st, kStatusBadArg, 821);
@@ -476,16 +571,28 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
     lo[e] = INFINITY;
     hi[e] = -INFINITY;
   }
-#pragma unroll 2
-  for (int t = lane / kLanes; t < n; t += kRows) {
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(t) * D + 16 * l);
-    const float f = S == 0.0f ? 0.0f : __fdiv_rn(ks[t], S);
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  // kBatch rows of each lane are on their way at once; rows past n repeat the last one
+  constexpr int kBatch = 4;
+  for (int t0 = lane / kLanes; t0 < n; t0 += kBatch * kRows) {
+    uint4 v[kBatch];
+    float f[kBatch];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float y = static_cast<float>(static_cast<int8_t>(x[e / 4] >> (8 * (e % 4)))) * f;
-      lo[e] = fminf(lo[e], y);
-      hi[e] = fmaxf(hi[e], y);
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = min(t0 + j * kRows, n - 1);
+      v[j] = *reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(t) * D + 16 * l);
+      f[j] = ks[t];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float r = S == 0.0f ? 0.0f : __fdiv_rn(f[j], S);
+      const uint32_t x[4] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u, v[j].z ^ 0x80808080u, v[j].w ^ 0x80808080u};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        // code + 128 as the low bits of 2^23 + code + 128: exact, without a conversion
+        const float y = (__uint_as_float(prmt(x[e / 4], 0x4b000000u, 0x7650 + e % 4)) - 8388736.0f) * r;
+        lo[e] = fminf(lo[e], y);
+        hi[e] = fmaxf(hi[e], y);
+      }
     }
   }
 #pragma unroll
@@ -535,22 +642,18 @@ cudaError_t launch_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens
                                 int32_t max_tokens, int32_t* seqlens, int32_t* granted, int32_t* cu_new,
                                 int32_t* slot_map, int32_t* token_pos, cudaStream_t s) {
   TraceScope tr("paged_assign", s);
-  const PlanArgs a{ctx_lens, new_lens, release, B, page_size, max_blocks, block_table, free_pages, free_capacity,
-                   free_count, free_count_out, max_tokens, seqlens, granted, cu_new, slot_map, token_pos};
-  // one CTA where its threads cover the step's tokens a few times over: a cluster only
-  // adds its barriers there
-  const unsigned ranks = static_cast<int64_t>(max_tokens) + B <= 4 * kPlanThreads ? 1 : kPlanCluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_assign_kernel, a, device_status_ptr());
+  PlanArgs a{ctx_lens, new_lens, release, B, page_size, max_blocks, block_table, free_pages, free_capacity,
+             free_count, free_count_out, max_tokens, seqlens, granted, cu_new, slot_map, token_pos,
+             ((reinterpret_cast<uintptr_t>(slot_map) | reinterpret_cast<uintptr_t>(token_pos)) & 15u) == 0, true};
+  // a small step: one small CTA, whose barriers cost least
+  if (B <= 256 && max_tokens <= 1024) return launch_plan<256>(a, 1, s);
+  // many tokens are mapped by a kernel of their own, on every SM (256 requests, 254,000 tokens:
+  // 13 us instead of 23)
+  a.map = max_tokens <= 16384;
+  const cudaError_t e = launch_plan<1024>(a, kPlanCluster, s);
+  if (a.map || e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((static_cast<int64_t>(max_tokens) + 1023) / 1024, 8ll * num_sms()));
+  return launch_pdl(map_tokens_kernel, dim3(grid), dim3(256), 0, s, a);
 }
 
 cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
@@ -583,7 +686,7 @@ cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
   // one warp per token once that fills the device (about 32 warps an SM); below, a token's
   // rows are cut into parts, whose warps each compute the angles again
   const int32_t rows_at_once = 256 / r.d;
-  const int32_t groups = (r.Hq + 2 * r.Hkv + rows_at_once - 1) / rows_at_once;
+  const int32_t groups = (r.Hq + rows_at_once - 1) / rows_at_once + 2 * ((r.Hkv + rows_at_once - 1) / rows_at_once);
   const int64_t fill = 32ll * num_sms();
   int64_t iters = (static_cast<int64_t>(r.T) * groups + fill - 1) / fill;
   if (iters > groups) iters = groups;
