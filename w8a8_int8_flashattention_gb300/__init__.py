@@ -535,44 +535,52 @@ def attn_int8_decode_logits_debug(q, k_cache, k_scale, v_cache, v_scale, seqlens
 
 # ------------------------------------------------------------------ serving from the paged cache
 
-def _device(*ts) -> torch.device:
-    """The one CUDA device that every given tensor (None aside) lives on."""
-    dev = None
+_I32T, _F32T, _I8T = torch.int32, torch.float32, torch.int8
+
+
+def _index(t) -> int:
+    """The CUDA device that a tensor lives on."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("sl8 takes CUDA tensors only (no CPU fallback)")
+    return i
+
+
+def _ptrs(dev, dtype, names, *ts):
+    """Addresses of contiguous tensors of one device and dtype (None stays None); names: theirs,
+    for the error."""
+    out = []
     for t in ts:
         if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("sl8 takes CUDA tensors only (no CPU fallback)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("sl8 takes tensors of one device")
-    return dev
-
-
-def _typed(dtype, **ts) -> None:
-    """Every given tensor (None aside) is contiguous and of this dtype."""
-    for name, t in ts.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}")
-        if not t.is_contiguous():
+            out.append(None)
+        elif t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            name = names.split()[len(out)]
+            if t.get_device() != dev:
+                _index(t)
+                raise ValueError(f"{name} is on another device")
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}")
             raise ValueError(f"{name} must be contiguous")
+    return out
 
 
 def _shaped(t, shape, name) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _call(fn: str, dev: torch.device, *args) -> None:
+def _call(fn: str, dev: int, *args) -> None:
     """Call an entry point on the device's current stream, with that device current."""
-    if dev.index == torch.cuda.current_device():
-        _check(getattr(lib(), fn)(*args, _stream(dev)), fn)
+    f = getattr(_lib or lib(), fn)
+    if dev == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(getattr(lib(), fn)(*args, _stream(dev)), fn)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != SL8_OK:
+        raise SL8Error(status, fn)
 
 
 def paged_assign(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, max_tokens, release=None,
@@ -583,47 +591,54 @@ def paged_assign(ctx_lens, new_lens, block_table, free_pages, free_count, page_s
     [capacity] are updated, free_count [1] int32 is read.  Returns a dict of int32 tensors:
     seqlens, granted [B], cu_new [B + 1], slot_map, token_pos [max_tokens], free_count [1]
     (out: a dict returned earlier, whose tensors are written again)."""
-    dev = _device(ctx_lens, new_lens, block_table, free_pages, free_count, release)
-    _typed(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages,
-           free_count=free_count, release=release)
+    dev = _index(block_table)
+    p = _ptrs(dev, _I32T, "ctx_lens new_lens release block_table free_pages free_count", ctx_lens, new_lens, release,
+              block_table, free_pages, free_count)
     B, max_blocks = block_table.shape
     max_tokens = int(max_tokens)
     if ctx_lens.numel() != B or new_lens.numel() != B or (release is not None and release.numel() != B):
         raise ValueError("ctx_lens, new_lens and release need one entry per row of block_table")
+    if free_count.numel() < 1:
+        raise ValueError("free_count needs one entry")
     if out is None:
         sizes = dict(seqlens=B, granted=B, cu_new=B + 1, slot_map=max_tokens, token_pos=max_tokens, free_count=1)
-        out = {n: torch.empty(size, dtype=torch.int32, device=dev) for n, size in sizes.items()}
-    else:
-        _device(ctx_lens, *out.values())
-        _typed(torch.int32, **out)
-        if (out["seqlens"].numel() != B or out["granted"].numel() != B or out["cu_new"].numel() != B + 1 or
-                out["slot_map"].numel() != max_tokens or out["token_pos"].numel() != max_tokens):
-            raise ValueError("out holds tensors of another batch or max_tokens")
-    _call("sl8_paged_assign", dev, _ptr(ctx_lens), _ptr(new_lens), _ptr(release), B, int(page_size), max_blocks,
-          _ptr(block_table), _ptr(free_pages), free_pages.numel(), _ptr(free_count), _ptr(out["free_count"]),
-          max_tokens, _ptr(out["seqlens"]), _ptr(out["granted"]), _ptr(out["cu_new"]), _ptr(out["slot_map"]),
-          _ptr(out["token_pos"]))
+        out = {n: torch.empty(size, dtype=_I32T, device=block_table.device) for n, size in sizes.items()}
+    elif (out["seqlens"].numel() != B or out["granted"].numel() != B or out["cu_new"].numel() != B + 1 or
+          out["slot_map"].numel() != max_tokens or out["token_pos"].numel() != max_tokens or
+          out["free_count"].numel() < 1):
+        raise ValueError("out holds tensors of another batch or max_tokens")
+    o = _ptrs(dev, _I32T, "free_count seqlens granted cu_new slot_map token_pos", out["free_count"], out["seqlens"],
+              out["granted"], out["cu_new"], out["slot_map"], out["token_pos"])
+    _call("sl8_paged_assign", dev, p[0], p[1], p[2], B, int(page_size), max_blocks, p[3], p[4], free_pages.numel(), p[5],
+          o[0], max_tokens, o[1], o[2], o[3], o[4], o[5])
     return out
 
 
-def _tokens(x, name, d=None):
-    """(heads, d, stride in elements) of [T, H, d] whose tokens may be strided."""
-    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
-        raise ValueError(f"{name} must be [T, heads, d] with each token's heads contiguous")
-    if d is not None and x.shape[2] != d:
-        raise ValueError(f"{name} has head dim {x.shape[2]}, not {d}")
-    return x.shape[1], x.shape[2], (x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2])
+def _tokens(x, name, dev, dtype, T, d):
+    """(address, heads, stride in elements) of [T, heads, d] whose tokens may be strided."""
+    if x.get_device() != dev:
+        _index(x)
+        raise ValueError(f"{name} is on another device")
+    if x.dtype is not dtype:
+        raise TypeError("q, k, v and q_out must have one dtype")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or stride[2] != 1 or (shape[1] > 1 and stride[1] != d):
+        raise ValueError(f"{name} must be [{T}, heads, {d}] with each token's heads contiguous")
+    return x.data_ptr(), shape[1], (stride[0] if T > 1 else shape[1] * d)
 
 
-def _pages_of(k_pages, k_scale_pages, v_pages=None, v_scale_pages=None):
-    _typed(torch.int8, k_pages=k_pages, v_pages=v_pages)
-    _typed(torch.float32, k_scale_pages=k_scale_pages, v_scale_pages=v_scale_pages)
-    num_pages, hkv, page_size, d = k_pages.shape
-    _shaped(k_scale_pages, (num_pages, hkv, page_size), "k_scale_pages")
+def _pages_of(dev, k_pages, k_scale_pages, v_pages=None, v_scale_pages=None):
+    """((num_pages, Hkv, page_size, d), code addresses, scale addresses)."""
+    c = _ptrs(dev, _I8T, "k_pages v_pages", k_pages, v_pages)
+    s = _ptrs(dev, _F32T, "k_scale_pages v_scale_pages", k_scale_pages, v_scale_pages)
+    shape = k_pages.shape
+    if len(shape) != 4:
+        raise ValueError("pages must be [num_pages, Hkv, page_size, d]")
+    _shaped(k_scale_pages, shape[:3], "k_scale_pages")
     if v_pages is not None:
-        _shaped(v_pages, (num_pages, hkv, page_size, d), "v_pages")
-        _shaped(v_scale_pages, (num_pages, hkv, page_size), "v_scale_pages")
-    return num_pages, hkv, page_size, d
+        _shaped(v_pages, shape, "v_pages")
+        _shaped(v_scale_pages, shape[:3], "v_scale_pages")
+    return shape, c, s
 
 
 def rope_pair_axis(sections, interleaved=False) -> bytes:
@@ -649,44 +664,41 @@ def rope_append(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, 
     see rope_pair_axis) for several axes; adjacent: pairs (2p, 2p+1) instead of halves.
     positions = inv_freq = None: no rotation.  q may be None.  Returns the rotated q (q_out,
     which may be q itself)."""
-    dev = _device(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, v_pages, v_scale_pages, q_out)
-    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages, v_pages, v_scale_pages)
-    _typed(torch.int32, positions=positions, slot_map=slot_map)
-    _typed(torch.float32, inv_freq=inv_freq)
-    T = k.shape[0]
-    if _tokens(k, "k", d)[0] != hkv or _tokens(v, "v", d)[0] != hkv or v.shape[0] != T or slot_map.numel() != T:
+    dev = _index(k_pages)
+    (num_pages, hkv, page_size, d), codes, scales = _pages_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    pos, slots = _ptrs(dev, _I32T, "positions slot_map", positions, slot_map)
+    freq, = _ptrs(dev, _F32T, "inv_freq", inv_freq)
+    T, dtype = k.shape[0], k.dtype
+    kp, kh, k_stride = _tokens(k, "k", dev, dtype, T, d)
+    vp, vh, v_stride = _tokens(v, "v", dev, dtype, T, d)
+    if kh != hkv or vh != hkv or slot_map.numel() != T:
         raise ValueError("k, v and slot_map must hold the same tokens, with the pages' kv heads")
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("q, k and v must have one dtype")
+    qp = op = None
     hq = q_stride = out_stride = 0
     if q is not None:
-        hq, _, q_stride = _tokens(q, "q", d)
+        qp, hq, q_stride = _tokens(q, "q", dev, dtype, T, d)
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
-        if q.shape[0] != T or q_out.shape != q.shape or q_out.dtype != q.dtype:
-            raise ValueError("q and q_out must be alike and hold k's tokens")
-        out_stride = _tokens(q_out, "q_out", d)[2]
+            q_out = torch.empty((T, hq, d), dtype=dtype, device=q.device)
+        op, oh, out_stride = _tokens(q_out, "q_out", dev, dtype, T, d)
+        if oh != hq:
+            raise ValueError("q_out must have q's heads")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if positions is not None and positions.numel() != axes * T:
-        raise ValueError("positions must be [T] or [axes, T]")
+    axes, rot = 1, 0
+    if positions is not None:
+        axes, rot = (1 if positions.dim() == 1 else positions.shape[0]), 2 * inv_freq.numel()
+        if positions.numel() != axes * T:
+            raise ValueError("positions must be [T] or [axes, T]")
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis needs one entry per rotary pair")
-    _call("sl8_rope_append", dev, _ptr(q), _ptr(k), _ptr(v), _dt(k), q_stride, _tokens(k, "k")[2], _tokens(v, "v")[2], T,
-          hq, hkv, d, _ptr(positions), axes, rot, _ptr(inv_freq), pair_axis, int(bool(adjacent)), _ptr(q_out), out_stride,
-          _ptr(slot_map), _ptr(k_pages), _ptr(k_scale_pages), _ptr(v_pages), _ptr(v_scale_pages), num_pages, page_size)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _call("sl8_rope_append", dev, qp, kp, vp, _DTYPES[dtype], q_stride, k_stride, v_stride, T, hq, hkv, d, pos, axes, rot,
+          freq, pair_axis, 1 if adjacent else 0, op, out_stride, slots, codes[0], scales[0], codes[1], scales[1],
+          num_pages, page_size)
     return q_out
-
-
-def _bounds_of(bounds, bound_scale, num_pages, hkv, d):
-    _typed(torch.int8, bounds=bounds)
-    _typed(torch.float32, bound_scale=bound_scale)
-    _shaped(bounds, (num_pages, hkv, 2, d), "bounds")
-    _shaped(bound_scale, (num_pages, hkv), "bound_scale")
 
 
 def page_bounds(k_pages, k_scale_pages, block_table, seqlens, bounds, bound_scale, new_lens=None, max_new=None):
@@ -694,18 +706,20 @@ def page_bounds(k_pages, k_scale_pages, block_table, seqlens, bounds, bound_scal
     fp32, updated) of the pages that the last new_lens [B] int32 tokens of each sequence lie
     in (max_new: a host int >= every entry), or of every page without new_lens.
     seqlens [B] int32 counts the new tokens."""
-    dev = _device(k_pages, k_scale_pages, block_table, seqlens, bounds, bound_scale, new_lens)
-    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages)
-    _bounds_of(bounds, bound_scale, num_pages, hkv, d)
-    _typed(torch.int32, block_table=block_table, seqlens=seqlens, new_lens=new_lens)
+    dev = _index(k_pages)
+    (num_pages, hkv, page_size, d), codes, scales = _pages_of(dev, k_pages, k_scale_pages)
+    bp, = _ptrs(dev, _I8T, "bounds", bounds)
+    sp, = _ptrs(dev, _F32T, "bound_scale", bound_scale)
+    _shaped(bounds, (num_pages, hkv, 2, d), "bounds")
+    _shaped(bound_scale, (num_pages, hkv), "bound_scale")
+    p = _ptrs(dev, _I32T, "block_table seqlens new_lens", block_table, seqlens, new_lens)
     B, max_blocks = block_table.shape
     if seqlens.numel() != B or (new_lens is not None and new_lens.numel() != B):
         raise ValueError("seqlens and new_lens need one entry per row of block_table")
     if (new_lens is None) != (max_new is None):
         raise ValueError("new_lens and max_new go together")
-    _call("sl8_page_bounds", dev, _ptr(k_pages), _ptr(k_scale_pages), num_pages, page_size, _ptr(block_table), max_blocks,
-          _ptr(seqlens), _ptr(new_lens), 0 if max_new is None else int(max_new), B, hkv, d, _ptr(bounds),
-          _ptr(bound_scale))
+    _call("sl8_page_bounds", dev, codes[0], scales[0], num_pages, page_size, p[0], max_blocks, p[1], p[2],
+          0 if max_new is None else int(max_new), B, hkv, d, bp, sp)
 
 
 def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel, first=1, last=2, out=None,
@@ -717,32 +731,34 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     blocks; -1 past the list) and lens [B,T,Hkv], the tokens listed (out: a dict returned
     earlier, written again).  scores fp32 [B,T,Hkv,max_blocks] receives the scores of
     the pages of every range longer than max_sel."""
-    dev = _device(q, bounds, bound_scale, block_table, seqlens, scores)
-    _need_cuda(q)
+    dev = _index(q)
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    qp, = _ptrs(dev, q.dtype, "q", q)
+    bp, = _ptrs(dev, _I8T, "bounds", bounds)
+    sp, scp = _ptrs(dev, _F32T, "bound_scale scores", bound_scale, scores)
+    table, lens = _ptrs(dev, _I32T, "block_table seqlens", block_table, seqlens)
+    if bounds.dim() != 4 or bounds.shape[2] != 2:
+        raise ValueError("bounds must be [num_pages, Hkv, 2, d]")
     num_pages, hkv, _, d = bounds.shape
-    _bounds_of(bounds, bound_scale, num_pages, hkv, d)
-    _typed(torch.int32, block_table=block_table, seqlens=seqlens)
-    _typed(torch.float32, scores=scores)
+    _shaped(bound_scale, (num_pages, hkv), "bound_scale")
     B, max_blocks = block_table.shape
-    T, hq = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
-    if q.shape[0] != B or q.shape[-1] != d or seqlens.numel() != B:
+    shape = q.shape
+    T, hq = (1, shape[1]) if len(shape) == 3 else (shape[1], shape[2])
+    if shape[0] != B or shape[-1] != d or seqlens.numel() != B:
         raise ValueError("q, block_table, seqlens and bounds do not belong together")
-    max_sel = int(max_sel)
+    max_sel, rows = int(max_sel), B * T * hkv
     if out is None:
-        out = {"blocks": torch.empty((B, T, hkv, max_sel), dtype=torch.int32, device=dev),
-               "pages": torch.empty((B, T, hkv, max_sel), dtype=torch.int32, device=dev),
-               "lens": torch.empty((B, T, hkv), dtype=torch.int32, device=dev)}
-    else:
-        _device(q, *out.values())
-        _typed(torch.int32, **out)
-        if out["blocks"].numel() != B * T * hkv * max_sel or out["pages"].numel() != B * T * hkv * max_sel or \
-                out["lens"].numel() != B * T * hkv:
-            raise ValueError("out holds tensors of another shape")
+        new = lambda *n: torch.empty(n, dtype=_I32T, device=q.device)  # noqa: E731
+        out = {"blocks": new(B, T, hkv, max_sel), "pages": new(B, T, hkv, max_sel), "lens": new(B, T, hkv)}
+    elif (out["blocks"].numel() != rows * max_sel or out["pages"].numel() != rows * max_sel or
+          out["lens"].numel() != rows):
+        raise ValueError("out holds tensors of another shape")
+    o = _ptrs(dev, _I32T, "blocks pages lens", out["blocks"], out["pages"], out["lens"])
     if scores is not None:
         _shaped(scores, (B, T, hkv, max_blocks), "scores")
-    _call("sl8_page_select", dev, _ptr(q), _dt(q), _ptr(bounds), _ptr(bound_scale), num_pages, int(page_size),
-          _ptr(block_table), max_blocks, _ptr(seqlens), B, T, hq, hkv, d, max_sel, int(first), int(last),
-          _ptr(out["blocks"]), _ptr(out["pages"]), _ptr(out["lens"]), _ptr(scores))
+    _call("sl8_page_select", dev, qp, _DTYPES[q.dtype], bp, sp, num_pages, int(page_size), table, max_blocks, lens, B, T,
+          hq, hkv, d, max_sel, int(first), int(last), o[0], o[1], o[2], scp)
     return out
 
 
@@ -758,31 +774,38 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
     returns them (or from any other policy: full pages, the last one up to the length).
     Returns out like q (dtype q.dtype unless given) and, with return_lse, the fp32 LSE.
     workspace: uint8, at least sparse_decode_workspace_bytes (16: none is used)."""
-    dev = _device(q, k_pages, k_scale_pages, v_pages, v_scale_pages, pages, lens, workspace, out, lse)
-    _need_cuda(q, workspace, out, lse)
-    num_pages, hkv, page_size, d = _pages_of(k_pages, k_scale_pages, v_pages, v_scale_pages)
-    _typed(torch.int32, pages=pages, lens=lens)
-    _typed(torch.float32, lse=lse)
-    hq, max_sel = q.shape[-2], pages.shape[-1]
+    dev = _index(q)
+    (num_pages, hkv, page_size, d), codes, scales = _pages_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    list_p, lens_p = _ptrs(dev, _I32T, "pages lens", pages, lens)
+    shape = q.shape
+    hq, max_sel = shape[-2], pages.shape[-1]
     rows = q.numel() // (hq * d) if hq * d else 0
-    if q.shape[-1] != d or lens.numel() != rows * hkv or pages.numel() != rows * hkv * max_sel:
+    if shape[-1] != d or lens.numel() != rows * hkv or pages.numel() != rows * hkv * max_sel:
         raise ValueError("q, pages and lens do not belong together")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
-    elif out.shape != q.shape:
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != shape:
         raise ValueError("out must have q's shape")
+    if q.dtype not in _DTYPES or out.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype} or {out.dtype}")
+    qp, = _ptrs(dev, q.dtype, "q", q)
+    op, = _ptrs(dev, out.dtype, "out", out)
+    lse_p = None
     if return_lse:
         if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-        elif lse.shape != q.shape[:-1]:
+            lse = torch.empty(shape[:-1], dtype=_F32T, device=q.device)
+        elif lse.shape != shape[:-1]:
             raise ValueError("lse must have one entry per query head")
+        lse_p, = _ptrs(dev, _F32T, "lse", lse)
     if workspace is None:
         need = sparse_decode_workspace_bytes(rows, hq, hkv, max_sel, page_size, d, num_splits)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 16 else None
-    _call("sl8_attn_int8_sparse_decode", dev, _ptr(q), _dt(q), _ptr(k_pages), _ptr(k_scale_pages), _ptr(v_pages),
-          _ptr(v_scale_pages), num_pages, page_size, _ptr(pages), _ptr(lens), max_sel, rows, hq, hkv, d, num_splits,
-          _ptr(out), _dt(out), _ptr(lse) if return_lse else None, _ptr(workspace),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 16 else None
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, = _ptrs(dev, workspace.dtype, "workspace", workspace)
+        nbytes = workspace.numel() * workspace.element_size()
+    _call("sl8_attn_int8_sparse_decode", dev, qp, _DTYPES[q.dtype], codes[0], scales[0], codes[1], scales[1], num_pages,
+          page_size, list_p, lens_p, max_sel, rows, hq, hkv, d, num_splits, op, _DTYPES[out.dtype], lse_p, ws, nbytes)
     return (out, lse) if return_lse else out
 
 
