@@ -106,11 +106,11 @@ __device__ __forceinline__ float quant_row_warp(const float (&v)[D / 32], int8_t
   return sc;
 }
 
-// The same quantiser without a division per value.  x * (1 / s) is within 2^-15 of the fp32
-// quotient x / s (|x / s| <= 127; one rounding each in 1 / s, the product and the
-// quotient), so wherever it lies more than 1e-4 from a rounding border, both round to the
-// same code; the few values nearer than that, rows whose scale has no fp32 reciprocal and
-// values that are not finite take the division.
+// The same quantiser without a division per value.  x * (1 / s) is within 2^-16 of the fp32
+// quotient x / s (|x / s| <= 127; one rounding each in 1 / s and the quotient, the product
+// is exact in the fma), so wherever it lies more than 1e-4 from a rounding border, both
+// round to the same code; the few values nearer than that, rows whose scale has no fp32
+// reciprocal and values that are not finite take the division.
 struct RowScale {
   float s, r;  // the scale; what to multiply with, or 0 where the division is always taken
 };
@@ -126,8 +126,8 @@ __device__ __forceinline__ uint32_t quant4(const float (&x)[4], const RowScale& 
   bool sure = q.r != 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y = x[i] * q.r, z = y + kRound;
-    sure = sure && fabsf(y - (z - kRound)) < 0.4999f;
+    const float z = fmaf(x[i], q.r, kRound);
+    sure = sure && fabsf(fmaf(x[i], q.r, kRound - z)) < 0.4999f;
     w[i] = __float_as_uint(z);
   }
   if (!sure) {

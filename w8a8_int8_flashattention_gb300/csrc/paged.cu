@@ -403,7 +403,7 @@ __device__ __forceinline__ void turn(int32_t pos, uint64_t g, float& c, float& s
 // HBM-bound: q, k and v are read once, q is written once and k, v as codes.
 template <typename T, int D, bool kAdjacent>
 __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a, DeviceStatus* st) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = sizeof(T) == 4 ? 2 : 4;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = sizeof(T) == 4 ? 2 : 3;
   const int lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
   const uint32_t tok = a.parts == 1 ? w : w / static_cast<uint32_t>(a.parts);
@@ -413,27 +413,60 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a, De
   const bool turned = 8 * l < a.rot;
   const int ea = !kAdjacent && turned ? 4 * l : 8 * l;
   const int eb = !kAdjacent && turned ? a.rot / 2 + 4 * l : 8 * l + 4;
-  // groups: gq of q rows, then gk of k rows, then gk of v rows
+  // groups: gq of q rows, then gk of k rows, then gk of v rows; this warp's are [g0, g1)
   const int gq = (a.Hq + kRows - 1) / kRows, gk = (a.Hkv + kRows - 1) / kRows;
-  const int g_begin = part * a.iters, g_end = min(gq + 2 * gk, g_begin + a.iters);
-  const T* const qt = static_cast<const T*>(a.q) + tok * a.q_stride;
-  const T* const kt = static_cast<const T*>(a.k) + tok * a.k_stride;
-  const T* const vt = static_cast<const T*>(a.v) + tok * a.v_stride;
+  const int g0 = part * a.iters, g1 = min(gq + 2 * gk, g0 + a.iters);
   const int32_t slot = a.slot_map[tok];
-  Raw4<T> ra[kBatch], rb[kBatch];
-  auto fetch = [&](int g, Raw4<T>& x, Raw4<T>& y) {
-    const bool is_q = g < gq;
-    const int h = (is_q ? g : g < gq + gk ? g - gq : g - gq - gk) * kRows + sub;
-    // the last head stands in for lanes past it, whose results are not stored
-    const T* src = (is_q ? qt : g < gq + gk ? kt : vt) + static_cast<int64_t>(min(h, (is_q ? a.Hq : a.Hkv) - 1)) * D;
-    x.load(src + ea);
-    y.load(src + eb);
-  };
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i)
-    if (g_begin + i < g_end) fetch(g_begin + i, ra[i], rb[i]);
   float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (turned && g_begin < gq + gk) {
+  auto rotate = [&](float (&x)[4], float (&y)[4]) {
+    if (!turned) return;
+    if constexpr (kAdjacent) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+        x[2 * j] = fmaf(x0, c[j], -(x1 * s[j]));
+        x[2 * j + 1] = fmaf(x1, c[j], x0 * s[j]);
+        y[2 * j] = fmaf(y0, c[j + 2], -(y1 * s[j + 2]));
+        y[2 * j + 1] = fmaf(y1, c[j + 2], y0 * s[j + 2]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x0 = x[j], y0 = y[j];
+        x[j] = fmaf(x0, c[j], -(y0 * s[j]));
+        y[j] = fmaf(y0, c[j], x0 * s[j]);
+      }
+    }
+  };
+  // Groups [from, to) of one kind, whose rows start at src: kBatch groups are on their way
+  // while one is worked on.  The last head stands in for lanes past it, which store nothing.
+  auto stream = [&](const T* src, int from, int to, int heads, auto first, auto work) {
+    Raw4<T> ra[kBatch], rb[kBatch];
+    auto fetch = [&](int g, Raw4<T>& x, Raw4<T>& y) {
+      const T* p = src + min(g * kRows + sub, heads - 1) * D;
+      x.load(p + ea);
+      y.load(p + eb);
+    };
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (from + i < to) fetch(from + i, ra[i], rb[i]);
+    first();
+    for (int g = from; g < to; g += kBatch) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (g + i >= to) break;
+        float x[4], y[4];
+        ra[i].widen(x);
+        rb[i].widen(y);
+        if (g + i + kBatch < to) fetch(g + i + kBatch, ra[i], rb[i]);
+        work((g + i) * kRows + sub, x, y);
+      }
+    }
+  };
+  bool angles = false;
+  auto make_angles = [&] {  // once, behind the first rows' loads
+    if (angles || !turned) return;
+    angles = true;
     float f[4];
     int32_t pos[4];
 #pragma unroll
@@ -443,70 +476,56 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a, De
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) turn(pos[i], turns_of(f[i]), c[i], s[i]);
+  };
+  if (g0 < gq) {
+    T* const out = static_cast<T*>(a.q_out) + tok * a.q_out_stride;
+    stream(static_cast<const T*>(a.q) + tok * a.q_stride, g0, min(g1, gq), a.Hq, make_angles,
+           [&](int h, float (&x)[4], float (&y)[4]) {
+             rotate(x, y);
+             if (h < a.Hq) {
+               store4<T>(out + h * D + ea, x);
+               store4<T>(out + h * D + eb, y);
+             }
+           });
   }
-  int64_t row0 = -1;  // the slot's row in the first head of its page
-  if (slot >= 0) {
-    const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);
-    if (pg < static_cast<uint32_t>(a.num_pages))
-      row0 = static_cast<int64_t>(pg) * a.Hkv * a.page + (static_cast<uint32_t>(slot) - pg * a.page);
-    else if (lane == 0 && part == 0)
-      record_status(st, kStatusBadArg, 810);
+  if (g1 <= gq || slot < 0) return;
+  const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);
+  if (pg >= static_cast<uint32_t>(a.num_pages)) {
+    if (lane == 0 && g1 == gq + 2 * gk) record_status(st, kStatusBadArg, 810);
+    return;
   }
-  T* const ot = static_cast<T*>(a.q_out) + tok * a.q_out_stride;
-  for (int g0 = g_begin; g0 < g_end; g0 += kBatch) {
+  // the slot's row in the first head of its page
+  const int64_t row0 = static_cast<int64_t>(pg) * a.Hkv * a.page + (static_cast<uint32_t>(slot) - pg * a.page);
+  auto store_codes = [&](int8_t* pages, float* scales, int h, const float (&x)[4], const float (&y)[4]) {
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int g = g0 + i;
-      if (g >= g_end) break;
-      float x[4], y[4];
-      ra[i].widen(x);
-      rb[i].widen(y);
-      if (g + kBatch < g_end) fetch(g + kBatch, ra[i], rb[i]);
-      if (g < gq + gk && turned) {
-        if constexpr (kAdjacent) {
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(x[j]), fabsf(y[j])));
+    if constexpr (kLanes == 32) {  // magnitudes order as their bits do
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
-            x[2 * j] = fmaf(x0, c[j], -(x1 * s[j]));
-            x[2 * j + 1] = fmaf(x1, c[j], x0 * s[j]);
-            y[2 * j] = fmaf(y0, c[j + 2], -(y1 * s[j + 2]));
-            y[2 * j + 1] = fmaf(y1, c[j + 2], y0 * s[j + 2]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x0 = x[j], y0 = y[j];
-            x[j] = fmaf(x0, c[j], -(y0 * s[j]));
-            y[j] = fmaf(y0, c[j], x0 * s[j]);
-          }
-        }
-      }
-      if (g < gq) {
-        const int h = g * kRows + sub;
-        if (h < a.Hq) {
-          store4<T>(ot + static_cast<int64_t>(h) * D + ea, x);
-          store4<T>(ot + static_cast<int64_t>(h) * D + eb, y);
-        }
-      } else if (row0 >= 0) {
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(x[j]), fabsf(y[j])));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const RowScale rs = row_scale(m);
-        const uint32_t ca = quant4(x, rs), cb = quant4(y, rs);
-        const bool is_k = g < gq + gk;
-        const int h = (is_k ? g - gq : g - gq - gk) * kRows + sub;
-        if (h < a.Hkv) {
-          const int64_t row = row0 + static_cast<int64_t>(h) * a.page;
-          int8_t* dst = (is_k ? a.k_pages : a.v_pages) + row * D;
-          *reinterpret_cast<uint32_t*>(dst + ea) = ca;
-          *reinterpret_cast<uint32_t*>(dst + eb) = cb;
-          if (l == 0) (is_k ? a.k_scale : a.v_scale)[row] = rs.s;
-        }
-      }
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-  }
+    const RowScale rs = row_scale(m);
+    const uint32_t ca = quant4(x, rs), cb = quant4(y, rs);
+    if (h < a.Hkv) {
+      const int64_t row = row0 + static_cast<int64_t>(h) * a.page;
+      *reinterpret_cast<uint32_t*>(pages + row * D + ea) = ca;
+      *reinterpret_cast<uint32_t*>(pages + row * D + eb) = cb;
+      if (l == 0) scales[row] = rs.s;
+    }
+  };
+  const int ka = max(g0 - gq, 0), kb = min(g1 - gq, gk);
+  if (ka < kb)
+    stream(static_cast<const T*>(a.k) + tok * a.k_stride, ka, kb, a.Hkv, make_angles,
+           [&](int h, float (&x)[4], float (&y)[4]) {
+             rotate(x, y);
+             store_codes(a.k_pages, a.k_scale, h, x, y);
+           });
+  const int va = max(g0 - gq - gk, 0), vb = g1 - gq - gk;
+  if (va < vb)
+    stream(static_cast<const T*>(a.v) + tok * a.v_stride, va, vb, a.Hkv, [] {},
+           [&](int h, float (&x)[4], float (&y)[4]) { store_codes(a.v_pages, a.v_scale, h, x, y); });
 }
 
 // ---------------------------------------------------------------- page bounds
@@ -526,12 +545,13 @@ struct BoundsArgs {
 // Per-channel bounds of a page's keys.  With S the largest row scale among the page's
 // valid rows, row t's keys are code * (s_t / S) in steps of S; the bounds are the floor
 // of the least and the ceiling of the largest, so lo S <= k <= hi S holds for every key
-// (up to the rounding of s_t / S and of the product).  A warp per (page, kv head): D / 16
-// lanes hold a row, 16 channels each, and the rows run over the remaining lanes.
-// HBM-bound on the codes, which the append has just left in L2.
+// (up to the rounding of s_t / S and of the product).  A warp per (page, kv head): D / 8
+// lanes hold a row, 8 channels each, and the rows run over the remaining lanes, kBatch of a
+// lane's rows on their way at once.  Bound by the latency of the chain length -> page id ->
+// rows on few pages, by the codes' bytes (which the append has just left in L2) on many.
 template <int D>
 __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, DeviceStatus* st) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
   const int lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
   const uint32_t u = w / static_cast<uint32_t>(a.Hkv), h = w - u * a.Hkv;
@@ -560,34 +580,36 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
   const int64_t ph = static_cast<int64_t>(pg) * a.Hkv + h;
   const int8_t* codes = a.k_pages + ph * a.page * D;
   const float* ks = a.k_scale + ph * a.page;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  uint2 v[kBatch];
+  float f[kBatch];
+  auto fetch = [&](int t0) {  // rows past n repeat the last one
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = min(t0 + j * kRows, n - 1);
+      v[j] = *reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(t) * D + 8 * l);
+      f[j] = ks[t];
+    }
+  };
+  fetch(sub);
   float S = 0.0f;
   for (int t = lane; t < n; t += 32) S = fmaxf(S, ks[t]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) S = fmaxf(S, __shfl_xor_sync(0xffffffffu, S, o));
-  const int l = lane % kLanes;
-  float lo[16], hi[16];
+  float lo[8], hi[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 8; ++e) {
     lo[e] = INFINITY;
     hi[e] = -INFINITY;
   }
-  // kBatch rows of each lane are on their way at once; rows past n repeat the last one
-  constexpr int kBatch = 4;
-  for (int t0 = lane / kLanes; t0 < n; t0 += kBatch * kRows) {
-    uint4 v[kBatch];
-    float f[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int t = min(t0 + j * kRows, n - 1);
-      v[j] = *reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(t) * D + 16 * l);
-      f[j] = ks[t];
-    }
+  for (int t0 = sub; t0 < n; t0 += kBatch * kRows) {
+    if (t0 != sub) fetch(t0);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const float r = S == 0.0f ? 0.0f : __fdiv_rn(f[j], S);
-      const uint32_t x[4] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u, v[j].z ^ 0x80808080u, v[j].w ^ 0x80808080u};
+      const uint32_t x[2] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u};
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 8; ++e) {
         // code + 128 as the low bits of 2^23 + code + 128: exact, without a conversion
         const float y = (__uint_as_float(prmt(x[e / 4], 0x4b000000u, 0x7650 + e % 4)) - 8388736.0f) * r;
         lo[e] = fminf(lo[e], y);
@@ -598,21 +620,21 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
 #pragma unroll
   for (int o = kLanes; o < 32; o <<= 1) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8; ++e) {
       lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
       hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
     }
   }
   if (lane < kLanes) {
-    uint32_t a4[4] = {0, 0, 0, 0}, b4[4] = {0, 0, 0, 0};
+    uint32_t a2[2] = {0, 0}, b2[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      a4[e / 4] |= static_cast<uint32_t>(static_cast<int>(floorf(lo[e])) & 0xff) << (8 * (e % 4));
-      b4[e / 4] |= static_cast<uint32_t>(static_cast<int>(ceilf(hi[e])) & 0xff) << (8 * (e % 4));
+    for (int e = 0; e < 8; ++e) {
+      a2[e / 4] |= static_cast<uint32_t>(static_cast<int>(floorf(lo[e])) & 0xff) << (8 * (e % 4));
+      b2[e / 4] |= static_cast<uint32_t>(static_cast<int>(ceilf(hi[e])) & 0xff) << (8 * (e % 4));
     }
-    int8_t* dst = a.bounds + ph * 2 * D + 16 * l;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
-    *reinterpret_cast<uint4*>(dst + D) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+    int8_t* dst = a.bounds + ph * 2 * D + 8 * l;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(a2[0], a2[1]);
+    *reinterpret_cast<uint2*>(dst + D) = make_uint2(b2[0], b2[1]);
     if (lane == 0) a.scale[ph] = S;
   }
 }
@@ -688,10 +710,9 @@ cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
   const int32_t rows_at_once = 256 / r.d;
   const int32_t groups = (r.Hq + rows_at_once - 1) / rows_at_once + 2 * ((r.Hkv + rows_at_once - 1) / rows_at_once);
   const int64_t fill = 32ll * num_sms();
-  int64_t iters = (static_cast<int64_t>(r.T) * groups + fill - 1) / fill;
-  if (iters > groups) iters = groups;
-  a.iters = static_cast<int32_t>(iters);
-  a.parts = static_cast<int32_t>((groups + iters - 1) / iters);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(groups, fill / r.T));
+  a.iters = static_cast<int32_t>((groups + parts - 1) / parts);
+  a.parts = (groups + a.iters - 1) / a.iters;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(r.T) * a.parts + 7) / 8);
   switch (r.dtype) {
     case SL8_F16: return launch_append_t<__half>(a, r.d, r.adjacent, grid, s);
