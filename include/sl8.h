@@ -453,7 +453,8 @@ SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, c
  *                 page_size or more is recorded (SL8_ERR_DEVICE_ARG) and not stored.
  *   k_pages, k_scale_pages, v_pages, v_scale_pages   device, updated rows only: int8 codes
  *                 [num_pages][Hkv][page_size][d] and fp32 scales [num_pages][Hkv][page_size].
- * The rotated k is quantised from its fp32 values.  num_pages * page_size < 2^31.
+ * The rotated k is quantised from its fp32 values.  A row with an infinity gets the scale
+ * inf and codes 0, a NaN the code 0.  num_pages * page_size < 2^31.
  */
 SL8_API int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
                             int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,

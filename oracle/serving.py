@@ -18,7 +18,7 @@ def _quant(x):
     s = np.abs(x).max(-1).astype(np.float32) / np.float32(127.0)
     with np.errstate(invalid="ignore", divide="ignore"):
         c = np.rint(x / s[..., None])
-    c = np.where(s[..., None] == 0, 0, np.clip(c, -127, 127))
+    c = np.where((s[..., None] == 0) | np.isinf(s[..., None]), 0, np.clip(c, -127, 127))
     return c.astype(np.int8), s
 
 

@@ -212,6 +212,34 @@ def test_rope_append_in_place_and_bad_slot():
     assert int((scales[0] != 0).sum()) == 4 * hkv
 
 
+def test_stored_rows_are_the_quantisers():
+    """Codes without a division per value: the bits of the quantiser's definition, on values that
+    sit on rounding borders and on tiny and huge rows; a row with an infinity gets the scale
+    inf and codes 0, a NaN the code 0."""
+    g = torch.Generator().manual_seed(9)
+    T, hkv, d = 512, 4, 64
+    v = torch.randn((T, hkv, d), generator=g)
+    v[0:64] = torch.randint(-254, 255, (64, hkv, d), generator=g).float() / 2  # halves of a step of 1
+    v[0:64, :, 0] = 127.0
+    v[64:128] *= torch.logspace(-44, 37, 64)[:, None, None]
+    v[128:192] = torch.randint(-254, 255, (64, hkv, d), generator=g).float() / 2 * (1 + 2.0 ** -23)
+    v[128:192, :, 1] = -127.0
+    v[192, :, 3], v[193, :, 3], v[194, :, 3] = float("inf"), float("-inf"), float("nan")
+    v[195, :, 3], v[195, :, 9] = float("nan"), float("inf")
+    v[196] = float("nan")
+    v[197] = 0
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        x = v.to(dtype).to(DEV)
+        pages, scales = torch.zeros((2, 1, hkv, T, d), dtype=torch.int8, device=DEV), torch.zeros((2, 1, hkv, T), device=DEV)
+        sl8.rope_append(None, x, x, None, None, i32(np.arange(T)), pages[0], scales[0], pages[1], scales[1])
+        h = x.float().cpu().numpy()
+        want, s = S._quant(np.where(np.isnan(h), 0, h))
+        want[np.isinf(h).any(-1)] = 0
+        for i in range(2):
+            np.testing.assert_array_equal(pages[i, 0].transpose(0, 1).cpu().numpy(), want)
+            np.testing.assert_array_equal(scales[i, 0].T.cpu().numpy(), s)
+
+
 def test_rope_append_to_a_contiguous_cache():
     """page_size = Lmax: the contiguous cache of attn_int8_decode."""
     B, hq, hkv, d, L = 3, 8, 2, 128, 50
@@ -385,7 +413,7 @@ def _check_attention(out, lse, want, wlse, vmax, n):
     dead = np.isinf(wlse)
     assert np.array_equal(got == -np.inf, dead)
     # logits: an exact integer times three fp32 factors; the sum: ex2.approx (2^-22) of each
-    assert np.all(np.abs(got - wlse)[~dead] <= 1e-5 + 1e-6 * np.abs(wlse[~dead]))
+    assert np.all(np.abs(got[~dead] - wlse[~dead]) <= 1e-5 + 1e-6 * np.abs(wlse[~dead]))
     assert np.all(np64(out).reshape(want.shape)[dead] == 0)
 
 
@@ -394,7 +422,13 @@ def _check_attention(out, lse, want, wlse, vmax, n):
     (5, 6, 2, 64, 48, 7, 1, torch.float16, torch.float16), (2, 16, 1, 128, 64, 9, 3, torch.float32, torch.float32),
     (4, 12, 1, 256, 16, 33, 0, torch.bfloat16, torch.float32), (2, 3, 3, 32, 32, 5, 2, torch.float16, torch.bfloat16),
     (70, 16, 8, 128, 16, 12, 0, torch.bfloat16, torch.bfloat16), (2, 64, 2, 64, 16, 40, 5, torch.bfloat16, torch.float32),
-    (300, 2, 2, 64, 16, 3, 0, torch.float16, torch.float16)])
+    (300, 2, 2, 64, 16, 3, 0, torch.float16, torch.float16),
+    # more than 8 splits: the split kernel and the combine
+    (2, 8, 2, 128, 16, 40, 20, torch.bfloat16, torch.float32), (1, 12, 1, 256, 32, 30, 9, torch.float16, torch.float16),
+    (1, 3, 3, 32, 16, 64, 30, torch.float32, torch.bfloat16), (1, 4, 1, 64, 64, 520, 0, torch.bfloat16, torch.float32),
+    # one CTA a list and more lists than one wave of them
+    (240, 4, 2, 128, 48, 5, 0, torch.bfloat16, torch.float32), (500, 8, 1, 64, 16, 20, 0, torch.float16, torch.float32),
+    (120, 4, 4, 32, 16, 11, 0, torch.bfloat16, torch.float32), (180, 9, 3, 256, 16, 6, 0, torch.bfloat16, torch.float32)])
 def test_sparse_decode(R, hq, hkv, d, page, max_sel, splits, dtype, odt):
     rng = np.random.default_rng(R * 31 + d)
     num_pages = max_sel * 2 + 3

@@ -277,8 +277,9 @@ struct CacheMaps {
 };
 
 // kVerify: the speculative-verify form (a.verify_T > 0), built apart so that plain decode
-// carries none of its per-column masks.
-template <int D, bool kV16, bool kVerify>
+// carries none of its per-column masks.  kLists: the form over page lists (a.list_heads >
+// 0), built apart for the same reason (its address arithmetic cost the paged loader 5%).
+template <int D, bool kV16, bool kVerify, bool kLists>
 __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     decode_split_kernel(const DecodeArgs a, const __grid_constant__ CacheMaps maps, uint32_t ticket,
                         DeviceStatus* st, uint64_t limit_ns) {
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         if (first >= 0) {
           j = first;
           first = -1;
-        } else if (a.list_heads) {
+        } else if (kLists) {
           j = last + gridDim.x;
         } else {
           if (!claiming) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         }
         last = j;
         // start the following claim now; its result is read at the next call
-        if (!a.list_heads) {
+        if (!kLists) {
           if (lane == 0) pending = atomicAdd(counter, 1u);
           claiming = true;
         }
@@ -453,8 +454,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
               pg = 0;
             }
             const int64_t prow =
-                (a.list_heads ? static_cast<int64_t>(pg) * a.list_heads + cur.b % a.list_heads
-                              : static_cast<int64_t>(pg) * (a.Hkv / a.kv_groups) + cur.hkv / a.kv_groups) * a.page_size +
+                (kLists ? static_cast<int64_t>(pg) * a.list_heads + cur.b % a.list_heads
+                        : static_cast<int64_t>(pg) * (a.Hkv / a.kv_groups) + cur.hkv / a.kv_groups) * a.page_size +
                 t % a.page_size;
             for (int r = 0; r < rows;) {
               const int left = rows - r;
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     }
     // This CTA claims no more; a claim still in flight is part of the count.  The last
     // CTA of the launch resets the ticket's counters.
-    if (lane == 0 && !a.list_heads) {
+    if (lane == 0 && !kLists) {
       if (claiming) {
         volatile uint32_t settled = pending;  // the claim in flight has completed
         (void)settled;
@@ -1133,10 +1134,10 @@ __global__ void timeout_selftest_kernel(uint64_t limit_ns, DeviceStatus* st) {
   if (threadIdx.x == 0) mbar_wait(&bar, 0, limit_ns, st, 999);
 }
 
-template <int D, bool kV16, bool kVerify = false>
+template <int D, bool kV16, bool kVerify = false, bool kLists = false>
 cudaError_t launch_split_d(const DecodeArgs& a, cudaStream_t s) {
   using C = DCfg<D, kV16>;
-  auto kern = decode_split_kernel<D, kV16, kVerify>;
+  auto kern = decode_split_kernel<D, kV16, kVerify, kLists>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
   // each cache as a 2-D [B * Hkv * Lmax rows][d bytes] tensor, loaded in boxes of
@@ -1144,7 +1145,7 @@ cudaError_t launch_split_d(const DecodeArgs& a, cudaStream_t s) {
   // loaded in boxes of one 16-token unit
   const bool paged = a.block_table != nullptr;
   // kv heads the cache holds
-  const uint64_t hkv_cache = static_cast<uint64_t>(a.list_heads ? a.list_heads : a.Hkv / a.kv_groups);
+  const uint64_t hkv_cache = static_cast<uint64_t>(kLists ? a.list_heads : a.Hkv / a.kv_groups);
   const uint64_t rows = paged ? static_cast<uint64_t>(a.num_pages) * hkv_cache * a.page_size
                               : static_cast<uint64_t>(a.B) * hkv_cache * a.Lmax;
   bool ok = true;
@@ -1186,6 +1187,15 @@ cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t s) {
       case 64: return launch_split_d<64, false, true>(a, s);
       case 128: return launch_split_d<128, false, true>(a, s);
       case 256: return launch_split_d<256, false, true>(a, s);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+  if (a.list_heads) {
+    switch (a.d) {
+      case 32: return launch_split_d<32, false, false, true>(a, s);
+      case 64: return launch_split_d<64, false, false, true>(a, s);
+      case 128: return launch_split_d<128, false, false, true>(a, s);
+      case 256: return launch_split_d<256, false, false, true>(a, s);
       default: return cudaErrorInvalidValue;
     }
   }
