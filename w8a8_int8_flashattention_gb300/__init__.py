@@ -12,7 +12,9 @@ per-row int8 quantisation ("Supporting kernels" table, quant_rowwise; "Quantizat
 table, per-row int8 with K-smoothing), W8A8 INT8 FlashAttention prefill, dense and
 varlen ("Attention kernels" table, attn_int8_fwd / attn_varlen_fwd; "Quick start"
 layouts) and split-KV decode over an int8 KV cache ("Attention kernels" table,
-attn_decode, int8-V variant).
+attn_decode, int8-V variant); and what serving from the paged int8 cache takes ("Engine"
+table, "Paged KV cache" row): the page plan of a step, the rotary append, page bounds,
+page selection and decode over page lists.
 """
 from __future__ import annotations
 

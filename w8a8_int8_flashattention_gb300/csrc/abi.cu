@@ -1,6 +1,7 @@
 // C ABI of libsl8: argument validation, workspace planning, the per-device status
-// word, tensor-map encoding and kernel tracing.  The kernels live in quant.cu,
-// prefill.cu and decode.cu; every entry point here only validates and enqueues.
+// word, tensor-map encoding and kernel tracing.  The kernels live in quant.cu, prefill.cu,
+// decode.cu, paged.cu, select.cu and list_decode.cu; every entry point here only validates
+// and enqueues.
 #include <cudaTypedefs.h>
 
 #include <atomic>

@@ -18,7 +18,10 @@
 //    take 29 of the 180 cycles that their bytes need); O^T[d x 8 q] += V^T P'^T as fp16
 //    MMAs on V codes biased by 128 (P' = p * s_v * 2^-E rounded to fp16, 2^-11 relative;
 //    sums and the output accumulate in fp32).
-// HBM is the bound; the listed pages are read once per 8 query heads of a kv head.
+// HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
+// 8 kv heads x 4,096 tokens (d = 128) take 94 us, 5.8 TB/s, 0.85 of the measured copy rate;
+// 448 lists of that length 0.92; 32 lists of 512 tokens 7.4 us, mostly launch, prologue and
+// merge.  (The split kernel and the combine over the same lists: 152 and 14.4 us.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
