@@ -576,7 +576,7 @@ def _shaped(t, shape, name) -> None:
 def _call(fn: str, dev: int, *args) -> None:
     """Call an entry point on the device's current stream, with that device current."""
     f = getattr(_lib or lib(), fn)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):

@@ -6,13 +6,13 @@
 //
 // GB300 design.  A list is short (some thousand tokens) and there are many, so the kernel
 // is not persistent: a cluster of S CTAs serves one list, each CTA a contiguous run of its
-// stages of 16 W tokens, and two or three CTAs share an SM, one's start and end hidden behind
+// stages of 64 tokens, and two to four CTAs share an SM, one's start and end hidden behind
 // the others' streams.  The S partial results meet over distributed shared memory, so one
 // launch does everything and no workspace or counter is shared between launches.
 //  * The last warp loads: per stage, one lane per piece of 64, 32 or 16 rows (the largest
 //    that divides the page) issues the piece's K and V tiles (TMA, 128-byte swizzle for
 //    d >= 128) and its two scale rows; page ids are read 32 pieces ahead.
-//  * Warps 0..W-1 take 16 tokens of every stage each, with an online-softmax state of
+//  * Warps 0..3 take 16 tokens of every stage each, with an online-softmax state of
 //    their own.  S^T[16 tokens x 8 q] = K Q^T runs as int8 m16n8k32 MMAs, whose A operand is the
 //    K rows as they lie in memory (this part's int8 rate is low, but 8 MMAs per 16 tokens
 //    take 29 of the 180 cycles that their bytes need); O^T[d x 8 q] += V^T P'^T as fp16
@@ -40,48 +40,49 @@ namespace {
 
 constexpr int kMaxSplits = 8;                // CTAs per list (portable cluster size)
 
-// W compute warps.  Four: three CTAs share an SM (two at d = 256).  Eight: two CTAs share an SM,
-// each nearly twice as fast alone.
-template <int D, int W>
+constexpr int kWarps = 4, kCThreads = 32 * kWarps;  // compute warps
+constexpr int kThreads = kCThreads + 32;            // and the loader
+constexpr int kTok = 16 * kWarps;                   // tokens per stage
+
+// kCtas CTAs share an SM: three (two at d = 256) with every register that the loop wants, or four
+// with 96 a thread, some of them spilled.
+template <int D, int kCtas>
 struct LCfg {
-  static constexpr int kWarps = W, kCThreads = 32 * W, kThreads = kCThreads + 32;
-  static constexpr int kTok = 16 * W;            // tokens per stage
   static constexpr int kBW = D < 128 ? D : 128;  // bytes in one row of a TMA box
   static constexpr int kBoxes = D / kBW;
   static constexpr bool kSwz = D >= 128;
   static constexpr int kTile = kTok * D;
   static constexpr int kSK = 0, kSV = kTile, kSKs = 2 * kTile, kSVs = kSKs + kTok * 4;
   static constexpr int kStageBytes = (kSVs + kTok * 4 + 1023) / 1024 * 1024;
-  static constexpr int kStages = D == 256 ? 3 : (W == 4 ? (D == 128 ? 4 : 8) : (D == 128 ? 3 : 6));
-  static constexpr int kCtas = W == 8 ? 2 : D == 256 ? 2 : 3;  // resident per SM
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kCtas == 4 ? 3 : 4) : (kCtas == 4 ? 6 : 8);
   // after the loop the ring holds the warps' O^T [warp][D][8] and the CTA's [D][8], fp32
-  static constexpr int kRed = 0, kPart = W * D * 32;
+  static constexpr int kRed = 0, kPart = kWarps * D * 32;
   static_assert(kPart + D * 32 <= kStages * kStageBytes, "the merge fits the ring");
   static constexpr int kQc = kStages * kStageBytes;       // [8][D] query codes
   static constexpr int kQs = kQc + 8 * D;                 // [8] scales
   static constexpr int kStat = kQs + 32;                  // [warp][8][2]: max (log2), sum
-  static constexpr int kWt = kStat + W * 64;        // [warp][8] weights of the warps
-  static constexpr int kMl = kWt + W * 32;          // [8] max, [8] sum of the CTA
+  static constexpr int kWt = kStat + kWarps * 64;        // [warp][8] weights of the warps
+  static constexpr int kMl = kWt + kWarps * 32;          // [8] max, [8] sum of the CTA
   static constexpr int kBar = kMl + 64;
   static constexpr int kBytes = kBar + 2 * kStages * 8 + 1024;  // + alignment slack
   static_assert(kStageBytes % 1024 == 0 && kTile % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 };
 
 // Byte offset of (row r, 16-byte chunk c of the row) in a stage tile of kBoxes boxes.
-template <int D, int W>
+template <int D>
 __device__ __forceinline__ uint32_t ltile_off(int r, int c) {
-  using C = LCfg<D, W>;
+  using C = LCfg<D, 3>;
   constexpr int cpb = C::kBW / 16;
   const int b = c / cpb, cc = c % cpb;
-  return static_cast<uint32_t>(b * (C::kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
+  return static_cast<uint32_t>(b * (kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
 }
 
-template <int D, int W>
-__global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
+template <int D, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas)
     list_decode_kernel(const ListDecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, DeviceStatus* st, uint64_t limit_ns) {
-  using C = LCfg<D, W>;
-  constexpr int kStages = C::kStages, kTok = C::kTok, kCThreads = C::kCThreads;
+  using C = LCfg<D, kCtas>;
+  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], W);
+      mbar_init(&empty[i], kWarps);
     }
     fence_barrier_init();
   }
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
   const int t0 = s0 * kTok, t1 = min(L, s1 * kTok), n = s1 - s0;
   __syncthreads();
 
-  if (warp == W) {
+  if (warp == kWarps) {
     // ------------------------------------------------------------ loader
     const int pieces = kTok / a.box;
     const int head = v % a.Hkv;
@@ -214,8 +215,8 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
     } else {
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
-        offk[h][0] = ltile_off<D, W>(u0 + pi, 4 * h + t);
-        offk[h][1] = ltile_off<D, W>(u0 + pi + 8, 4 * h + t);
+        offk[h][0] = ltile_off<D>(u0 + pi, 4 * h + t);
+        offk[h][1] = ltile_off<D>(u0 + pi + 8, 4 * h + t);
       }
     }
     // V rows of the lane: unit tokens tok(2t), tok(2t + 1) and the same + 8, chunk pi
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
         const int row = u0 + tok(2 * t + (c & 1)) + 8 * (c >> 1);
         offv[b][c] = D == 32   ? static_cast<uint32_t>(row * 32 + 4 * pi)
                      : D == 64 ? static_cast<uint32_t>(row * 64 + 8 * pi)
-                               : ltile_off<D, W>(row, 8 * b + pi);
+                               : ltile_off<D>(row, 8 * b + pi);
       }
 
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.0f, l_b = 0.0f;
@@ -391,16 +392,16 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
       *reinterpret_cast<float2*>(r + 8) = make_float2(fmaf(o[j][2], k2p24, ca) * pe, fmaf(o[j][3], k2p24, cb) * pe);
     }
     named_bar_sync(1, kCThreads);
-    if (threadIdx.x < 8 * W) {  // column c: the weight of warp w's state, and (w = 0) max and sum
+    if (threadIdx.x < 8 * kWarps) {  // column c: the weight of warp w's state, and (w = 0) max and sum
       const int c = threadIdx.x & 7, w = threadIdx.x >> 3;
       float M = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) M = fmaxf(M, stat[(i * 8 + c) * 2]);
+      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, stat[(i * 8 + c) * 2]);
       const float mw = stat[(w * 8 + c) * 2];
       wt[w * 8 + c] = mw == -INFINITY ? 0.0f : ex2(mw - M);
       if (w == 0) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < kWarps; ++i) {
           const float mi = stat[(i * 8 + c) * 2];
           if (mi != -INFINITY) sum = fmaf(ex2(mi - M), stat[(i * 8 + c) * 2 + 1], sum);
         }
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
       if (4 * h >= GC) continue;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float4 r = *reinterpret_cast<const float4*>(red + (w * D + dim) * 8 + 4 * h);
         const float4 f = *reinterpret_cast<const float4*>(wt + w * 8 + 4 * h);
         acc.x = fmaf(r.x, f.x, acc.x);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
   const uint8_t* peer[kMaxSplits];
 #pragma unroll
   for (int r = 0; r < kMaxSplits; ++r) peer[r] = cluster.map_shared_rank(smem, r < S ? r : 0);
-  for (int u = rank * C::kThreads + threadIdx.x; u < 2 * D; u += S * C::kThreads) {
+  for (int u = rank * kThreads + threadIdx.x; u < 2 * D; u += S * kThreads) {
     const int dim = u % D, h = u / D;
     if (4 * h >= GC) continue;
     float4 m[kMaxSplits], l[kMaxSplits], x[kMaxSplits];
@@ -484,10 +485,10 @@ __global__ void __launch_bounds__(LCfg<D, W>::kThreads, LCfg<D, W>::kCtas)
   cluster.sync();  // no CTA leaves while another reads its part
 }
 
-template <int D, int W>
+template <int D, int kCtas>
 cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
-  using C = LCfg<D, W>;
-  auto kern = list_decode_kernel<D, W>;
+  using C = LCfg<D, kCtas>;
+  auto kern = list_decode_kernel<D, kCtas>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
   bool ok = true;
@@ -499,7 +500,7 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.Hkv * a.groups * a.splits);
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -515,13 +516,8 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
 
 int list_decode_max_splits() { return kMaxSplits; }
 
-// Lists that fill the device once, with four warps a CTA and with eight.
-static int64_t list_wave(int32_t d, bool eight) {
-  return static_cast<int64_t>(eight || d == 256 ? 2 : 3) * num_sms();
-}
-
 int list_decode_splits(int64_t lists, int64_t tokens, int32_t d) {
-  const int64_t fit = list_wave(d, false);
+  const int64_t fit = (d == 256 ? 2 : 3) * static_cast<int64_t>(num_sms());
   // few long lists: clusters of kMaxSplits CTAs would leave SMs without work (8 lists of
   // 65,536 tokens, d = 128: 81 us with 8 splits, 51 with 32; 1 list: 80 and 26 with 64)
   if (lists * kMaxSplits < num_sms() && tokens >= 4096 * kMaxSplits)
@@ -538,16 +534,16 @@ cudaError_t launch_list_decode(const ListDecodeArgs& args, int32_t d, cudaStream
   // rows per TMA box: the largest of a stage's 64, 32 or 16 that divides the page, so that
   // no piece straddles two pages
   a.box = a.page % 64 == 0 ? 64 : a.page % 32 == 0 ? 32 : 16;
-  // Eight warps where four would leave a second wave nearly empty while eight nearly fill
-  // theirs: 512 lists of 4,096 tokens (d = 128) take 93 us with eight and 110 with four (104
-  // in two splits); 448 lists 91 and 76, 768 lists of 2,048 tokens 78 and 73.
-  const int64_t lists = static_cast<int64_t>(a.rows) * a.Hkv * a.groups;
-  const bool eight = d != 256 && a.splits == 1 && lists > list_wave(d, false) && lists <= 2 * list_wave(d, true);
+  // Three CTAs an SM or four, whichever fills its last wave better: 512 lists of 4,096 tokens
+  // (d = 128) take 110 us with three and 90 with four, 512 of 1,024 tokens 35 and 28; 768
+  // lists of 2,048 tokens 73 and 84, 448 of 4,096 76 and 76.
+  const int64_t ctas = static_cast<int64_t>(a.rows) * a.Hkv * a.groups * a.splits, w3 = 3ll * num_sms(), w4 = 4ll * num_sms();
+  const bool four = a.splits == 1 && ctas > w3 && (ctas + w4 - 1) / w4 * w4 < (ctas + w3 - 1) / w3 * w3;
   switch (d) {
-    case 32: return eight ? launch_list_d<32, 8>(a, s) : launch_list_d<32, 4>(a, s);
-    case 64: return eight ? launch_list_d<64, 8>(a, s) : launch_list_d<64, 4>(a, s);
-    case 128: return eight ? launch_list_d<128, 8>(a, s) : launch_list_d<128, 4>(a, s);
-    case 256: return launch_list_d<256, 4>(a, s);
+    case 32: return four ? launch_list_d<32, 4>(a, s) : launch_list_d<32, 3>(a, s);
+    case 64: return four ? launch_list_d<64, 4>(a, s) : launch_list_d<64, 3>(a, s);
+    case 128: return four ? launch_list_d<128, 4>(a, s) : launch_list_d<128, 3>(a, s);
+    case 256: return launch_list_d<256, 2>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
