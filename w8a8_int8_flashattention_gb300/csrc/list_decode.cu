@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
   uint64_t* empty = full + kStages;
   cg::cluster_group cluster = cg::this_cluster();
-  const int S = a.splits, rank = S > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  // four CTAs an SM only run unsplit lists
+  const int S = kCtas == 4 ? 1 : a.splits, rank = S > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // list v = row * Hkv + kv head; its G query heads are cut into groups of GC <= 8
   const int vg = static_cast<int>(blockIdx.x / static_cast<unsigned>(S));
