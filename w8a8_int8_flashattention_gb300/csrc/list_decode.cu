@@ -19,9 +19,9 @@
 //    MMAs on V codes biased by 128 (P' = p * s_v * 2^-E rounded to fp16, 2^-11 relative;
 //    sums and the output accumulate in fp32).
 // HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
-// 8 kv heads x 4,096 tokens (d = 128) take 94 us, 5.8 TB/s, 0.85 of the measured copy rate;
-// 448 lists of that length 0.92; 32 lists of 512 tokens 7.4 us, mostly launch, prologue and
-// merge.  (The split kernel and the combine over the same lists: 152 and 14.4 us.)
+// 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
+// 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
+// the combine over the same lists: 152 and 14.4 us.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,8 +44,8 @@ constexpr int kWarps = 4, kCThreads = 32 * kWarps;  // compute warps
 constexpr int kThreads = kCThreads + 32;            // and the loader
 constexpr int kTok = 16 * kWarps;                   // tokens per stage
 
-// kCtas CTAs share an SM: three (two at d = 256) with every register that the loop wants, or four
-// with 96 a thread, some of them spilled.
+// kCtas CTAs share an SM: three (two at d = 256), or four with 96 registers a thread and one
+// stage less, which only run unsplit lists and so carry no merge.
 template <int D, int kCtas>
 struct LCfg {
   static constexpr int kBW = D < 128 ? D : 128;  // bytes in one row of a TMA box
@@ -55,7 +55,7 @@ struct LCfg {
   static constexpr int kSK = 0, kSV = kTile, kSKs = 2 * kTile, kSVs = kSKs + kTok * 4;
   static constexpr int kStageBytes = (kSVs + kTok * 4 + 1023) / 1024 * 1024;
   static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kCtas == 4 ? 3 : 4) : (kCtas == 4 ? 6 : 8);
-  // after the loop the ring holds the warps' O^T [warp][D][8] and the CTA's [D][8], fp32
+  // after the loop the ring holds the warps' O^T [warp][D][8] and the CTA's [8][D], fp32
   static constexpr int kRed = 0, kPart = kWarps * D * 32;
   static_assert(kPart + D * 32 <= kStages * kStageBytes, "the merge fits the ring");
   static constexpr int kQc = kStages * kStageBytes;       // [8][D] query codes
@@ -425,10 +425,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         acc.z = fmaf(r.z, f.z, acc.z);
         acc.w = fmaf(r.w, f.w, acc.w);
       }
+      const float x[4] = {acc.x, acc.y, acc.z, acc.w};
       if (S > 1) {
-        *reinterpret_cast<float4*>(smem + C::kPart + (dim * 8 + 4 * h) * 4) = acc;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reinterpret_cast<float*>(smem + C::kPart)[(4 * h + c) * D + dim] = x[c];
       } else {
-        const float x[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float l = ml[8 + 4 * h + c];
@@ -445,43 +446,34 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   if (S == 1) return;
 
-  // ---- merge the S parts: each CTA takes every S-th run of units
+  // ---- merge the S parts: each CTA takes every S-th run of (column, channel) units
   cluster.sync();
-  const uint8_t* peer[kMaxSplits];
-#pragma unroll
-  for (int r = 0; r < kMaxSplits; ++r) peer[r] = cluster.map_shared_rank(smem, r < S ? r : 0);
-  for (int u = rank * kThreads + threadIdx.x; u < 2 * D; u += S * kThreads) {
-    const int dim = u % D, h = u / D;
-    if (4 * h >= GC) continue;
-    float4 m[kMaxSplits], l[kMaxSplits], x[kMaxSplits];
+  for (int u = rank * kThreads + threadIdx.x; u < GC * D; u += S * kThreads) {
+    const int c = u / D, dim = u % D;
+    float m[kMaxSplits], l[kMaxSplits], x[kMaxSplits];  // all on their way at once
 #pragma unroll
     for (int r = 0; r < kMaxSplits; ++r) {
       if (r < S) {
-        m[r] = *reinterpret_cast<const float4*>(peer[r] + C::kMl + 16 * h);
-        l[r] = *reinterpret_cast<const float4*>(peer[r] + C::kMl + 32 + 16 * h);
-        x[r] = *reinterpret_cast<const float4*>(peer[r] + C::kPart + (dim * 8 + 4 * h) * 4);
+        const float* peer = reinterpret_cast<const float*>(cluster.map_shared_rank(smem, r));
+        m[r] = peer[C::kMl / 4 + c];
+        l[r] = peer[C::kMl / 4 + 8 + c];
+        x[r] = peer[C::kPart / 4 + c * D + dim];
       }
     }
+    float M = -INFINITY, sum = 0.0f, acc = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (4 * h + c >= GC) continue;
-      auto at = [c](const float4& f) { return c == 0 ? f.x : c == 1 ? f.y : c == 2 ? f.z : f.w; };
-      float M = -INFINITY;
+    for (int r = 0; r < kMaxSplits; ++r)
+      if (r < S) M = fmaxf(M, m[r]);
 #pragma unroll
-      for (int r = 0; r < kMaxSplits; ++r)
-        if (r < S) M = fmaxf(M, at(m[r]));
-      float sum = 0.0f, acc = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kMaxSplits; ++r) {
-        if (r < S && at(m[r]) != -INFINITY) {
-          const float f = ex2(at(m[r]) - M);
-          sum = fmaf(f, at(l[r]), sum);
-          acc = fmaf(f, at(x[r]), acc);
-        }
+    for (int r = 0; r < kMaxSplits; ++r) {
+      if (r < S && m[r] != -INFINITY) {
+        const float f = ex2(m[r] - M);
+        sum = fmaf(f, l[r], sum);
+        acc = fmaf(f, x[r], acc);
       }
-      store_out(a.out, a.out_dtype, (row0 + 4 * h + c) * D + dim, sum > 0.0f ? acc / sum : 0.0f);
-      if (a.lse && dim == 0) a.lse[row0 + 4 * h + c] = sum > 0.0f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
+    store_out(a.out, a.out_dtype, (row0 + c) * D + dim, sum > 0.0f ? acc / sum : 0.0f);
+    if (a.lse && dim == 0) a.lse[row0 + c] = sum > 0.0f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }
   cluster.sync();  // no CTA leaves while another reads its part
 }
@@ -536,8 +528,8 @@ cudaError_t launch_list_decode(const ListDecodeArgs& args, int32_t d, cudaStream
   // no piece straddles two pages
   a.box = a.page % 64 == 0 ? 64 : a.page % 32 == 0 ? 32 : 16;
   // Three CTAs an SM or four, whichever fills its last wave better: 512 lists of 4,096 tokens
-  // (d = 128) take 110 us with three and 90 with four, 512 of 1,024 tokens 35 and 28; 768
-  // lists of 2,048 tokens 73 and 84, 448 of 4,096 76 and 76.
+  // (d = 128) take 110 us with three and 87.5 with four, 512 of 1,024 tokens 35 and 27; 768
+  // lists of 2,048 tokens 72 and 82, 448 of 4,096 76 and 74.
   const int64_t ctas = static_cast<int64_t>(a.rows) * a.Hkv * a.groups * a.splits, w3 = 3ll * num_sms(), w4 = 4ll * num_sms();
   const bool four = a.splits == 1 && ctas > w3 && (ctas + w4 - 1) / w4 * w4 < (ctas + w3 - 1) / w3 * w3;
   switch (d) {
