@@ -106,6 +106,7 @@ def test_sparse_decode(lib, p):
         assert f(*_changed(long, change)) == WORKSPACE, change
     size = lib.sl8_attn_int8_sparse_decode_workspace_size
     assert size(2, 8, 2, 8, 24, 128, 0) == 0 and size(0, 8, 2, 8, 16, 128, 0) == 0 and size(2, 7, 2, 8, 16, 128, 0) == 0
+    assert size(1, 8, 1, 1 << 22, 16, 128, 1 << 21) == 0  # more than 65,535 splits
     # more splits need more room
     assert size(1, 8, 1, 512, 64, 128, 64) > size(1, 8, 1, 512, 64, 128, 9) > 16
 

@@ -106,6 +106,26 @@ def test_paged_assign_in_place_and_steps():
         seqlens, table, free, count = want["seqlens"], want["block_table"], want["free_pages"], want["free_count"]
 
 
+def test_paged_assign_captured_with_many_tokens():
+    """The plan and the kernel that maps the tokens, captured and replayed on new lengths."""
+    rng = np.random.default_rng(5)
+    B, nb, page, T = 40, 100, 16, 20000
+    ctx, table, free, count, _ = _plan_case(rng, B, nb, page, False, 1500)
+    d = dict(ctx=i32(ctx), new=i32(np.zeros(B)), table=i32(table), free=i32(free), count=i32([count]))
+    call = lambda out: sl8.paged_assign(d["ctx"], d["new"], d["table"], d["free"], d["count"], page, T, out=out)  # noqa: E731
+    out = call(None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out)
+    for _ in range(3):
+        new = rng.integers(0, 900, B)
+        d["new"].copy_(i32(new))
+        d["table"].copy_(i32(table))
+        g.replay()
+        _check_plan(out, S.paged_assign(ctx, new, None, table, free, count, page, T), d["table"], d["free"], "replay")
+
+
 def test_paged_assign_no_requests_and_bad_lengths():
     z = torch.zeros(0, dtype=torch.int32, device=DEV)
     out = sl8.paged_assign(z, z, z.view(0, 4), i32([1, 2]), i32([2]), 16, 3)
@@ -453,6 +473,66 @@ def test_sparse_decode(R, hq, hkv, d, page, max_sel, splits, dtype, odt):
     again = sl8.attn_int8_sparse_decode(q.to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens), num_splits=splits,
                                         out_dtype=odt)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("splits", [0, 3, 9])
+def test_what_lies_past_a_list_does_not_matter(d, splits):
+    """NaN and infinite scales and codes of -128 in the rows of the last page past the list, and
+    page ids past it that are none."""
+    rng = np.random.default_rng(d + splits)
+    R, hq, hkv, page, max_sel = 3, 4, 2, 32, 24
+    num_pages = R * hkv * max_sel
+    _, _, dc, ds = _pool(rng, num_pages, hkv, page, d)
+    pages = rng.permutation(num_pages).reshape(R, hkv, max_sel)  # no page in two lists
+    lens = np.array([[1, 33], [page * max_sel - 1, 17], [page * 9 + 16, page * 20 + 5]])
+    q = torch.randn((R, hq, d), generator=torch.Generator().manual_seed(d)).half().to(DEV)
+    call = lambda p: sl8.attn_int8_sparse_decode(q, dc[0], ds[0], dc[1], ds[1], i32(p), i32(lens), num_splits=splits,  # noqa: E731
+                                                 return_lse=True)
+    want, wl = call(pages)
+    for r in range(R):
+        for h in range(hkv):
+            last, used = pages[r, h, (lens[r, h] - 1) // page], (lens[r, h] - 1) % page + 1
+            for i in range(2):
+                dc[i][last, h, used:] = -128
+                ds[i][last, h, used:] = float("nan")
+                ds[i][last, h, used + 1::2] = float("inf")
+            pages[r, h, (lens[r, h] - 1) // page + 1:] = 1 << 30
+    got, gl = call(pages)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 4 GB for each of K and V: the last pages through every operator."""
+    hq, hkv, d, page, num_pages = 8, 4, 256, 64, 70000
+    k, v = (torch.empty((num_pages, hkv, page, d), dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.empty((num_pages, hkv, page), device=DEV) for _ in range(2))
+    b, bs = torch.empty((num_pages, hkv, 2, d), dtype=torch.int8, device=DEV), torch.empty((num_pages, hkv), device=DEV)
+    assert k.numel() > 1 << 32
+    ids, n = np.array([num_pages - 1, 3, num_pages - 2, num_pages - 7]), 3 * page + 21
+    slots = (ids[:, None] * page + np.arange(page)).reshape(-1)[:n]
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((n, hkv, 2 * d), generator=g).bfloat16()
+    xd = x.to(DEV)
+    sl8.rope_append(None, xd[..., :d].contiguous(), xd[..., d:].contiguous(), None, None, i32(slots), k, ks, v, vs)
+    sl8.page_bounds(k, ks, i32(ids[None]), i32([n]), b, bs)
+    q = torch.randn((1, hq, d), generator=g).bfloat16()
+    sel = sl8.page_select(q.to(DEV), b, bs, i32(ids[None]), i32([n]), page, 3, 1, 1)
+    out = sl8.attn_int8_sparse_decode(q.to(DEV), k, ks, v, vs, sel["pages"], sel["lens"], out_dtype=torch.float32)
+    kc, kscale = S._quant(x[..., :d].float().numpy())
+    vc, vscale = S._quant(x[..., d:].float().numpy())
+    pad = lambda a: np.concatenate([a, np.zeros((4 * page - n, *a.shape[1:]), a.dtype)]).reshape(4, page, *a.shape[1:]).swapaxes(1, 2)  # noqa: E731,E501
+    kc, kscale, vc, vscale = (pad(a) for a in (kc, kscale, vc, vscale))
+    for h in range(hkv):
+        box = [S.page_bounds(kc[j, h, :n - j * page], kscale[j, h, :n - j * page]) for j in range(4)]
+        score = S.page_scores(q[0, 2 * h:2 * h + 2].float().numpy(), np.stack([x[0] for x in box]), np.stack([x[1] for x in box]),
+                              np.array([x[2] for x in box]))
+        kept = S.select(score, 3, 1, 1)
+        assert sel["blocks"][0, 0, h].tolist() == kept and sel["pages"][0, 0, h].tolist() == ids[kept].tolist()
+    blocks, lens = sel["blocks"].cpu().numpy()[0], sel["lens"].cpu().numpy()[0]
+    want, _ = S.sparse_attention(q.float().numpy(), kc, kscale, vc, vscale, blocks, lens)
+    vmax = np.abs(vc.astype(np.float64) * vscale[..., None]).max()
+    assert np.all(np.abs(np64(out) - want) <= (2.0 ** -11 + 2.0 ** -24 * n) * vmax)
 
 
 def test_sparse_decode_of_every_page_is_the_paged_decode():

@@ -1033,8 +1033,9 @@ static int32_t list_splits(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_se
     const int64_t lists = static_cast<int64_t>(rows) * Hkv * decode_kv_groups(Hq, Hkv);
     n = list_decode_splits(lists, static_cast<int64_t>(max_sel) * page_size, d);
   }
-  return n <= most ? static_cast<int32_t>(n)
-                   : sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, static_cast<int32_t>(n));
+  if (n <= most) return static_cast<int32_t>(n);
+  const int32_t S = sl8_attn_decode_num_splits(rows * Hkv, 1, max_sel * page_size, d, static_cast<int32_t>(n));
+  return S <= 65535 ? S : 0;
 }
 
 static size_t list_lse_offset(int32_t rows, int32_t Hq, int32_t d, int32_t S) {
