@@ -12,12 +12,12 @@
 //  * The last warp loads: per stage, one lane per piece of 64, 32 or 16 rows (the largest
 //    that divides the page) issues the piece's K and V tiles (TMA, 128-byte swizzle for
 //    d >= 128) and its two scale rows; page ids are read 32 pieces ahead.
-//  * Warps 0..3 take 16 tokens of every stage each, with an online-softmax state of
-//    their own.  S^T[16 tokens x 8 q] = K Q^T runs as int8 m16n8k32 MMAs, whose A operand is the
-//    K rows as they lie in memory (this part's int8 rate is low, but 8 MMAs per 16 tokens
-//    take 29 of the 180 cycles that their bytes need); O^T[d x 8 q] += V^T P'^T as fp16
-//    MMAs on V codes biased by 128 (P' = p * s_v * 2^-E rounded to fp16, 2^-11 relative;
-//    sums and the output accumulate in fp32).
+//  * Warps 0..3 take 16 tokens of every stage each, with an online-softmax state of their
+//    own.  S^T[16 tokens x 8 q] = K Q^T runs as int8 m16n8k32 MMAs, whose A operand is the K
+//    rows as they lie in memory (this part's int8 rate is low, 4 cycles an MMA and SM, but 4
+//    MMAs per 16 tokens at d = 128 take 16 of the 180 cycles that their bytes need);
+//    O^T[d x 8 q] += V^T P'^T as fp16 MMAs on V codes biased by 128 (P' = p * s_v * 2^-E
+//    rounded to fp16, 2^-11 relative; sums and the output accumulate in fp32).
 // HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
 // 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
 // 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
