@@ -135,6 +135,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
     if (c < G) load_runs<kRuns>(a.q, a.q_dtype, (static_cast<int64_t>(bt) * a.Hq + h * G + c) * D + 4 * ql, 32, x);
   };
   load_q(qr);
+  // so are the ids of the warp's first 16 pages, where they do not depend on the length
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
+  const int g = lane >> 2, tq = lane & 3;
+  int32_t pa = 0, pb = 0;  // checked where they are used, so that nothing waits for them here
+  int p = 16 * warp;
+  if (ranks == 1) {
+    if (p + g < a.max_blocks) pa = table[p + g];
+    if (p + g + 8 < a.max_blocks) pb = table[p + g + 8];
+  }
   const int32_t cap = a.max_blocks * a.page;  // below 2^31
   int32_t L = a.seqlens[b];
   if (L < 0 || L > cap) {
@@ -143,7 +152,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
   }
   L = max(0, L - (a.T - 1 - static_cast<int32_t>(t)));
   const int n = static_cast<int>((static_cast<uint32_t>(L) + a.page - 1) / static_cast<uint32_t>(a.page));
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
   int32_t* out_blocks = a.blocks + static_cast<int64_t>(row) * a.max_sel;
   int32_t* out_pages = a.pages + static_cast<int64_t>(row) * a.max_sel;
   if (n <= a.max_sel) {  // every page is kept; the same for every CTA of the cluster
@@ -155,17 +163,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
     return;
   }
 
-  // the pages of this CTA, and the ids of the warp's first 16 (checked where they are used, so
-  // that nothing waits for them here)
+  // the pages of this CTA; lanes past the last one score page 0 and store nothing
   const int per = ranks == 1 ? n : static_cast<int>((n + ranks - 1) / ranks);
   const int p0 = min(n, static_cast<int>(rank) * per), p1 = min(n, p0 + per), m = p1 - p0;
-  const int g = lane >> 2, tq = lane & 3;
-  int32_t pa = 0, pb = 0;
-  int p = p0 + 16 * warp;
-  if (p < p1) {
+  p += p0;
+  if (ranks > 1 && p < p1) {
     pa = table[min(p + g, p1 - 1)];
     pb = table[min(p + g + 8, p1 - 1)];
   }
+  if (p + g >= p1) pa = 0;
+  if (p + g + 8 >= p1) pb = 0;
 
   // ---- the query heads' codes as rows [min(c, 0) | max(c, 0)] of 2 d, and their scales
   uint2* keys = reinterpret_cast<uint2*>(smem);  // key and page id of each of this CTA's pages
