@@ -497,12 +497,12 @@ SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, i
  *   sel_pages    device, the same of their pages (block_table entries), -1 after;
  *   sel_lens     device, [B][T][Hkv] int32: the tokens that the list holds for the query:
  *                its pages are full but the query's own last one.
- *   scores       device, nullable, [B][T][Hkv][max_blocks] fp32: receives the scores of the
- *                blocks of every range of more than max_sel (all else is left).
- * The same selection on every run.  Hq / Hkv <= 64, B * T * Hkv <= 2^27 and some 190,000
- * blocks a sequence at most (SL8_ERR_UNSUPPORTED).  A length out of range, or a page out of
- * range that is scored, is recorded (SL8_ERR_DEVICE_ARG) and clamped, or scored as page 0
- * (and listed as that).
+ *   scores       device, [B][T][Hkv][max_blocks] fp32: receives the scores of the blocks of
+ *                every range of more than max_sel (all else is left).  Nullable when
+ *                max_blocks <= 4096; launches that run at the same time need their own.
+ * The same selection on every run.  Hq / Hkv <= 64 and B * T * Hkv <= 2^27
+ * (SL8_ERR_UNSUPPORTED).  A length out of range, or a page out of range that is scored, is
+ * recorded (SL8_ERR_DEVICE_ARG) and clamped, or scored as page 0 (and listed as that).
  */
 SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const float* bound_scale,
                             int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,

@@ -82,7 +82,8 @@ def test_page_select(lib, p):
     for change in ({1: sl8.SL8_I8}, {4: 0}, {5: 0}, {7: 0}, {9: -1}, {10: -1}, {11: 7}, {12: 0}, {14: 0}, {15: -1},
                    {15: 7}, {16: 9}, {0: p + 8}, {2: p + 8}):
         assert f(*_changed(ok, change)) == INVALID, change
-    for change in ({13: 96}, {11: 130}, {5: 1 << 16, 7: 1 << 15}, {5: 16, 7: 1 << 20}, {9: 1 << 20, 10: 1 << 10}):
+    assert f(*_changed(ok, {7: 4097})) == INVALID               # a wide table needs the scores
+    for change in ({13: 96}, {11: 130}, {5: 1 << 16, 7: 1 << 15}, {9: 1 << 20, 10: 1 << 10}):
         assert f(*_changed(ok, change)) == UNSUPPORTED, change
 
 

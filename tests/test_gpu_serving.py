@@ -408,6 +408,29 @@ def test_page_select_long_table():
     assert out["lens"].item() == 512 * page - 3
 
 
+@pytest.mark.parametrize("B,lens,max_sel,first,last", [(40, 9000, 5000, 2, 3), (200, 5000, 64, 1, 2), (3, 40000, 30000, 0, 0)])
+def test_page_select_wide_tables(B, lens, max_sel, first, last):
+    """Tables wider than a CTA holds keys of: long rows, short rows and rows that are kept whole."""
+    nb, page, hkv, d = 40000, 16, 2, 32
+    rng = np.random.default_rng(B)
+    b, s, db, ds = _bounds_pool(rng, 500, hkv, d, coarse=B == 200)
+    table = rng.integers(0, 500, (B, nb)).astype(np.int32)
+    n = rng.integers(1, lens + 1, B)
+    n[0] = lens
+    q = torch.randn((B, 2 * hkv, d), generator=torch.Generator().manual_seed(B))
+    out = sl8.page_select(q.to(DEV), db, ds, i32(table), i32(n * page - 5), page, max_sel, first, last)
+    blocks, pages, got = (out[x].cpu().numpy()[:, 0] for x in ("blocks", "pages", "lens"))
+    for i in list(range(min(B, 6))) + [B - 1]:
+        ids = table[i, :n[i]]
+        for h in range(hkv):
+            score = S.page_scores(q[i, 2 * h:2 * h + 2].numpy(), b[ids, h, 0].astype(np.int64), b[ids, h, 1].astype(np.int64),
+                                  s[ids, h])
+            kept = S.select(score, max_sel, first, last)
+            np.testing.assert_array_equal(blocks[i, h], kept + [-1] * (max_sel - len(kept)))
+            np.testing.assert_array_equal(pages[i, h, :len(kept)], ids[kept])
+            assert got[i, h] == len(kept) * page - (5 if n[i] - 1 in set(kept) else 0)
+
+
 def test_page_select_reports_bad_lengths_and_pages():
     b, s = torch.ones((2, 1, 2, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1), device=DEV)
     q = torch.ones((1, 1, 64), device=DEV)

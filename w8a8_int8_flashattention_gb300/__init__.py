@@ -732,7 +732,8 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     them.  Returns a dict of int32 tensors: blocks and pages [B,T,Hkv,max_sel] (ascending
     blocks; -1 past the list) and lens [B,T,Hkv], the tokens listed (out: a dict returned
     earlier, written again).  scores fp32 [B,T,Hkv,max_blocks] receives the scores of
-    the pages of every range longer than max_sel."""
+    the pages of every range longer than max_sel (allocated here where none is given and the
+    table is wider than the 4,096 blocks whose scores stay on chip)."""
     dev = _index(q)
     if q.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {q.dtype}")
@@ -759,6 +760,9 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     o = _ptrs(dev, _I32T, "blocks pages lens", out["blocks"], out["pages"], out["lens"])
     if scores is not None:
         _shaped(scores, (B, T, hkv, max_blocks), "scores")
+    elif max_blocks > 4096:  # more than one CTA holds
+        scores = torch.empty((B, T, hkv, max_blocks), dtype=_F32T, device=q.device)
+        scp = scores.data_ptr()
     _call("sl8_page_select", dev, qp, _DTYPES[q.dtype], bp, sp, num_pages, int(page_size), table, max_blocks, lens, B, T,
           hq, hkv, d, max_sel, int(first), int(last), o[0], o[1], o[2], scp)
     return out

@@ -14,8 +14,11 @@
 //
 // GB300 design: one kernel.  A CTA (a cluster of CTAs where there are few rows) serves one
 // (query row, kv head): it reads the bounds of the row's pages once (2 d + 4 bytes each),
-// keeps the scores' keys in shared memory, finds the threshold and writes the list.  Long
-// contexts and large batches are bound by the bounds' bytes, small calls by the latency of
+// keeps the scores' keys in shared memory, finds the threshold and writes the list.  What
+// passes kHeld pages a CTA is read back from `scores`: keys held for every block of a wide
+// table would cost resident CTAs (64 x 8 rows of 256 to 1,024 pages: 22.6 us with a table of
+// 4,096 blocks, 23.6 with 65,536, and 27 / 61 / 100 with 8,192 / 32,768 / 65,536 if all are
+// held).  Long contexts and large batches are bound by the bounds' bytes, small calls by the latency of
 // the chain length -> page id -> bounds -> threshold -> list, so every row of a batch runs
 // at once.  Measured against two kernels (scores, then lists) for 64 sequences of 8k to 32k
 // tokens in 32-token pages, 8 kv heads, d = 128: 26.6 us against 33, and 9.9 against 12 for
@@ -23,6 +26,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "decode_unit.cuh"
 #include "sl8_internal.h"
@@ -38,6 +43,7 @@ constexpr int kMaxCluster = 8;
 constexpr uint32_t kForced = 0xffffffffu;  // key of a page that is always kept
 constexpr int kBins = 4 * kThreads;        // bins of one narrowing step, four per thread
 constexpr int kCand = kThreads;            // keys that are ranked against each other
+constexpr int kHeld = kPageSelectHeld;     // keys that a CTA holds in shared memory
 static_assert(kMaxCluster <= kWarps, "a warp collects each CTA's candidates");
 
 struct SelectArgs {
@@ -52,8 +58,8 @@ struct SelectArgs {
   int32_t B, T, Hq, Hkv;
   int32_t max_sel, first, last;
   int32_t *blocks, *pages, *lens;
-  float* scores;          // nullable
-  int32_t cap;            // pages of a row that one CTA of the cluster can hold
+  float* scores;          // nullable while no table is wider than kHeld
+  int32_t cap;            // pages whose keys a CTA holds in shared memory
   uint32_t ranks;         // CTAs of the cluster
 };
 
@@ -68,7 +74,7 @@ struct __align__(16) SelectSmem {
   uint32_t own_cand;
   uint32_t bin, above, count;    // the threshold's bin: its number, the keys above it, its keys
   uint32_t key, want;            // the threshold key, and how many of the keys equal to it to keep
-  uint32_t warp_sum[kWarps];
+  uint2 warp_sum[kWarps];
 };
 
 // Order-preserving map of a float to an unsigned above 0 and below kForced; + 0 turns a -0
@@ -115,7 +121,9 @@ __device__ __forceinline__ uint32_t positives(uint32_t c) { return c & ~__vcmplt
 
 // Index arithmetic is 32-bit throughout: divisions of 64 bits by numbers known only at run
 // time cost more than the rest of the prologue.
-template <int D>
+// kWide: a CTA's pages can pass kHeld; built apart, since the reading back costs 0.6 us of 26.4
+// where it is not needed.
+template <int D, bool kWide>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel(const SelectArgs a, DeviceStatus* st) {
   using R = RowCfg<D>;
   constexpr int kSeg = R::kSeg, kWords = R::kWords, kRuns = D / 32;
@@ -175,7 +183,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
   if (p + g + 8 >= p1) pb = 0;
 
   // ---- the query heads' codes as rows [min(c, 0) | max(c, 0)] of 2 d, and their scales
-  uint2* keys = reinterpret_cast<uint2*>(smem);  // key and page id of each of this CTA's pages
+  uint2* keys = reinterpret_cast<uint2*>(smem);  // key and page id of this CTA's first pages
+  auto score_at = [&](int pp) { return a.scores + static_cast<int64_t>(row) * a.max_blocks + pp; };
+  auto forced = [&](int pp) { return pp < a.first || pp >= n - a.last; };
+  auto key_at = [&](int i) {  // of this CTA's page i
+    return !kWide || i < a.cap ? keys[i].x : forced(p0 + i) ? kForced : key_of(__ldcg(score_at(p0 + i)));
+  };
   int8_t* qrows = reinterpret_cast<int8_t*>(smem + (static_cast<size_t>(a.cap) * 8 + 15) / 16 * 16);
   float* qscale = reinterpret_cast<float*>(qrows + tiles * 8 * R::kStride);
   for (int c = qr; c < tiles * 8; c += 4 * kWarps) {
@@ -263,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
       const int pp = p + g + 8 * tq;
       const float score = tq ? best_b : best_a;
       if (pp < p1) {
-        const bool forced = pp < a.first || pp >= n - a.last;
-        const uint32_t k = forced ? kForced : key_of(score);
-        keys[pp - p0] = make_uint2(k, static_cast<uint32_t>(tq ? pb : pa));
-        if (!forced) atomicAdd(&sm.hist[first_bin(k)], 1u);
-        if (a.scores) a.scores[static_cast<int64_t>(row) * a.max_blocks + pp] = score;
+        const bool always = forced(pp);
+        const uint32_t k = always ? kForced : key_of(score);
+        if (!kWide || pp - p0 < a.cap) keys[pp - p0] = make_uint2(k, static_cast<uint32_t>(tq ? pb : pa));
+        if (!always) atomicAdd(&sm.hist[first_bin(k)], 1u);
+        if (a.scores) *score_at(pp) = score;
       }
     }
     pa = na;
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
     const int shift = start ? kFirstShift : max(0, (32 - __clz(hi - lo)) - (31 - __clz(kBins)));
     if (!start) {
       for (int i = tid; i < m; i += kThreads) {
-        const uint32_t k = keys[i].x;
+        const uint32_t k = key_at(i);
         if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> shift], 1u);
       }
     }
@@ -316,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
       const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) sm.warp_sum[warp] = incl;
+    if (lane == 31) sm.warp_sum[warp].x = incl;
     __syncthreads();
-    uint32_t above = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_sum[lane] : 0u);
+    uint32_t above = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_sum[lane].x : 0u);
     const uint32_t cnt[4] = {c4.w, c4.z, c4.y, c4.x};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
     }
     if (count <= kCand) {
       for (int i = tid; i < m; i += kThreads) {
-        const uint32_t k = keys[i].x;
+        const uint32_t k = key_at(i);
         if (k >= lo && k <= hi) sm.cand[rank][atomicAdd(&sm.own_cand, 1u)] = k;
       }
       __syncthreads();
@@ -393,32 +406,36 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
   }
 
   // ---- the list, ascending: keys above thr, and the first `want` that equal it.  Each thread
-  // takes a run of pages; exclusive prefixes of both counts place its entries (a CTA holds
-  // fewer than 2^16 pages, so both fit one word).
+  // takes a run of pages; exclusive prefixes of both counts place its entries.
   const int run = (m + kThreads - 1) / kThreads;
   const int i0 = min(m, static_cast<int>(tid) * run), i1 = min(m, i0 + run);
-  uint32_t mine = 0;
+  uint32_t gt = 0, eq = 0;
   __syncthreads();  // the keys; the narrowing is done with warp_sum
   for (int i = i0; i < i1; ++i) {
-    const uint32_t k = keys[i].x;
-    mine += (k > thr ? 1u << 16 : 0u) + (k == thr ? 1u : 0u);
+    const uint32_t k = key_at(i);
+    gt += k > thr;
+    eq += k == thr;
   }
-  uint32_t incl = mine;
+  uint32_t gt0 = gt, eq0 = eq;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, gt0, o), y = __shfl_up_sync(0xffffffffu, eq0, o);
+    if (lane >= o) {
+      gt0 += x;
+      eq0 += y;
+    }
   }
-  if (lane == 31) sm.warp_sum[warp] = incl;
+  if (lane == 31) sm.warp_sum[warp] = make_uint2(gt0, eq0);
   __syncthreads();
-  const uint32_t before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_sum[lane] : 0u);
-  uint32_t gt0 = before >> 16, eq0 = before & 0xffffu;
+  const uint2 before = lane < warp ? sm.warp_sum[lane] : make_uint2(0u, 0u);
+  gt0 += __reduce_add_sync(0xffffffffu, before.x) - gt;
+  eq0 += __reduce_add_sync(0xffffffffu, before.y) - eq;
   if (ranks > 1) {  // those of the CTAs before this one count too
     if (tid == kThreads - 1) {
       for (uint32_t r = rank + 1; r < ranks; ++r) {
         uint32_t* sum = cluster.map_shared_rank(sm.sum[rank], r);
-        sum[0] = (before + mine) >> 16;
-        sum[1] = (before + mine) & 0xffffu;
+        sum[0] = gt0 + gt;
+        sum[1] = eq0 + eq;
       }
     }
     cluster.sync();  // the last one: no CTA reads or writes another's memory after it
@@ -427,13 +444,20 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
   }
   uint32_t at = gt0 + min(eq0, want);
   for (int i = i0; i < i1; ++i) {
-    const uint2 kp = keys[i];
-    bool take = kp.x > thr;
-    if (kp.x == thr) take = eq0++ < want;
+    const uint32_t k = key_at(i);
+    bool take = k > thr;
+    if (k == thr) take = eq0++ < want;
     const int blk = p0 + i;
     if (take) {
+      int32_t pg;
+      if (!kWide || i < a.cap) {
+        pg = static_cast<int32_t>(keys[i].y);
+      } else {
+        pg = table[blk];
+        if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(a.num_pages)) pg = 0;
+      }
       out_blocks[at] = blk;
-      out_pages[at] = static_cast<int32_t>(kp.y);
+      out_pages[at] = pg;
       ++at;
     }
     // the row's last page decides how many tokens the list holds
@@ -445,9 +469,9 @@ size_t select_smem(int32_t cap, int32_t d, int32_t tiles) {
   return (static_cast<size_t>(cap) * 8 + 15) / 16 * 16 + static_cast<size_t>(tiles) * 8 * (2 * d + 16 + 4);
 }
 
-template <int D>
-cudaError_t launch_select_d(const SelectArgs& a, unsigned rows, size_t smem, cudaStream_t s) {
-  auto kern = page_select_kernel<D>;
+template <int D, bool kWide>
+cudaError_t launch_select_w(const SelectArgs& a, unsigned rows, size_t smem, cudaStream_t s) {
+  auto kern = page_select_kernel<D, kWide>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -464,22 +488,20 @@ cudaError_t launch_select_d(const SelectArgs& a, unsigned rows, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
 }
 
-constexpr size_t kSelectSmemMax = 200 * 1024;
+template <int D>
+cudaError_t launch_select_d(const SelectArgs& a, unsigned rows, size_t smem, cudaStream_t s) {
+  const bool wide = (a.max_blocks + static_cast<int64_t>(a.ranks) - 1) / a.ranks > a.cap;
+  return wide ? launch_select_w<D, true>(a, rows, smem, s) : launch_select_w<D, false>(a, rows, smem, s);
+}
 
-// CTAs of a row's cluster: as many as there are SMs for, at least 128 pages each, and enough
-// that each CTA's keys fit its shared memory; 0 if eight cannot hold them.
-int select_ranks(int64_t rows, int32_t max_blocks, int32_t d, int32_t tiles) {
+// CTAs of a row's cluster: as many as there are SMs for, at least 128 pages each.
+int select_ranks(int64_t rows, int32_t max_blocks) {
   int ranks = 1;
   while (ranks < kMaxCluster && rows * ranks * 2 <= num_sms() && max_blocks / (2 * ranks) >= 128) ranks *= 2;
-  while (ranks <= kMaxCluster && select_smem((max_blocks + ranks - 1) / ranks, d, tiles) > kSelectSmemMax) ranks *= 2;
-  return ranks <= kMaxCluster ? ranks : 0;
+  return ranks;
 }
 
 }  // namespace
-
-bool page_select_fits(int64_t rows, int32_t max_blocks, int32_t d, int32_t group) {
-  return select_ranks(rows, max_blocks, d, (group + 7) / 8) != 0;
-}
 
 cudaError_t launch_page_select(const void* q, sl8_dtype q_dtype, const int8_t* bounds, const float* bound_scale,
                                int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,
@@ -489,11 +511,10 @@ cudaError_t launch_page_select(const void* q, sl8_dtype q_dtype, const int8_t* b
   TraceScope tr("page_select", s);
   const int64_t rows = static_cast<int64_t>(B) * T * Hkv;
   const int32_t tiles = (Hq / Hkv + 7) / 8;
-  const int ranks = select_ranks(rows, max_blocks, d, tiles);
-  if (ranks == 0) return cudaErrorInvalidValue;
+  const int ranks = select_ranks(rows, max_blocks);
   SelectArgs a{q, q_dtype, bounds, bound_scale, num_pages, page_size, block_table, max_blocks, seqlens, B, T, Hq, Hkv,
                max_sel, first, last, sel_blocks, sel_pages, sel_lens, scores, 0, 0};
-  a.cap = (max_blocks + ranks - 1) / ranks;
+  a.cap = std::min((max_blocks + ranks - 1) / ranks, kHeld);
   a.ranks = static_cast<uint32_t>(ranks);
   const size_t smem = select_smem(a.cap, d, tiles);
   switch (d) {

@@ -180,8 +180,8 @@ cudaError_t launch_page_bounds(const int8_t* k_pages, const float* k_scale_pages
                                const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
                                const int32_t* new_lens, int32_t max_new, int32_t B, int32_t Hkv, int32_t d,
                                int8_t* bounds, float* bound_scale, cudaStream_t s);
-// Whether the keys of a row's pages fit the shared memory of the largest cluster.
-bool page_select_fits(int64_t rows, int32_t max_blocks, int32_t d, int32_t group);
+// Blocks up to which a selection needs no `scores` (the keys that one CTA holds).
+constexpr int32_t kPageSelectHeld = 4096;
 cudaError_t launch_page_select(const void* q, sl8_dtype q_dtype, const int8_t* bounds, const float* bound_scale,
                                int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t max_blocks,
                                const int32_t* seqlens, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
