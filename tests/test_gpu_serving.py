@@ -431,6 +431,26 @@ def test_page_select_wide_tables(B, lens, max_sel, first, last):
             assert got[i, h] == len(kept) * page - (5 if n[i] - 1 in set(kept) else 0)
 
 
+@pytest.mark.parametrize("first,last", [(4, 4), (8, 0), (0, 8), (1, 0)])
+def test_page_select_only_forced_pages_over_a_cluster(first, last):
+    """Nothing is left to choose by score, in rows that several CTAs share."""
+    nb, page, hkv, d, keep = 2050, 16, 2, 64, first + last
+    rng = np.random.default_rng(keep)
+    _, _, db, ds = _bounds_pool(rng, 300, hkv, d)
+    table = rng.integers(0, 300, (2, nb)).astype(np.int32)
+    lens = [nb * page - 1, 700 * page]
+    q = torch.randn((2, 2 * hkv, d), generator=torch.Generator().manual_seed(1)).to(DEV)
+    for _ in range(5):
+        out = sl8.page_select(q, db, ds, i32(table), i32(lens), page, keep, first, last)
+        for i, L in enumerate(lens):
+            n = -(-L // page)
+            kept = [*range(first), *range(n - last, n)]
+            for h in range(hkv):
+                assert out["blocks"][i, 0, h].tolist() == kept
+                assert out["pages"][i, 0, h].tolist() == table[i, kept].tolist()
+                assert out["lens"][i, 0, h].item() == keep * page - (n * page - L if last else 0)
+
+
 def test_page_select_reports_bad_lengths_and_pages():
     b, s = torch.ones((2, 1, 2, 64), dtype=torch.int8, device=DEV), torch.ones((2, 1), device=DEV)
     q = torch.ones((1, 1, 64), device=DEV)

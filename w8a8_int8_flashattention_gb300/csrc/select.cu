@@ -292,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) page_select_kernel
   // one that holds it becomes the next range, until the bin is kept whole, has few enough
   // keys to rank against each other (the usual end of the first step), or is a single key.
   uint32_t lo = 0, hi = kForced - 1, want = static_cast<uint32_t>(a.max_sel - a.first - a.last), thr = kForced - 1;
+  // no narrowing, so no barrier yet: every CTA has to be there before its memory is written below
+  if (want == 0 && ranks > 1) cluster.sync();
   for (bool start = true; want > 0; start = false) {
     const int shift = start ? kFirstShift : max(0, (32 - __clz(hi - lo)) - (31 - __clz(kBins)));
     if (!start) {
