@@ -486,7 +486,8 @@ SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, i
  * tokens up to itself (T = 1: the decode's query; more: drafts or a prompt chunk).
  *   q            device, [B][T][Hq][d] (F16, BF16 or F32), quantised per row to codes c and
  *                scale s_q as the decode does.
- *   bounds, bound_scale  as sl8_page_bounds leaves them for every page of the sequences.
+ *   bounds, bound_scale  as sl8_page_bounds leaves them for every page of the sequences; bounds
+ *                32-byte aligned.
  *   score        of a page: the maximum over the kv head's query heads of
  *                (float(sum_i max(c_i lo_i, c_i hi_i)) * S) * s_q, fp32 products in this
  *                order: an upper bound of every q . k of the page (before 1 / sqrt(d)).

@@ -83,6 +83,7 @@ def test_page_select(lib, p):
                    {15: 7}, {16: 9}, {0: p + 8}, {2: p + 8}):
         assert f(*_changed(ok, change)) == INVALID, change
     assert f(*_changed(ok, {7: 4097})) == INVALID               # a wide table needs the scores
+    assert f(*_changed(ok, {2: p | 16})) == INVALID              # bounds are read 32 bytes at a time
     for change in ({13: 96}, {11: 130}, {5: 1 << 16, 7: 1 << 15}, {9: 1 << 20, 10: 1 << 10}):
         assert f(*_changed(ok, change)) == UNSUPPORTED, change
 

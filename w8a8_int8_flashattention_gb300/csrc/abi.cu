@@ -1011,7 +1011,8 @@ int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const floa
   SL8_CHECK(static_cast<int64_t>(B) * T <= (int64_t(1) << 27) / Hkv, SL8_ERR_UNSUPPORTED);
   SL8_CHECK(q && bounds && bound_scale && block_table && seqlens && sel_blocks && sel_pages && sel_lens,
             SL8_ERR_INVALID_ARG);
-  SL8_CHECK(aligned16(q) && aligned16(bounds), SL8_ERR_INVALID_ARG);
+  // bounds are read 32 bytes at a time
+  SL8_CHECK(aligned16(q) && (reinterpret_cast<uintptr_t>(bounds) & 31u) == 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(scores || max_blocks <= kPageSelectHeld, SL8_ERR_INVALID_ARG);
   SL8_LAUNCH(launch_page_select(q, static_cast<sl8_dtype>(q_dtype), bounds, bound_scale, num_pages, page_size,
                                 block_table, max_blocks, seqlens, B, T, Hq, Hkv, d, max_sel, first, last, sel_blocks,
