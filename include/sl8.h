@@ -425,7 +425,7 @@ SL8_API int sl8_attn_decode_combine(const float* o_partial, const float* lse_par
  * A negative length, ctx_lens above max_blocks * page_size or a free_count outside [0,
  * free_capacity] is recorded (SL8_ERR_DEVICE_ARG) and its request refused, its pages not
  * released, the count clamped; pushes past free_capacity are recorded and dropped.
- * page_size * max_blocks must stay below 2^31.
+ * page_size * max_blocks <= 2^31 - 256 (SL8_ERR_UNSUPPORTED).
  */
 SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
                              int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,
@@ -472,8 +472,8 @@ SL8_API int sl8_rope_append(const void* q, const void* k, const void* v, int dty
  * Written for the pages that the last new_lens[b] (<= max_new, a host bound) tokens of each
  * sequence lie in, over all tokens of those pages; new_lens NULL: for every page of the
  * sequences.  seqlens [B] counts the new tokens.  Sequences must not share pages that take
- * new tokens.  Scales are >= 0.  A length or page out of range is recorded
- * (SL8_ERR_DEVICE_ARG) and clamped or skipped.
+ * new tokens.  Scales are >= 0.  page_size * max_blocks <= 2^31 - 256.  A length or page out
+ * of range is recorded (SL8_ERR_DEVICE_ARG) and clamped or skipped.
  */
 SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,
                             const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
@@ -501,8 +501,8 @@ SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, i
  *   scores       device, [B][T][Hkv][max_blocks] fp32: receives the scores of the blocks of
  *                every range of more than max_sel (all else is left).  Nullable when
  *                max_blocks <= 4096; launches that run at the same time need their own.
- * The same selection on every run.  Hq / Hkv <= 64 and B * T * Hkv <= 2^27
- * (SL8_ERR_UNSUPPORTED).  A length out of range, or a page out of range that is scored, is
+ * The same selection on every run.  Hq / Hkv <= 64, B * T * Hkv <= 2^27, page_size *
+ * max_blocks and page_size * max_sel <= 2^31 - 256 (SL8_ERR_UNSUPPORTED).  A length out of range, or a page out of range that is scored, is
  * recorded (SL8_ERR_DEVICE_ARG) and clamped, or scored as page 0 (and listed as that).
  */
 SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const float* bound_scale,
@@ -517,8 +517,8 @@ SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, co
  *   q            device, [rows][Hq][d] of q_dtype (F16, BF16 or F32), quantised per row.
  *   page_list    device, [rows][Hkv][max_sel] int32 pages, as sl8_page_select's sel_pages or
  *                from any other policy; list_lens device, [rows][Hkv] int32: the tokens that
- *                the list holds, 0 .. max_sel * page_size: every page of the list is full
- *                but the last one.  Entries past the list are not read.
+ *                the list holds, 0 .. max_sel * page_size (<= 2^31 - 256): every page of the
+ *                list is full but the last one.  Entries past the list are not read.
  *   pages        as sl8_attn_int8_paged_decode_splitkv (page_size a multiple of 16).
  *   num_splits   requested splits of each list (0 = automatic).  Up to 8 run as one launch,
  *                a cluster of CTAs per list that merges its parts itself; more, which pays

@@ -125,3 +125,18 @@ def test_binding_refuses_cpu_tensors(lib):
         sl8.page_bounds(pages, scales, i.view(1, 4), i[:1], torch.zeros(1, 1, 2, 64, dtype=torch.int8), torch.zeros(1, 1))
     with pytest.raises(ValueError):
         sl8.attn_int8_sparse_decode(k, pages, scales, pages, scales, i.view(2, 1, 2), i[:2].view(2, 1))
+
+
+def test_tables_and_lists_of_almost_2_31_tokens_are_refused(lib, p):
+    """Counters that step past the last token stay below 2^31."""
+    full, fits = (1 << 27) - 8, (1 << 27) - 16  # pages of 16 tokens: 2^31 - 128 and 2^31 - 256
+    assign = [p, p, None, 0, 16, fits, p, p, 8, p, p, 8, p, p, p, p, None, None]
+    bounds = [p, p, 16, 16, p, fits, p, p, 4, 0, 1, 32, p, p, None]
+    select = [p, sl8.SL8_BF16, p, p, 16, 16, p, fits, p, 0, 1, 1, 1, 32, 8, 1, 2, p, p, p, p, None]
+    size = lib.sl8_attn_int8_sparse_decode_workspace_size
+    assert lib.sl8_paged_assign(*_changed(assign, {5: full})) == UNSUPPORTED
+    assert lib.sl8_page_bounds(*bounds) == OK and lib.sl8_page_bounds(*_changed(bounds, {5: full})) == UNSUPPORTED
+    assert lib.sl8_page_select(*select) == OK
+    for i in (7, 14):
+        assert lib.sl8_page_select(*_changed(select, {i: full})) == UNSUPPORTED
+    assert size(1, 1, 1, fits, 16, 32, 1) == 16 and size(1, 1, 1, full, 16, 32, 1) == 0

@@ -896,13 +896,17 @@ int sl8_attn_int8_decode_logits_debug(const void* q, int q_dtype, const int8_t* 
 }
 
 // ---------------------------------------------------------------- paged cache: plan, append, bounds, selection
+// Tokens of a block table's row or of a page list: the kernels' counters step past the last
+// one by less than 256.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
+
 int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
                      int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,
                      int32_t free_capacity, const int32_t* free_count, int32_t* free_count_out, int32_t max_tokens,
                      int32_t* seqlens, int32_t* granted, int32_t* cu_new, int32_t* slot_map, int32_t* token_pos,
                      void* stream) {
   SL8_CHECK(B >= 0 && page_size > 0 && max_blocks > 0 && free_capacity >= 0 && max_tokens >= 0, SL8_ERR_INVALID_ARG);
-  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks <= kMaxTokens, SL8_ERR_UNSUPPORTED);
   SL8_CHECK(free_count && free_count_out && cu_new, SL8_ERR_INVALID_ARG);
   SL8_CHECK(B == 0 || (ctx_lens && new_lens && block_table && seqlens && granted), SL8_ERR_INVALID_ARG);
   SL8_CHECK((free_capacity == 0 || free_pages) && (max_tokens == 0 || slot_map), SL8_ERR_INVALID_ARG);
@@ -984,7 +988,7 @@ int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t n
   SL8_CHECK(B >= 0 && Hkv > 0 && d > 0 && num_pages > 0 && page_size > 0 && max_blocks > 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(!new_lens || max_new >= 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
-  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks <= kMaxTokens, SL8_ERR_UNSUPPORTED);
   SL8_CHECK(static_cast<int64_t>(B) * max_blocks < (int64_t(1) << 31) / Hkv, SL8_ERR_UNSUPPORTED);
   if (B == 0 || (new_lens && max_new == 0)) return SL8_OK;
   SL8_CHECK(k_pages && k_scale_pages && block_table && seqlens && bounds && bound_scale, SL8_ERR_INVALID_ARG);
@@ -1004,8 +1008,8 @@ int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const floa
   SL8_CHECK(first >= 0 && last >= 0 && max_sel > 0 && first <= max_sel && last <= max_sel - first, SL8_ERR_INVALID_ARG);
   SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
   SL8_CHECK(Hq / Hkv <= 64, SL8_ERR_UNSUPPORTED);
-  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks < (int64_t(1) << 31) &&
-                static_cast<int64_t>(page_size) * max_sel < (int64_t(1) << 31),
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks <= kMaxTokens &&
+                static_cast<int64_t>(page_size) * max_sel <= kMaxTokens,
             SL8_ERR_UNSUPPORTED);
   if (B == 0 || T == 0) return SL8_OK;
   SL8_CHECK(static_cast<int64_t>(B) * T <= (int64_t(1) << 27) / Hkv, SL8_ERR_UNSUPPORTED);
@@ -1026,7 +1030,7 @@ int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, const floa
 static int32_t list_splits(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel, int32_t page_size, int32_t d,
                            int32_t num_splits) {
   if (rows <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_sel <= 0 || page_size <= 0 || num_splits < 0) return 0;
-  if (static_cast<int64_t>(max_sel) * page_size >= (int64_t(1) << 31) || page_size % 16) return 0;
+  if (static_cast<int64_t>(max_sel) * page_size > kMaxTokens || page_size % 16) return 0;
   if (static_cast<int64_t>(rows) > (int64_t(1) << 27) / Hq || !decode_head_dim_ok(d)) return 0;
   const int32_t most = list_decode_max_splits();
   int64_t n = num_splits;
