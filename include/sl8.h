@@ -468,7 +468,7 @@ SL8_API int sl8_rope_append(const void* q, const void* k, const void* v, int dty
  * the largest scale s_t among the page's rows that hold tokens, row t's keys are
  * y = code * (s_t / S) in steps of S (fp32 division and product):
  *   bounds       device, [num_pages][Hkv][2][d] int8: floor(min y), ceil(max y);
- *   bound_scale  device, [num_pages][Hkv] fp32: S (zero: the codes are zero too).
+ *   bound_scale  device, [num_pages][Hkv] fp32: S (zero or infinite: the codes are zero).
  * Written for the pages that the last new_lens[b] (<= max_new, a host bound) tokens of each
  * sequence lie in, over all tokens of those pages; new_lens NULL: for every page of the
  * sequences.  seqlens [B] counts the new tokens.  Sequences must not share pages that take
@@ -490,7 +490,8 @@ SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, i
  *                32-byte aligned.
  *   score        of a page: the maximum over the kv head's query heads of
  *                (float(sum_i max(c_i lo_i, c_i hi_i)) * S) * s_q, fp32 products in this
- *                order: an upper bound of every q . k of the page (before 1 / sqrt(d)).
+ *                order: an upper bound of every q . k of the page (before 1 / sqrt(d)).  A
+ *                head's NaN (an infinite S or s_q: the codes are zero) counts as -inf.
  *   first, last  the first `first` and last `last` pages of a query's range are always kept,
  *                first + last <= max_sel.  The others are kept in the order of their scores,
  *                ties to the lowest block.  A range of at most max_sel pages is kept whole.

@@ -82,7 +82,7 @@ def page_bounds(codes, scales):
     """Bounds of one page and head from its valid rows: codes [n, d] int8, scales [n] fp32.
     Returns (lo, hi) int and S fp32."""
     S = np.float32(scales.max())
-    if S == 0:
+    if S == 0 or np.isinf(S):
         z = np.zeros(codes.shape[1], np.int64)
         return z, z.copy(), S
     y = codes.astype(np.float32) * (scales.astype(np.float32) / S)[:, None]
@@ -94,7 +94,9 @@ def page_scores(q, lo, hi, S):
     c, sq = _quant(q)
     c = c.astype(np.int64)[:, None]
     dots = np.maximum(c * lo[None], c * hi[None]).sum(-1)
-    return (dots.astype(np.float32) * S[None].astype(np.float32) * sq[:, None]).max(0)
+    with np.errstate(invalid="ignore"):
+        s = dots.astype(np.float32) * S[None].astype(np.float32) * sq[:, None]
+    return np.where(np.isnan(s), np.float32(-np.inf), s).max(0)
 
 
 def select(scores, max_sel, first, last):

@@ -336,6 +336,44 @@ def test_page_bounds_reports_bad_lengths_and_pages():
         assert bs[0, 0] == 1.0
 
 
+def test_rows_with_infinities_stay_out_of_a_selection():
+    """A key row with an infinity: its page's bounds are zero, its score -inf, and only a
+    forced page is listed in spite of it; the same for a query row."""
+    num_pages, page, hkv, d = 40, 16, 2, 64
+    rng = np.random.default_rng(3)
+    k = torch.randn((num_pages * page, hkv, d), generator=torch.Generator().manual_seed(2))
+    k[5 * page + 3, 0, 7] = float("inf")    # one row of a page
+    k[9 * page, 1, 0] = -float("inf")       # the only row of a page (the last: page 39 of the table)
+    codes, scales = (torch.zeros(s, dtype=t, device=DEV) for s, t in (((num_pages, hkv, page, d), torch.int8),
+                                                                      ((num_pages, hkv, page), torch.float32)))
+    vc, vs = codes.clone(), scales.clone()
+    sl8.rope_append(None, k.to(DEV), k.to(DEV), None, None, torch.arange(num_pages * page, dtype=torch.int32, device=DEV),
+                    codes, scales, vc, vs)
+    table = [[i for i in range(num_pages) if i != 9] + [9]]
+    L = (num_pages - 1) * page + 1
+    bounds, bs = torch.full((num_pages, hkv, 2, d), 99, dtype=torch.int8, device=DEV), torch.zeros((num_pages, hkv), device=DEV)
+    sl8.page_bounds(codes, scales, i32(table), i32([L]), bounds, bs)
+    nc, ns, gb, gs = (x.cpu().numpy() for x in (codes, scales, bounds, bs))
+    for j, pg in enumerate(table[0]):
+        for h in range(hkv):
+            lo, hi, s = S.page_bounds(nc[pg, h, :min(page, L - j * page)], ns[pg, h, :min(page, L - j * page)])
+            np.testing.assert_array_equal(gb[pg, h], np.stack([lo, hi]))
+            assert gs[pg, h] == s
+    assert np.isinf(gs[5, 0]) and np.isinf(gs[9, 1]) and not gb[5, 0].any() and not gb[9, 1].any()
+    q = torch.randn((1, 2 * hkv, d), generator=torch.Generator().manual_seed(4))
+    q[0, 1, 3] = float("inf")               # one of the first kv head's two query heads
+    for last in (0, 1):
+        out = sl8.page_select(q.to(DEV), bounds, bs, i32(table), i32([L]), page, 38, 0, last)
+        for h in range(hkv):
+            ids = np.array(table[0])
+            want = S.page_scores(q[0, 2 * h:2 * h + 2].numpy(), gb[ids, h, 0].astype(np.int64), gb[ids, h, 1].astype(np.int64),
+                                 gs[ids, h])
+            assert np.isneginf(want[5 if h == 0 else 39])
+            kept = S.select(want, 38, 0, last)
+            assert (5 not in kept) if h == 0 else ((39 in kept) == bool(last))
+            np.testing.assert_array_equal(out["blocks"][0, 0, h].cpu().numpy(), kept)
+
+
 # ------------------------------------------------------------------ page selection
 
 def _bounds_pool(rng, num_pages, hkv, d, coarse=False):

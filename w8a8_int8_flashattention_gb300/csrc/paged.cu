@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
     if (t0 != sub) fetch(t0);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const float r = S == 0.0f ? 0.0f : __fdiv_rn(f[j], S);
+      const float r = S > 0.0f && S < INFINITY ? __fdiv_rn(f[j], S) : 0.0f;
       const uint32_t x[2] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
