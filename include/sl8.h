@@ -423,8 +423,8 @@ SL8_API int sl8_attn_decode_combine(const float* o_partial, const float* lse_par
  *   token_pos           device, nullable, [max_tokens] int32: its position in its sequence, 0
  *                       past the last token.
  * A negative length, ctx_lens above max_blocks * page_size or a free_count outside [0,
- * free_capacity] is recorded (SL8_ERR_DEVICE_ARG) and its request refused, its pages not
- * released, the count clamped; pushes past free_capacity are recorded and dropped.
+ * free_capacity] is recorded (SL8_ERR_DEVICE_ARG) and the slot's request refused, the pages
+ * of an ended one not released, the count clamped; pushes past free_capacity are recorded and dropped.
  * page_size * max_blocks <= 2^31 - 256 (SL8_ERR_UNSUPPORTED).
  */
 SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,

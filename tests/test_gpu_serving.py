@@ -148,6 +148,21 @@ def test_paged_assign_no_requests_and_bad_lengths():
     assert out["free_count"].item() == 1 and out["seqlens"].tolist() == [0]
 
 
+def test_paged_assign_released_slots_with_bad_lengths():
+    """An ended request whose length is out of range: its pages are not released and no new
+    one starts in its slot; the other slots go on."""
+    table, free = i32([[0, 1], [2, 3], [4, -1]]), i32([5, 6, -1, -1, -1])
+    out = sl8.paged_assign(i32([-3, 9, 4]), i32([2, 2, 2]), table, free, i32([2]), 4, 8, release=i32([1, 1, 1]))
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["granted"].tolist() == [0, 0, 2] and out["seqlens"].tolist() == [0, 0, 2]
+    assert out["cu_new"].tolist() == [0, 0, 0, 2] and out["slot_map"].tolist() == [16, 17] + [-1] * 6
+    assert table.tolist() == [[0, 1], [2, 3], [4, -1]] and out["free_count"].item() == 2 and free[:2].tolist() == [5, 6]
+    # a bad count of new tokens leaves the release as it is
+    out = sl8.paged_assign(i32([5]), i32([-1]), i32([[7, 8]]), free, i32([2]), 4, 8, release=i32([1]))
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["free_count"].item() == 4 and free[:4].tolist() == [5, 6, 7, 8] and out["seqlens"].tolist() == [0]
+
+
 # ------------------------------------------------------------------ rotary append
 
 def _rotation_tol(x, rot, adjacent):

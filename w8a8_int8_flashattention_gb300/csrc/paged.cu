@@ -243,11 +243,11 @@ __global__ void __launch_bounds__(kT, 1) paged_assign_kernel(const PlanArgs a, D
     bool valid = false;
     if (live) {
       const bool gone = a.release && (b0 == 0 ? rel0 : a.release[b]) != 0;
-      c = gone ? 0 : b0 == 0 ? ctx0 : a.ctx[b];
+      c = b0 == 0 ? ctx0 : a.ctx[b];
       const int32_t add = b0 == 0 ? add0 : a.add[b];
       valid = c >= 0 && c <= cap && add >= 0;
       if (!valid && rank == 0) record_status(st, kStatusBadArg, 803);
-      c = c < 0 ? 0 : (c > cap ? cap : c);
+      c = gone || c < 0 ? 0 : (c > cap ? cap : c);
       if (valid) tokens = add;
     }
     int64_t cu_total, need_total;
