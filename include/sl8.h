@@ -471,8 +471,8 @@ SL8_API int sl8_rope_append(const void* q, const void* k, const void* v, int dty
  *   bound_scale  device, [num_pages][Hkv] fp32: S (zero or infinite: the codes are zero).
  * Written for the pages that the last new_lens[b] (<= max_new, a host bound) tokens of each
  * sequence lie in, over all tokens of those pages; new_lens NULL: for every page of the
- * sequences.  seqlens [B] counts the new tokens.  Sequences must not share pages that take
- * new tokens.  Scales are >= 0.  page_size * max_blocks <= 2^31 - 256.  A length or page out
+ * sequences.  seqlens [B] counts the new tokens.  Sequences may share pages that they all
+ * fill, and no others among those written.  Scales are >= 0.  page_size * max_blocks <= 2^31 - 256.  A length or page out
  * of range is recorded (SL8_ERR_DEVICE_ARG) and clamped or skipped.
  */
 SL8_API int sl8_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,

@@ -747,6 +747,8 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     _shaped(bound_scale, (num_pages, hkv), "bound_scale")
     B, max_blocks = block_table.shape
     shape = q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [B, Hq, d] or [B, T, Hq, d]")
     T, hq = (1, shape[1]) if len(shape) == 3 else (shape[1], shape[2])
     if shape[0] != B or shape[-1] != d or seqlens.numel() != B:
         raise ValueError("q, block_table, seqlens and bounds do not belong together")

@@ -239,13 +239,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     float o[D / 16][4], osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    bool ok = true;
     for (int k = 0; k < n; ++k) {
       const int stg = k % kStages;
-      if (!warp_wait(&full[stg], (k / kStages) & 1, limit_ns, st, 853)) {
-        ok = false;
-        break;
-      }
+      if (!warp_wait(&full[stg], (k / kStages) & 1, limit_ns, st, 853)) break;
       const uint8_t* base = smem + stg * C::kStageBytes;
       const int nv = t1 - (t0 + k * kTok) - u0;  // valid tokens of this warp's unit
       if (nv > 0) {
@@ -442,7 +438,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const float l = ml[8 + threadIdx.x];
       a.lse[row0 + threadIdx.x] = l > 0.0f ? (ml[threadIdx.x] + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
-    (void)ok;
   }
   if (S == 1) return;
 
