@@ -636,10 +636,12 @@ def _pages_of(dev, k_pages, k_scale_pages, v_pages=None, v_scale_pages=None):
     shape = k_pages.shape
     if len(shape) != 4:
         raise ValueError("pages must be [num_pages, Hkv, page_size, d]")
-    _shaped(k_scale_pages, shape[:3], "k_scale_pages")
+    num_pages, hkv, page_size, _ = shape
+    rows = (num_pages, hkv, page_size)
+    _shaped(k_scale_pages, rows, "k_scale_pages")
     if v_pages is not None:
         _shaped(v_pages, shape, "v_pages")
-        _shaped(v_scale_pages, shape[:3], "v_scale_pages")
+        _shaped(v_scale_pages, rows, "v_scale_pages")
     return shape, c, s
 
 
