@@ -573,19 +573,31 @@ struct BoundsArgs {
   float* scale;
 };
 
+// (y0, y1) = (y0 - 8388736, y1 - 8388736) r, each operation rounded to fp32, two at a time.
+__device__ __forceinline__ void codes_times(float& y0, float& y1, float r) {
+  asm("{\n\t.reg .b64 y, c;\n\tmov.b64 y, {%0, %1};\n\tmov.b64 c, {%3, %3};\n\tadd.rn.f32x2 y, y, c;\n\t"
+      "mov.b64 c, {%2, %2};\n\tmul.rn.f32x2 y, y, c;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "+f"(y0), "+f"(y1)
+      : "f"(r), "f"(-8388736.0f));
+}
+
 // Per-channel bounds of a page's keys.  With S the largest row scale among the page's
 // valid rows, row t's keys are code * (s_t / S) in steps of S; the bounds are the floor
 // of the least and the ceiling of the largest, so lo S <= k <= hi S holds for every key
 // (up to the rounding of s_t / S and of the product).  A warp per (page, kv head): D / 8
 // lanes hold a row, 8 channels each, and the rows run over the remaining lanes, kBatch of a
-// lane's rows on their way at once.  Bound by the latency of the chain length -> page id ->
-// rows: 7.2 us for one page of 64 rows in each of 64 sequences (8 kv heads, d = 128), 16.4
-// for the 16-row pages of four chunks of 4k to 8k tokens, whose bytes take 4.
+// lane's rows on their way at once.  Small calls are bound by the latency of the chain
+// length -> page id -> rows, large ones by instruction issue, so a row's ratio is divided by
+// one lane and shuffled to the others, products go two at a time and extrema take two rows
+// at once; four warps a CTA, so that a CTA's slots are free again sooner: 4.7 us for one page
+// of 64 rows in each of 64 sequences (8 kv heads, d = 128), 11.3 for the 16-row pages of four
+// chunks of 4k to 8k tokens, whose bytes take 4.8 (7.2 and 16.4 without these four).
 template <int D>
-__global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, DeviceStatus* st) {
+__global__ void __launch_bounds__(128, 8) page_bounds_kernel(const BoundsArgs a, DeviceStatus* st) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+  constexpr int kSpan = kBatch * kRows, kScales = (kSpan + 31) / 32;  // rows of a batch; scales a lane holds of them
   const int lane = threadIdx.x & 31;
-  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
   const uint32_t u = w / static_cast<uint32_t>(a.Hkv), h = w - u * a.Hkv;
   const uint32_t b = u / static_cast<uint32_t>(a.per_seq), i = u - b * a.per_seq;
   if (b >= static_cast<uint32_t>(a.B)) return;
@@ -614,18 +626,19 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
   const float* ks = a.k_scale + ph * a.page;
   const int l = lane % kLanes, sub = lane / kLanes;
   uint2 v[kBatch];
-  float f[kBatch];
+  float f[kScales];
   auto fetch = [&](int t0) {  // rows past n repeat the last one
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int t = min(t0 + j * kRows, n - 1);
-      v[j] = *reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(t) * D + 8 * l);
-      f[j] = ks[t];
-    }
+    for (int j = 0; j < kBatch; ++j)
+      v[j] = *reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(min(t0 + sub + j * kRows, n - 1)) * D + 8 * l);
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) f[i] = ks[min(t0 + 32 * i + lane, n - 1)];
   };
-  fetch(sub);
+  fetch(0);
   float S = 0.0f;
-  for (int t = lane; t < n; t += 32) S = fmaxf(S, ks[t]);
+#pragma unroll
+  for (int i = 0; i < kScales; ++i) S = fmaxf(S, f[i]);
+  for (int t = 32 * kScales + lane; t < n; t += 32) S = fmaxf(S, ks[t]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) S = fmaxf(S, __shfl_xor_sync(0xffffffffu, S, o));
   float lo[8], hi[8];
@@ -634,18 +647,30 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const BoundsArgs a, De
     lo[e] = INFINITY;
     hi[e] = -INFINITY;
   }
-  for (int t0 = sub; t0 < n; t0 += kBatch * kRows) {
-    if (t0 != sub) fetch(t0);
+  for (int t0 = 0; t0 < n; t0 += kSpan) {
+    if (t0 != 0) fetch(t0);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const float r = S > 0.0f && S < INFINITY ? __fdiv_rn(f[j], S) : 0.0f;
-      const uint32_t x[2] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u};
+    for (int i = 0; i < kScales; ++i) f[i] = S > 0.0f && S < INFINITY ? __fdiv_rn(f[i], S) : 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // code + 128 as the low bits of 2^23 + code + 128: exact, without a conversion
-        const float y = (__uint_as_float(prmt(x[e / 4], 0x4b000000u, 0x7650 + e % 4)) - 8388736.0f) * r;
-        lo[e] = fminf(lo[e], y);
-        hi[e] = fmaxf(hi[e], y);
+    for (int j = 0; j < kBatch; j += 2) {  // two rows at a time: least and largest of three
+      float r[2], y[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[i] = __shfl_sync(0xffffffffu, f[(j + i) * kRows / 32], ((j + i) * kRows + sub) & 31);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // code + 128 as the low bits of 2^23 + code + 128: exact, without a conversion
+          const uint32_t x = (e < 4 ? v[j + i].x : v[j + i].y) ^ 0x80808080u;
+          y[i][0] = __uint_as_float(prmt(x, 0x4b000000u, 0x7650 + e % 4));
+          y[i][1] = __uint_as_float(prmt(x, 0x4b000000u, 0x7651 + e % 4));
+          codes_times(y[i][0], y[i][1], r[i]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          asm("min.f32 %0, %0, %1, %2;" : "+f"(lo[e + c]) : "f"(y[0][c]), "f"(y[1][c]));
+          asm("max.f32 %0, %0, %1, %2;" : "+f"(hi[e + c]) : "f"(y[0][c]), "f"(y[1][c]));
+        }
       }
     }
   }
@@ -766,12 +791,12 @@ cudaError_t launch_page_bounds(const int8_t* k_pages, const float* k_scale_pages
   if (per_seq > max_blocks) per_seq = max_blocks;
   const BoundsArgs a{k_pages, k_scale_pages, num_pages, page_size, block_table, max_blocks, seqlens, new_lens, max_new,
                      static_cast<int32_t>(per_seq), B, Hkv, bounds, bound_scale};
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(B) * per_seq * Hkv + 7) / 8);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(B) * per_seq * Hkv + 3) / 4);
   switch (d) {
-    case 32: page_bounds_kernel<32><<<grid, 256, 0, s>>>(a, device_status_ptr()); break;
-    case 64: page_bounds_kernel<64><<<grid, 256, 0, s>>>(a, device_status_ptr()); break;
-    case 128: page_bounds_kernel<128><<<grid, 256, 0, s>>>(a, device_status_ptr()); break;
-    case 256: page_bounds_kernel<256><<<grid, 256, 0, s>>>(a, device_status_ptr()); break;
+    case 32: page_bounds_kernel<32><<<grid, 128, 0, s>>>(a, device_status_ptr()); break;
+    case 64: page_bounds_kernel<64><<<grid, 128, 0, s>>>(a, device_status_ptr()); break;
+    case 128: page_bounds_kernel<128><<<grid, 128, 0, s>>>(a, device_status_ptr()); break;
+    case 256: page_bounds_kernel<256><<<grid, 128, 0, s>>>(a, device_status_ptr()); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
