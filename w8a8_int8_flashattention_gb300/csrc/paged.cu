@@ -432,11 +432,13 @@ __device__ __forceinline__ void turn(int32_t pos, uint64_t g, float& c, float& s
 // HBM-bound: q, k and v are read once, q is written once and k, v as codes; 16,384 tokens of
 // 16 + 2 x 8 heads at d = 256 take 85 us, 5.5 TB/s, 0.81 of the measured copy rate (with
 // four groups in flight 89, five 98: the registers cost more warps than they add loads).
+// One wave of 4,099 tokens (16 + 2 x 2 heads, d = 128) takes 11 us, and 11.8 with eight warps a
+// CTA instead of four, whose slots are free only once all of them end.
 template <typename T, int D, bool kAdjacent>
-__global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a, DeviceStatus* st) {
+__global__ void __launch_bounds__(128) rope_append_kernel(const AppendArgs a, DeviceStatus* st) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = sizeof(T) == 4 ? 2 : 3;
   const int lane = threadIdx.x & 31;
-  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
   const uint32_t tok = a.parts == 1 ? w : w / static_cast<uint32_t>(a.parts);
   if (tok >= static_cast<uint32_t>(a.T)) return;
   const int part = static_cast<int>(w - tok * a.parts);
@@ -698,8 +700,8 @@ __global__ void __launch_bounds__(128, 8) page_bounds_kernel(const BoundsArgs a,
 
 template <typename T, int D>
 cudaError_t launch_append_td(const AppendArgs& a, bool adjacent, unsigned grid, cudaStream_t s) {
-  if (adjacent) rope_append_kernel<T, D, true><<<grid, 256, 0, s>>>(a, device_status_ptr());
-  else rope_append_kernel<T, D, false><<<grid, 256, 0, s>>>(a, device_status_ptr());
+  if (adjacent) rope_append_kernel<T, D, true><<<grid, 128, 0, s>>>(a, device_status_ptr());
+  else rope_append_kernel<T, D, false><<<grid, 128, 0, s>>>(a, device_status_ptr());
   return cudaGetLastError();
 }
 template <typename T>
@@ -772,7 +774,7 @@ cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(groups, fill / r.T));
   a.iters = static_cast<int32_t>((groups + parts - 1) / parts);
   a.parts = (groups + a.iters - 1) / a.iters;
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(r.T) * a.parts + 7) / 8);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(r.T) * a.parts + 3) / 4);
   switch (r.dtype) {
     case SL8_F16: return launch_append_t<__half>(a, r.d, r.adjacent, grid, s);
     case SL8_BF16: return launch_append_t<__nv_bfloat16>(a, r.d, r.adjacent, grid, s);
