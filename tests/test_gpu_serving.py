@@ -571,6 +571,14 @@ def test_sparse_decode(R, hq, hkv, d, page, max_sel, splits, dtype, odt):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("R,hq,hkv,d,page,max_sel,splits", [
+    (330, 4, 2, 64, 16, 6, 0), (350, 2, 2, 32, 32, 3, 0), (270, 4, 2, 128, 16, 6, 0), (80, 4, 2, 64, 32, 31, 0),
+    (20, 8, 2, 32, 16, 70, 0), (110, 2, 1, 64, 64, 9, 8), (330, 2, 2, 64, 16, 9, 2)])
+def test_sparse_decode_where_ctas_crowd_an_sm(R, hq, hkv, d, page, max_sel, splits):
+    """Every number of CTAs an SM runs, with whole lists and with split ones."""
+    test_sparse_decode(R, hq, hkv, d, page, max_sel, splits, torch.bfloat16, torch.float32)
+
+
 @pytest.mark.parametrize("d", [32, 64, 128, 256])
 @pytest.mark.parametrize("splits", [0, 3, 9])
 def test_what_lies_past_a_list_does_not_matter(d, splits):

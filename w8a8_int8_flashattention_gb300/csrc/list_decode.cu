@@ -6,7 +6,7 @@
 //
 // GB300 design.  A list is short (some thousand tokens) and there are many, so the kernel
 // is not persistent: a cluster of S CTAs serves one list, each CTA a contiguous run of its
-// stages of 64 tokens, and two to four CTAs share an SM, one's start and end hidden behind
+// stages of 64 tokens, and two to five CTAs share an SM, one's start and end hidden behind
 // the others' streams.  The S partial results meet over distributed shared memory, so one
 // launch does everything and no workspace or counter is shared between launches.
 //  * The last warp loads: per stage, one lane per piece of 64, 32 or 16 rows (the largest
@@ -21,7 +21,8 @@
 // HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
 // 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
 // 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
-// the combine over the same lists: 152 and 14.4 us.)
+// the combine over the same lists: 152 and 14.4 us.)  At d = 64 a stage is half the bytes for
+// the same chain of steps: 600 lists of 4,096 tokens take 61 us, 0.80 of the copy rate.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,17 +45,20 @@ constexpr int kWarps = 4, kCThreads = 32 * kWarps;  // compute warps
 constexpr int kThreads = kCThreads + 32;            // and the loader
 constexpr int kTok = 16 * kWarps;                   // tokens per stage
 
-// kCtas CTAs share an SM: three (two at d = 256), or four with 96 registers a thread and one
-// stage less, which only run unsplit lists and so carry no merge.
+// kCtas CTAs share an SM: list_ctas(d), or one more at d = 64 and 128, with fewer registers and
+// stages, which only run unsplit lists and so carry no merge.
+constexpr int list_ctas(int d) { return d == 256 ? 2 : d == 128 ? 3 : 4; }
 template <int D, int kCtas>
 struct LCfg {
+  static constexpr bool kMerge = kCtas == list_ctas(D);
   static constexpr int kBW = D < 128 ? D : 128;  // bytes in one row of a TMA box
   static constexpr int kBoxes = D / kBW;
   static constexpr bool kSwz = D >= 128;
   static constexpr int kTile = kTok * D;
   static constexpr int kSK = 0, kSV = kTile, kSKs = 2 * kTile, kSVs = kSKs + kTok * 4;
-  static constexpr int kStageBytes = (kSVs + kTok * 4 + 1023) / 1024 * 1024;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kCtas == 4 ? 3 : 4) : (kCtas == 4 ? 6 : 8);
+  static constexpr int kAlign = kSwz ? 1024 : 128;  // swizzled tiles need 1024-byte alignment
+  static constexpr int kStageBytes = (kSVs + kTok * 4 + kAlign - 1) / kAlign * kAlign;
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kMerge ? 4 : 3) : kMerge ? 6 : 4;
   // after the loop the ring holds the warps' O^T [warp][D][8] and the CTA's [8][D], fp32
   static constexpr int kRed = 0, kPart = kWarps * D * 32;
   static_assert(kPart + D * 32 <= kStages * kStageBytes, "the merge fits the ring");
@@ -65,13 +69,15 @@ struct LCfg {
   static constexpr int kMl = kWt + kWarps * 32;          // [8] max, [8] sum of the CTA
   static constexpr int kBar = kMl + 64;
   static constexpr int kBytes = kBar + 2 * kStages * 8 + 1024;  // + alignment slack
-  static_assert(kStageBytes % 1024 == 0 && kTile % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  static_assert(!kSwz || kTile % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  // an SM has 228 KB, of which each CTA takes one more for itself
+  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "kCtas CTAs fit an SM");
 };
 
 // Byte offset of (row r, 16-byte chunk c of the row) in a stage tile of kBoxes boxes.
 template <int D>
 __device__ __forceinline__ uint32_t ltile_off(int r, int c) {
-  using C = LCfg<D, 3>;
+  using C = LCfg<D, 2>;  // the tile is the same for all
   constexpr int cpb = C::kBW / 16;
   const int b = c / cpb, cc = c % cpb;
   return static_cast<uint32_t>(b * (kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
@@ -88,8 +94,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
   uint64_t* empty = full + kStages;
   cg::cluster_group cluster = cg::this_cluster();
-  // four CTAs an SM only run unsplit lists
-  const int S = kCtas == 4 ? 1 : a.splits, rank = S > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  const int S = C::kMerge ? a.splits : 1, rank = S > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // list v = row * Hkv + kv head; its G query heads are cut into groups of GC <= 8
   const int vg = static_cast<int>(blockIdx.x / static_cast<unsigned>(S));
@@ -505,7 +510,7 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
 int list_decode_max_splits() { return kMaxSplits; }
 
 int list_decode_splits(int64_t lists, int64_t tokens, int32_t d) {
-  const int64_t fit = (d == 256 ? 2 : 3) * static_cast<int64_t>(num_sms());
+  const int64_t fit = list_ctas(d) * static_cast<int64_t>(num_sms());
   // few long lists: clusters of kMaxSplits CTAs would leave SMs without work (8 lists of
   // 65,536 tokens, d = 128: 81 us with 8 splits, 51 with 32; 1 list: 80 and 26 with 64)
   if (lists * kMaxSplits < num_sms() && tokens >= 4096 * kMaxSplits)
@@ -522,16 +527,18 @@ cudaError_t launch_list_decode(const ListDecodeArgs& args, int32_t d, cudaStream
   // rows per TMA box: the largest of a stage's 64, 32 or 16 that divides the page, so that
   // no piece straddles two pages
   a.box = a.page % 64 == 0 ? 64 : a.page % 32 == 0 ? 32 : 16;
-  // Three CTAs an SM or four, whichever fills its last wave better: 512 lists of 4,096 tokens
-  // (d = 128) take 110 us with three and 87.5 with four, 512 of 1,024 tokens 35 and 27; 768
-  // lists of 2,048 tokens 72 and 82, 448 of 4,096 76 and 74.
-  const int64_t ctas = static_cast<int64_t>(a.rows) * a.Hkv * a.groups * a.splits, w3 = 3ll * num_sms(), w4 = 4ll * num_sms();
-  const bool four = a.splits == 1 && ctas > w3 && (ctas + w4 - 1) / w4 * w4 < (ctas + w3 - 1) / w3 * w3;
+  // list_ctas(d) CTAs an SM or one more, whichever fills its last wave better: d = 128, 512 lists
+  // of 4,096 tokens take 110 us with three and 87.5 with four, 512 of 1,024 tokens 35 and 27; 768
+  // lists of 2,048 tokens 72 and 82, 448 of 4,096 76 and 74.  d = 64, 720 lists of 4,096 tokens:
+  // 102 with four, 77 with five; 600 of them 61.4 and 62.5.
+  const int64_t ctas = static_cast<int64_t>(a.rows) * a.Hkv * a.groups * a.splits;
+  const int64_t w = static_cast<int64_t>(list_ctas(d)) * num_sms(), w1 = w + num_sms();
+  const bool more = a.splits == 1 && ctas > w && (ctas + w1 - 1) / w1 * w1 < (ctas + w - 1) / w * w;
   switch (d) {
-    case 32: return four ? launch_list_d<32, 4>(a, s) : launch_list_d<32, 3>(a, s);
-    case 64: return four ? launch_list_d<64, 4>(a, s) : launch_list_d<64, 3>(a, s);
-    case 128: return four ? launch_list_d<128, 4>(a, s) : launch_list_d<128, 3>(a, s);
-    case 256: return launch_list_d<256, 2>(a, s);
+    case 32: return launch_list_d<32, list_ctas(32)>(a, s);
+    case 64: return more ? launch_list_d<64, list_ctas(64) + 1>(a, s) : launch_list_d<64, list_ctas(64)>(a, s);
+    case 128: return more ? launch_list_d<128, list_ctas(128) + 1>(a, s) : launch_list_d<128, list_ctas(128)>(a, s);
+    case 256: return launch_list_d<256, list_ctas(256)>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
