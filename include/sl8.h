@@ -526,6 +526,9 @@ SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, co
  *                for a few long lists, as the split kernel and the combine.
  *   out          device, [rows][Hq][d] of out_dtype; a row whose list is empty gets 0.
  *   lse_out      device, nullable, [rows][Hq] fp32 (natural log; -inf for an empty list).
+ *                A NaN logit (an infinite k scale with codes of 0, or such a query row, as
+ *                rows with infinities are quantised) makes out and lse_out of its query NaN,
+ *                an infinite v scale out alone: the definition's values.
  *   workspace    for more than 8 splits, at least
  *                sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
  *                unsupported shape; 16: none is used and it may be null); launches that run

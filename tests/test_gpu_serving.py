@@ -802,3 +802,50 @@ def test_side_stream_and_refusals():
         sl8.rope_append(None, k, k, slots, None, slots, *args[:4])
     with pytest.raises(ValueError):
         sl8.rope_append(k, k, k, i32([0, 1, 2]), torch.ones(32, device=DEV), slots, *args[:4])
+
+
+# ------------------------------------------------------------------ sparse decode: NaN, ranges and long lists
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("splits", [0, 1, 3, 8, 9, 20])
+def test_nan_logits_reach_the_output(splits, d):
+    """An infinite scale with codes of 0, as the append stores a row that holds an infinity, and
+    an infinite query row have NaN logits: out and lse of their queries are NaN, as the
+    definition has it, and no others' are."""
+    rng = np.random.default_rng(d + splits)
+    R, hq, hkv, page, max_sel = 8, 4, 2, 32, 40
+    num_pages = R * hkv * max_sel
+    codes, scales, _, _ = _pool(rng, num_pages, hkv, page, d)
+    pages = rng.permutation(num_pages).reshape(R, hkv, max_sel)  # no page in two lists
+    lens = rng.integers(page * 30, max_sel * page + 1, (R, hkv))
+    lens[4], lens[5, 0], lens[6] = 0, 1, 1
+    q = torch.randn((R, hq, d), generator=torch.Generator().manual_seed(d)).half()
+
+    def infinite(i, r, h, t):
+        at = pages[r, h, t // page], h, t % page
+        codes[i][at], scales[i][at] = 0, np.inf
+
+    infinite(0, 1, 0, lens[1, 0] - 1)             # one key, in the list's last stage
+    for t in range(0, 48):
+        infinite(0, 2, 1, t)                      # all keys of some warps, before and behind finite ones
+    for t in range(lens[3, 0]):
+        infinite(0, 3, 0, t)                      # every key
+    q[3, 3, 5], q[4, 0, 0] = np.inf, -np.inf      # a query row; one whose list is empty
+    infinite(0, 5, 0, 0)                          # the only key
+    infinite(1, 6, 1, 0), infinite(1, 7, 0, 77)   # value rows
+    dc, ds = ([torch.from_numpy(x).to(DEV) for x in y] for y in (codes, scales))
+    out, lse = sl8.attn_int8_sparse_decode(q.to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens), num_splits=splits,
+                                           out_dtype=torch.float32, return_lse=True)
+    with np.errstate(invalid="ignore"):
+        want, wlse = S.sparse_attention(q.float().numpy(), codes[0], scales[0], codes[1], scales[1], pages, lens)
+    nan = np.zeros((R, hq), bool)
+    nan[1, :2] = nan[2, 2:] = nan[3, :2] = nan[3, 3] = nan[5, :2] = True
+    assert np.array_equal(np.isnan(wlse), nan) and np.array_equal(np.isnan(np64(lse)), nan)
+    assert np.array_equal(np64(lse) == -np.inf, np.arange(R)[:, None].repeat(hq, 1) == 4)
+    nan[6, 2:] = nan[7, :2] = True
+    assert np.array_equal(np.isnan(want), np.broadcast_to(nan[..., None], want.shape))
+    assert np.array_equal(np.isnan(np64(out)), np.isnan(want))
+    assert np.all(np64(out)[4] == 0)
+    vmax = np.abs(codes[1].astype(np.float64) * np.where(np.isinf(scales[1]), 0, scales[1])[..., None]).max()
+    tol = (2.0 ** -11 + 2.0 ** -24 * max_sel * page) * vmax
+    assert np.all(np.abs(np64(out)[~nan] - want[~nan]) <= tol)

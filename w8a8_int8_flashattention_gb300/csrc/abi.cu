@@ -1127,7 +1127,7 @@ int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_page
   a.list_heads = Hkv;
   SL8_LAUNCH(launch_decode_split(a, s));
   SL8_LAUNCH(launch_decode_combine(a.o_partial, a.lse_partial, list_lens, a.B, a.Hq, d, S, a.split_size, out,
-                                   static_cast<sl8_dtype>(out_dtype), lse_out, s));
+                                   static_cast<sl8_dtype>(out_dtype), lse_out, s, 1, true));
   return SL8_OK;
 }
 

@@ -1008,6 +1008,10 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     // sum, and O = (2^24 O' - 128 rowsum(P')) * 2^E
     l_a = col_sum(l_a);
     l_b = col_sum(l_b);
+    if constexpr (kLists) {
+      m_a = keep_nan(m_a, l_a);
+      m_b = keep_nan(m_b, l_b);
+    }
     if (n > 0 && !warp_wait(red_empty, (n - 1) & 1, limit_ns, st, 47)) {
       ok = false;
       break;
@@ -1061,12 +1065,13 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
   }
 }
 
-// One warp per (b, hq): merge the non-empty splits of the row.
+// One warp per (b, hq): merge the non-empty splits of the row.  nan: a split whose LSE is NaN
+// makes the row NaN (page lists); without it such a split counts as an empty one.
 template <int D>
 __global__ void decode_combine_kernel(const float* __restrict__ o_partial, const float* __restrict__ lse_partial,
                                       const int32_t* __restrict__ seqlens, int32_t B, int32_t Hq, int32_t num_splits,
                                       int32_t split_size, void* out, sl8_dtype out_dtype, float* lse_out,
-                                      int32_t seq_div) {
+                                      int32_t seq_div, bool nan) {
   const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (row >= B * Hq) return;
@@ -1079,6 +1084,7 @@ __global__ void decode_combine_kernel(const float* __restrict__ o_partial, const
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
   float m = -INFINITY, wsum = 0.0f;
+  bool bad = false;
   // K splits at a time: their LSEs (the same word for every lane) and partial rows are
   // all loaded before any is used, together with the length.  An empty split (past the
   // length, or lse = -inf) gets weight 0 and its unwritten row is never multiplied.
@@ -1095,7 +1101,10 @@ __global__ void decode_combine_kernel(const float* __restrict__ o_partial, const
     float m_new = m;
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (s0 + k < ns) m_new = fmaxf(m_new, ls[k]);
+      if (s0 + k < ns) {
+        m_new = fmaxf(m_new, ls[k]);
+        bad = bad || (nan && isnan(ls[k]));
+      }
     if (m_new == -INFINITY) continue;  // every split so far is empty
     const float c = m == -INFINITY ? 0.0f : expf(m - m_new);
     wsum *= c;
@@ -1114,13 +1123,13 @@ __global__ void decode_combine_kernel(const float* __restrict__ o_partial, const
   const float inv = wsum > 0.0f ? 1.0f / wsum : 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float v = o[e] * inv;
+    const float v = bad ? NAN : o[e] * inv;
     const int64_t idx = static_cast<int64_t>(row) * D + lane * E + e;
     if (out_dtype == SL8_F32) static_cast<float*>(out)[idx] = v;
     else if (out_dtype == SL8_BF16) static_cast<__nv_bfloat16*>(out)[idx] = __float2bfloat16_rn(v);
     else static_cast<__half*>(out)[idx] = __float2half_rn(v);
   }
-  if (lse_out && lane == 0) lse_out[row] = m == -INFINITY ? -INFINITY : m + logf(wsum);
+  if (lse_out && lane == 0) lse_out[row] = bad ? NAN : m == -INFINITY ? -INFINITY : m + logf(wsum);
 }
 
 __global__ void timeout_selftest_kernel(uint64_t limit_ns, DeviceStatus* st) {
@@ -1217,15 +1226,15 @@ cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_decode_combine(const float* o_partial, const float* lse_partial, const int32_t* seqlens, int32_t B,
                                   int32_t Hq, int32_t d, int32_t num_splits, int32_t split_size, void* out,
-                                  sl8_dtype out_dtype, float* lse_out, cudaStream_t s, int32_t seq_div) {
+                                  sl8_dtype out_dtype, float* lse_out, cudaStream_t s, int32_t seq_div, bool nan) {
   TraceScope tr("decode_combine", s);
   const int rows = B * Hq;
   const int grid = (rows + 7) / 8;
   switch (d) {
-    case 32: decode_combine_kernel<32><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div); break;
-    case 64: decode_combine_kernel<64><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div); break;
-    case 128: decode_combine_kernel<128><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div); break;
-    case 256: decode_combine_kernel<256><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div); break;
+    case 32: decode_combine_kernel<32><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div, nan); break;
+    case 64: decode_combine_kernel<64><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div, nan); break;
+    case 128: decode_combine_kernel<128><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div, nan); break;
+    case 256: decode_combine_kernel<256><<<grid, 256, 0, s>>>(o_partial, lse_partial, seqlens, B, Hq, num_splits, split_size, out, out_dtype, lse_out, seq_div, nan); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

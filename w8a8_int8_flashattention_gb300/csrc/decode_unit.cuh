@@ -31,6 +31,10 @@ __device__ __forceinline__ float col_sum(float a) {
   a += __shfl_xor_sync(0xffffffffu, a, 8);
   return a + __shfl_xor_sync(0xffffffffu, a, 16);
 }
+// A sum that a NaN logit has made NaN belongs to no maximum where all of a warp's logits were
+// NaN (maxima drop it): with the reference 0 instead of -inf, which says that there was no
+// token, the merges keep it.
+__device__ __forceinline__ float keep_nan(float m, float l) { return isnan(l) && m == -INFINITY ? 0.0f : m; }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, DeviceStatus* st,
                                           int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, st, site));

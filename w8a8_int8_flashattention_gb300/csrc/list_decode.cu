@@ -372,6 +372,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     // O = (2^24 O' - 128 rowsum(P')) * 2^E.  The ring is free once every warp is here.
     l_a = col_sum(l_a);
     l_b = col_sum(l_b);
+    m_a = keep_nan(m_a, l_a);
+    m_b = keep_nan(m_b, l_b);
     named_bar_sync(1, kCThreads);
     float* stat = reinterpret_cast<float*>(smem + C::kStat);
     float* red = reinterpret_cast<float*>(smem + C::kRed);
@@ -435,13 +437,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         for (int c = 0; c < 4; ++c) {
           const float l = ml[8 + 4 * h + c];
           if (4 * h + c < GC)
-            store_out(a.out, a.out_dtype, (row0 + 4 * h + c) * D + dim, l > 0.0f ? x[c] / l : 0.0f);
+            store_out(a.out, a.out_dtype, (row0 + 4 * h + c) * D + dim, l == 0.0f ? 0.0f : x[c] / l);
         }
       }
     }
     if (S == 1 && a.lse && threadIdx.x < GC) {
       const float l = ml[8 + threadIdx.x];
-      a.lse[row0 + threadIdx.x] = l > 0.0f ? (ml[threadIdx.x] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      a.lse[row0 + threadIdx.x] = l == 0.0f ? -INFINITY : (ml[threadIdx.x] + log2f(l)) * 0.6931471805599453f;
     }
   }
   if (S == 1) return;
@@ -472,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         acc = fmaf(f, x[r], acc);
       }
     }
-    store_out(a.out, a.out_dtype, (row0 + c) * D + dim, sum > 0.0f ? acc / sum : 0.0f);
-    if (a.lse && dim == 0) a.lse[row0 + c] = sum > 0.0f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    store_out(a.out, a.out_dtype, (row0 + c) * D + dim, sum == 0.0f ? 0.0f : acc / sum);
+    if (a.lse && dim == 0) a.lse[row0 + c] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
   }
   cluster.sync();  // no CTA leaves while another reads its part
 }

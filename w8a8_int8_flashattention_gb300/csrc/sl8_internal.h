@@ -279,7 +279,7 @@ cudaError_t launch_decode_split(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_combine(const float* o_partial, const float* lse_partial, const int32_t* seqlens,
                                   int32_t B, int32_t Hq, int32_t d, int32_t num_splits, int32_t split_size,
                                   void* out, sl8_dtype out_dtype, float* lse_out, cudaStream_t s,
-                                  int32_t seq_div = 1);
+                                  int32_t seq_div = 1, bool nan = false);
 // Decode over page lists in one launch (list_decode.cu): `splits` CTAs (a cluster, at most
 // list_decode_max_splits()) per list and group of at most 8 query heads.
 struct ListDecodeArgs {
