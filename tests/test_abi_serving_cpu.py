@@ -140,3 +140,21 @@ def test_tables_and_lists_of_almost_2_31_tokens_are_refused(lib, p):
     for i in (7, 14):
         assert lib.sl8_page_select(*_changed(select, {i: full})) == UNSUPPORTED
     assert size(1, 1, 1, fits, 16, 32, 1) == 16 and size(1, 1, 1, full, 16, 32, 1) == 0
+
+
+def test_the_longest_lists_have_a_split_plan(lib):
+    """Lists up to the limit are split as shorter ones are, for every number of splits."""
+    size = lib.sl8_attn_int8_sparse_decode_workspace_size
+    fits = (1 << 27) - 16  # pages of 16 tokens: 2^31 - 256
+    assert size(1, 1, 1, fits, 16, 32, 0) >= 16
+    for splits in (9, 64, 300, 4096, 65535):
+        assert size(1, 1, 1, fits, 16, 32, splits) > 16, splits
+        n = lib.sl8_attn_decode_num_splits(1, 1, fits * 16, 32, splits)
+        ss = lib.sl8_attn_decode_split_size(1, 1, fits * 16, 32, splits)
+        assert n > 0 and (n - 1) * ss < fits * 16 <= n * ss and ss % 16 == 0
+    # the arithmetic of lengths that never came near 2^31 is what it was
+    for L in (1, 15, 16, 17, 159, 160, 161, 4096, 100000, 1 << 20):
+        for splits in (1, 2, 7, 64, 1000):
+            n = lib.sl8_attn_decode_num_splits(3, 2, L, 64, splits)
+            ss = lib.sl8_attn_decode_split_size(3, 2, L, 64, splits)
+            assert 1 <= n <= splits and (n - 1) * ss < L <= n * ss

@@ -849,3 +849,40 @@ def test_nan_logits_reach_the_output(splits, d):
     vmax = np.abs(codes[1].astype(np.float64) * np.where(np.isinf(scales[1]), 0, scales[1])[..., None]).max()
     tol = (2.0 ** -11 + 2.0 ** -24 * max_sel * page) * vmax
     assert np.all(np.abs(np64(out)[~nan] - want[~nan]) <= tol)
+
+
+def test_a_length_out_of_range_counts_as_the_whole_list():
+    """Also where several splits are joined, and where the length is the largest number."""
+    rng = np.random.default_rng(8)
+    hq, hkv, d, page, max_sel = 4, 2, 64, 32, 60
+    _, _, dc, ds = _pool(rng, 64, hkv, page, d)
+    pages = i32(rng.permutation(64)[:max_sel][None, None].repeat(hkv, 1))
+    q = torch.randn((1, hq, d), generator=torch.Generator().manual_seed(4)).to(DEV)
+    for splits in (1, 4, 12, 40):
+        call = lambda n: sl8.attn_int8_sparse_decode(q, dc[0], ds[0], dc[1], ds[1], pages, i32([[n, n]]), num_splits=splits,  # noqa: E731
+                                                     return_lse=True)
+        want, wl = call(max_sel * page)
+        assert sl8.last_device_status()[0] == sl8.SL8_OK and torch.isfinite(wl).all()
+        for n in ((1 << 31) - 1, (1 << 31) - 40, max_sel * page + 1):
+            got, gl = call(n)
+            assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+            assert torch.equal(got, want) and torch.equal(gl, wl), (splits, n)
+
+
+def test_a_list_of_almost_2_31_tokens():
+    """2,047 times the same page of 2^20 tokens: the attention over one, its LSE above by
+    log(2047)."""
+    hq, d, page, times = 2, 32, 1 << 20, 2047
+    g = torch.Generator(device=DEV).manual_seed(7)
+    k, v = (torch.randint(-127, 128, (1, 1, page, d), generator=g, device=DEV, dtype=torch.int8) for _ in range(2))
+    ks, vs = (torch.rand((1, 1, page), generator=g, device=DEV) * 0.01 + 0.005 for _ in range(2))
+    q = torch.randn((1, hq, d), generator=g, device=DEV)
+    lists = torch.zeros((1, 1, times), dtype=torch.int32, device=DEV)
+    out, lse = sl8.attn_int8_sparse_decode(q, k, ks, v, vs, lists, i32([[times * page]]), return_lse=True)
+    one, lse1 = sl8.attn_int8_sparse_decode(q, k, ks, v, vs, lists[..., :1].contiguous(), i32([[page]]), return_lse=True)
+    # 64 splits, ten warps each: a lane adds to its sums once for every 160 tokens, each time off by
+    # at most 2^-24 of the sum so far; the values' sum runs over codes offset by 128
+    off = times * page / 64 / 160 * 2.0 ** -24
+    assert off < 0.02 and (lse - lse1 - np.log(times)).abs().max() <= 2 * off
+    vmax = float((v.float() * vs[..., None]).abs().max())
+    assert (out - one).abs().max() <= (2.0 ** -10 + 6 * off) * vmax

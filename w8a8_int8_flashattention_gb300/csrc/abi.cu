@@ -4,7 +4,9 @@
 // and enqueues.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -665,10 +667,11 @@ int sl8_attn_w8a8_qk_logits_debug(const void* q, const void* k, int qk_dtype, in
 // S = ceil(Lmax / split_size_for(Lmax, n, d)) splits; the split kernel and the combine
 // both use split_size_for(Lmax, S, d).
 static int32_t split_size_for(int32_t Lmax, int32_t S, int32_t d) {
-  const int32_t per = (Lmax + S - 1) / S;
+  // Lmax may be just below 2^31
+  const int64_t per = (static_cast<int64_t>(Lmax) + S - 1) / S;
   const int32_t chunk = decode_chunk_tokens(d);
   const int32_t step = per >= chunk ? chunk : 16;
-  return (per + step - 1) / step * step;
+  return static_cast<int32_t>(std::min<int64_t>((per + step - 1) / step * step, INT32_MAX / step * step));
 }
 
 int32_t sl8_attn_decode_num_splits(int32_t B, int32_t Hkv, int32_t Lmax, int32_t d, int32_t num_splits) {
@@ -677,14 +680,14 @@ int32_t sl8_attn_decode_num_splits(int32_t B, int32_t Hkv, int32_t Lmax, int32_t
   if (n == 0) {
     const int64_t pairs = static_cast<int64_t>(B) * Hkv;
     n = (10ll * num_sms() + pairs - 1) / pairs;
-    const int64_t chunks = (Lmax + decode_chunk_tokens(d) - 1) / decode_chunk_tokens(d);
+    const int64_t chunks = (static_cast<int64_t>(Lmax) + decode_chunk_tokens(d) - 1) / decode_chunk_tokens(d);
     if (n > chunks) n = chunks;
   }
-  const int64_t cap = (Lmax + 15) / 16;
+  const int64_t cap = (static_cast<int64_t>(Lmax) + 15) / 16;
   if (n > cap) n = cap;
   if (n < 1) n = 1;
   const int32_t ss = split_size_for(Lmax, static_cast<int32_t>(n), d);
-  return (Lmax + ss - 1) / ss;
+  return static_cast<int32_t>((static_cast<int64_t>(Lmax) + ss - 1) / ss);
 }
 
 int32_t sl8_attn_decode_split_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t d, int32_t num_splits) {
@@ -897,7 +900,7 @@ int sl8_attn_int8_decode_logits_debug(const void* q, int q_dtype, const int8_t* 
 
 // ---------------------------------------------------------------- paged cache: plan, append, bounds, selection
 // Tokens of a block table's row or of a page list: the kernels' counters step past the last
-// one by less than 256.
+// one by less than 256 (a whole stage at most), and a length plus a split's size is unsigned.
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
 
 int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,

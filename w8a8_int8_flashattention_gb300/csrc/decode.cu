@@ -162,6 +162,11 @@ __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b, DeviceStatu
   return L;
 }
 
+// Splits that L >= 0 tokens reach into; L may be just below 2^31.
+__device__ __forceinline__ int splits_of(int L, int split_size) {
+  return static_cast<int>((static_cast<uint32_t>(L) + static_cast<uint32_t>(split_size - 1)) / static_cast<uint32_t>(split_size));
+}
+
 // Lengths, tail keys (unsorted) and the prefix of the full slots; one warp.
 __device__ void sched_prefix_warp(const DecodeArgs& a, Sched* sc, DeviceStatus* st) {
   const int lane = threadIdx.x & 31;
@@ -239,7 +244,7 @@ __device__ __forceinline__ bool slot_at(const DecodeArgs& a, const Sched* sc, bo
     int L = a.seqlens[cache_seq(a, s.b)];
     L = L < 0 ? 0 : (L > a.Lmax ? a.Lmax : L);
     s.t0 = s.split * a.split_size;
-    s.t1 = min(s.t0 + a.split_size, L);
+    s.t1 = s.t0 + min(a.split_size, L - s.t0);
     return s.t0 < s.t1;
   }
   if (j < sc->n_full) {
@@ -433,8 +438,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         uint8_t* base = smem + stg * C::kStageBytes;
         // paged cache: the page of this lane's unit, read before the wait for the stage
         // so that the wait covers the load's latency
-        const int t = c0 + lane * kUnit;
         const int units = (nt + kUnit - 1) / kUnit;
+        const int t = c0 + min(lane, units - 1) * kUnit;
         int pg = 0;
         if (paged && lane < units) pg = a.block_table[static_cast<int64_t>(cur.b) * a.max_blocks + t / a.page_size];
         if (k >= kStages) ok = warp_wait(&empty[stg], ((k / kStages) - 1) & 1, limit_ns, st, 41);
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
   // an empty sequence when asked; sequences b = blockIdx.x + k * gridDim.x
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const int L = clamp_len(a, b, st, !balanced && ct == 0);
-    const int ns = (L + a.split_size - 1) / a.split_size;
+    const int ns = splits_of(L, a.split_size);
     // the rows of sequence b: its Hq heads, or (verify) those of its drafts
     const int nd = kVerify ? min(a.verify_dps, a.verify_T - (b % a.verify_ng) * a.verify_dps) : 1;
     const int n_empty = (a.num_splits - ns) * nd * a.Hq;
@@ -1097,7 +1102,7 @@ __global__ void decode_combine_kernel(const float* __restrict__ o_partial, const
 #pragma unroll
       for (int e = 0; e < E; ++e) pre[k][e] = in ? op[static_cast<int64_t>(s0 + k) * D + e] : 0.0f;
     }
-    const int ns = min(num_splits, (L + split_size - 1) / split_size);
+    const int ns = min(num_splits, splits_of(L, split_size));
     float m_new = m;
 #pragma unroll
     for (int k = 0; k < K; ++k)
