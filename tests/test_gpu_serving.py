@@ -886,3 +886,63 @@ def test_a_list_of_almost_2_31_tokens():
     assert off < 0.02 and (lse - lse1 - np.log(times)).abs().max() <= 2 * off
     vmax = float((v.float() * vs[..., None]).abs().max())
     assert (out - one).abs().max() <= (2.0 ** -10 + 6 * off) * vmax
+
+
+def _attention_tol(q, codes, scales, pages, lens, want, wlse, dtype):
+    """Per channel, from the weights w_t = p_t s_v,t of the normalised probabilities:
+    each P' is rounded to fp16, off by 2^-11 of itself or by 2^-24 of the list's largest weight;
+    a logit is three fp32 products of an exact integer (3 * 2^-24 of itself), which moves its p
+    and the sum alike; ex2.approx and the sum add 2^-20; and the fp32 sums run over V codes offset
+    by 128, in which each of a warp's additions of 16 tokens and each of the merge's 20 is off by
+    2^-22 of the 255 sum w so far."""
+    R, hq, d = q.shape
+    hkv, P = codes[0].shape[1], codes[0].shape[2]
+    eps = torch.finfo(dtype).eps / 2
+    c, sq = S._quant(q)
+    tol = np.zeros((R, hq, d))
+    for r in range(R):
+        for h in range(hkv):
+            n = int(lens[r, h])
+            if n == 0:
+                continue
+            ids = pages[r, h, :-(-n // P)]
+            rows = lambda x: x[ids, h].astype(np.float64).reshape(-1, *x.shape[3:])[:n]  # noqa: E731
+            k, v = rows(codes[0]) * rows(scales[0])[:, None], rows(codes[1])
+            for j in range(h * (hq // hkv), (h + 1) * (hq // hkv)):
+                x = k @ c[r, j].astype(np.float64) * float(sq[r, j]) / np.sqrt(d)
+                w = np.exp(x - wlse[r, j]) * rows(scales[1])
+                logit = 2 * 3 * 2.0 ** -24 * np.abs(x).max()
+                tol[r, j] = ((2.0 ** -11 + 2.0 ** -20 + logit) * (w @ np.abs(v)) + n * 2.0 ** -24 * 127 * w.max()
+                             + (n / 64 + 20) * 2.0 ** -22 * 255 * w.sum())
+    return tol * (1 + eps) + eps * np.abs(want) + 2.0 ** -25
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 3, 8, 12])
+def test_a_huge_value_row_of_no_weight(splits, d):
+    """Value rows whose scales are 2^18 and 2^60 times the others' and whose probabilities are
+    nothing: they take no bits from the other rows, wherever they stand."""
+    rng = np.random.default_rng(d * splits)
+    R, hq, hkv, page, max_sel = 5, 4, 2, 32, 40
+    num_pages = max_sel + 5
+    codes, scales, _, _ = _pool(rng, num_pages, hkv, page, d)
+    scales[0][:], scales[1][:] = 0.004, rng.random(scales[1].shape) * 0.02 + 0.01
+    pages = np.stack([np.stack([rng.permutation(num_pages - 2)[:max_sel] for _ in range(hkv)]) for _ in range(R)])
+    pages[3, :, :2] = num_pages - 2, num_pages - 1  # a list that begins with nothing else
+    lens = rng.integers(page * 30, max_sel * page + 1, (R, hkv))
+    q = rng.integers(50, 128, (R, hq, d)).astype(np.float32) / 16  # all positive
+    q[..., 0] = 127.0 / 16
+    # the first row of some pages, one in the middle, the last; keys against every query, some 60
+    # below the others' logits
+    for at, far, row in ((slice(0, -2, 9), 2.0 ** 18, 0), (slice(1, -2, 9), 2.0 ** 18, 17), (slice(2, -2, 9), 2.0 ** 60, 31),
+                         (slice(-2, None), 2.0 ** 18, slice(None))):
+        codes[0][at, :, row], scales[0][at, :, row] = -127, 0.086 / np.sqrt(d)
+        scales[1][at, :, row] *= far
+    dc, ds = ([torch.from_numpy(x).to(DEV) for x in y] for y in (codes, scales))
+    out, lse = sl8.attn_int8_sparse_decode(torch.from_numpy(q).to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens),
+                                           num_splits=splits, return_lse=True)
+    want, wlse = S.sparse_attention(q, codes[0], scales[0], codes[1], scales[1], pages, lens)
+    tol = _attention_tol(q, codes, scales, pages, lens, want, wlse, torch.float32)
+    err = np.abs(np64(out) - want)
+    assert np.all(err <= tol), (err / tol).max()
+    assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))

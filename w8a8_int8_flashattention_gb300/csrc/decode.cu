@@ -36,7 +36,8 @@
 //    rescales of the online softmax stay inside the lane.
 //  * Rescaling is lazy: the running max moves only when a tile exceeds it by more
 //    than 2^8 (p then stays below 256), and the power-of-two V range E only when a
-//    token's V scale exceeds 2^E; both keep P' inside the fp16 range.
+//    token's V scale exceeds 2^E; both keep P' inside the fp16 range.  (Over page lists E
+//    follows the largest p * s_v instead: grow_column.)
 #include <cuda_bf16.h>
 #include <atomic>
 #include <type_traits>
@@ -801,6 +802,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     float tha = -INFINITY, thb = -INFINITY;  // m + lazy headroom
     int E = -126;                            // P' carries s_v * 2^-E
     float vlim = pow2i(-126), inv = pow2i(126);
+    float inv_a = inv, inv_b = inv;          // page lists: 2^-E of each query column (grow_column)
+    if constexpr (kLists) vlim = scale_limit(inv_a, inv_b);
     float o[D / 16][4], osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
@@ -893,30 +896,36 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         const float xb0 = vBa ? d10 * kc : -INFINITY, xb1 = vBb ? d11 * kd : -INFINITY;
         const bool grow = (fmaxf(xa0, xb0) > tha) || (fmaxf(xa1, xb1) > thb) || (fmaxf(vsA, vsB) > vlim);
         if (__any_sync(0xffffffffu, grow)) {
-          const float ma = col_max(fmaxf(xa0, xb0)), mb = col_max(fmaxf(xa1, xb1));
-          const float vm = col_max(fmaxf(vsA, vsB));
           float fa = 1.0f, fb = 1.0f;
-          if (ma > tha) {
-            fa = m_a == -INFINITY ? 0.0f : ex2(m_a - ma);
-            l_a *= fa;
-            m_a = ma;
-            tha = ma + kLazy;
-          }
-          if (mb > thb) {
-            fb = m_b == -INFINITY ? 0.0f : ex2(m_b - mb);
-            l_b *= fb;
-            m_b = mb;
-            thb = mb + kLazy;
-          }
-          if (vm > vlim) {  // uniform: vm is the unit's max over all lanes
-            int e = static_cast<int>((__float_as_uint(vm) >> 23) & 0xffu) - 126;  // vm < 2^e
-            e = e > 126 ? 126 : e;
-            const float fe = pow2i(E - e);
-            fa *= fe;
-            fb *= fe;
-            E = e;
-            vlim = pow2i(e);
-            inv = pow2i(-e);
+          if constexpr (kLists) {
+            fa = grow_column(xa0, xb0, vsA, vsB, m_a, tha, l_a, inv_a);
+            fb = grow_column(xa1, xb1, vsA, vsB, m_b, thb, l_b, inv_b);
+            vlim = scale_limit(inv_a, inv_b);
+          } else {
+            const float ma = col_max(fmaxf(xa0, xb0)), mb = col_max(fmaxf(xa1, xb1));
+            const float vm = col_max(fmaxf(vsA, vsB));
+            if (ma > tha) {
+              fa = m_a == -INFINITY ? 0.0f : ex2(m_a - ma);
+              l_a *= fa;
+              m_a = ma;
+              tha = ma + kLazy;
+            }
+            if (mb > thb) {
+              fb = m_b == -INFINITY ? 0.0f : ex2(m_b - mb);
+              l_b *= fb;
+              m_b = mb;
+              thb = mb + kLazy;
+            }
+            if (vm > vlim) {  // uniform: vm is the unit's max over all lanes
+              int e = static_cast<int>((__float_as_uint(vm) >> 23) & 0xffu) - 126;  // vm < 2^e
+              e = e > 126 ? 126 : e;
+              const float fe = pow2i(E - e);
+              fa *= fe;
+              fb *= fe;
+              E = e;
+              vlim = pow2i(e);
+              inv = pow2i(-e);
+            }
           }
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
@@ -938,8 +947,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         l_b += pa1 + pb1;
         const float wA = vsA * inv, wB = vsB * inv;
         // ---- P'^T as B fragments: the fp16 S^T layout of P', each 8-row half transposed
-        const uint32_t pb0r = movm_t(f16x2_of(pa0 * wA, pa1 * wA));
-        const uint32_t pb1r = movm_t(f16x2_of(pb0 * wB, pb1 * wB));
+        const uint32_t pb0r = movm_t(kLists ? weights_f16x2(pa0, pa1, vsA, inv_a, inv_b) : f16x2_of(pa0 * wA, pa1 * wA));
+        const uint32_t pb1r = movm_t(kLists ? weights_f16x2(pb0, pb1, vsB, inv_a, inv_b) : f16x2_of(pb0 * wB, pb1 * wB));
         // ---- O'^T += V_biased^T . P'^T (V codes + 128 as fp16 subnormals), and the row
         // sums of P' from an all-ones A for the offset; fp16 V: O'^T += V^T . P'^T with the
         // A fragments read transposed from the [token][dim] tile
@@ -1028,7 +1037,7 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
       sa[4] = m_b;
       sa[5] = l_b;
     }
-    const float pe = pow2i(E);
+    const float pe = kLists ? pow2_inverse(inv_a) : pow2i(E), pe1 = kLists ? pow2_inverse(inv_b) : pe;  // 2^E of the columns
     constexpr float k2p24 = 16777216.0f;
     const float ca = -128.0f * osum[0], cb = -128.0f * osum[1];
     if constexpr (kV16) {
@@ -1052,9 +1061,9 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         dim = 128 * (j >> 3) + 16 * cg + 4 * ((j & 7) >> 1) + 2 * (j & 1);
       }
       *reinterpret_cast<float2*>(red + (cw * D + dim) * 8 + 2 * t) =
-          make_float2(fmaf(o[j][0], k2p24, ca) * pe, fmaf(o[j][1], k2p24, cb) * pe);
+          make_float2(fmaf(o[j][0], k2p24, ca) * pe, fmaf(o[j][1], k2p24, cb) * pe1);
       *reinterpret_cast<float2*>(red + (cw * D + dim + 1) * 8 + 2 * t) =
-          make_float2(fmaf(o[j][2], k2p24, ca) * pe, fmaf(o[j][3], k2p24, cb) * pe);
+          make_float2(fmaf(o[j][2], k2p24, ca) * pe, fmaf(o[j][3], k2p24, cb) * pe1);
     }
     if (cw == 0 && lane == 0) sc->merge = s;
     __syncwarp();

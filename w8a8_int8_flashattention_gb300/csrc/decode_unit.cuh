@@ -48,6 +48,57 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float pow2i(int n) {
   return n < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
 }
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// P' of one token and two query columns: (p s_v) 2^-E in this order, two at a time (s_v 2^-E alone may
+// pass fp32 where p is 0).
+__device__ __forceinline__ uint32_t weights_f16x2(float pa, float pb, float v, float inv_a, float inv_b) {
+  asm("{\n\t.reg .b64 p, f;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmul.rn.f32x2 p, p, f;\n\t"
+      "mov.b64 f, {%3, %4};\n\tmul.rn.f32x2 p, p, f;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(pa), "+f"(pb)
+      : "f"(v), "f"(inv_a), "f"(inv_b));
+  return f16x2_of(pa, pb);
+}
+// 1 / x of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+// The slow step of the online softmax over page lists, for one query column of a unit: logits xA
+// and xB (log2 units) of the lane's two tokens, whose V scales are vA and vB.  P' = p s_v 2^-E
+// goes to the MMAs in fp16, and E has to follow the weights p s_v, not the scales alone: a
+// token of no weight and a huge scale would push all other P' below fp16's normal range.  So 2^E
+// is about the largest weight, the unit's or what the earlier ones' has become under the new
+// maximum, and at most twice it: P' is off by 2^-11 of itself or by 2^-24 of that weight.  The
+// unit's comes from x plus s_v's exponent, whose maximum needs no wait for x's (where |x| passes
+// 2^20, from s_v alone).  Returns what the O' so far is multiplied with.
+__device__ __forceinline__ float grow_column(float xA, float xB, float vA, float vB, float& m, float& th, float& l,
+                                             float& inv) {  // inv = 2^-E
+  auto bounded = [](float x) { return fminf(fmaxf(x, -1048576.0f), 1048576.0f); };
+  auto with_scale = [&](float x, float v) {  // v < 2^(its exponent field - 126)
+    return bounded(x) + static_cast<float>(static_cast<int>((__float_as_uint(v) >> 23) & 0xffu) - 126);
+  };
+  const float mx = col_max(fmaxf(xA, xB)), my = col_max(fmaxf(with_scale(xA, vA), with_scale(xB, vB)));
+  float shift = 0.0f;
+  if (mx > th) {
+    shift = m - mx;
+    l *= ex2(shift);
+    m = mx;
+    th = mx + kLazy;
+  }
+  const int before = 127 - static_cast<int>(__float_as_uint(inv) >> 23);
+  const int now = __float2int_ru(my - bounded(m)) - 1;  // the weight is in [2^(now - 1), 2^(now + 1))
+  const int E = max(-126, min(126, max(now, before + __float2int_rd(fmaxf(shift, -252.0f)))));
+  inv = pow2i(-E);
+  return ex2(shift + static_cast<float>(before - E));  // at most 2
+}
+// The V scale up to which no column needs the slow step: with p <= 2^8 and s_v <= 2^7 2^E for the
+// least E of the columns, P' stays below 2^15.
+__device__ __forceinline__ float scale_limit(float inv_a, float inv_b) {
+  float inv = fmaxf(inv_a, inv_b);
+  inv = fmaxf(inv, __shfl_xor_sync(0xffffffffu, inv, 1));
+  inv = fmaxf(inv, __shfl_xor_sync(0xffffffffu, inv, 2));
+  return pow2i(min(127, 127 - static_cast<int>(__float_as_uint(inv) >> 23) + 7));
+}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -84,10 +135,6 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Quantise one q row of D values (f16/bf16/f32) held by a warp, D / 32 per lane.

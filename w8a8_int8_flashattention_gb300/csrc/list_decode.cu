@@ -17,7 +17,8 @@
 //    rows as they lie in memory (this part's int8 rate is low, 4 cycles an MMA and SM, but 4
 //    MMAs per 16 tokens at d = 128 take 16 of the 180 cycles that their bytes need);
 //    O^T[d x 8 q] += V^T P'^T as fp16 MMAs on V codes biased by 128 (P' = p * s_v * 2^-E
-//    rounded to fp16, 2^-11 relative; sums and the output accumulate in fp32).
+//    rounded to fp16, off by 2^-11 of itself or by 2^-24 of the list's largest p * s_v; E
+//    follows that weight, see grow_column; sums and the output accumulate in fp32).
 // HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
 // 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
 // 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
@@ -239,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.0f, l_b = 0.0f;
     float tha = -INFINITY, thb = -INFINITY;  // max + lazy headroom
-    int E = -126;                            // P' carries s_v * 2^-E
-    float vlim = pow2i(-126), inv = pow2i(126);
+    float inv_a = pow2i(126), inv_b = inv_a;  // P' carries s_v * 2^-E, inv = 2^-E (see grow_column)
+    float vlim = scale_limit(inv_a, inv_b);
     float o[D / 16][4], osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
@@ -280,31 +281,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         const float xb0 = vB ? d10 * (ksB * qsa) : -INFINITY, xb1 = vB ? d11 * (ksB * qsb) : -INFINITY;
         const bool grow = (fmaxf(xa0, xb0) > tha) || (fmaxf(xa1, xb1) > thb) || (fmaxf(vsA, vsB) > vlim);
         if (__any_sync(0xffffffffu, grow)) {
-          const float ma = col_max(fmaxf(xa0, xb0)), mb = col_max(fmaxf(xa1, xb1));
-          const float vm = col_max(fmaxf(vsA, vsB));
-          float fa = 1.0f, fb = 1.0f;
-          if (ma > tha) {
-            fa = m_a == -INFINITY ? 0.0f : ex2(m_a - ma);
-            l_a *= fa;
-            m_a = ma;
-            tha = ma + kLazy;
-          }
-          if (mb > thb) {
-            fb = m_b == -INFINITY ? 0.0f : ex2(m_b - mb);
-            l_b *= fb;
-            m_b = mb;
-            thb = mb + kLazy;
-          }
-          if (vm > vlim) {  // uniform: vm is the unit's max over all lanes
-            int e = static_cast<int>((__float_as_uint(vm) >> 23) & 0xffu) - 126;  // vm < 2^e
-            e = e > 126 ? 126 : e;
-            const float fe = pow2i(E - e);
-            fa *= fe;
-            fb *= fe;
-            E = e;
-            vlim = pow2i(e);
-            inv = pow2i(-e);
-          }
+          const float fa = grow_column(xa0, xb0, vsA, vsB, m_a, tha, l_a, inv_a);
+          const float fb = grow_column(xa1, xb1, vsA, vsB, m_b, thb, l_b, inv_b);
+          vlim = scale_limit(inv_a, inv_b);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             o[j][0] *= fa;
@@ -321,9 +300,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         const float pa0 = ex2(xa0 - ra), pa1 = ex2(xa1 - rb), pb0 = ex2(xb0 - ra), pb1 = ex2(xb1 - rb);
         l_a += pa0 + pb0;
         l_b += pa1 + pb1;
-        const float wA = vsA * inv, wB = vsB * inv;
-        const uint32_t pb0r = movm_t(f16x2_of(pa0 * wA, pa1 * wA));
-        const uint32_t pb1r = movm_t(f16x2_of(pb0 * wB, pb1 * wB));
+        const uint32_t pb0r = movm_t(weights_f16x2(pa0, pa1, vsA, inv_a, inv_b));
+        const uint32_t pb1r = movm_t(weights_f16x2(pb0, pb1, vsB, inv_a, inv_b));
         // ---- O'^T += V_biased^T . P'^T (V codes + 128 as fp16 subnormals), the row sums of
         // P' from an all-ones A for the offset
         auto pv = [&](float (&acc)[4], uint32_t x01, uint32_t x23) {
@@ -382,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     if (g == 0) {
       *reinterpret_cast<float4*>(stat + (warp * 8 + 2 * t) * 2) = make_float4(m_a, l_a, m_b, l_b);
     }
-    const float pe = pow2i(E);
+    const float pea = pow2_inverse(inv_a), peb = pow2_inverse(inv_b);  // 2^E
     constexpr float k2p24 = 16777216.0f;
     const float ca = -128.0f * osum[0], cb = -128.0f * osum[1];
 #pragma unroll
@@ -392,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       else if constexpr (D == 64) dim = 8 * pi + 4 * (j >> 1) + 2 * (j & 1);
       else dim = 128 * (j >> 3) + 16 * pi + 4 * ((j & 7) >> 1) + 2 * (j & 1);
       float* r = red + (warp * D + dim) * 8 + 2 * t;
-      *reinterpret_cast<float2*>(r) = make_float2(fmaf(o[j][0], k2p24, ca) * pe, fmaf(o[j][1], k2p24, cb) * pe);
-      *reinterpret_cast<float2*>(r + 8) = make_float2(fmaf(o[j][2], k2p24, ca) * pe, fmaf(o[j][3], k2p24, cb) * pe);
+      *reinterpret_cast<float2*>(r) = make_float2(fmaf(o[j][0], k2p24, ca) * pea, fmaf(o[j][1], k2p24, cb) * peb);
+      *reinterpret_cast<float2*>(r + 8) = make_float2(fmaf(o[j][2], k2p24, ca) * pea, fmaf(o[j][3], k2p24, cb) * peb);
     }
     named_bar_sync(1, kCThreads);
     if (threadIdx.x < 8 * kWarps) {  // column c: the weight of warp w's state, and (w = 0) max and sum
