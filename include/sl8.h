@@ -442,11 +442,11 @@ SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, c
  *   positions     device, [axes][T] int32 (time, height, width, ...), 1 <= axes <= 4.
  *   rot_dim       rotated channels of each head, a multiple of 8 up to d; the others pass
  *                 through.  0: no rotation (positions, inv_freq and axes are not used).
- *   inv_freq      device, [rot_dim / 2] fp32: radians per position of each pair.
+ *   inv_freq      device, [rot_dim / 2] fp32: radians per position of each pair, finite.
  *   pair_axis     HOST, [rot_dim / 2] uint8: axis of each pair (nullable when axes is 1).
  *   adjacent      0: pair p is channels (p, rot_dim / 2 + p); nonzero: (2 p, 2 p + 1).  Pair
  *                 (x, y) becomes (x cos - y sin, y cos + x sin) in fp32, the angle exact to
- *                 about 1e-6 rad at any int32 position.
+ *                 about 1e-6 rad at any int32 position (frequencies up to 1,000).
  *   q_out         device, [T][Hq][d] of dtype, tokens q_out_stride elements apart; may be q.
  *   slot_map      device, [T] int32: slot of each token; negative: the token is not stored
  *                 (its q is rotated all the same).  Slots must differ.  A slot of num_pages *

@@ -946,3 +946,34 @@ def test_a_huge_value_row_of_no_weight(splits, d):
     err = np.abs(np64(out) - want)
     assert np.all(err <= tol), (err / tol).max()
     assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_slow_and_fast_frequencies_at_far_positions(adjacent):
+    """Frequencies down to where no int32 position turns by 1e-6 rad, and up to 1,000 rad a
+    position."""
+    inv = np.array([2.0 ** -39, 2.0 ** -40, 0.999 * 2.0 ** -40, 2.0 ** -41, 1.7 * 2.0 ** -42, 2.0 ** -45, 1.3 * 2.0 ** -50,
+                    2.0 ** -60, 2.0 ** -100, 0.0, -2.0 ** -41, 1.0, -1.0, 3.7, 255.9, 1000.0], np.float32)
+    pos = np.array([(1 << 31) - 1, -(1 << 31), 1 << 30, -12345678, 0, 1, 77777777])
+    T, h, d = len(pos), 2, 32
+    x = torch.randn((T, h, d), generator=torch.Generator().manual_seed(5))
+    pages, scales = torch.zeros((2, 1, h, T, d), dtype=torch.int8, device=DEV), torch.zeros((2, 1, h, T), device=DEV)
+    out = sl8.rope_append(x.to(DEV), x.to(DEV), x.to(DEV), i32(pos), torch.from_numpy(inv).to(DEV), i32(np.arange(T)),
+                          pages[0], scales[0], pages[1], scales[1], adjacent=adjacent)
+    # the definition's angle in 64 bits is off by 2^-53 of itself: 1000 * 2^31 * 2^-53 = 2.4e-4 rad is
+    # too much, so whole turns are taken out of exact integers first
+    turns = np.array([[float(_turns(int(p), float(f))) for f in inv] for p in pos]) * 2 * np.pi
+    host = x.double().numpy()
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if adjacent else (slice(0, d // 2), slice(d // 2, d))
+    c, s = np.cos(turns)[:, None], np.sin(turns)[:, None]
+    want = np.empty_like(host)
+    want[..., a], want[..., b] = host[..., a] * c - host[..., b] * s, host[..., b] * c + host[..., a] * s
+    assert np.all(np.abs(np64(out) - want) <= _rotation_tol(host, d, adjacent) + 2.0 ** -24 * np.abs(want))
+
+
+def _turns(pos, f):
+    """pos * f / (2 pi) mod 1, from integers: 1 / (2 pi) to 200 bits."""
+    from fractions import Fraction
+    inv_2pi = Fraction(0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E4107F9458, 1 << 216)
+    x = Fraction(f) * pos * inv_2pi
+    return x - round(x)

@@ -400,10 +400,11 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, const fl
 }
 
 // Angles as fixed-point turns.  turns_of(f) is f / (2 pi) mod 1 in units of 2^-64: the
-// 24-bit mantissa of f times 2^64 / (2 pi), shifted by f's exponent (frequencies below
-// 2^-41 count as 0).  Times an int32 position, mod 2^64, the top 32 bits are the turns of
-// the position's angle to 2^-32 at any position, where a product in fp32 would lose
-// 0.06 rad at position 2^20; whole turns drop out by themselves.
+// 24-bit mantissa of f times 2^64 / (2 pi), shifted by f's exponent.  Times an int32 position,
+// mod 2^64, the top 32 bits are the turns of the position's angle at any position, where a
+// product in fp32 would lose 0.06 rad at position 2^20; whole turns drop out by themselves.
+// What g drops of f / (2 pi), less than 2^-63 turns (for f above 1, f times that), is at most
+// 2^-32 turns at position 2^31, and 2^-22 (1.5e-6 rad) at f = 1,000.
 __device__ __forceinline__ uint64_t turns_of(float f) {
   constexpr uint64_t kInv2Pi = 0x28be60db9391054aull;  // 2^64 / (2 pi)
   const uint32_t u = __float_as_uint(f);
@@ -414,6 +415,7 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   uint64_t g = 0;
   if (sh <= 0) g = sh > -64 ? lo << -sh : 0;
   else if (sh < 64) g = (hi << (64 - sh)) | (lo >> sh);
+  else if (sh < 128) g = hi >> (sh - 64);
   return (u >> 31) ? 0 - g : g;
 }
 // Cosine and sine of the angle of `pos`: sincospif takes half turns.
