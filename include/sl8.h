@@ -425,7 +425,8 @@ SL8_API int sl8_attn_decode_combine(const float* o_partial, const float* lse_par
  * A negative length, ctx_lens above max_blocks * page_size or a free_count outside [0,
  * free_capacity] is recorded (SL8_ERR_DEVICE_ARG) and the slot's request refused, the pages
  * of an ended one not released, the count clamped; pushes past free_capacity are recorded and dropped.
- * page_size * max_blocks <= 2^31 - 256 (SL8_ERR_UNSUPPORTED).
+ * A page id below 0 or with slots past 2^31 - 1, where a new token needs it, is recorded, and
+ * the token's slot is -1.  page_size * max_blocks <= 2^31 - 256 (SL8_ERR_UNSUPPORTED).
  */
 SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* release, int32_t B,
                              int32_t page_size, int32_t max_blocks, int32_t* block_table, int32_t* free_pages,

@@ -977,3 +977,21 @@ def _turns(pos, f):
     inv_2pi = Fraction(0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E4107F9458, 1 << 216)
     x = Fraction(f) * pos * inv_2pi
     return x - round(x)
+
+
+@pytest.mark.parametrize("max_tokens", [8, 20000])
+def test_paged_assign_of_pages_past_2_31_slots(max_tokens):
+    """A page id whose slots do not fit 31 bits (a pool too large, an entry that is none) is
+    recorded and its tokens get no slot, instead of another page's."""
+    last = (1 << 27) - 1  # pages of 16 tokens: the slots of this one end at 2^31 - 1
+    ids = [last, last + 1, (1 << 28) + 3, -1, (1 << 31) - 1]
+    table = i32(np.array(ids + [5])[:, None].repeat(2, 1))
+    ctx, new = [14, 3, 2, 1, 0, 15], [1, 1, 1, 1, 1, 2]
+    out = sl8.paged_assign(i32(ctx), i32(new), table, i32([(1 << 28) - 2, (1 << 31) - 7]), i32([2]), 16, max_tokens)
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    assert out["granted"].tolist() == new and out["free_count"].item() == 0
+    assert out["slot_map"][:8].tolist() == [(1 << 31) - 2, -1, -1, -1, -1, 5 * 16 + 15, -1, -1]
+    assert out["token_pos"][:8].tolist() == [14, 3, 2, 1, 0, 15, 16, 0]
+    out = sl8.paged_assign(i32([14]), i32([2]), i32([[last]]), i32([1]), i32([0]), 16, max_tokens)
+    assert sl8.last_device_status()[0] == sl8.SL8_OK
+    assert out["slot_map"][:3].tolist() == [(1 << 31) - 2, (1 << 31) - 1, -1]

@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstdint>
 
 #include "decode_unit.cuh"
 #include "sl8_internal.h"
@@ -76,15 +77,17 @@ struct PlanArgs {
   int32_t *seqlens, *granted, *cu_new, *slot_map, *token_pos;
   bool vec;  // slot_map and token_pos take 16-byte stores
   bool map;  // the plan maps the tokens too
+  uint32_t num_ids;  // page ids whose slots all stay below 2^31
 };
 
 // Slots and positions of the tokens [t0, t1) of a step's packed order, which belong to n
 // requests with cu[i] tokens before the i-th (counted from `base`): four tokens a search,
 // from a multiple of four.  length(i, p) says how many tokens request i had before the step
 // and whether it was granted; row(i) is its table row, with the new pages already entered.
+// The tokens of a page whose slots do not fit an int32 get none.
 template <typename P, typename Length, typename Row>
 __device__ __forceinline__ void map_tokens(const PlanArgs& a, int64_t base, int64_t t0, int64_t t1, uint32_t first,
-                                           uint32_t step, const P* cu, int n, Length length, Row row) {
+                                           uint32_t step, const P* cu, int n, Length length, Row row, DeviceStatus* st) {
   const uint32_t page = static_cast<uint32_t>(a.page);
   for (int64_t t4 = (t0 & ~int64_t(3)) + 4 * static_cast<int64_t>(first); t4 < t1; t4 += 4 * static_cast<int64_t>(step)) {
     int32_t slot[4], pos[4];
@@ -117,8 +120,12 @@ __device__ __forceinline__ void map_tokens(const PlanArgs& a, int64_t base, int6
             off = 0;
           }
           pg = row(i)[blk];
+          if (static_cast<uint32_t>(pg) >= a.num_ids) {
+            record_status(st, kStatusBadArg, 804);
+            pg = -1;
+          }
         }
-        slot[j] = pg * a.page + static_cast<int32_t>(off);
+        if (pg >= 0) slot[j] = pg * a.page + static_cast<int32_t>(off);
       }
       ++p;
       ++off;
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kT, 1) paged_assign_kernel(const PlanArgs a, D
             had = sm.ctx[i];
             return sm.ok[i] != 0;
           },
-          [&](int i) { return a.table + static_cast<int64_t>(b0 + i) * a.max_blocks; });
+          [&](int i) { return a.table + static_cast<int64_t>(b0 + i) * a.max_blocks; }, st);
     }
     cu0 += cu_total;
     need0 += need_total;
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kT, 1) paged_assign_kernel(const PlanArgs a, D
 
 // The slots and positions of a step with many tokens, from what the plan left: a request's
 // length before the step is its length after it less what it was granted.
-__global__ void __launch_bounds__(256) map_tokens_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(256) map_tokens_kernel(const PlanArgs a, DeviceStatus* st) {
   __shared__ int32_t held[kMapRequests];
   grid_dependency_wait();
   const bool fits = a.B <= kMapRequests;
@@ -321,8 +328,8 @@ __global__ void __launch_bounds__(256) map_tokens_kernel(const PlanArgs a) {
     return got > 0;
   };
   auto row = [&](int i) { return a.table + static_cast<int64_t>(i) * a.max_blocks; };
-  if (fits) map_tokens(a, 0, 0, t1, first, step, held, a.B, length, row);
-  else map_tokens(a, 0, 0, t1, first, step, a.cu_new, a.B, length, row);
+  if (fits) map_tokens(a, 0, 0, t1, first, step, held, a.B, length, row, st);
+  else map_tokens(a, 0, 0, t1, first, step, a.cu_new, a.B, length, row, st);
   map_padding(a, t1, first, step);
 }
 
@@ -727,7 +734,8 @@ cudaError_t launch_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens
   TraceScope tr("paged_assign", s);
   PlanArgs a{ctx_lens, new_lens, release, B, page_size, max_blocks, block_table, free_pages, free_capacity,
              free_count, free_count_out, max_tokens, seqlens, granted, cu_new, slot_map, token_pos,
-             ((reinterpret_cast<uintptr_t>(slot_map) | reinterpret_cast<uintptr_t>(token_pos)) & 15u) == 0, true};
+             ((reinterpret_cast<uintptr_t>(slot_map) | reinterpret_cast<uintptr_t>(token_pos)) & 15u) == 0, true,
+             (uint32_t(1) << 31) / static_cast<uint32_t>(page_size)};
   // a small step: one small CTA, whose barriers cost least (8 requests of one token: 5.1 us, and
   // 6.7 with a cluster), unless it may have many pages to push
   if (B <= 256 && max_tokens <= 1024 && (!release || static_cast<int64_t>(B) * max_blocks <= 16384))
@@ -738,7 +746,7 @@ cudaError_t launch_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens
   const cudaError_t e = launch_plan<1024>(a, kPlanCluster, s);
   if (a.map || e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((static_cast<int64_t>(max_tokens) + 1023) / 1024, 8ll * num_sms()));
-  return launch_pdl(map_tokens_kernel, dim3(grid), dim3(256), 0, s, a);
+  return launch_pdl(map_tokens_kernel, dim3(grid), dim3(256), 0, s, a, device_status_ptr());
 }
 
 cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
