@@ -995,3 +995,111 @@ def test_paged_assign_of_pages_past_2_31_slots(max_tokens):
     out = sl8.paged_assign(i32([14]), i32([2]), i32([[last]]), i32([1]), i32([0]), 16, max_tokens)
     assert sl8.last_device_status()[0] == sl8.SL8_OK
     assert out["slot_map"][:3].tolist() == [(1 << 31) - 2, (1 << 31) - 1, -1]
+
+
+@pytest.mark.parametrize("d,hq,hkv,splits", [(32, 2, 1, 1), (64, 4, 2, 0), (64, 8, 1, 5), (128, 4, 2, 1), (128, 8, 2, 8), (128, 2, 1, 12),
+                                            (256, 3, 1, 3), (256, 2, 1, 9)])
+def test_every_value_row_counts(d, hq, hkv, splits):
+    """Lists of some 4,096 tokens whose value rows each hold one channel, so that a row that is
+    lost, doubled or exchanged moves its channel by more than the roundings of all others."""
+    rng = np.random.default_rng(d + splits)
+    R, page, max_sel = 2, 32, 128
+    num_pages = max_sel + 6
+    codes, scales, _, _ = _pool(rng, num_pages, hkv, page, d)
+    codes[1][:] = 0
+    at = rng.integers(0, d, (num_pages, hkv, page))
+    np.put_along_axis(codes[1], at[..., None], rng.choice([-1, 1], at.shape)[..., None] * rng.integers(100, 128, at.shape)[..., None], -1)
+    scales[0][:], scales[1][:] = 0.01, rng.random(scales[1].shape) * 0.02 + 0.01
+    pages = np.stack([np.stack([rng.permutation(num_pages)[:max_sel] for _ in range(hkv)]) for _ in range(R)])
+    lens = rng.integers(page * 120, max_sel * page + 1, (R, hkv))
+    q = rng.standard_normal((R, hq, d)).astype(np.float32)
+    dc, ds = ([torch.from_numpy(x).to(DEV) for x in y] for y in (codes, scales))
+    out, lse = sl8.attn_int8_sparse_decode(torch.from_numpy(q).to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens),
+                                           num_splits=splits, return_lse=True)
+    want, wlse = S.sparse_attention(q, codes[0], scales[0], codes[1], scales[1], pages, lens)
+    tol = _attention_tol(q, codes, scales, pages, lens, want, wlse, torch.float32)
+    # what half of the rows add to their channels is above twice what the channels may be off
+    k = (codes[0][pages[0, 0], 0].astype(np.float64) * 0.01).reshape(-1, d)[:lens[0, 0]]
+    c, sq = S._quant(q[0, 0])
+    w = np.exp(k @ c.astype(np.float64) * float(sq) / np.sqrt(d) - wlse[0, 0]) * scales[1][pages[0, 0], 0].reshape(-1)[:lens[0, 0]]
+    assert np.median(w) * 100 > 2 * tol[0, 0].max()
+    assert np.all(np.abs(np64(out) - want) <= tol)
+    assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))
+
+
+@pytest.mark.parametrize("G,hkv,d,splits", [(11, 2, 128, 0), (13, 1, 64, 1), (22, 1, 32, 3), (11, 1, 256, 10), (26, 2, 128, 12)])
+def test_sparse_decode_of_heads_that_do_not_divide_by_eight(G, hkv, d, splits):
+    test_sparse_decode(3, G * hkv, hkv, d, 16, 40, splits, torch.bfloat16, torch.float32)
+
+
+def test_sparse_decode_of_many_split_lists():
+    """More lists than the split kernel sorts by length."""
+    test_sparse_decode(90, 16, 8, 64, 16, 30, 9, torch.bfloat16, torch.float32)
+
+
+@pytest.mark.parametrize("T,G,d,page,dtype,splits", [(1, 4, 64, 16, torch.float32, 0), (3, 4, 128, 32, torch.bfloat16, 0),
+                                                     (5, 2, 64, 16, torch.float16, 4), (4, 16, 32, 48, torch.float32, 0),
+                                                     (2, 1, 256, 64, torch.bfloat16, 11)])
+def test_drafts_from_selection_to_attention(T, G, d, page, dtype, splits):
+    """q [B, T, Hq, d]: the drafts' own lists as the selection returns them, into the attention,
+    with out and lse of the caller's."""
+    rng = np.random.default_rng(T * d)
+    B, hkv, nb, max_sel = 3, 2, 24, 9
+    lens = [nb * page - 3, 7 * page + T, T - 1]
+    table, num_pages = _tables(rng, lens, nb, page)
+    codes, scales, dc, ds = _pool(rng, num_pages, hkv, page, d)
+    bounds = torch.zeros((num_pages, hkv, 2, d), dtype=torch.int8, device=DEV)
+    bs = torch.zeros((num_pages, hkv), device=DEV)
+    sl8.page_bounds(dc[0], ds[0], i32(table), i32(lens), bounds, bs)
+    q = torch.randn((B, T, G * hkv, d), generator=torch.Generator().manual_seed(T)).to(dtype)
+    sel = sl8.page_select(q.to(DEV), bounds, bs, i32(table), i32(lens), page, max_sel, 1, 1)
+    out = torch.empty((B, T, G * hkv, d), dtype=torch.float32, device=DEV)
+    lse = torch.empty((B, T, G * hkv), device=DEV)
+    got = sl8.attn_int8_sparse_decode(q.to(DEV), dc[0], ds[0], dc[1], ds[1], sel["pages"], sel["lens"], num_splits=splits,
+                                      out=out, lse=lse, return_lse=True)
+    assert got[0] is out and got[1] is lse
+    # the definition, from lists of its own
+    pages, n = np.full((B * T, hkv, max_sel), -1), np.zeros((B * T, hkv), int)
+    x = q.float().numpy()
+    for b in range(B):
+        for t in range(T):
+            L = max(0, lens[b] - (T - 1 - t))
+            ids = table[b, :-(-L // page)]
+            for h in range(hkv):
+                box = [S.page_bounds(codes[0][p, h, :lens[b] - j * page], scales[0][p, h, :lens[b] - j * page]) for j, p in enumerate(ids)]
+                score = S.page_scores(x[b, t, h * G:(h + 1) * G], np.stack([y[0] for y in box]), np.stack([y[1] for y in box]),
+                                      np.array([y[2] for y in box])) if L else []
+                kept = S.select(score, max_sel, 1, 1)
+                pages[b * T + t, h, :len(kept)] = ids[kept]
+                n[b * T + t, h] = len(kept) * page - (len(ids) * page - L)  # the last page is always kept
+    assert np.array_equal(sel["pages"].cpu().numpy().reshape(pages.shape), pages)
+    assert np.array_equal(sel["lens"].cpu().numpy().reshape(n.shape), n)
+    flat = x.reshape(B * T, G * hkv, d)
+    want, wlse = S.sparse_attention(flat, codes[0], scales[0], codes[1], scales[1], pages, n)
+    tol = _attention_tol(flat, codes, scales, pages, n, want, wlse, torch.float32)
+    assert np.all(np.abs(np64(out).reshape(want.shape) - want) <= tol)
+    got, dead = np64(lse).reshape(wlse.shape), np.isinf(wlse)
+    assert np.array_equal(got == -np.inf, dead) and np.all(np64(out).reshape(want.shape)[dead] == 0)
+    assert np.all(np.abs(got[~dead] - wlse[~dead]) <= 1e-5 + 1e-6 * np.abs(wlse[~dead]))
+
+
+def test_a_contiguous_cache_from_append_to_decode():
+    """page_size = Lmax: what the append stores is what attn_int8_decode reads, against attention in
+    64 bits over the quantised rows."""
+    B, hq, hkv, d, L, cap = 3, 8, 2, 128, 50, 64
+    lens = [50, 1, 33]
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn((B * L, hkv, d), generator=g).bfloat16() for _ in range(2))
+    q = torch.randn((B, hq, d), generator=g).bfloat16()
+    kc, vc = (torch.zeros((B, hkv, cap, d), dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((B, hkv, cap), device=DEV) for _ in range(2))
+    slots = torch.cat([torch.where(torch.arange(L) < n, torch.arange(L) + cap * b, -1) for b, n in enumerate(lens)])
+    sl8.rope_append(None, k.to(DEV), v.to(DEV), None, None, i32(slots), kc, ks, vc, vs)
+    out, lse = sl8.attn_int8_decode(q.to(DEV), kc, ks, vc, vs, i32(lens), out_dtype=torch.float32, return_lse=True)
+    rows = [S._quant(x.view(B, L, hkv, d).transpose(1, 2).float().numpy()) for x in (k, v)]
+    codes, scales = [r[0] for r in rows], [r[1] for r in rows]
+    pages, n = np.arange(B)[:, None, None].repeat(hkv, 1), np.array(lens)[:, None].repeat(hkv, 1)
+    want, wlse = S.sparse_attention(q.float().numpy(), codes[0], scales[0], codes[1], scales[1], pages, n)
+    tol = _attention_tol(q.float().numpy(), codes, scales, pages, n, want, wlse, torch.float32)
+    assert np.all(np.abs(np64(out) - want) <= tol)
+    assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))
