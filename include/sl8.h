@@ -436,7 +436,9 @@ SL8_API int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, c
 
 /*
  * Rotary positions and the int8 append in one pass: rotate q and k, quantise k and v per
- * row as sl8_quant_rowwise and store them in their slots.
+ * row (s = max|x| / 127, code = round-half-even(x / s)) and store them in their slots.  The codes
+ * are those of sl8_quant_rowwise but for rows whose scale is below 2^-126: those are divided
+ * here, as the definition has it, where sl8_quant_rowwise may give them codes of +-127.
  *   q, k, v       device, [T][Hq or Hkv][d] of dtype (F16, BF16 or F32; one for all three);
  *                 a token's heads are contiguous, tokens are *_stride elements apart (a
  *                 multiple of 16 bytes: slices of a fused projection).  Hq = 0: k, v only.
@@ -536,9 +538,10 @@ SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, co
  *                sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
  *                unsupported shape; 16: none is used and it may be null); launches that run
  *                at the same time need their own.
- * Any Hq that is a multiple of Hkv (above 8 heads a group, each 8 read the list again).  A
- * page outside [0, num_pages) or a length out of range is recorded (SL8_ERR_DEVICE_ARG), and
- * page 0 read or the length clamped.
+ * Any Hq that is a multiple of Hkv.  A kv head's G = Hq / Hkv query heads are taken in the
+ * fewest equal groups of at most 8, each of which reads the list: once for G <= 8, twice for
+ * 16, but 11 times for 11.  A page outside [0, num_pages) or a length out of range is
+ * recorded (SL8_ERR_DEVICE_ARG), and page 0 read or the length clamped.
  */
 SL8_API size_t sl8_attn_int8_sparse_decode_workspace_size(int32_t rows, int32_t Hq, int32_t Hkv, int32_t max_sel,
                                                           int32_t page_size, int32_t d, int32_t num_splits);

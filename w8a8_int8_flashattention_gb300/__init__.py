@@ -538,6 +538,7 @@ def attn_int8_decode_logits_debug(q, k_cache, k_scale, v_cache, v_scale, seqlens
 # ------------------------------------------------------------------ serving from the paged cache
 
 _I32T, _F32T, _I8T = torch.int32, torch.float32, torch.int8
+_SELECT_HELD = 4096  # blocks up to which a selection needs no scores (kPageSelectHeld of the library)
 
 
 def _index(t) -> int:
@@ -764,7 +765,7 @@ def page_select(q, bounds, bound_scale, block_table, seqlens, page_size, max_sel
     o = _ptrs(dev, _I32T, "blocks pages lens", out["blocks"], out["pages"], out["lens"])
     if scores is not None:
         _shaped(scores, (B, T, hkv, max_blocks), "scores")
-    elif max_blocks > 4096:  # more than one CTA holds
+    elif max_blocks > _SELECT_HELD:
         scores = torch.empty((B, T, hkv, max_blocks), dtype=_F32T, device=q.device)
         scp = scores.data_ptr()
     _call("sl8_page_select", dev, qp, _DTYPES[q.dtype], bp, sp, num_pages, int(page_size), table, max_blocks, lens, B, T,
@@ -782,7 +783,8 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
     """Decode attention of each query over a page list of its own per kv head: q [B,Hq,d] or
     [B,T,Hq,d], pages [B(,T),Hkv,max_sel] int32 and lens [B(,T),Hkv] int32 as page_select
     returns them (or from any other policy: full pages, the last one up to the length).
-    Returns out like q (dtype q.dtype unless given) and, with return_lse, the fp32 LSE.
+    Returns out like q (dtype q.dtype unless given) and, with return_lse, the fp32 LSE: 0 and
+    -inf for an empty list, NaN where a logit is NaN (rows quantised with infinities).
     workspace: uint8, at least sparse_decode_workspace_bytes (16: none is used)."""
     dev = _index(q)
     (num_pages, hkv, page_size, d), codes, scales = _pages_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)

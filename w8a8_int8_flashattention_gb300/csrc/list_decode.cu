@@ -19,7 +19,7 @@
 //    O^T[d x 8 q] += V^T P'^T as fp16 MMAs on V codes biased by 128 (P' = p * s_v * 2^-E
 //    rounded to fp16, off by 2^-11 of itself or by 2^-24 of the list's largest p * s_v; E
 //    follows that weight, see grow_column; sums and the output accumulate in fp32).
-// HBM is the bound; the listed pages are read once per 8 query heads of a kv head.  64 rows x
+// HBM is the bound; the listed pages are read once per group of at most 8 query heads of a kv head.  64 rows x
 // 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
 // 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
 // the combine over the same lists: 152 and 14.4 us.)  At d = 64 a stage is half the bytes for
