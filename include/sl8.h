@@ -532,8 +532,8 @@ SL8_API int sl8_page_select(const void* q, int q_dtype, const int8_t* bounds, co
  *                A NaN logit (an infinite k scale with codes of 0, or such a query row, as
  *                rows with infinities are quantised) makes out and lse_out of its query NaN,
  *                an infinite v scale out alone: the definition's values.
- *                Whatever the types, each weight p * s_v is rounded to fp16 before it meets its
- *                value row: off by 2^-11 of itself, or by 2^-24 of the list's largest weight.
+ *                Each weight p * s_v is rounded before it meets its value row: off by 2^-11 of
+ *                itself (2^-22 for an fp32 out), or by 2^-24 of the list's largest weight.
  *   workspace    for more than 8 splits, at least
  *                sl8_attn_int8_sparse_decode_workspace_size() bytes (0: invalid or
  *                unsupported shape; 16: none is used and it may be null); launches that run

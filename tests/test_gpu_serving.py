@@ -1103,3 +1103,42 @@ def test_a_contiguous_cache_from_append_to_decode():
     tol = _attention_tol(q.float().numpy(), codes, scales, pages, n, want, wlse, torch.float32)
     assert np.all(np.abs(np64(out) - want) <= tol)
     assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("R,splits", [(1, 0), (4, 1), (300, 0), (2, 2), (3, 10)])
+def test_fp32_outputs_keep_more_than_fp16_of_the_weights(R, splits, d):
+    """Short lists, flat and peaked, with fp32 queries and outputs: what rounding the weights to
+    fp16 alone would leave is above the bound."""
+    rng = np.random.default_rng(d + R)
+    hq, hkv, page, max_sel = 4, 2, 16, 10
+    num_pages = 40
+    codes, scales, _, _ = _pool(rng, num_pages, hkv, page, d)
+    scales[0][:], scales[1][:] = 0.02, rng.random(scales[1].shape) * 0.02 + 0.01
+    pages = np.stack([np.stack([rng.permutation(num_pages)[:max_sel] for _ in range(hkv)]) for _ in range(R)])
+    lens = rng.integers(1, max_sel * page + 1, (R, hkv))
+    q = (rng.standard_normal((R, hq, d)) * np.array([0.05, 0.3, 1, 2])[None, :, None]).astype(np.float32)
+    dc, ds = ([torch.from_numpy(x).to(DEV) for x in y] for y in (codes, scales))
+    out, lse = sl8.attn_int8_sparse_decode(torch.from_numpy(q).to(DEV), dc[0], ds[0], dc[1], ds[1], i32(pages), i32(lens),
+                                           num_splits=splits, return_lse=True)
+    want, wlse = S.sparse_attention(q, codes[0], scales[0], codes[1], scales[1], pages, lens)
+    # as _attention_tol, but 2^-22 for the weights, and for the offset codes' sums two additions
+    # a unit of 16 tokens a warp and four for the warps
+    tol, coarse = np.zeros(want.shape), 0.0
+    c, sq = S._quant(q)
+    for r in range(R):
+        for j in range(hq):
+            h, n = j // (hq // hkv), int(lens[r, j // (hq // hkv)])
+            ids = pages[r, h, :-(-n // page)]
+            k, v = (x[ids, h].astype(np.float64).reshape(-1, d)[:n] for x in codes)
+            ks, vs = (x[ids, h].astype(np.float64).reshape(-1)[:n] for x in scales)
+            x = k @ c[r, j].astype(np.float64) * ks * float(sq[r, j]) / np.sqrt(d)
+            w = np.exp(x - wlse[r, j]) * vs
+            tol[r, j] = ((2.0 ** -22 + 2.0 ** -20 + 6 * 2.0 ** -24 * np.abs(x).max()) * (w @ np.abs(v)) + n * 2.0 ** -24 * 127 * w.max()
+                         + (2 * -(-n // 64) + 4) * 2.0 ** -22 * 255 * w.sum())
+            half = w.astype(np.float16).astype(np.float64)  # weights of some 2^-7: normal numbers of fp16
+            coarse = max(coarse, (np.abs((half - w) @ v) / tol[r, j]).max())
+    assert R == 1 or coarse > 1.5
+    err = np.abs(np64(out) - want)
+    assert np.all(err <= tol), (err / tol).max()
+    assert np.all(np.abs(np64(lse) - wlse) <= 1e-5 + 1e-6 * np.abs(wlse))

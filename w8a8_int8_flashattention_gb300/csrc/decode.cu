@@ -284,7 +284,8 @@ struct CacheMaps {
 
 // kVerify: the speculative-verify form (a.verify_T > 0), built apart so that plain decode
 // carries none of its per-column masks.  kLists: the form over page lists (a.list_heads >
-// 0), built apart for the same reason (its address arithmetic cost the paged loader 5%).
+// 0), built apart for the same reason (its address arithmetic cost the paged loader 5%).  Its
+// partial outputs are fp32, so P' has two fp16 terms there (8 lists of 65,536 tokens 49.9 -> 50.1 us).
 template <int D, bool kV16, bool kVerify, bool kLists>
 __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
     decode_split_kernel(const DecodeArgs a, const __grid_constant__ CacheMaps maps, uint32_t ticket,
@@ -947,11 +948,27 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
         l_b += pa1 + pb1;
         const float wA = vsA * inv, wB = vsB * inv;
         // ---- P'^T as B fragments: the fp16 S^T layout of P', each 8-row half transposed
-        const uint32_t pb0r = movm_t(kLists ? weights_f16x2(pa0, pa1, vsA, inv_a, inv_b) : f16x2_of(pa0 * wA, pa1 * wA));
-        const uint32_t pb1r = movm_t(kLists ? weights_f16x2(pb0, pb1, vsB, inv_a, inv_b) : f16x2_of(pb0 * wB, pb1 * wB));
+        uint32_t pb0r, pb1r, lo0 = 0, lo1 = 0;
+        if constexpr (kLists) {
+          weights_f16x2(pa0, pa1, vsA, inv_a, inv_b, pb0r, lo0);
+          weights_f16x2(pb0, pb1, vsB, inv_a, inv_b, pb1r, lo1);
+          lo0 = movm_t(lo0);
+          lo1 = movm_t(lo1);
+        } else {
+          pb0r = f16x2_of(pa0 * wA, pa1 * wA);
+          pb1r = f16x2_of(pb0 * wB, pb1 * wB);
+        }
+        pb0r = movm_t(pb0r);
+        pb1r = movm_t(pb1r);
         // ---- O'^T += V_biased^T . P'^T (V codes + 128 as fp16 subnormals), and the row
         // sums of P' from an all-ones A for the offset; fp16 V: O'^T += V^T . P'^T with the
         // A fragments read transposed from the [token][dim] tile
+        auto pv = [&](float (&acc)[4], uint32_t x01, uint32_t x23) {
+          const uint32_t a0 = prmt(x01, 0u, 0x4140), a1 = prmt(x01, 0u, 0x4342);
+          const uint32_t a2 = prmt(x23, 0u, 0x4140), a3 = prmt(x23, 0u, 0x4342);
+          mma_f16(acc, a0, a1, a2, a3, pb0r, pb1r);
+          if constexpr (kLists) mma_f16(acc, a0, a1, a2, a3, lo0, lo1);
+        };
         if constexpr (kV16) {
           const uint32_t svb = smem_u32(sv);
 #pragma unroll
@@ -967,10 +984,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
           for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint32_t*>(sv + offv[0][c]);
           const uint32_t x01 = prmt(w[0], w[1], 0x5140) ^ 0x80808080u, y01 = prmt(w[0], w[1], 0x7362) ^ 0x80808080u;
           const uint32_t x23 = prmt(w[2], w[3], 0x5140) ^ 0x80808080u, y23 = prmt(w[2], w[3], 0x7362) ^ 0x80808080u;
-          mma_f16(o[0], prmt(x01, 0u, 0x4140), prmt(x01, 0u, 0x4342), prmt(x23, 0u, 0x4140), prmt(x23, 0u, 0x4342),
-                  pb0r, pb1r);
-          mma_f16(o[1], prmt(y01, 0u, 0x4140), prmt(y01, 0u, 0x4342), prmt(y23, 0u, 0x4140), prmt(y23, 0u, 0x4342),
-                  pb0r, pb1r);
+          pv(o[0], x01, x23);
+          pv(o[1], y01, y23);
         } else if constexpr (D == 64) {
           uint2 w[4];
 #pragma unroll
@@ -981,10 +996,8 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
             const uint32_t w2 = ii ? w[2].y : w[2].x, w3 = ii ? w[3].y : w[3].x;
             const uint32_t x01 = prmt(w0, w1, 0x5140) ^ 0x80808080u, y01 = prmt(w0, w1, 0x7362) ^ 0x80808080u;
             const uint32_t x23 = prmt(w2, w3, 0x5140) ^ 0x80808080u, y23 = prmt(w2, w3, 0x7362) ^ 0x80808080u;
-            mma_f16(o[2 * ii], prmt(x01, 0u, 0x4140), prmt(x01, 0u, 0x4342), prmt(x23, 0u, 0x4140),
-                    prmt(x23, 0u, 0x4342), pb0r, pb1r);
-            mma_f16(o[2 * ii + 1], prmt(y01, 0u, 0x4140), prmt(y01, 0u, 0x4342), prmt(y23, 0u, 0x4140),
-                    prmt(y23, 0u, 0x4342), pb0r, pb1r);
+            pv(o[2 * ii], x01, x23);
+            pv(o[2 * ii + 1], y01, y23);
           }
         } else {
 #pragma unroll
@@ -1000,14 +1013,13 @@ __global__ void __launch_bounds__(DCfg<D, kV16>::kThreads, 1)
               const uint32_t w3 = ii == 0 ? w[3].x : ii == 1 ? w[3].y : ii == 2 ? w[3].z : w[3].w;
               const uint32_t x01 = prmt(w0, w1, 0x5140) ^ 0x80808080u, y01 = prmt(w0, w1, 0x7362) ^ 0x80808080u;
               const uint32_t x23 = prmt(w2, w3, 0x5140) ^ 0x80808080u, y23 = prmt(w2, w3, 0x7362) ^ 0x80808080u;
-              mma_f16(o[8 * b + 2 * ii], prmt(x01, 0u, 0x4140), prmt(x01, 0u, 0x4342), prmt(x23, 0u, 0x4140),
-                      prmt(x23, 0u, 0x4342), pb0r, pb1r);
-              mma_f16(o[8 * b + 2 * ii + 1], prmt(y01, 0u, 0x4140), prmt(y01, 0u, 0x4342),
-                      prmt(y23, 0u, 0x4140), prmt(y23, 0u, 0x4342), pb0r, pb1r);
+              pv(o[8 * b + 2 * ii], x01, x23);
+              pv(o[8 * b + 2 * ii + 1], y01, y23);
             }
           }
         }
         if constexpr (!kV16) mma_f16(osum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb0r, pb1r);
+        if constexpr (kLists) mma_f16(osum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, lo0, lo1);
       };
       if (nv >= kUnit && !(kVerify && c0 + u0 + kUnit > v_tail)) {
         unit(std::true_type{});

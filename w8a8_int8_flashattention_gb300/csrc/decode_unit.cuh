@@ -52,14 +52,18 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// P' of one token and two query columns: (p s_v) 2^-E in this order, two at a time (s_v 2^-E alone may
-// pass fp32 where p is 0).
-__device__ __forceinline__ uint32_t weights_f16x2(float pa, float pb, float v, float inv_a, float inv_b) {
+// P' of one token and two query columns as fp16 pairs, rounded, and what the rounding left:
+// (p s_v) 2^-E in this order, two at a time (s_v 2^-E alone may pass fp32 where p is 0).
+__device__ __forceinline__ void weights_f16x2(float pa, float pb, float v, float inv_a, float inv_b, uint32_t& hi,
+                                              uint32_t& lo) {
   asm("{\n\t.reg .b64 p, f;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmul.rn.f32x2 p, p, f;\n\t"
       "mov.b64 f, {%3, %4};\n\tmul.rn.f32x2 p, p, f;\n\tmov.b64 {%0, %1}, p;\n\t}"
       : "+f"(pa), "+f"(pb)
       : "f"(v), "f"(inv_a), "f"(inv_b));
-  return f16x2_of(pa, pb);
+  const __half2 h = __floats2half2_rn(pa, pb);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = f16x2_of(pa - f.x, pb - f.y);
 }
 // 1 / x of a power of two between 2^-126 and 2^126.
 __device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }

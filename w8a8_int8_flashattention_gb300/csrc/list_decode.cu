@@ -17,12 +17,13 @@
 //    rows as they lie in memory (this part's int8 rate is low, 4 cycles an MMA and SM, but 4
 //    MMAs per 16 tokens at d = 128 take 16 of the 180 cycles that their bytes need);
 //    O^T[d x 8 q] += V^T P'^T as fp16 MMAs on V codes biased by 128 (P' = p * s_v * 2^-E
-//    rounded to fp16, off by 2^-11 of itself or by 2^-24 of the list's largest p * s_v; E
-//    follows that weight, see grow_column; sums and the output accumulate in fp32).
-// HBM is the bound; the listed pages are read once per group of at most 8 query heads of a kv head.  64 rows x
-// 8 kv heads x 4,096 tokens (d = 128) take 87.5 us, 6.2 TB/s, 0.91 of the measured copy rate;
-// 32 lists of 512 tokens 6.2 us, mostly launch, prologue and merge.  (The split kernel and
-// the combine over the same lists: 152 and 14.4 us.)  At d = 64 a stage is half the bytes for
+//    rounded to fp16, off by 2^-11 of itself, 2^-22 for fp32 outputs (kFine), or by 2^-24 of the
+//    list's largest p * s_v; E follows that weight, see grow_column; sums and the output
+//    accumulate in fp32).
+// HBM is the bound; the listed pages are read once per group of at most 8 query heads of a kv
+// head.  64 rows x 8 kv heads x 4,096 tokens (d = 128) take 87.9 us, 6.2 TB/s, 0.91 of the measured
+// copy rate; 32 lists of 512 tokens 6.3 us, mostly launch, prologue and merge.  (The split kernel
+// and the combine over the same lists: 152 and 14.4 us.)  At d = 64 a stage is half the bytes for
 // the same chain of steps: 600 lists of 4,096 tokens take 61 us, 0.80 of the copy rate.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -84,7 +85,11 @@ __device__ __forceinline__ uint32_t ltile_off(int r, int c) {
   return static_cast<uint32_t>(b * (kTok * C::kBW) + r * C::kBW + 16 * (C::kSwz ? (cc ^ (r & 7)) : cc));
 }
 
-template <int D, int kCtas>
+// kFine: P' goes to the MMAs as two fp16 terms, its rounding and what that left, which keeps 22
+// bits of it; for fp32 outputs.  The second half of the P V MMAs costs an eighth of the time at
+// worst (512 lists of 4,096 tokens, d = 128: 93.1 us instead of 88.4; 256 of them with 16 query
+// heads: 92.8 instead of 82.2), and bf16 and fp16 outputs round to 8 and 11 bits themselves.
+template <int D, int kCtas, bool kFine>
 __global__ void __launch_bounds__(kThreads, kCtas)
     list_decode_kernel(const ListDecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, DeviceStatus* st, uint64_t limit_ns) {
@@ -300,15 +305,24 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         const float pa0 = ex2(xa0 - ra), pa1 = ex2(xa1 - rb), pb0 = ex2(xb0 - ra), pb1 = ex2(xb1 - rb);
         l_a += pa0 + pb0;
         l_b += pa1 + pb1;
-        const uint32_t pb0r = movm_t(weights_f16x2(pa0, pa1, vsA, inv_a, inv_b));
-        const uint32_t pb1r = movm_t(weights_f16x2(pb0, pb1, vsB, inv_a, inv_b));
+        uint32_t pb0r, pb1r, lo0, lo1;
+        weights_f16x2(pa0, pa1, vsA, inv_a, inv_b, pb0r, lo0);
+        weights_f16x2(pb0, pb1, vsB, inv_a, inv_b, pb1r, lo1);
+        pb0r = movm_t(pb0r);
+        pb1r = movm_t(pb1r);
+        if constexpr (kFine) {
+          lo0 = movm_t(lo0);
+          lo1 = movm_t(lo1);
+        }
         // ---- O'^T += V_biased^T . P'^T (V codes + 128 as fp16 subnormals), the row sums of
         // P' from an all-ones A for the offset
         auto pv = [&](float (&acc)[4], uint32_t x01, uint32_t x23) {
           x01 ^= 0x80808080u;
           x23 ^= 0x80808080u;
-          mma_f16(acc, prmt(x01, 0u, 0x4140), prmt(x01, 0u, 0x4342), prmt(x23, 0u, 0x4140), prmt(x23, 0u, 0x4342), pb0r,
-                  pb1r);
+          const uint32_t a0 = prmt(x01, 0u, 0x4140), a1 = prmt(x01, 0u, 0x4342);
+          const uint32_t a2 = prmt(x23, 0u, 0x4140), a3 = prmt(x23, 0u, 0x4342);
+          mma_f16(acc, a0, a1, a2, a3, pb0r, pb1r);
+          if constexpr (kFine) mma_f16(acc, a0, a1, a2, a3, lo0, lo1);
         };
         if constexpr (D == 32) {
           uint32_t w[4];
@@ -342,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           }
         }
         mma_f16(osum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb0r, pb1r);
+        if constexpr (kFine) mma_f16(osum, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, lo0, lo1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stg]);
@@ -458,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   cluster.sync();  // no CTA leaves while another reads its part
 }
 
-template <int D, int kCtas>
-cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
+template <int D, int kCtas, bool kFine>
+cudaError_t launch_list_f(const ListDecodeArgs& a, cudaStream_t s) {
   using C = LCfg<D, kCtas>;
-  auto kern = list_decode_kernel<D, kCtas>;
+  auto kern = list_decode_kernel<D, kCtas, kFine>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
   bool ok = true;
@@ -483,6 +498,11 @@ cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a, km, vm, device_status_ptr(), spin_limit_ns());
+}
+
+template <int D, int kCtas>
+cudaError_t launch_list_d(const ListDecodeArgs& a, cudaStream_t s) {
+  return a.out_dtype == SL8_F32 ? launch_list_f<D, kCtas, true>(a, s) : launch_list_f<D, kCtas, false>(a, s);
 }
 
 }  // namespace
