@@ -553,6 +553,55 @@ SL8_API int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t
                                         size_t workspace_bytes, void* stream);
 
 /*
+ * ---- The paged cache in 4 bits ("Engine" table, "Paged KV cache" row; "Attention kernels" table,
+ * attn_decode's int4 V variant; the pages name 4-bit values and give no layout: a reading).
+ * A row (one token, one kv head) of d channels is cut into groups of 32 consecutive channels,
+ * each with a bf16 scale s = bf16(max|x| / 7) (fp32 division) and codes c = the integer nearest to x / s,
+ * ties to even, within +-7.  It is held as
+ *   k_pages, v_pages              [num_pages][Hkv][page_size][d / 2] bytes: c + 8 of channel 2 i in
+ *                                 the low half of byte i, of channel 2 i + 1 in its high half;
+ *   k_scale_pages, v_scale_pages  [num_pages][Hkv][page_size][d / 32] bf16;
+ * 18 bytes for 32 values.  A half of 0 (which no append writes) is the code -8.  A group with an
+ * infinity has the scale inf and codes 0, which stand for NaN; a NaN has the code 0.  Scales below
+ * 2^-126 hold fewer than 8 bits, and codes stay within +-7 all the same.  All four
+ * arrays are 16-byte aligned.  Slots, block tables and the page plan are those of the int8 pages.
+ *
+ * Rotary positions and the 4-bit append: sl8_rope_append (all of its arguments, checks and
+ * guarantees) with these pages, and
+ *   k_mean        device, nullable, [Hkv][d] fp32, 16-byte aligned: offsets taken off the rotated
+ *                 k (fp32) before it is quantised, as K-smoothing does with the channel means.  A
+ *                 softmax does not see an offset that all keys share; the pages hold k - k_mean.
+ */
+SL8_API int sl8_rope_append_int4(const void* q, const void* k, const void* v, int dtype, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                                 const int32_t* positions, int32_t axes, int32_t rot_dim, const float* inv_freq,
+                                 const uint8_t* pair_axis, int adjacent, void* q_out, int64_t q_out_stride,
+                                 const int32_t* slot_map, const float* k_mean, uint8_t* k_pages, void* k_scale_pages,
+                                 uint8_t* v_pages, void* v_scale_pages, int32_t num_pages, int32_t page_size,
+                                 void* stream);
+
+/*
+ * The first seqlens[b] tokens of each sequence as dense keys and values (code * s, + k_mean; rounded
+ * once to out_dtype), for a prefill that continues from them.
+ *   block_table   device, [B][max_blocks] int32; seqlens device, [B] int32.
+ *   cu_seqlens    device, nullable.  NULL: k_out, v_out are [B][Hkv][N][d] and every length is
+ *                 at most N.  Else [B + 1] int32, and they are [total_tokens][Hkv][d]: token i of
+ *                 sequence b is row cu_seqlens[b] + i, and its tokens fit before cu_seqlens[b + 1]
+ *                 (which may leave room for more); N is a host bound of the lengths.
+ *   k_mean        as in the append, nullable: added to the keys.
+ *   k_out, v_out  device, of out_dtype (F16, BF16 or F32), 16-byte aligned; either may be NULL.
+ * Rows past a sequence's tokens are left as they were.  A length or a row out of range is recorded
+ * (SL8_ERR_DEVICE_ARG) and the length cut; a page out of range is recorded and read as page 0.
+ * Any page_size; page_size * max_blocks <= 2^31 - 256.
+ */
+SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_pages, const uint8_t* v_pages,
+                                const void* v_scale_pages, int32_t num_pages, int32_t page_size,
+                                const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
+                                const int32_t* cu_seqlens, int32_t B, int32_t Hkv, int32_t N, int32_t d,
+                                int64_t total_tokens, const float* k_mean, void* k_out, void* v_out, int out_dtype,
+                                void* stream);
+
+/*
  * Debug view of the decode's q quantisation and int32 logits (same kernel as the
  * split call, with num_splits automatic: o_partial/lse_partial sized for
  * S = sl8_attn_decode_num_splits(B, Hkv, Lmax, d, 0)).

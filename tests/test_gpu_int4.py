@@ -1,0 +1,282 @@
+"""The paged 4-bit cache on the GPU, against its CPU definitions: the rotary append, reading it back
+and decode attention over its pages, alone and as one serving step.
+
+Tolerances.  Codes and scales of rows that do not turn are fixed bit for bit.  Rotations are within
+2e-6 of a pair's length (the append's bound, as for the int8 pages), so a scale is a bf16 rounding
+of something that near, and a stored value within half a step of it.  Values read back take one fma
+and one rounding to their type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_flashattention_gb300 as sl8
+from oracle import int4 as Q
+from oracle import serving as S
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from w8a8_int8_flashattention_gb300 import build
+    build.build()
+    sl8.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    st, site = sl8.last_device_status()
+    assert st == sl8.SL8_OK, (st, site)
+
+
+def i32(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device=DEV)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def f32(t):
+    return t.detach().float().cpu().numpy()
+
+
+def _pool(num_pages, hkv, page, d, fill=True):
+    """k_pages, k_scale_pages, v_pages, v_scale_pages; filled with bytes that no test writes."""
+    p = sl8.int4_pages(num_pages, hkv, page, d, DEV)
+    if fill:
+        p[0].fill_(0x5a), p[2].fill_(0x5a), p[1].fill_(-7.0), p[3].fill_(-7.0)
+    return p
+
+
+# ------------------------------------------------------------------ rotary append
+
+def _pair_length(x, rot, adjacent):
+    """Each rotated channel's pair length; 0 for the others."""
+    t = np.zeros_like(x)
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if adjacent else (slice(0, rot // 2), slice(rot // 2, rot))
+    t[..., a] = t[..., b] = np.hypot(x[..., a], x[..., b])
+    return t
+
+
+def _check_keys(codes, scales, want, tol, tag=""):
+    """Stored rows [n, d] against exact keys that the kernel knows to within tol."""
+    lo = np.maximum(np.abs(want) - tol, 0).reshape(*want.shape[:-1], -1, 32).max(-1)
+    hi = (np.abs(want) + tol).reshape(*want.shape[:-1], -1, 32).max(-1)
+    # two roundings to fp32 (the maximum, the division) before the one to bf16
+    assert np.all(Q.to_bf16((lo / 7 * (1 - 2.0 ** -22)).astype(np.float32)) <= scales), tag
+    assert np.all(scales <= Q.to_bf16((hi / 7 * (1 + 2.0 ** -22)).astype(np.float32))), tag
+    step = np.repeat(scales.astype(np.float64), 32, -1)
+    assert np.abs(codes).max() <= 7
+    assert np.all(np.abs(codes * step - want) <= step * 0.5 + tol), tag
+
+
+@pytest.mark.parametrize("d,rot,axes,adjacent,hq,hkv,dtype,T,page,mean", [
+    (128, 128, 1, False, 32, 8, torch.bfloat16, 1, 16, False), (128, 96, 3, False, 5, 1, torch.float16, 37, 16, True),
+    (64, 64, 1, True, 7, 3, torch.bfloat16, 130, 7, True), (32, 8, 2, False, 3, 3, torch.float32, 65, 32, False),
+    (256, 256, 4, True, 2, 2, torch.float32, 9, 16, True), (256, 64, 1, False, 16, 8, torch.float16, 700, 64, False),
+    (256, 256, 1, False, 2, 1, torch.bfloat16, 33, 16, False), (256, 208, 2, False, 2, 3, torch.float32, 33, 16, True),
+    (64, 56, 1, False, 1, 5, torch.float32, 40, 16, False), (64, 24, 1, False, 2, 2, torch.bfloat16, 40, 16, True),
+    (32, 32, 1, False, 4, 9, torch.float32, 21, 5, True), (32, 32, 1, True, 1, 1, torch.float16, 2000, 1000, False),
+    (64, 0, 0, False, 2, 2, torch.bfloat16, 20, 16, False), (128, 128, 1, False, 0, 2, torch.bfloat16, 20, 16, True)])
+def test_rope_append(d, rot, axes, adjacent, hq, hkv, dtype, T, page, mean):
+    g = torch.Generator().manual_seed(T + d)
+    rng = np.random.default_rng(T)
+    qkv = torch.randn((T, (hq + 2 * hkv) * d + 16), generator=g).to(dtype)
+    qkv[T // 2, -1 - 16 - d:-16] = 0  # part of a row of zeros
+    qkv[:, hq * d:(hq + 1) * d] *= 30
+    dq = qkv.to(DEV)
+    view = lambda x, a, n: x[:, a * d:(a + n) * d].unflatten(1, (n, d)) if n else None  # noqa: E731
+    q, k, v = view(dq, 0, hq), view(dq, hq, hkv), view(dq, hq + hkv, hkv)
+    pos = rng.integers(0, 1 << 20, (max(axes, 1), T))
+    pos[:, -1] = (1 << 31) - 1 - np.arange(max(axes, 1))
+    pos[:, 0] = -5 if T > 1 else 3
+    inv = (10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))).astype(np.float32)
+    axis = rng.integers(0, max(axes, 1), rot // 2).tolist()
+    num_pages = -(-T // page) + 1
+    slots = rng.permutation(num_pages * page)[:T]
+    if T > 4:
+        slots[[1, 3]] = -1
+    off = rng.standard_normal((hkv, d)).astype(np.float32) * 2 if mean else np.zeros((hkv, d), np.float32)
+    pool = _pool(num_pages, hkv, page, d)
+    out = sl8.rope_append_int4(q, k, v, i32(pos if axes > 1 else pos[0]) if rot else None,
+                               torch.from_numpy(inv).to(DEV) if rot else None, i32(slots), *pool,
+                               pair_axis=axis if axes > 1 else None, adjacent=adjacent,
+                               k_mean=torch.from_numpy(off).to(DEV) if mean else None)
+    host = qkv.double().numpy()
+    eps = torch.finfo(dtype).eps / 2
+    used = axis if axes > 1 else None
+    if hq:
+        x = host[:, :hq * d].reshape(T, hq, d)
+        want = S.rope(x, pos, inv, used, adjacent)
+        # a value rounds from within the rotation's error; tiny fp16 results round to 2^-25
+        assert np.all(np.abs(np64(out) - want) <= 2e-6 * _pair_length(x, rot, adjacent) * (1 + eps) + eps * np.abs(want) + 2.0 ** -25)
+    kx = host[:, hq * d:(hq + hkv) * d].reshape(T, hkv, d)
+    turned = S.rope(kx, pos, inv, used, adjacent)
+    tol = 2e-6 * _pair_length(kx, rot, adjacent) + (2.0 ** -24 * (np.abs(turned) + np.abs(off)) if mean else 0.0)
+    want = turned - off
+    vc, vs = Q.quant4(host[:, (hq + hkv) * d:(hq + 2 * hkv) * d].reshape(T, hkv, d).astype(np.float32))
+    gk, gv = (Q.unpack(pool[i].cpu().numpy()) for i in (0, 2))
+    ks, gs = f32(pool[1]), f32(pool[3])
+    touched = np.zeros((num_pages, page), bool)
+    for t in range(T):
+        if slots[t] < 0:
+            continue
+        at = slots[t] // page, slice(None), slots[t] % page
+        touched[at[0], at[2]] = True
+        np.testing.assert_array_equal(gv[at], vc[t])
+        np.testing.assert_array_equal(gs[at], vs[t])
+        _check_keys(gk[at], ks[at], want[t], tol[t], t)
+    # rows without a slot stay as they were
+    for x, was in zip(pool, (0x5a, -7.0, 0x5a, -7.0)):
+        assert bool((x.transpose(1, 2)[torch.from_numpy(~touched).to(DEV)] == was).all())
+
+
+def test_stored_rows_are_the_definitions():
+    """The bits of the definition on values that sit on rounding borders, on tiny and huge rows and
+    groups; a group with an infinity gets the scale inf and codes 0, a NaN the code 0."""
+    g = torch.Generator().manual_seed(9)
+    T, hkv, d = 512, 4, 64
+    v = torch.randn((T, hkv, d), generator=g)
+    v[0:64] = torch.randint(-14, 15, (64, hkv, d), generator=g).float() / 2  # halves of a step of 1
+    v[0:64, :, 0] = v[0:64, :, 40] = 7.0
+    v[64:128] *= torch.logspace(-44, 37, 64)[:, None, None]
+    v[128:192] = torch.randint(-14, 15, (64, hkv, d), generator=g).float() / 2 * (1 + 2.0 ** -23)
+    v[128:192, :, 1] = v[128:192, :, 33] = -7.0
+    v[192, :, 3], v[193, :, 3], v[194, :, 3] = float("inf"), float("-inf"), float("nan")
+    v[195, :, 3], v[195, :, 9] = float("nan"), float("inf")
+    v[196] = float("nan")
+    v[197] = 0
+    v[198:262, :, :32] *= torch.logspace(-38, 30, 64)[:, None, None]  # groups of one row far apart
+    v[262:290] = torch.randn((28, hkv, d), generator=g) * (2.0 ** -torch.arange(120.0, 148.0))[:, None, None]
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        x = v.to(dtype).to(DEV)
+        pool = _pool(1, hkv, T, d)
+        sl8.rope_append_int4(None, x, x, None, None, i32(np.arange(T)), *pool)
+        want, s = Q.quant4(x.float().cpu().numpy())
+        for i in (0, 2):
+            np.testing.assert_array_equal(Q.unpack(pool[i][0].transpose(0, 1).cpu().numpy()), want)
+            np.testing.assert_array_equal(f32(pool[i + 1][0].transpose(0, 1)), s)
+
+
+def test_append_in_place_and_a_bad_slot():
+    T, hq, hkv, d = 6, 4, 2, 64
+    qkv = torch.randn((T, (hq + 2 * hkv) * d), device=DEV).half()
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hkv * d, hkv * d], 1))
+    pos, inv = torch.arange(T, dtype=torch.int32, device=DEV), torch.rand(d // 2, device=DEV)
+    pool = sl8.int4_pages(2, hkv, 4, d, DEV)
+    want = sl8.rope_append_int4(q, k, v, pos, inv, i32([0, 1, 2, 8, -3, 5]), *pool)  # slot 8 lies past the two pages
+    assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+    kept = k.clone()
+    got = sl8.rope_append_int4(q, k, v, pos, inv, i32([0, 1, 2, -1, -3, 5]), *pool, q_out=q)
+    assert got.data_ptr() == qkv.data_ptr() and torch.equal(got, want) and torch.equal(k, kept)
+    assert int((pool[1][..., 0] != 0).sum()) == 4 * hkv
+    # both appends turn q alike
+    codes, scales = torch.zeros((2, 2, hkv, 4, d), dtype=torch.int8, device=DEV), torch.zeros((2, 2, hkv, 4), device=DEV)
+    q8 = torch.randn((T, hq, d), device=DEV)
+    a = sl8.rope_append(q8, k.float(), v.float(), pos, inv, i32([0, 1, 2, -1, -3, 5]), codes[0], scales[0], codes[1], scales[1])
+    b = sl8.rope_append_int4(q8, k.float(), v.float(), pos, inv, i32([0, 1, 2, -1, -3, 5]), *pool)
+    assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ reading back
+
+def _filled(rng, num_pages, hkv, page, d, spread=1.0):
+    """A pool of random codes (-8 among them) and scales up to `spread` powers of ten apart."""
+    pool = _pool(num_pages, hkv, page, d)
+    host = []
+    for i in (0, 2):
+        c = rng.integers(0, 256, tuple(pool[i].shape)).astype(np.uint8)
+        s = Q.to_bf16((10.0 ** rng.uniform(-spread, 0, tuple(pool[i + 1].shape))).astype(np.float32))
+        pool[i].copy_(torch.from_numpy(c))
+        pool[i + 1].copy_(torch.from_numpy(s))
+        host += [c, s]
+    return pool, host
+
+
+def _tables(rng, lens, nb, page, num_pages):
+    """Block tables of distinct pages; entries past a sequence's last block name no page."""
+    perm, tables, at = rng.permutation(num_pages), np.full((len(lens), nb), -9), 0
+    for b, n in enumerate(lens):
+        k = -(-n // page)
+        tables[b, :k] = perm[at:at + k]
+        at += k
+    return tables
+
+
+@pytest.mark.parametrize("d,hkv,page,lens,dtype,mean", [
+    (32, 1, 16, [1], torch.float32, False), (64, 3, 7, [50, 0, 13, 64], torch.float16, True),
+    (128, 2, 64, [130, 1, 65], torch.bfloat16, True), (256, 8, 16, [33, 70], torch.float32, True),
+    (128, 1, 300, [299, 300, 301], torch.bfloat16, False), (256, 2, 1, [5, 3], torch.float16, False)])
+def test_read(d, hkv, page, lens, dtype, mean):
+    rng = np.random.default_rng(d + page)
+    B, nb = len(lens), -(-max(lens) // page) + 1
+    num_pages = sum(-(-n // page) for n in lens) + 2
+    pool, (kc, ks, vc, vs) = _filled(rng, num_pages, hkv, page, d)
+    tables = _tables(rng, lens, nb, page, num_pages)
+    off = rng.standard_normal((hkv, d)).astype(np.float32) if mean else np.zeros((hkv, d), np.float32)
+    km = torch.from_numpy(off).to(DEV) if mean else None
+    N = max(lens) + 3
+    ko, vo = (torch.full((B, hkv, N, d), 5.0, dtype=dtype, device=DEV) for _ in range(2))
+    got = sl8.paged_read_int4(*pool, i32(tables), i32(lens), max_seqlen=N, k_mean=km, k_out=ko, v_out=vo)
+    assert got[0] is ko and got[1] is vo
+    room = 4
+    cu = np.concatenate([[0], np.cumsum(np.array(lens) + room)])
+    pk, pv = sl8.paged_read_int4(*pool, i32(tables), i32(lens), cu_seqlens=i32(cu), max_seqlen=N, total_tokens=int(cu[-1]) + 2,
+                                 k_mean=km, out_dtype=dtype)
+    eps = torch.finfo(dtype).eps / 2
+    for b, n in enumerate(lens):
+        for dense, packed, c, s, o in ((ko, pk, kc, ks, off), (vo, pv, vc, vs, np.zeros_like(off))):
+            want = Q.values(Q.gather(c, tables[b], n), Q.gather(s, tables[b], n)) + o[:, None]
+            # the fma's rounding to fp32, then the type's; fp16 below 2^-14 rounds to 2^-25
+            tol = np.abs(want) * (2.0 ** -24 * (1 + eps) + eps) + (2.0 ** -25 if dtype == torch.float16 else 0)
+            assert np.all(np.abs(np64(dense[b, :, :n]) - want) <= tol), b
+            assert bool((dense[b, :, n:] == 5.0).all())
+            rows = packed[cu[b]:cu[b + 1]].transpose(0, 1)
+            assert torch.equal(rows[:, :n], dense[b, :, :n]) and bool((rows[:, n:] == 0).all())
+    # without a length bound the table's width counts
+    wide, _ = sl8.paged_read_int4(*pool, i32(tables), i32(lens), k_mean=km, out_dtype=dtype)
+    assert wide.shape == (B, hkv, nb * page, d) and torch.equal(wide[:, :, :min(N, nb * page)][:, :, :max(lens)][0, :, :lens[0]], ko[0, :, :lens[0]])
+
+
+def test_read_reports_what_is_out_of_range():
+    rng = np.random.default_rng(1)
+    pool, (kc, ks, _, _) = _filled(rng, 4, 1, 16, 32)
+    bad = lambda: sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG  # noqa: E731
+    out = lambda n: torch.full((1, 1, n, 32), 9.0, device=DEV)  # noqa: E731
+    table = i32([[2, 1]])
+    for n, N, rows in ((-1, 20, 0), (33, 40, 32), (25, 20, 20)):
+        k, v = out(N), out(N)
+        sl8.paged_read_int4(*pool, table, i32([n]), max_seqlen=N, k_out=k, v_out=v)
+        assert bad()
+        assert bool((k[:, :, rows:] == 9).all())
+        np.testing.assert_array_equal(f32(k[0, :, :rows]), Q.values(Q.gather(kc, [2, 1], rows), Q.gather(ks, [2, 1], rows)).astype(np.float32))
+    for page in (-1, 4):  # read as page 0
+        k, _ = sl8.paged_read_int4(*pool, i32([[2, page]]), i32([20]), out_dtype=torch.float32)
+        assert bad()
+        np.testing.assert_array_equal(f32(k[0, :, 16:20]), Q.values(kc[0, :, :4], ks[0, :, :4]).astype(np.float32))
+    for cu, rows in (([0, 10], 10), ([3, 30], 9), ([-1, 30], 0), ([0, -5], 0), ([12, 30], 0)):
+        k, v = (torch.full((12, 1, 32), 9.0, device=DEV) for _ in range(2))
+        sl8.paged_read_int4(*pool, table, i32([20]), cu_seqlens=i32(cu), max_seqlen=32, k_out=k, v_out=v)
+        assert bad(), cu
+        first = max(cu[0], 0)
+        assert bool((k[:first] == 9).all()) and bool((k[first + rows:] == 9).all()), cu
+        np.testing.assert_array_equal(f32(k[first:first + rows, 0]), Q.values(Q.gather(kc, [2, 1], rows), Q.gather(ks, [2, 1], rows))[0].astype(np.float32))
+
+
+def test_read_of_infinite_groups_and_what_was_appended():
+    T, hkv, d = 20, 2, 64
+    x = torch.randn((T, hkv, d), device=DEV)
+    x[3, 0, 5], x[4, 1, 40] = float("inf"), float("nan")
+    pool = sl8.int4_pages(2, hkv, 16, d, DEV)
+    sl8.rope_append_int4(None, x, x, None, None, i32(np.arange(T)), *pool)
+    k, v = sl8.paged_read_int4(*pool, i32([[0, 1]]), i32([T]), max_seqlen=T, out_dtype=torch.float32)
+    assert torch.equal(torch.isnan(k[0, 0, 3]), torch.arange(d, device=DEV) < 32) and k[0, 1, 4, 40] == 0
+    ok = torch.isfinite(k[0].transpose(0, 1)) & torch.isfinite(x)
+    step = x.unflatten(-1, (-1, 32)).nan_to_num(0.0, 0.0, 0.0).abs().amax(-1, keepdim=True).expand(-1, -1, -1, 32).flatten(-2) / 7 * (1 + 2.0 ** -8)
+    assert bool(((k[0].transpose(0, 1) - x).abs() <= step * 0.5)[ok].all()) and torch.equal(k.nan_to_num(), v.nan_to_num())

@@ -107,6 +107,10 @@ _SIGNATURES = {
     "sl8_attn_int8_sparse_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
     "sl8_attn_int8_sparse_decode": (_INT, [_P, _INT, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                            _I32, _P, _INT, _P, _P, _SZ, _P]),
+    "sl8_rope_append_int4": (_INT, [_P, _P, _P, _INT, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32, _P,
+                                    ctypes.c_char_p, _INT, _P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I32, _P]),
+    "sl8_paged_read_int4": (_INT, [_P, _P, _P, _P, _I32, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I64, _P, _P, _P,
+                                   _INT, _P]),
     "sl8_last_device_status": (_INT, [_P, ctypes.POINTER(_INT)]),
     "sl8_set_spin_limit_ns": (None, [_U64]),
     "sl8_get_spin_limit_ns": (_U64, []),
@@ -671,6 +675,12 @@ def rope_append(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, 
     which may be q itself)."""
     dev = _index(k_pages)
     (num_pages, hkv, page_size, d), codes, scales = _pages_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    return _append("sl8_rope_append", dev, hkv, d, q, k, v, positions, inv_freq, slot_map, pair_axis, adjacent, q_out,
+                   (codes[0], scales[0], codes[1], scales[1], num_pages, page_size))
+
+
+def _append(fn, dev, hkv, d, q, k, v, positions, inv_freq, slot_map, pair_axis, adjacent, q_out, pages):
+    """The appends' checks and call; pages: the arguments after slot_map."""
     pos, slots = _ptrs(dev, _I32T, "positions slot_map", positions, slot_map)
     freq, = _ptrs(dev, _F32T, "inv_freq", inv_freq)
     T, dtype = k.shape[0], k.dtype
@@ -700,9 +710,8 @@ def rope_append(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, 
             raise ValueError("pair_axis needs one entry per rotary pair")
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
-    _call("sl8_rope_append", dev, qp, kp, vp, _DTYPES[dtype], q_stride, k_stride, v_stride, T, hq, hkv, d, pos, axes, rot,
-          freq, pair_axis, 1 if adjacent else 0, op, out_stride, slots, codes[0], scales[0], codes[1], scales[1],
-          num_pages, page_size)
+    _call(fn, dev, qp, kp, vp, _DTYPES[dtype], q_stride, k_stride, v_stride, T, hq, hkv, d, pos, axes, rot, freq,
+          pair_axis, 1 if adjacent else 0, op, out_stride, slots, *pages)
     return q_out
 
 
@@ -819,6 +828,94 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
     _call("sl8_attn_int8_sparse_decode", dev, qp, _DTYPES[q.dtype], codes[0], scales[0], codes[1], scales[1], num_pages,
           page_size, list_p, lens_p, max_sel, rows, hq, hkv, d, num_splits, op, _DTYPES[out.dtype], lse_p, ws, nbytes)
     return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ the paged cache in 4 bits
+
+_U8T, _BF16T = torch.uint8, torch.bfloat16
+
+
+def _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages):
+    """((num_pages, Hkv, page_size, d), code addresses, scale addresses) of 4-bit pages."""
+    c = _ptrs(dev, _U8T, "k_pages v_pages", k_pages, v_pages)
+    s = _ptrs(dev, _BF16T, "k_scale_pages v_scale_pages", k_scale_pages, v_scale_pages)
+    shape = k_pages.shape
+    if len(shape) != 4:
+        raise ValueError("4-bit pages must be [num_pages, Hkv, page_size, d / 2]")
+    num_pages, hkv, page_size, half = shape
+    _shaped(v_pages, shape, "v_pages")
+    rows = (num_pages, hkv, page_size, half // 16)
+    _shaped(k_scale_pages, rows, "k_scale_pages")
+    _shaped(v_scale_pages, rows, "v_scale_pages")
+    return (num_pages, hkv, page_size, 2 * half), c, s
+
+
+def _mean_of(dev, k_mean, hkv, d):
+    if k_mean is None:
+        return None
+    _shaped(k_mean, (hkv, d), "k_mean")
+    return _ptrs(dev, _F32T, "k_mean", k_mean)[0]
+
+
+def int4_pages(num_pages, Hkv, page_size, d, device=None):
+    """An empty 4-bit pool (zeros): k_pages, k_scale_pages, v_pages, v_scale_pages."""
+    def codes():
+        return torch.full((num_pages, Hkv, page_size, d // 2), 0x88, dtype=_U8T, device=device or "cuda")
+
+    def scales():
+        return torch.zeros((num_pages, Hkv, page_size, d // 32), dtype=_BF16T, device=device or "cuda")
+
+    return codes(), scales(), codes(), scales()
+
+
+def rope_append_int4(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pages, v_pages, v_scale_pages,
+                     pair_axis=None, adjacent=False, q_out=None, k_mean=None):
+    """rope_append to 4-bit pages: codes [num_pages,Hkv,page_size,d/2] uint8 (channel 2i in the low
+    half of byte i) with a bf16 scale for each group of 32 channels [num_pages,Hkv,page_size,d/32].
+    k_mean fp32 [Hkv,d] is taken off the rotated keys before they are quantised.  The rest, and what
+    is returned, as rope_append."""
+    dev = _index(k_pages)
+    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    return _append("sl8_rope_append_int4", dev, hkv, d, q, k, v, positions, inv_freq, slot_map, pair_axis, adjacent, q_out,
+                   (_mean_of(dev, k_mean, hkv, d), codes[0], scales[0], codes[1], scales[1], num_pages, page_size))
+
+
+def paged_read_int4(k_pages, k_scale_pages, v_pages, v_scale_pages, block_table, seqlens, cu_seqlens=None,
+                    max_seqlen=None, total_tokens=None, k_mean=None, out_dtype=None, k_out=None, v_out=None):
+    """The first seqlens [B] int32 tokens of each sequence as dense keys and values: [B,Hkv,N,d] with
+    N = max_seqlen (default: block_table's width in tokens), as attn_int8_fwd_chunk takes them; or,
+    with cu_seqlens [B + 1] int32, packed [total_tokens,Hkv,d], token i of sequence b at row
+    cu_seqlens[b] + i.  k_mean: as in the append, added to the keys.  Rows past a sequence's tokens are
+    left as they were (zeros where the outputs, of out_dtype, default bfloat16, are made here).
+    Returns (k_out, v_out)."""
+    dev = _index(k_pages)
+    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    table, lens, cu = _ptrs(dev, _I32T, "block_table seqlens cu_seqlens", block_table, seqlens, cu_seqlens)
+    B, max_blocks = block_table.shape
+    if seqlens.numel() != B or (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
+        raise ValueError("seqlens and cu_seqlens need one entry per row of block_table (and one more)")
+    N = max_blocks * page_size if max_seqlen is None else int(max_seqlen)
+    given = k_out if k_out is not None else v_out
+    if cu_seqlens is None:
+        total, shape = 0, (B, hkv, N, d)
+    else:
+        if total_tokens is None and given is None:
+            raise ValueError("a packed read needs total_tokens or an output")
+        total = int(total_tokens) if total_tokens is not None else given.shape[0]
+        shape = (total, hkv, d)
+    dtype = given.dtype if given is not None else (out_dtype or _BF16T)
+    if dtype not in _DTYPES or (out_dtype is not None and out_dtype is not dtype):
+        raise TypeError(f"unsupported dtype {dtype}")
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=dtype, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.zeros(shape, dtype=dtype, device=k_pages.device)
+    _shaped(k_out, shape, "k_out")
+    _shaped(v_out, shape, "v_out")
+    o = _ptrs(dev, dtype, "k_out v_out", k_out, v_out)
+    _call("sl8_paged_read_int4", dev, codes[0], scales[0], codes[1], scales[1], num_pages, page_size, table, max_blocks, lens,
+          cu, B, hkv, N, d, total, _mean_of(dev, k_mean, hkv, d), o[0], o[1], _DTYPES[dtype])
+    return k_out, v_out
 
 
 # ------------------------------------------------------------------ status / tracing

@@ -18,9 +18,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "sl8")
 LIB = os.path.join(PKG, "libsl8.so")
-SOURCES = ["abi.cu", "quant.cu", "prefill.cu", "decode.cu", "noalloc.cu", "paged.cu", "select.cu", "list_decode.cu"]
+SOURCES = ["abi.cu", "quant.cu", "prefill.cu", "decode.cu", "noalloc.cu", "paged.cu", "select.cu", "list_decode.cu",
+           "cache4.cu"]
 HEADERS = [os.path.join(CSRC, "sl8_internal.h"), os.path.join(CSRC, "sm103_ptx.cuh"), os.path.join(CSRC, "decode_unit.cuh"),
-           os.path.join(ROOT, "include", "sl8.h")]
+           os.path.join(CSRC, "append.cuh"), os.path.join(CSRC, "cache4.cuh"), os.path.join(ROOT, "include", "sl8.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

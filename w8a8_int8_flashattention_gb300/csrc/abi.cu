@@ -1,6 +1,6 @@
 // C ABI of libsl8: argument validation, workspace planning, the per-device status
 // word, tensor-map encoding and kernel tracing.  The kernels live in quant.cu, prefill.cu,
-// decode.cu, paged.cu, select.cu and list_decode.cu; every entry point here only validates
+// decode.cu, paged.cu, select.cu, list_decode.cu and cache4.cu; every entry point here only validates
 // and enqueues.
 #include <cudaTypedefs.h>
 
@@ -919,11 +919,12 @@ int sl8_paged_assign(const int32_t* ctx_lens, const int32_t* new_lens, const int
   return SL8_OK;
 }
 
-int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
-                    int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
-                    int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis, int adjacent,
-                    void* q_out, int64_t q_out_stride, const int32_t* slot_map, int8_t* k_pages, float* k_scale_pages,
-                    int8_t* v_pages, float* v_scale_pages, int32_t num_pages, int32_t page_size, void* stream) {
+// The append's checks, and its arguments for the kernels; `T == 0` has nothing to do.
+static int append_args(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
+                       int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis, int adjacent,
+                       void* q_out, int64_t q_out_stride, const int32_t* slot_map, void* k_pages, void* k_scale_pages,
+                       void* v_pages, void* v_scale_pages, int32_t num_pages, int32_t page_size, RopeAppendArgs* out) {
   SL8_CHECK(dtype == SL8_F16 || dtype == SL8_BF16 || dtype == SL8_F32, SL8_ERR_INVALID_ARG);
   SL8_CHECK(T >= 0 && Hq >= 0 && Hkv > 0 && d > 0 && num_pages > 0 && page_size > 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
@@ -953,7 +954,7 @@ int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int6
   }
   // one warp per part of a token, at most one part per row group
   SL8_CHECK(static_cast<int64_t>(T) * (Hq + 2 * static_cast<int64_t>(Hkv) + 2) < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
-  RopeAppendArgs r{};
+  RopeAppendArgs& r = *out;
   r.q = q;
   r.k = k;
   r.v = v;
@@ -980,7 +981,81 @@ int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int6
   r.v_scale = v_scale_pages;
   r.num_pages = num_pages;
   r.page_size = page_size;
+  return SL8_OK;
+}
+
+int sl8_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
+                    int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
+                    int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis, int adjacent,
+                    void* q_out, int64_t q_out_stride, const int32_t* slot_map, int8_t* k_pages, float* k_scale_pages,
+                    int8_t* v_pages, float* v_scale_pages, int32_t num_pages, int32_t page_size, void* stream) {
+  RopeAppendArgs r{};
+  const int e = append_args(q, k, v, dtype, q_stride, k_stride, v_stride, T, Hq, Hkv, d, positions, axes, rot_dim,
+                            inv_freq, pair_axis, adjacent, q_out, q_out_stride, slot_map, k_pages, k_scale_pages, v_pages,
+                            v_scale_pages, num_pages, page_size, &r);
+  if (e != SL8_OK || T == 0) return e;
   SL8_LAUNCH(launch_rope_append(r, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+int sl8_rope_append_int4(const void* q, const void* k, const void* v, int dtype, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t d, const int32_t* positions,
+                         int32_t axes, int32_t rot_dim, const float* inv_freq, const uint8_t* pair_axis, int adjacent,
+                         void* q_out, int64_t q_out_stride, const int32_t* slot_map, const float* k_mean,
+                         uint8_t* k_pages, void* k_scale_pages, uint8_t* v_pages, void* v_scale_pages,
+                         int32_t num_pages, int32_t page_size, void* stream) {
+  RopeAppendArgs r{};
+  const int e = append_args(q, k, v, dtype, q_stride, k_stride, v_stride, T, Hq, Hkv, d, positions, axes, rot_dim,
+                            inv_freq, pair_axis, adjacent, q_out, q_out_stride, slot_map, k_pages, k_scale_pages, v_pages,
+                            v_scale_pages, num_pages, page_size, &r);
+  if (e != SL8_OK || T == 0) return e;
+  SL8_CHECK(aligned16(k_mean) && aligned16(k_scale_pages) && aligned16(v_scale_pages), SL8_ERR_INVALID_ARG);
+  r.k_mean = k_mean;
+  SL8_LAUNCH(launch_rope_append_int4(r, static_cast<cudaStream_t>(stream)));
+  return SL8_OK;
+}
+
+int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_pages, const uint8_t* v_pages,
+                        const void* v_scale_pages, int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                        int32_t max_blocks, const int32_t* seqlens, const int32_t* cu_seqlens, int32_t B, int32_t Hkv,
+                        int32_t N, int32_t d, int64_t total_tokens, const float* k_mean, void* k_out, void* v_out,
+                        int out_dtype, void* stream) {
+  SL8_CHECK(out_dtype == SL8_F16 || out_dtype == SL8_BF16 || out_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(B >= 0 && Hkv > 0 && N >= 0 && d > 0 && num_pages > 0 && page_size > 0 && max_blocks > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(!cu_seqlens || total_tokens >= 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(decode_head_dim_ok(d), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(Hkv <= (1 << 16), SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks <= kMaxTokens && N <= kMaxTokens, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  if (B == 0 || N == 0 || (cu_seqlens && total_tokens == 0)) return SL8_OK;
+  // one CTA per 64 tokens of a sequence's kv head
+  SL8_CHECK((static_cast<int64_t>(N) + 63) / 64 * B < (int64_t(1) << 31) / Hkv, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(block_table && seqlens && (k_out || v_out), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(!k_out || (k_pages && k_scale_pages), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(!v_out || (v_pages && v_scale_pages), SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(k_pages) && aligned16(v_pages) && aligned16(k_scale_pages) && aligned16(v_scale_pages) &&
+                aligned16(k_mean) && aligned16(k_out) && aligned16(v_out),
+            SL8_ERR_INVALID_ARG);
+  Read4Args a{};
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = static_cast<const uint16_t*>(k_scale_pages);
+  a.v_scale = static_cast<const uint16_t*>(v_scale_pages);
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.seqlens = seqlens;
+  a.cu_seqlens = cu_seqlens;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.total = total_tokens;
+  a.k_mean = k_mean;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.out_dtype = static_cast<sl8_dtype>(out_dtype);
+  SL8_LAUNCH(launch_paged_read_int4(a, d, static_cast<cudaStream_t>(stream)));
   return SL8_OK;
 }
 

@@ -169,13 +169,28 @@ struct RopeAppendArgs {
   void* q_out;
   int64_t q_out_stride;
   const int32_t* slot_map;
-  int8_t* k_pages;
-  float* k_scale;
-  int8_t* v_pages;
-  float* v_scale;
+  void *k_pages, *k_scale, *v_pages, *v_scale;  // int8 codes and fp32 scales, or 4 bits and bf16
+  const float* k_mean;                          // 4 bits: [Hkv][d], nullable
   int32_t num_pages, page_size;
 };
 cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s);
+// The 4-bit cache (cache4.cu): the same append, and its rows as dense keys and values.
+cudaError_t launch_rope_append_int4(const RopeAppendArgs& r, cudaStream_t s);
+struct Read4Args {
+  const uint8_t *k_pages, *v_pages;    // [num_pages][Hkv][page][d / 2]
+  const uint16_t *k_scale, *v_scale;   // [num_pages][Hkv][page][d / 32] bf16
+  int32_t num_pages, page;
+  const int32_t* table;                // [B][max_blocks]
+  int32_t max_blocks;
+  const int32_t* seqlens;              // [B]
+  const int32_t* cu_seqlens;           // [B + 1], nullable: dense
+  int32_t B, Hkv, N;
+  int64_t total;                       // rows of a packed output
+  const float* k_mean;                 // [Hkv][d], nullable
+  void *k_out, *v_out;                 // nullable: not read
+  sl8_dtype out_dtype;
+};
+cudaError_t launch_paged_read_int4(const Read4Args& a, int32_t d, cudaStream_t s);
 cudaError_t launch_page_bounds(const int8_t* k_pages, const float* k_scale_pages, int32_t num_pages, int32_t page_size,
                                const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
                                const int32_t* new_lens, int32_t max_new, int32_t B, int32_t Hkv, int32_t d,
