@@ -602,6 +602,45 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
                                 void* stream);
 
 /*
+ * Decode attention over the paged 4-bit cache, in one launch or with a merge step:
+ *   x_t = s_q sum_g s_k[t, g] int32(q_i8[g] . c_k[t, g]) / sqrt(d), p = softmax(x) over the tokens t that the
+ *   query sees, out = sum_t p_t s_v[t, g] c_v[t], g the groups of 32 channels.
+ *   q             device, [B][T][Hq][d] of q_dtype (F16, BF16 or F32), quantised per row as in the
+ *                 int8 decode.  1 <= T <= 32 queries a sequence (SL8_ERR_UNSUPPORTED above), at
+ *                 positions seqlens[b] - T + t: T = 1 is a decode step, more are drafts, whose
+ *                 tokens the cache already holds.
+ *   block_table   device, [B][max_blocks] int32; seqlens device, [B] int32 (drafts included).
+ *   tree_mask     device, nullable, [B][T] uint32.  NULL: query t sees the tokens up to its own
+ *                 position.  Else, as in sl8_attn_int8_decode_verify, those below seqlens[b] - T
+ *                 and draft u iff bit u is set.
+ *   num_splits    parts that each sequence is cut into (0 = automatic; above 1024 counts as
+ *                 1024).  Up to 8 are a cluster of CTAs that merges them, more go through the workspace.
+ *   out           device, [B][T][Hq][d] of out_dtype; a query that sees no token gets 0.
+ *   lse_out       device, nullable, [B][T][Hq] fp32 (natural log; -inf for no token), of the stored
+ *                 keys: with a k_mean, sum_c q_c k_mean_c / sqrt(d) below that of the keys themselves.
+ *                 A NaN logit (a group with an infinite k scale, or such a query row) makes out and
+ *                 lse_out of its query NaN, an infinite v scale the group's channels of out.
+ *                 Each weight p * s_v is off by 2^-17 of itself before it meets its row (2^-24 for an
+ *                 fp32 out).  V scales stay below 2^112.
+ *   workspace     at least sl8_attn_int4_paged_decode_workspace_size() bytes (0: invalid or
+ *                 unsupported shape; 16: none is used and it may be null), 16-byte aligned; launches
+ *                 that run at the same time need their own.
+ * Any Hq that is a multiple of Hkv.  The T * Hq / Hkv (query, head) columns of a kv head are taken in
+ * the fewest groups of at most 16 (8 at d = 256), each of which reads the cache.  page_size a multiple of 16,
+ * page_size * max_blocks <= 2^31 - 256.  A page or a length out of range is recorded
+ * (SL8_ERR_DEVICE_ARG), and page 0 read or the length clamped.
+ */
+SL8_API size_t sl8_attn_int4_paged_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv,
+                                                         int32_t max_blocks, int32_t page_size, int32_t d,
+                                                         int32_t num_splits);
+SL8_API int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_pages, const void* k_scale_pages,
+                                       const uint8_t* v_pages, const void* v_scale_pages, int32_t num_pages,
+                                       int32_t page_size, const int32_t* block_table, int32_t max_blocks,
+                                       const int32_t* seqlens, const uint32_t* tree_mask, int32_t T, int32_t B,
+                                       int32_t Hq, int32_t Hkv, int32_t d, int32_t num_splits, void* out, int out_dtype,
+                                       float* lse_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Debug view of the decode's q quantisation and int32 logits (same kernel as the
  * split call, with num_splits automatic: o_partial/lse_partial sized for
  * S = sl8_attn_decode_num_splits(B, Hkv, Lmax, d, 0)).

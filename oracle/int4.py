@@ -62,12 +62,14 @@ def visible(L, T, t, mask=None):
     return [p for p in range(L) if p < L - T or (p - (L - T) <= t if mask is None else (int(mask) >> (p - (L - T))) & 1)]
 
 
-def attention(q, kc, ks, vc, vs, tables, lens, masks=None):
-    """q [B, T, Hq, d] fp32; packed pages and scales; (out fp64, lse fp64)."""
+def attention(q, kc, ks, vc, vs, tables, lens, masks=None, bounds=False):
+    """q [B, T, Hq, d] fp32; packed pages and scales; (out fp64, lse fp64).  bounds: also
+    sum_t p_t |v_t| like out, and the largest sum_c |q_c k_c| / sqrt(d) of each query's tokens."""
     B, T, Hq, d = q.shape
     Hkv = kc.shape[1]
     G = Hq // Hkv
     out, lse = np.zeros(q.shape), np.full(q.shape[:-1], -np.inf)
+    size, reach = np.zeros(q.shape), np.zeros(q.shape[:-1])
     codes, sq = _quant(q)
     for b in range(B):
         n = int(lens[b])
@@ -80,9 +82,13 @@ def attention(q, kc, ks, vc, vs, tables, lens, masks=None):
             if not see:
                 continue
             for h in range(Hq):
-                x = k[h // G][see] @ codes[b, t, h].astype(np.float64) * float(sq[b, t, h]) / np.sqrt(d)
+                row = codes[b, t, h].astype(np.float64) * float(sq[b, t, h]) / np.sqrt(d)
+                x = k[h // G][see] @ row
                 m = x.max()
                 e = np.exp(x - m)
                 out[b, t, h] = e @ v[h // G][see] / e.sum()
                 lse[b, t, h] = m + np.log(e.sum())
-    return out, lse
+                if bounds:
+                    size[b, t, h] = e @ np.abs(v[h // G][see]) / e.sum()
+                    reach[b, t, h] = (np.abs(k[h // G][see]) @ np.abs(row)).max()
+    return (out, lse, size, reach) if bounds else (out, lse)

@@ -66,6 +66,33 @@ def test_paged_read(lib, p):
         assert f(*_changed(ok, change)) == UNSUPPORTED, change
 
 
+def test_paged_decode(lib, p):
+    f = lib.sl8_attn_int4_paged_decode
+    #    0  1             2  3  4  5  6   7   8  9  10 11   12 13 14 15 16   17 18 19            20    21 22       23
+    ok = [p, sl8.SL8_BF16, p, p, p, p, 16, 16, p, 8, p, None, 1, 2, 8, 2, 128, 0, p, sl8.SL8_BF16, None, p, 1 << 30, None]
+    assert f(*_changed(ok, {13: 0})) == OK
+    for i in (0, 2, 3, 4, 5, 8, 10, 18):
+        assert f(*_changed(ok, {i: None})) == INVALID, i
+    for change in ({1: sl8.SL8_I8}, {19: sl8.SL8_I8}, {6: 0}, {7: 0}, {9: 0}, {12: 0}, {13: -1}, {14: 7}, {15: 0}, {17: -1}, {0: p + 4},
+                   {2: p + 4}, {3: p + 2}, {4: p + 8}, {5: p + 8}):
+        assert f(*_changed(ok, change)) == INVALID, change
+    for change in ({16: 96}, {7: 24}, {12: 33}, {6: 1 << 20, 7: 1 << 12}, {7: 16, 9: (1 << 27) - 8}, {13: 1 << 24, 12: 32}):
+        assert f(*_changed(ok, change)) == UNSUPPORTED, change
+    size = lib.sl8_attn_int4_paged_decode_workspace_size
+    assert size(2, 1, 8, 2, 8, 16, 128, 8) == 16  # one launch, nothing kept
+    long = _changed(ok, {9: 64, 17: 20})
+    need = size(2, 1, 8, 2, 64, 16, 128, 20)
+    assert need >= 2 * 8 * 130 * 4 * 20
+    for change in ({22: need - 1}, {21: None}, {21: p + 8}):
+        assert f(*_changed(long, change)) == WORKSPACE, change
+    for args in ((2, 1, 8, 2, 8, 24, 128, 0), (0, 1, 8, 2, 8, 16, 128, 0), (2, 1, 7, 2, 8, 16, 128, 0), (2, 33, 8, 2, 8, 16, 128, 0),
+                 (2, 0, 8, 2, 8, 16, 128, 0), (2, 1, 8, 2, 0, 16, 128, 0), (2, 1, 8, 2, 8, 16, 96, 0), (2, 1, 8, 2, 8, 16, 128, -1),
+                 (1, 1, 1, 1, (1 << 27) - 8, 16, 32, 1)):
+        assert size(*args) == 0, args
+    assert size(1, 1, 1, 1, (1 << 27) - 16, 16, 32, 1) == 16
+    assert size(1, 1, 8, 1, 512, 64, 128, 1 << 30) == size(1, 1, 8, 1, 512, 64, 128, 1024) > size(1, 1, 8, 1, 512, 64, 128, 64) > 16
+
+
 def _pool(d=64, page=16):
     codes, scales = torch.zeros((1, 1, page, d // 2), dtype=torch.uint8), torch.zeros((1, 1, page, d // 32), dtype=torch.bfloat16)
     return codes, scales, codes.clone(), scales.clone()
@@ -78,3 +105,5 @@ def test_binding_refuses_cpu_tensors(lib):
         sl8.rope_append_int4(None, k, k, None, None, i[:2], *_pool())
     with pytest.raises(ValueError):
         sl8.paged_read_int4(*_pool(), i.view(1, 4), i[:1])
+    with pytest.raises(ValueError):
+        sl8.attn_int4_paged_decode(torch.zeros(1, 2, 64), *_pool(), i.view(1, 4), i[:1])

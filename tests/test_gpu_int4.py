@@ -5,6 +5,15 @@ Tolerances.  Codes and scales of rows that do not turn are fixed bit for bit.  R
 2e-6 of a pair's length (the append's bound, as for the int8 pages), so a scale is a bf16 rounding
 of something that near, and a stored value within half a step of it.  Values read back take one fma
 and one rounding to their type.
+
+Attention, for n tokens and kN = d / 32 groups (2^-24 is half a step of fp32):
+  a logit takes kN fused sums, the scale of q and log2 e, and the reference comes off: (kN + 4) 2^-24 of
+  sum |q k| / sqrt(d), in units of log2 1.45 times that; exponentials are good to 2^-22; so each p to
+    ep = 1.45 (kN + 4) 2^-24 reach + 2^-22, and the quotient by their sum to twice that;
+  weights are off by 2^-17 of themselves (two bf16 terms, 2^-9 2^-9 and a bit for the product's rounding), 2^-23 for fp32 outputs;
+  sums: each MMA's addition may truncate (2^-23 of the partial sum), at most 3 an m16n8k16 step and 16 tokens,
+  and some thirty in merges: (3 n / 16 + 32) 2^-23.
+All of these are relative to sum_t p_t |v_t|; then half a step of the output's type.
 """
 import numpy as np
 import pytest
@@ -280,3 +289,169 @@ def test_read_of_infinite_groups_and_what_was_appended():
     ok = torch.isfinite(k[0].transpose(0, 1)) & torch.isfinite(x)
     step = x.unflatten(-1, (-1, 32)).nan_to_num(0.0, 0.0, 0.0).abs().amax(-1, keepdim=True).expand(-1, -1, -1, 32).flatten(-2) / 7 * (1 + 2.0 ** -8)
     assert bool(((k[0].transpose(0, 1) - x).abs() <= step * 0.5)[ok].all()) and torch.equal(k.nan_to_num(), v.nan_to_num())
+
+
+# ------------------------------------------------------------------ decode attention
+
+def _check_attention(out, lse, q, host, tables, lens, masks=None, tag=""):
+    """out [B,T,Hq,d], lse [B,T,Hq] against the definition with the bounds above."""
+    want, wlse, size, reach = Q.attention(f32(q), *host, tables, lens, masks, bounds=True)
+    n, groups = max(int(np.max(lens)), 1), q.shape[-1] // 32
+    ep = 1.45 * (groups + 4) * 2.0 ** -24 * reach + 2.0 ** -22
+    ew = 2.0 ** -23 if out.dtype == torch.float32 else 2.0 ** -17
+    rel = 2 * ep[..., None] + ew + (3 * n / 16 + 32) * 2.0 ** -23
+    eps = torch.finfo(out.dtype).eps / 2
+    got = np64(out)
+    assert np.all(np.isfinite(got)), tag
+    tol = size * rel * (1 + eps) + eps * np.abs(want) + (2.0 ** -25 if out.dtype == torch.float16 else 0)
+    worst = np.max((np.abs(got - want) - tol))
+    assert worst <= 0, (tag, worst, np.max(np.abs(got - want) / np.maximum(tol, 1e-30)))
+    empty = np.isinf(wlse)
+    gl = np64(lse)
+    assert np.all(np.isneginf(gl[empty])), tag
+    tl = 2 * ep + (n / 16 + 32) * 2.0 ** -24 + 2.0 ** -23 * (1 + np.abs(np.where(empty, 0, wlse)))
+    assert np.all(np.abs(gl - wlse)[~empty] <= tl[~empty]), tag
+
+
+def _attend(B, T, hq, hkv, d, page, lens, qdt, odt, splits=0, tree=False, spread=1.0, seed=0, workspace=None):
+    rng = np.random.default_rng(seed + d + 7 * T)
+    nb = -(-max(max(lens), 1) // page) + 1
+    num_pages = sum(-(-n // page) for n in lens) + 2
+    pool, host = _filled(rng, num_pages, hkv, page, d, spread)
+    tables = _tables(rng, lens, nb, page, num_pages)
+    q = torch.from_numpy(rng.standard_normal((B, T, hq, d)).astype(np.float32)).to(qdt).to(DEV)
+    masks = rng.integers(0, 1 << T, (B, T)) if tree else None
+    mask = None
+    if tree:
+        mask = torch.from_numpy(masks.astype(np.uint32).view(np.int32).copy() if T == 32 else masks.astype(np.int32)).to(DEV)
+    out, lse = sl8.attn_int4_paged_decode(q if T > 1 else q[:, 0], *pool, i32(tables), i32(lens), tree_mask=mask, num_splits=splits,
+                                          out_dtype=odt, return_lse=True, workspace=workspace)
+    assert out.dtype == odt and out.shape == (q.shape if T > 1 else q[:, 0].shape)
+    _check_attention(out.view(q.shape), lse.view(q.shape[:-1]), q, host, tables, lens, masks, (d, T, splits))
+
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("G,hkv,splits,qdt,odt", [
+    (1, 1, 0, BF16, BF16), (4, 2, 1, BF16, F32), (8, 1, 2, F16, F16), (16, 2, 3, F32, BF16), (11, 1, 8, BF16, F32), (3, 3, 9, F32, F32),
+    (40, 1, 20, F16, F32), (17, 2, 0, BF16, F16)])
+def test_decode(d, G, hkv, splits, qdt, odt):
+    """Lengths of zero and one, around units and pages, and some hundred tokens."""
+    for page, lens in ((16, [0, 1, 15, 16, 17]), (64, [63, 64, 65, 500]), (48, [331, 2])):
+        _attend(len(lens), 1, G * hkv, hkv, d, page, lens, qdt, odt, splits, seed=page)
+
+
+@pytest.mark.parametrize("T,G,hkv,d,splits,tree,odt", [
+    (2, 4, 2, 128, 0, False, BF16), (5, 4, 2, 128, 1, True, F32), (7, 1, 2, 64, 3, True, F16), (32, 2, 1, 32, 2, True, F32),
+    (32, 1, 1, 256, 12, False, BF16), (31, 3, 1, 64, 0, True, BF16), (4, 16, 1, 128, 5, False, F32), (3, 5, 2, 256, 1, True, F16)])
+def test_drafts(T, G, hkv, d, splits, tree, odt):
+    """Causal drafts and random trees, among them queries that see nothing; sequences shorter than
+    their drafts."""
+    lens = [0, 1, T, T + 1, 16, 33, 200 + T]
+    _attend(len(lens), T, G * hkv, hkv, d, 16, lens, BF16, odt, splits, tree)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 5, 64])
+def test_a_long_sequence(splits):
+    _attend(1, 1, 8, 2, 128, 32, [20011], BF16, F32, splits, spread=0.3)
+
+
+@pytest.mark.parametrize("d,G", [(32, 4), (64, 16), (128, 2), (256, 8)])
+def test_scales_far_apart(d, G):
+    """Groups and rows whose scales are up to 10^12 apart keep their own relative accuracy."""
+    for splits in (1, 4, 10):
+        _attend(3, 1, G, 1, d, 16, [90, 7, 300], BF16, F32, splits, spread=12.0)
+        _attend(3, 1, G, 1, d, 16, [90, 7, 300], BF16, F16, splits, spread=4.0)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 3, 9])
+def test_what_lies_past_a_sequence_does_not_matter(d, splits):
+    """Infinities and NaN in the scales of rows that a query does not see: past the length, or of a
+    draft that its mask hides.  -8 codes and all bytes are codes."""
+    rng = np.random.default_rng(5)
+    T, hkv, G, page, L = 3, 2, 3, 16, 70
+    pool, host = _filled(rng, 8, hkv, page, d)
+    tables = _tables(rng, [L], 6, page, 8)
+    bad = [float("nan"), float("inf")]
+    for row in range(L - 2, 80):  # drafts 1 and 2 and what lies behind them in the last page
+        for i, val in ((1, bad[row % 2]), (3, bad[(row + 1) % 2])):
+            pool[i][tables[0][row // page], :, row % page] = val
+    q = torch.from_numpy(rng.standard_normal((1, T, hkv * G, d)).astype(np.float32)).to(DEV)
+    masks = [[0b001, 0b001, 0b000]]
+    out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), tree_mask=i32(masks), num_splits=splits, return_lse=True)
+    clean = [h.copy() for h in host]
+    _check_attention(out, lse, q, clean, tables, [L], masks)
+    # a query that sees the NaN scales has no other value
+    seen, sl = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), tree_mask=i32([[1, 3, 2]]), num_splits=splits, return_lse=True)
+    assert torch.equal(seen[:, 0], out[:, 0]) and torch.isnan(sl[:, 1:]).all() and torch.isnan(seen[:, 1:]).all()
+
+
+def test_infinite_value_groups_reach_their_channels():
+    rng = np.random.default_rng(6)
+    d, hkv, page, L = 128, 2, 16, 40
+    pool, host = _filled(rng, 4, hkv, page, d)
+    tables = _tables(rng, [L], 3, page, 4)
+    pool[2][tables[0][1], 1, 3, 16:32] = 0x88  # row 19 of head 1, group 1: codes 0 with the scale inf
+    pool[3][tables[0][1], 1, 3, 1] = float("inf")
+    q = torch.randn((1, 4, d), device=DEV)
+    out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), return_lse=True)
+    nan = torch.isnan(out[0])
+    assert not nan[:2].any() and nan[2:, 32:64].all() and not nan[2:, :32].any() and not nan[2:, 64:].any()
+    assert torch.isfinite(lse).all()
+    # and a query row with an infinity is NaN, alone
+    q[0, 1, 7] = float("inf")
+    out2, lse2 = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), return_lse=True)
+    assert torch.isnan(out2[0, 1]).all() and torch.isnan(lse2[0, 1]) and torch.equal(out2[0, 0], out[0, 0])
+
+
+@pytest.mark.parametrize("d,splits", [(32, 1), (64, 0), (128, 1), (128, 8), (256, 2), (128, 12)])
+def test_every_row_and_channel_counts(d, splits):
+    """Value rows one by one: with the others zero, a row's weight comes out of each of its channels;
+    key channels one by one: each moves the logits by its own q."""
+    rng = np.random.default_rng(d)
+    L, page, hkv, hq = 150, 16, 1, 5
+    pool, (kc, ks, vc, vs) = _filled(rng, 10, hkv, page, d)
+    tables = np.arange(10)[None]
+    q = torch.from_numpy(rng.standard_normal((1, hq, d)).astype(np.float32)).to(DEV)
+    for row in (0, 1, 2, 3, 15, 16, 63, 64, 97, 148, 149):
+        pool[2].fill_(0x88)
+        c = rng.integers(0, 256, d // 2).astype(np.uint8)
+        pool[2][row // page, 0, row % page] = torch.from_numpy(c).to(DEV)
+        v = np.full_like(vc, 0x88)
+        v[row // page, 0, row % page] = c
+        out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), num_splits=splits, return_lse=True)
+        _check_attention(out[:, None], lse[:, None], q[:, None], (kc, ks, v, vs), tables, [L], tag=row)
+    pool[2].copy_(torch.from_numpy(vc))
+    for ch in range(0, d, 3):
+        one = torch.zeros((1, hq, d), device=DEV)
+        one[..., ch] = torch.tensor([3.0, -2.0, 1.0, 0.5, 0.0], device=DEV)
+        out, lse = sl8.attn_int4_paged_decode(one, *pool, i32(tables), i32([L]), num_splits=splits, return_lse=True)
+        _check_attention(out[:, None], lse[:, None], one[:, None], (kc, ks, vc, vs), tables, [L], tag=ch)
+
+
+def test_decode_reports_bad_pages_and_lengths():
+    rng = np.random.default_rng(8)
+    pool, host = _filled(rng, 4, 1, 16, 64)
+    q = torch.randn((1, 1, 2, 64), device=DEV)
+    for tables, lens, as_tables, as_lens in (([[2, 7]], [30], [[2, 0]], [30]), ([[2, -1]], [30], [[2, 0]], [30]), ([[2, 1]], [33], [[2, 1]], [32]),
+                                             ([[2, 1]], [-4], [[2, 1]], [0])):
+        for splits in (1, 4, 9):
+            out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32(lens), num_splits=splits, return_lse=True)
+            assert sl8.last_device_status()[0] == sl8.SL8_ERR_DEVICE_ARG
+            _check_attention(out, lse, q, host, as_tables, as_lens)
+
+
+def test_the_same_bits_every_time_and_shared_pages():
+    rng = np.random.default_rng(9)
+    pool, host = _filled(rng, 6, 2, 32, 128)
+    tables, lens = [[1, 2, 3], [1, 2, 5], [4, 4, 4]], [90, 70, 96]
+    q = torch.randn((3, 8, 128), device=DEV).bfloat16()
+    for splits in (0, 2, 12):
+        a = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32(lens), num_splits=splits, return_lse=True)
+        for _ in range(3):
+            b = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32(lens), num_splits=splits, return_lse=True)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        _check_attention(a[0][:, None], a[1][:, None], q[:, None], host, tables, lens)

@@ -111,6 +111,9 @@ _SIGNATURES = {
                                     ctypes.c_char_p, _INT, _P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I32, _P]),
     "sl8_paged_read_int4": (_INT, [_P, _P, _P, _P, _I32, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I64, _P, _P, _P,
                                    _INT, _P]),
+    "sl8_attn_int4_paged_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "sl8_attn_int4_paged_decode": (_INT, [_P, _INT, _P, _P, _P, _P, _I32, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                          _I32, _I32, _P, _INT, _P, _P, _SZ, _P]),
     "sl8_last_device_status": (_INT, [_P, ctypes.POINTER(_INT)]),
     "sl8_set_spin_limit_ns": (None, [_U64]),
     "sl8_get_spin_limit_ns": (_U64, []),
@@ -916,6 +919,55 @@ def paged_read_int4(k_pages, k_scale_pages, v_pages, v_scale_pages, block_table,
     _call("sl8_paged_read_int4", dev, codes[0], scales[0], codes[1], scales[1], num_pages, page_size, table, max_blocks, lens,
           cu, B, hkv, N, d, total, _mean_of(dev, k_mean, hkv, d), o[0], o[1], _DTYPES[dtype])
     return k_out, v_out
+
+
+def int4_decode_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, max_blocks: int, page_size: int, d: int,
+                                num_splits: int = 0) -> int:
+    return int(lib().sl8_attn_int4_paged_decode_workspace_size(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits))
+
+
+def attn_int4_paged_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, block_table, seqlens, tree_mask=None,
+                           num_splits=0, out_dtype=None, return_lse=False, workspace=None, out=None, lse=None):
+    """Decode attention over the paged 4-bit cache: q [B,Hq,d], or [B,T,Hq,d] with T <= 32 drafts whose
+    tokens the cache holds (query t at position seqlens - T + t).  tree_mask [B,T] int32: bit u says
+    that the query sees draft u (without it each sees the tokens up to itself).  Returns out like q
+    (dtype q.dtype unless given) and, with return_lse, the fp32 LSE: 0 and -inf for a query that sees no
+    token.  workspace: uint8, at least int4_decode_workspace_bytes (16: none is used)."""
+    dev = _index(k_pages)
+    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    table, lens, mask = _ptrs(dev, _I32T, "block_table seqlens tree_mask", block_table, seqlens, tree_mask)
+    B, max_blocks = block_table.shape
+    shape = q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [B, Hq, d] or [B, T, Hq, d]")
+    T, hq = (1, shape[1]) if len(shape) == 3 else (shape[1], shape[2])
+    if shape[0] != B or shape[-1] != d or seqlens.numel() != B or (tree_mask is not None and tree_mask.numel() != B * T):
+        raise ValueError("q, block_table, seqlens, tree_mask and the pages do not belong together")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != shape:
+        raise ValueError("out must have q's shape")
+    if q.dtype not in _DTYPES or out.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype} or {out.dtype}")
+    qp, = _ptrs(dev, q.dtype, "q", q)
+    op, = _ptrs(dev, out.dtype, "out", out)
+    lse_p = None
+    if return_lse:
+        if lse is None:
+            lse = torch.empty(shape[:-1], dtype=_F32T, device=q.device)
+        elif lse.shape != shape[:-1]:
+            raise ValueError("lse must have one entry per query head")
+        lse_p, = _ptrs(dev, _F32T, "lse", lse)
+    ws, nbytes = None, 0
+    if workspace is None:
+        need = int4_decode_workspace_bytes(B, T, hq, hkv, max_blocks, page_size, d, num_splits)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 16 else None
+    if workspace is not None:
+        ws, = _ptrs(dev, workspace.dtype, "workspace", workspace)
+        nbytes = workspace.numel() * workspace.element_size()
+    _call("sl8_attn_int4_paged_decode", dev, qp, _DTYPES[q.dtype], codes[0], scales[0], codes[1], scales[1], num_pages,
+          page_size, table, max_blocks, lens, mask, T, B, hq, hkv, d, num_splits, op, _DTYPES[out.dtype], lse_p, ws, nbytes)
+    return (out, lse) if return_lse else out
 
 
 # ------------------------------------------------------------------ status / tracing

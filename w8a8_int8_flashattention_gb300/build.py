@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "sl8")
 LIB = os.path.join(PKG, "libsl8.so")
 SOURCES = ["abi.cu", "quant.cu", "prefill.cu", "decode.cu", "noalloc.cu", "paged.cu", "select.cu", "list_decode.cu",
-           "cache4.cu"]
+           "cache4.cu", "decode4.cu"]
 HEADERS = [os.path.join(CSRC, "sl8_internal.h"), os.path.join(CSRC, "sm103_ptx.cuh"), os.path.join(CSRC, "decode_unit.cuh"),
            os.path.join(CSRC, "append.cuh"), os.path.join(CSRC, "cache4.cuh"), os.path.join(ROOT, "include", "sl8.h")]
 

@@ -1,7 +1,7 @@
 // C ABI of libsl8: argument validation, workspace planning, the per-device status
 // word, tensor-map encoding and kernel tracing.  The kernels live in quant.cu, prefill.cu,
-// decode.cu, paged.cu, select.cu, list_decode.cu and cache4.cu; every entry point here only validates
-// and enqueues.
+// decode.cu, paged.cu, select.cu, list_decode.cu, cache4.cu
+// and decode4.cu; every entry point here only validates and enqueues.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1206,6 +1206,97 @@ int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_page
   SL8_LAUNCH(launch_decode_split(a, s));
   SL8_LAUNCH(launch_decode_combine(a.o_partial, a.lse_partial, list_lens, a.B, a.Hq, d, S, a.split_size, out,
                                    static_cast<sl8_dtype>(out_dtype), lse_out, s, 1, true));
+  return SL8_OK;
+}
+
+// ---------------------------------------------------------------- decode over the paged 4-bit cache
+struct Decode4Plan {
+  int32_t groups, cols, splits;  // splits 0: invalid or unsupported
+};
+static Decode4Plan decode4_plan(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int32_t page_size,
+                                int32_t d, int32_t num_splits) {
+  Decode4Plan p{0, 0, 0};
+  if (B <= 0 || T <= 0 || T > 32 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_blocks <= 0 || page_size <= 0 || num_splits < 0)
+    return p;
+  if (static_cast<int64_t>(max_blocks) * page_size > kMaxTokens || page_size % 16 || !decode_head_dim_ok(d)) return p;
+  if (static_cast<int64_t>(B) * T > (int64_t(1) << 27) / Hq) return p;
+  const int64_t columns = static_cast<int64_t>(T) * (Hq / Hkv);
+  const int64_t most = decode4_max_columns(d);
+  p.groups = static_cast<int32_t>((columns + most - 1) / most);
+  p.cols = static_cast<int32_t>((columns + p.groups - 1) / p.groups);
+  const int64_t items = static_cast<int64_t>(B) * Hkv * p.groups;
+  int64_t n = num_splits;
+  if (n == 0) n = decode4_splits(items, static_cast<int64_t>(max_blocks) * page_size, d);
+  n = std::min<int64_t>(n, 1024);
+  if (items * n < (int64_t(1) << 31)) p.splits = static_cast<int32_t>(n);
+  return p;
+}
+
+static size_t decode4_ml_offset(int64_t rows, int32_t d, int32_t S) {
+  return align_up(static_cast<size_t>(rows) * S * d * sizeof(float), 256);
+}
+
+size_t sl8_attn_int4_paged_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks,
+                                                 int32_t page_size, int32_t d, int32_t num_splits) {
+  const Decode4Plan p = decode4_plan(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
+  if (p.splits <= 0) return 0;
+  if (p.splits <= decode4_max_cluster()) return 16;  // none is used
+  const int64_t rows = static_cast<int64_t>(B) * T * Hq;
+  return decode4_ml_offset(rows, d, p.splits) + static_cast<size_t>(rows) * p.splits * 2 * sizeof(float);
+}
+
+int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_pages, const void* k_scale_pages,
+                               const uint8_t* v_pages, const void* v_scale_pages, int32_t num_pages, int32_t page_size,
+                               const int32_t* block_table, int32_t max_blocks, const int32_t* seqlens,
+                               const uint32_t* tree_mask, int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                               int32_t num_splits, void* out, int out_dtype, float* lse_out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  SL8_CHECK(q_dtype == SL8_F16 || q_dtype == SL8_BF16 || q_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(out_dtype == SL8_F16 || out_dtype == SL8_BF16 || out_dtype == SL8_F32, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(B >= 0 && T > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && d > 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(num_pages > 0 && page_size > 0 && max_blocks > 0 && num_splits >= 0, SL8_ERR_INVALID_ARG);
+  SL8_CHECK(T <= 32 && decode_head_dim_ok(d) && page_size % 16 == 0, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  if (B == 0) return SL8_OK;
+  SL8_CHECK(q && k_pages && k_scale_pages && v_pages && v_scale_pages && block_table && seqlens && out,
+            SL8_ERR_INVALID_ARG);
+  SL8_CHECK(aligned16(q) && aligned16(k_pages) && aligned16(v_pages) && aligned16(k_scale_pages) &&
+                aligned16(v_scale_pages),
+            SL8_ERR_INVALID_ARG);
+  const Decode4Plan p = decode4_plan(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
+  SL8_CHECK(p.splits > 0, SL8_ERR_UNSUPPORTED);
+  Decode4Args a{};
+  a.q = q;
+  a.q_dtype = static_cast<sl8_dtype>(q_dtype);
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = static_cast<const uint16_t*>(k_scale_pages);
+  a.v_scale = static_cast<const uint16_t*>(v_scale_pages);
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.seqlens = seqlens;
+  a.mask = tree_mask;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.groups = p.groups;
+  a.cols = p.cols;
+  a.splits = p.splits;
+  a.out = out;
+  a.out_dtype = static_cast<sl8_dtype>(out_dtype);
+  a.lse = lse_out;
+  if (p.splits > decode4_max_cluster()) {
+    const size_t need =
+        sl8_attn_int4_paged_decode_workspace_size(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
+    SL8_CHECK(workspace && workspace_bytes >= need && aligned16(workspace), SL8_ERR_WORKSPACE);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
+                                          decode4_ml_offset(static_cast<int64_t>(B) * T * Hq, d, p.splits));
+  }
+  SL8_LAUNCH(launch_decode4(a, d, static_cast<cudaStream_t>(stream)));
   return SL8_OK;
 }
 

@@ -319,6 +319,32 @@ int list_decode_max_splits();
 // The splits for `lists` lists (counted per group of query heads) of up to `tokens` tokens.
 int list_decode_splits(int64_t lists, int64_t tokens, int32_t d);
 cudaError_t launch_list_decode(const ListDecodeArgs& a, int32_t d, cudaStream_t s);
+// Decode over the paged 4-bit cache (decode4.cu).  The T * Hq / Hkv columns (draft, query head) of a
+// kv head are cut into `groups` of at most `cols`, each of which reads the cache; `splits`
+// CTAs share a sequence: a cluster up to decode4_max_cluster(), more with the combine.
+struct Decode4Args {
+  const void* q;  // [B][T][Hq][d]
+  sl8_dtype q_dtype;
+  const uint8_t *k_pages, *v_pages;
+  const uint16_t *k_scale, *v_scale;
+  int32_t num_pages, page;
+  const int32_t* table;  // [B][max_blocks]
+  int32_t max_blocks;
+  const int32_t* seqlens;
+  const uint32_t* mask;  // [B][T], nullable: causal
+  int32_t B, T, Hq, Hkv;
+  int32_t groups, cols, splits;
+  void* out;
+  sl8_dtype out_dtype;
+  float* lse;
+  float* part_o;    // [B * T * Hq][splits][d], not normalised
+  float2* part_ml;  // [B * T * Hq][splits]: max (log2), sum
+};
+int decode4_max_cluster();
+int32_t decode4_max_columns(int32_t d);
+// The splits for `items` (sequence, kv head, column group)s of up to `tokens` tokens.
+int decode4_splits(int64_t items, int64_t tokens, int32_t d);
+cudaError_t launch_decode4(const Decode4Args& a, int32_t d, cudaStream_t s);
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, cudaStream_t s);
 
 // tokens per stage of the decode kernel for head dim d
