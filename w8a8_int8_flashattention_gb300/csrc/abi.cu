@@ -1256,7 +1256,10 @@ int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_page
   SL8_CHECK(B >= 0 && T > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && d > 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(num_pages > 0 && page_size > 0 && max_blocks > 0 && num_splits >= 0, SL8_ERR_INVALID_ARG);
   SL8_CHECK(T <= 32 && decode_head_dim_ok(d) && page_size % 16 == 0, SL8_ERR_UNSUPPORTED);
-  SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
+  // units of 16 rows are counted in 32 bits
+  SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31) &&
+                static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 35) / Hkv,
+            SL8_ERR_UNSUPPORTED);
   if (B == 0) return SL8_OK;
   SL8_CHECK(q && k_pages && k_scale_pages && v_pages && v_scale_pages && block_table && seqlens && out,
             SL8_ERR_INVALID_ARG);

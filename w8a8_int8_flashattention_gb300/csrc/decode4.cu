@@ -7,16 +7,20 @@
 // GB300 design.  A column is one query row of a kv head: a draft and a query head.  A CTA takes
 // up to 16 columns of one (sequence, kv head) and a contiguous run of its tokens; a cluster of S
 // CTAs, or more with a combine, share a sequence.
-//  * Four warps, each on its own: units of 16 tokens, taken in turn, arrive by 16-byte cp.async in a ring of the
-//    warp's own, so that no warp waits for another before the end.  Page ids are read 32 units ahead.
-//  * S[16 columns x 16 tokens] = Q K^T as fp16 m16n8k16 MMAs: a 4-bit code is or-ed into the
-//    mantissa of 1024 (or, where it lies four bits higher, 16 times as much, against q / 16),
-//    and what that adds, 1032 and 72 times the q's, is in the accumulator from the start: all are
-//    integers below 2^23, so that the group's integer product is exact.  Each group's product meets its scale in fp32.
+//  * Four warps, each on its own: units of 16 tokens, taken in turn, arrive by 16-byte cp.async in a ring of
+//    the warp's own, so that no warp waits for another before the end.  Page ids are read 32 units ahead.
+//  * S[16 tokens x 8 columns] = K Q^T as fp16 m16n8k16 MMAs: a 4-bit code is or-ed into the
+//    mantissa of 1024 (or, where it lies four bits higher, 16 times as much, against q / 16); what
+//    that adds, 1032 and 72 times the q's, comes off again: all are integers below 2^23, so that a
+//    group's integer product is exact.  It meets its scale in fp32.  (The int8 MMA that
+//    would take the codes as they are is slow on this part: 8 of them took 17 cycles an SM each.)
 //  * O^T[d x 8 columns] += V^T P^T as bf16 MMAs: ldmatrix.trans hands each lane the four nibbles of
-//    two tokens' channels, which are codes of bf16 after an or and a subtraction, both exact.  The weights p * s_v
-//    of a group are a sum of bf16 terms, two (2^-17 of themselves left over; 16-bit outputs) or three (fp32).  They have
-//    fp32's range, so that no scale, however far from the others, costs another one its bits.
+//    two tokens' channels, which are codes of bf16 after an or and a subtraction, both exact.  The
+//    weights p * s_v of a group are sums of bf16 terms, two (2^-17 of themselves left over; 16-bit
+//    outputs) or three (fp32).  They have fp32's range, so that no scale, however far from the
+//    others, costs another one its bits.
+//  * The logits of the next unit are computed beside the output of this one, so that neither
+//    chain waits alone; the units that end behind the first draft, at most one a warp, come last, with masks.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,6 +45,28 @@ constexpr int kUnit = 16;  // tokens that a warp takes at a time
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// N 16-bit values from shared memory, as words (N = 1: in the low half).
+template <int N, int M>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[M]) {
+  if constexpr (N == 1) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    w[0] = v;
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a) : "memory");
+  } else if constexpr (N == 4) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(a + 4 * i) : "memory");
+  }
+}
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -58,26 +84,57 @@ __device__ __forceinline__ void ldsm2(uint32_t a, uint32_t& r0, uint32_t& r1) {
 __device__ __forceinline__ void ldsm2_t(uint32_t a, uint32_t& r0, uint32_t& r1) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(a) : "memory");
 }
-// d = a b + c in fp16 with fp32 sums.
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+// d = a b in fp16 with fp32 sums, and d += a b.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// (w & mask) | with as one instruction: written as two operations it stays two, since only one of
+// the constants fits.
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t with) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(kMask), "r"(with));
+  return r;
+}
+constexpr uint32_t k1024 = 0x64006400u, k128 = 0x43004300u;  // fp16 and bf16
 // Two nibbles (bits 0..3 of each half) as bf16 codes: 128 + n, less 136.
 __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((w & 0x000f000fu) | 0x43004300u), "r"(0x43084308u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or<0x000f000fu>(w, k128)), "r"(0x43084308u));
   return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// (x0, x1) += s (a0 + b0, a1 + b1), each operation rounded to fp32, two at a time.
+__device__ __forceinline__ void add_scaled(float& x0, float& x1, float a0, float a1, float b0, float b1, float s) {
+  asm("{\n\t.reg .b64 x, a, b;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 b, {%6, %6};\n\tfma.rn.f32x2 x, a, b, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(s));
 }
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -88,7 +145,7 @@ template <int D, int kCols>
 struct Cfg4 {
   static constexpr int kN = D / kGroup4;                  // groups (and 16-byte chunks) of a row
   static constexpr int kK = 0, kV = 8 * D, kKs = 16 * D, kVs = 17 * D, kUnitBytes = 18 * D;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? (kCols == 8 ? 4 : 5) : D == 64 ? 6 : 8;
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : D == 64 ? 6 : 8;
   static constexpr int kCtas = D == 256 ? 3 : D == 128 ? (kCols == 8 ? 4 : 3) : D == 64 ? (kCols == 8 ? 5 : 4) : 5;
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
   // after the loop the ring holds the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
@@ -103,10 +160,6 @@ struct Cfg4 {
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "kCtas CTAs fit an SM");
 };
 
-// Row of a unit's tile in shared memory that token tau has: tokens 4 t, 4 t + 1 and 4 t + 2,
-// 4 t + 3 of lane t's quad are rows 2 t, 2 t + 1 of the two halves, so that a lane's accumulators are four
-// tokens in a row.
-__device__ __forceinline__ int row_of(int tau) { return ((tau >> 1) & 1) * 8 + (tau >> 2) * 2 + (tau & 1); }
 // Byte offset of chunk j of row r: eight rows' chunks j lie in different banks.
 template <int D>
 __device__ __forceinline__ uint32_t chunk_off(int r, int j) {
@@ -119,7 +172,7 @@ template <int D, int kCols, int kTerms>
 __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     decode4_kernel(const Decode4Args a, DeviceStatus* st) {
   using C = Cfg4<D, kCols>;
-  constexpr int kN = C::kN, kStages = C::kStages, kH = kCols / 8;
+  constexpr int kN = C::kN, kStages = C::kStages, kT = kCols / 8;  // tiles of eight columns
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const bool clustered = a.splits <= kMaxCluster;
@@ -153,48 +206,52 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 
   // ------------------------------------------------------------ loads
   const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
-  auto ids_at = [&](int k) { return k + lane < n ? table[(first + (k + lane) * kWarps) * kUnit / a.page] : 0; };
-  int32_t ids = ids_at(0), next_ids = n > 32 ? ids_at(32) : 0;
-  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * C::kUnitBytes);
-  // the lane's chunks of a unit: K's and V's 16 kN, then the scales' 2 kN each
+  // the sixteenth of a row index at which unit k + lane lies
+  auto rows_at = [&](int k) -> uint32_t {
+    if (k + lane >= n) return 0;
+    const int tok = (first + (k + lane) * kWarps) * kUnit, blk = tok / a.page;
+    int32_t pg = table[blk];
+    if (pg < 0 || pg >= a.num_pages) {
+      record_status(st, kStatusBadArg, 871);
+      pg = 0;
+    }
+    return (static_cast<uint32_t>(pg) * a.Hkv + head) * (a.page / kUnit) + (tok - blk * a.page) / kUnit;
+  };
+  uint32_t rows = rows_at(0), next_rows = n > 32 ? rows_at(32) : 0;
+  // The lane's chunks of a unit: c0, c0 + 32, ... of K's and V's 16 kN, then one of the scales' 2 kN each.
+  // 32 chunks further is 512 bytes further, at d = 256 (four rows) with another swizzle.
   constexpr int kChunks = 16 * kN, kPer = kChunks >= 32 ? kChunks / 32 : 1;
-  auto issue = [&](int k) {  // unit k of this warp
-    if (k < n) {
-      if (k > 0 && k % 32 == 0) {
-        ids = next_ids;
-        next_ids = ids_at(k + 32);
+  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * C::kUnitBytes);
+  const int c0 = kChunks >= 32 ? lane : lane & 15;
+  const uint32_t dst = (kChunks >= 32 || lane < 16 ? C::kK : C::kV) + chunk_off<D>(c0 / kN, c0 % kN);
+  const uint8_t* const src = (kChunks >= 32 || lane < 16 ? a.k_pages : a.v_pages) + 16 * c0;
+  const uint8_t* const src_v = a.v_pages + 16 * lane;
+  const uint8_t* const src_s = reinterpret_cast<const uint8_t*>(lane < 2 * kN ? a.k_scale : a.v_scale) + 16 * (lane % (2 * kN));
+  const uint32_t dst_s = (lane < 2 * kN ? C::kKs : C::kVs) + 16 * (lane % (2 * kN));
+  int issued = 0;
+  uint32_t in = ring;  // the stage that takes the next unit
+  auto issue = [&] {
+    if (issued < n) {
+      if ((issued & 31) == 0 && issued > 0) {
+        rows = next_rows;
+        next_rows = rows_at(issued + 32);
       }
-      int32_t pg = __shfl_sync(0xffffffffu, ids, k & 31);
-      if (pg < 0 || pg >= a.num_pages) {
-        if (lane == 0) record_status(st, kStatusBadArg, 871);
-        pg = 0;
-      }
-      const int64_t row = (static_cast<int64_t>(pg) * a.Hkv + head) * a.page + (first + k * kWarps) * kUnit % a.page;
-      const uint32_t base = ring + static_cast<uint32_t>(k % kStages * C::kUnitBytes);
-      const uint8_t* ksrc = a.k_pages + row * (D / 2);
-      const uint8_t* vsrc = a.v_pages + row * (D / 2);
-      if constexpr (kChunks >= 32) {
+      const uint64_t row = __shfl_sync(0xffffffffu, rows, issued & 31);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int c = lane + 32 * i;
-          const uint32_t dst = base + chunk_off<D>(row_of(c / kN), c % kN);
-          cp_async16(dst + C::kK, ksrc + 16 * c);
-          cp_async16(dst + C::kV, vsrc + 16 * c);
-        }
-      } else {
-        const int c = lane & 15;
-        cp_async16(base + (lane < 16 ? C::kK : C::kV) + chunk_off<D>(row_of(c), 0), (lane < 16 ? ksrc : vsrc) + 16 * c);
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t to = in + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i;
+        cp_async16(to, src + row * (8 * D) + 512 * i);
+        if constexpr (kChunks >= 32) cp_async16(to + (C::kV - C::kK), src_v + row * (8 * D) + 512 * i);
       }
-      if (lane < 4 * kN) {  // scales: 32 kN bytes each
-        const int c = lane % (2 * kN);
-        const uint16_t* src = lane < 2 * kN ? a.k_scale : a.v_scale;
-        cp_async16(base + (lane < 2 * kN ? C::kKs : C::kVs) + 16 * c, reinterpret_cast<const uint8_t*>(src + row * kN) + 16 * c);
-      }
+      cp_async16_if(lane < 4 * kN, in + dst_s, src_s + row * D);
     }
     cp_async_commit();
+    ++issued;
+    in += C::kUnitBytes;
+    if (in == ring + kStages * C::kUnitBytes) in = ring;
   };
 #pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) issue(k);
+  for (int k = 0; k < kStages - 1; ++k) issue();
 
   // ------------------------------------------------------------ the query columns: eight lanes a row
   int8_t* qc = reinterpret_cast<int8_t*>(smem + C::kQc);
@@ -215,208 +272,250 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     if (l8 == 0) qsc[c] = rs.s;
   }
   __syncthreads();
-  // A fragments: rows g and g + 8 are columns; word t of a group's chunk holds channels 8 t .. 8 t + 7,
-  // of which the even ones meet one MMA, the odd ones (whose nibbles stand 16 times as high) another
-  uint32_t qa[kN][2][2 * kH];
-  float bias[kN][4];
-  float qs[kH];
-  uint32_t seen[kH];  // drafts that the column sees
+  // B fragments of Q^T: word t of a group's chunk holds channels 8 t .. 8 t + 7 of column g, of which
+  // the even ones meet one MMA, the odd ones (whose nibbles stand 16 times as high) another
+  uint32_t qb[kN][kT][2][2];
+  float bias[kN][kT][2], qs[kT][2];  // of the lane's accumulator columns 2 t and 2 t + 1
 #pragma unroll
-  for (int h = 0; h < kH; ++h) {
-    const int c = g + 8 * h;
-    qs[h] = qsc[c] * (1.4426950408889634f / sqrtf(static_cast<float>(D)));
-    const int dr = c < GC ? (col0 + c) / G : 0;
-    seen[h] = a.mask ? a.mask[static_cast<int64_t>(b) * a.T + dr] : 0xffffffffu >> (31 - dr);
+  for (int h = 0; h < kT; ++h) {
+    qs[h][0] = qsc[8 * h + 2 * t] * (1.4426950408889634f / sqrtf(static_cast<float>(D)));
+    qs[h][1] = qsc[8 * h + 2 * t + 1] * (1.4426950408889634f / sqrtf(static_cast<float>(D)));
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const uint2 w = *reinterpret_cast<const uint2*>(qc + c * D + 32 * j + 8 * t);
-      float x[8];
-      float even = 0.0f, odd = 0.0f;
+      const uint2 w = *reinterpret_cast<const uint2*>(qc + (g + 8 * h) * D + 32 * j + 8 * t);
+      float x[8], even = 0.0f, odd = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3))));
         if (i & 1) odd += x[i], x[i] *= 0.0625f;
         else even += x[i];
       }
-      qa[j][0][h] = f16x2_of(x[0], x[4]);
-      qa[j][0][kH + h] = f16x2_of(x[2], x[6]);
-      qa[j][1][h] = f16x2_of(x[1], x[5]);
-      qa[j][1][kH + h] = f16x2_of(x[3], x[7]);
+      qb[j][h][0][0] = f16x2_of(x[0], x[4]);
+      qb[j][h][0][1] = f16x2_of(x[2], x[6]);
+      qb[j][h][1][0] = f16x2_of(x[1], x[5]);
+      qb[j][h][1][1] = f16x2_of(x[3], x[7]);
       float f = -(1032.0f * even + 72.0f * odd);
       f += __shfl_xor_sync(0xffffffffu, f, 1);
       f += __shfl_xor_sync(0xffffffffu, f, 2);
-      bias[j][2 * h] = bias[j][2 * h + 1] = f;
-      if (kH == 1) bias[j][2] = bias[j][3] = 0.0f;
+      bias[j][h][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      bias[j][h][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
   }
 
   // ------------------------------------------------------------ the tokens
   const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row and matrix that the lane's address is for
-  float m[kH], th[kH], l[kH];
-  float o[D / 16][kH][4];
+  // columns 2 t and 2 t + 1 of each tile: running maximum, the lazy one's limit, sum over the lane's tokens
+  float m[kT][2], th[kT][2], l[kT][2];
+  float o[D / 16][kT][4];
 #pragma unroll
-  for (int h = 0; h < kH; ++h) m[h] = th[h] = -INFINITY, l[h] = 0.0f;
+  for (int h = 0; h < kT; ++h)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) m[h][c] = th[h][c] = -INFINITY, l[h][c] = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int h = 0; h < kH; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.0f;
+    for (int h = 0; h < kT; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.0f;
   const int base_tok = L - a.T;  // position of the first draft
+  const uint32_t frag = kN == 1   ? chunk_off<D>(8 * (lm & 1) + lr, 0)
+                        : kN == 2 ? chunk_off<D>(8 * (lm >> 1) + lr, lm & 1)
+                                  : chunk_off<D>(lr, lm);
 
-  auto unit = [&](uint32_t base, int tok, auto masked) {
-    constexpr bool kMasked = decltype(masked)::value;
-    // the lane's tokens tok + 4 t + i; seen or not by each of its columns
-    bool vis[kH][4];
-    if constexpr (kMasked) {
-#pragma unroll
-      for (int h = 0; h < kH; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = tok + 4 * t + i;
-          vis[h][i] = p < base_tok || (p < L && ((seen[h] >> (p - base_tok)) & 1u));
-        }
-    }
-    // ---- logits
-    uint32_t kw[2][kN];
+  // Logits of a unit (log2 units): x[h][0], [1] of token g, [2], [3] of token g + 8.
+  auto logits = [&](uint32_t base, float (&x)[kT][4]) {
+    uint32_t kw[2][kN], s0[(kN + 1) / 2], s1[(kN + 1) / 2];
     if constexpr (kN == 1) {
-      ldsm2(base + C::kK + chunk_off<D>(8 * (lm & 1) + lr, 0), kw[0][0], kw[1][0]);
+      ldsm2(base + C::kK + frag, kw[0][0], kw[1][0]);
     } else if constexpr (kN == 2) {
-      ldsm4(base + C::kK + chunk_off<D>(8 * (lm >> 1) + lr, lm & 1), kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
+      ldsm4(base + C::kK + frag, kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
     } else {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int j = 0; j < kN; j += 4)
-          ldsm4(base + C::kK + chunk_off<D>(8 * s + lr, lm + j), kw[s][j], kw[s][j + 1], kw[s][j + 2], kw[s][j + 3]);
+          ldsm4(base + C::kK + (frag ^ (16 * j)) + 16 * D / 4 * s, kw[s][j], kw[s][j + 1], kw[s][j + 2], kw[s][j + 3]);
     }
-    float ks[4][kN];
-    auto scales_at = [&](uint32_t off, float (&f)[4][kN]) {
-      uint32_t w[2 * kN];
-      const uint8_t* p = smem + (base - smem_u32(smem)) + off + 8 * kN * t;
+    lds_words<kN>(base + C::kKs + 2 * kN * g, s0);
+    lds_words<kN>(base + C::kKs + 2 * kN * (g + 8), s1);
 #pragma unroll
-      for (int i = 0; i < 2 * kN; i += 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
-        w[i] = v.x, w[i + 1] = v.y;
-      }
-#pragma unroll
-      for (int i = 0; i < 4 * kN; ++i) f[i / kN][i % kN] = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    };
-    scales_at(C::kKs, ks);
-    float x[kH][4] = {};
-#pragma unroll
-    for (int j = 0; j < kN; ++j)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t w0 = kw[s][j], w8 = w0 >> 8;
-        float acc[4];
-        mma_f16_from(acc, bias[j], qa[j][0][0], kH == 2 ? qa[j][0][1] : 0u, qa[j][0][kH], kH == 2 ? qa[j][0][3] : 0u,
-                     (w0 & 0x000f000fu) | 0x64006400u, (w8 & 0x000f000fu) | 0x64006400u);
-        mma_f16(acc, qa[j][1][0], kH == 2 ? qa[j][1][1] : 0u, qa[j][1][kH], kH == 2 ? qa[j][1][3] : 0u,
-                (w0 & 0x00f000f0u) | 0x64006400u, (w8 & 0x00f000f0u) | 0x64006400u);
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) x[h][2 * s + i] = fmaf(acc[2 * h + i], ks[2 * s + i][j], x[h][2 * s + i]);
-      }
-    // ---- online softmax (log2 units), lazily rescaled
-    bool grow = false;
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[h][i] *= qs[h];
-        if constexpr (kMasked) x[h][i] = vis[h][i] ? x[h][i] : -INFINITY;
-      }
-      grow = grow || fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3])) > th[h];
-    }
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int h = 0; h < kH; ++h) {
-        float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        float f = 1.0f;
-        if (mx > th[h]) {
-          f = ex2(m[h] - mx);
-          m[h] = mx;
-          th[h] = mx + kLazy;
-          l[h] *= f;
-        }
-        const float fa = __shfl_sync(0xffffffffu, f, 8 * t), fb = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          o[i][h][0] *= fa;
-          o[i][h][1] *= fb;
-          o[i][h][2] *= fa;
-          o[i][h][3] *= fb;
-        }
-      }
-    }
-    float p[kH][4];
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[h][i] = ex2(x[h][i] - ref);
-        l[h] += p[h][i];
-      }
-    }
-    // ---- output
-    uint32_t vw[2][kN];
-    if constexpr (kN == 1) {
-      ldsm2_t(base + C::kV + chunk_off<D>(8 * (lm & 1) + lr, 0), vw[0][0], vw[1][0]);
-    } else if constexpr (kN == 2) {
-      ldsm4_t(base + C::kV + chunk_off<D>(8 * (lm >> 1) + lr, lm & 1), vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
-    } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < kN; j += 4)
-          ldsm4_t(base + C::kV + chunk_off<D>(8 * s + lr, lm + j), vw[s][j], vw[s][j + 1], vw[s][j + 2], vw[s][j + 3]);
-    }
-    float vs[4][kN];
-    scales_at(C::kVs, vs);
+    for (int h = 0; h < kT; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      uint32_t wt[kH][kTerms][2];
+      const uint32_t u0 = kw[0][j], u1 = kw[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
+      float acc[kT][4];
 #pragma unroll
-      for (int h = 0; h < kH; ++h)
+      for (int h = 0; h < kT; ++h) {
+        mma_f16_new(acc[h], and_or<0x000f000fu>(u0, k1024), and_or<0x000f000fu>(u1, k1024), and_or<0x000f000fu>(v0, k1024),
+                    and_or<0x000f000fu>(v1, k1024), qb[j][h][0][0], qb[j][h][0][1]);
+        mma_f16_add(acc[h], and_or<0x00f000f0u>(u0, k1024), and_or<0x00f000f0u>(u1, k1024), and_or<0x00f000f0u>(v0, k1024),
+                    and_or<0x00f000f0u>(v1, k1024), qb[j][h][1][0], qb[j][h][1][1]);
+      }
+      const float f0 = __uint_as_float((j & 1) ? s0[j / 2] & 0xffff0000u : s0[j / 2] << 16);
+      const float f1 = __uint_as_float((j & 1) ? s1[j / 2] & 0xffff0000u : s1[j / 2] << 16);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          float w0 = p[h][2 * s] * vs[2 * s][j], w1 = p[h][2 * s + 1] * vs[2 * s + 1][j];
-          if constexpr (kMasked) {  // whatever the scales of rows that are not seen hold
-            w0 = vis[h][2 * s] ? w0 : 0.0f;
-            w1 = vis[h][2 * s + 1] ? w1 : 0.0f;
-          }
+      for (int h = 0; h < kT; ++h) {
+        add_scaled(x[h][0], x[h][1], acc[h][0], acc[h][1], bias[j][h][0], bias[j][h][1], f0);
+        add_scaled(x[h][2], x[h][3], acc[h][2], acc[h][3], bias[j][h][0], bias[j][h][1], f1);
+      }
+    }
 #pragma unroll
-          for (int e = 0; e < kTerms; ++e) {
-            const uint32_t r = bf16x2_of(w0, w1);
-            wt[h][e][s] = r;
-            w0 -= __uint_as_float(r << 16);
-            w1 -= __uint_as_float(r & 0xffff0000u);
+    for (int h = 0; h < kT; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][i] *= qs[h][i & 1];
+  };
+
+  // Online softmax, lazily rescaled: where a logit passes its column's limit, the maximum moves.
+  auto move_maxima = [&](const float (&x)[kT][4]) {
+    bool grow = false;
+#pragma unroll
+    for (int h = 0; h < kT; ++h) grow = grow || fmaxf(x[h][0], x[h][2]) > th[h][0] || fmaxf(x[h][1], x[h][3]) > th[h][1];
+    if (!__any_sync(0xffffffffu, grow)) return;
+#pragma unroll
+    for (int h = 0; h < kT; ++h)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mx = col_max(fmaxf(x[h][c], x[h][2 + c]));
+        if (mx <= th[h][c]) continue;
+        const float f = ex2(m[h][c] - mx);
+        m[h][c] = mx;
+        th[h][c] = mx + kLazy;
+        l[h][c] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][h][c] *= f;
+          o[i][h][2 + c] *= f;
+        }
+      }
+  };
+
+  // O += the unit's weighted rows.  vis: masks of the V scales of column g + 8 h's token pairs (masked).
+  auto output = [&](uint32_t base, const float (&x)[kT][4], const bool masked, const uint32_t (&vis)[kT][2]) {
+    uint32_t vw[2][kN], sc[2][kN];
+    if constexpr (kN == 1) {
+      ldsm2_t(base + C::kV + frag, vw[0][0], vw[1][0]);
+    } else if constexpr (kN == 2) {
+      ldsm4_t(base + C::kV + frag, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < kN; j += 4)
+          ldsm4_t(base + C::kV + (frag ^ (16 * j)) + 16 * D / 4 * s, vw[s][j], vw[s][j + 1], vw[s][j + 2], vw[s][j + 3]);
+    }
+    // scales of tokens 2 t, 2 t + 1 (and + 8), words of two groups a token; below a word of two tokens a group
+    lds_words<2 * kN>(base + C::kVs + 4 * kN * t, sc[0]);
+    lds_words<2 * kN>(base + C::kVs + 4 * kN * (t + 4), sc[1]);
+    // p as bf16 terms, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
+    uint32_t p[kT][kTerms][2];
+#pragma unroll
+    for (int h = 0; h < kT; ++h) {
+      const float ra = m[h][0] == -INFINITY ? 0.0f : m[h][0], rb = m[h][1] == -INFINITY ? 0.0f : m[h][1];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float pa = ex2(x[h][2 * s] - ra), pb = ex2(x[h][2 * s + 1] - rb);
+        l[h][0] += pa;
+        l[h][1] += pb;
+#pragma unroll
+        for (int e = 0; e < kTerms; ++e) {
+          const uint32_t r = bf16x2_of(pa, pb);
+          p[h][e][s] = movm_t(r);
+          pa -= __uint_as_float(r << 16);
+          pb -= __uint_as_float(r & 0xffff0000u);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      uint32_t wt[kT][kTerms][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t pair = kN == 1 ? sc[s][0] : prmt(sc[s][j / 2], sc[s][(kN + j) / 2], (j & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int h = 0; h < kT; ++h) {
+          const uint32_t f = masked ? pair & vis[h][s] : pair;
+          if constexpr (kTerms == 2) {
+            // p0 s less its rounding is exact in bf16, and p1 s joins it
+            wt[h][0][s] = mul_bf16x2(p[h][0][s], f);
+            wt[h][1][s] = fma_bf16x2(p[h][1][s], f, fma_bf16x2(p[h][0][s], f, mul_bf16x2(p[h][0][s] ^ 0x80008000u, f)));
+          } else {
+            float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll
+            for (int e = kTerms - 1; e >= 0; --e) {
+              w0 += __uint_as_float(p[h][e][s] << 16);
+              w1 += __uint_as_float(p[h][e][s] & 0xffff0000u);
+            }
+            w0 *= __uint_as_float(f << 16);
+            w1 *= __uint_as_float(f & 0xffff0000u);
+#pragma unroll
+            for (int e = 0; e < kTerms; ++e) {
+              const uint32_t r = bf16x2_of(w0, w1);
+              wt[h][e][s] = r;
+              w0 -= __uint_as_float(r << 16);
+              w1 -= __uint_as_float(r & 0xffff0000u);
+            }
           }
         }
+      }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
         const uint32_t a0 = codes_bf16x2(vw[0][j] >> (8 * y)), a1 = codes_bf16x2(vw[0][j] >> (8 * y + 4));
         const uint32_t a2 = codes_bf16x2(vw[1][j] >> (8 * y)), a3 = codes_bf16x2(vw[1][j] >> (8 * y + 4));
 #pragma unroll
-        for (int h = 0; h < kH; ++h)
+        for (int h = 0; h < kT; ++h)
 #pragma unroll
           for (int e = 0; e < kTerms; ++e) mma_bf16(o[2 * j + y][h], a0, a1, a2, a3, wt[h][e][0], wt[h][e][1]);
       }
     }
   };
 
-  for (int k = 0; k < n; ++k) {
+  const uint32_t no_mask[kT][2] = {};
+  auto next_stage = [&](uint32_t p) { return p + C::kUnitBytes == ring + kStages * C::kUnitBytes ? ring : p + C::kUnitBytes; };
+  // this warp's last unit can reach past the first draft's position (a sequence has at most three such units)
+  const int whole = n > 0 && (first + (n - 1) * kWarps + 1) * kUnit > base_tok ? n - 1 : n;
+  uint32_t at = ring;
+  float x[kT][4];
+  if (n > 0) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    issue(k + kStages - 1);  // into the stage that the last iteration read
-    const uint32_t base = ring + static_cast<uint32_t>(k % kStages * C::kUnitBytes);
-    const int tok = (first + k * kWarps) * kUnit;
-    if (tok + kUnit > base_tok) unit(base, tok, std::true_type{});
-    else unit(base, tok, std::false_type{});
+    logits(at, x);
+  }
+  for (int k = 0; k < whole; ++k) {
+    move_maxima(x);
     __syncwarp();
+    issue();  // into the stage that the last iteration read
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t next = next_stage(at);
+    float y[kT][4];
+    output(at, x, false, no_mask);
+    logits(next, y);  // of the masked unit, or of a stage that holds none: those are not used
+#pragma unroll
+    for (int h = 0; h < kT; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][i] = y[h][i];
+    at = next;
+  }
+  if (whole < n) {
+    const int tok = (first + whole * kWarps) * kUnit;
+    // the drafts that column c sees
+    auto seen = [&](int c) {
+      const int dr = c < GC ? (col0 + c) / G : 0;
+      return a.mask ? a.mask[static_cast<int64_t>(b) * a.T + dr] : 0xffffffffu >> (31 - dr);
+    };
+    auto visible = [&](uint32_t drafts, int p) { return p < base_tok || (p < L && ((drafts >> (p - base_tok)) & 1u)); };
+    uint32_t vis[kT][2];
+#pragma unroll
+    for (int h = 0; h < kT; ++h) {
+      const uint32_t da = seen(8 * h + 2 * t), db = seen(8 * h + 2 * t + 1), dg = seen(8 * h + g);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int p = tok + g + 8 * s, q = tok + 2 * t + 8 * s;
+        if (!visible(da, p)) x[h][2 * s] = -INFINITY;
+        if (!visible(db, p)) x[h][2 * s + 1] = -INFINITY;
+        vis[h][s] = (visible(dg, q) ? 0xffffu : 0u) | (visible(dg, q + 1) ? 0xffff0000u : 0u);
+      }
+    }
+    move_maxima(x);
+    output(at, x, true, vis);
   }
   cp_async_wait<0>();
 
@@ -428,11 +527,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   float* part = reinterpret_cast<float*>(smem + C::kPart);
   __syncthreads();  // the rings are free
 #pragma unroll
-  for (int h = 0; h < kH; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    m[h] = keep_nan(m[h], l[h]);
-    if (t == 0) *reinterpret_cast<float2*>(stat + (warp * kCols + g + 8 * h) * 2) = make_float2(m[h], l[h]);
+  for (int h = 0; h < kT; ++h) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      l[h][c] = col_sum(l[h][c]);
+      m[h][c] = keep_nan(m[h][c], l[h][c]);
+    }
+    if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(m[h][0], l[h][0], m[h][1], l[h][1]);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
       float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
