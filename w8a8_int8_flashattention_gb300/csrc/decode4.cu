@@ -9,13 +9,14 @@
 // CTAs, or more with a combine, share a sequence.
 //  * Four warps, each on its own: units of 16 tokens, taken in turn, arrive by 16-byte cp.async in a ring of
 //    the warp's own, so that no warp waits for another before the end.  Page ids are read 32 units ahead.
-//  * S[16 tokens x 8 columns] = K Q^T as fp16 m16n8k16 MMAs: a 4-bit code is or-ed into the
-//    mantissa of 1024 (or, where it lies four bits higher, 16 times as much, against q / 16); what
-//    that adds, 1032 and 72 times the q's, comes off again: all are integers below 2^23, so that a
-//    group's integer product is exact.  It meets its scale in fp32.  (The int8 MMA that
-//    would take the codes as they are is slow on this part: 8 of them took 17 cycles an SM each.)
+//  * S[16 tokens x 8 columns] = K Q^T as fp16 m16n8k16 MMAs on the nibbles where they lie, which are
+//    fp16 subnormals, n 2^-24 (or, four bits higher, 16 times that, against q / 16); 8 times the sum of the
+//    q's comes off again.  All partial sums are whole multiples of 2^-24 below 2^17 of them, so that a
+//    group's integer product is exact.  It meets its scale in fp32.  (The int8 MMA that would take the codes as
+//    they are takes 17 cycles an SM on this part, where the fp16 one takes 2 and does half; e4m3
+//    operands, in which nibbles are numbers too, are converted to fp16 one by one.)
 //  * O^T[d x 8 columns] += V^T P^T as bf16 MMAs: ldmatrix.trans hands each lane the four nibbles of
-//    two tokens' channels, which are codes of bf16 after an or and a subtraction, both exact.  The
+//    two tokens' channels; where they lie they are bf16 numbers too, and one fma makes codes of them.  The
 //    weights p * s_v of a group are sums of bf16 terms, two (2^-17 of themselves left over; 16-bit
 //    outputs) or three (fp32).  They have fp32's range, so that no scale, however far from the
 //    others, costs another one its bits.
@@ -42,9 +43,6 @@ constexpr int kMaxCluster = 8;  // CTAs of a cluster (portable)
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = 16;  // tokens that a warp takes at a time
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // N 16-bit values from shared memory, as words (N = 1: in the low half).
 template <int N, int M>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[M]) {
@@ -104,21 +102,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// (w & mask) | with as one instruction: written as two operations it stays two, since only one of
-// the constants fits.
-template <uint32_t kMask>
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t with) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(kMask), "r"(with));
-  return r;
-}
-constexpr uint32_t k1024 = 0x64006400u, k128 = 0x43004300u;  // fp16 and bf16
-// Two nibbles (bits 0..3 of each half) as bf16 codes: 128 + n, less 136.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(and_or<0x000f000fu>(w, k128)), "r"(0x43084308u));
-  return r;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -129,13 +112,15 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-// (x0, x1) += s (a0 + b0, a1 + b1), each operation rounded to fp32, two at a time.
-__device__ __forceinline__ void add_scaled(float& x0, float& x1, float a0, float a1, float b0, float b1, float s) {
-  asm("{\n\t.reg .b64 x, a, b;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 b, {%6, %6};\n\tfma.rn.f32x2 x, a, b, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+// (x0, x1) += (a0, a1) in fp32, as one instruction.
+__device__ __forceinline__ void add_pair(float& x0, float& x1, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, a;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tadd.rn.f32x2 x, x, a;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(x0), "+f"(x1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(s));
+      : "f"(a0), "f"(a1));
 }
+// Nibbles where they lie in a 16-bit word are bf16 numbers, n 2^-133 (bits 0..3) and n 2^-129
+// (bits 4..7, since the exponents 0 and 1 have the same step): times 2^127 and less 8 such, codes.
+constexpr uint32_t k2p127 = 0x7f007f00u, kLow8 = 0xbe00be00u, kHigh8 = 0xc000c000u;  // 2^127, -8 2^-6, -8 2^-2
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -231,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   int issued = 0;
   uint32_t in = ring;  // the stage that takes the next unit
   auto issue = [&] {
-    if (issued < n) {
+    {
+      const bool on = issued < n;
       if ((issued & 31) == 0 && issued > 0) {
         rows = next_rows;
         next_rows = rows_at(issued + 32);
@@ -240,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t to = in + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i;
-        cp_async16(to, src + row * (8 * D) + 512 * i);
-        if constexpr (kChunks >= 32) cp_async16(to + (C::kV - C::kK), src_v + row * (8 * D) + 512 * i);
+        cp_async16_if(on, to, src + row * (8 * D) + 512 * i);
+        if constexpr (kChunks >= 32) cp_async16_if(on, to + (C::kV - C::kK), src_v + row * (8 * D) + 512 * i);
       }
-      cp_async16_if(lane < 4 * kN, in + dst_s, src_s + row * D);
+      cp_async16_if(on && lane < 4 * kN, in + dst_s, src_s + row * D);
     }
     cp_async_commit();
     ++issued;
@@ -278,25 +264,28 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   float bias[kN][kT][2], qs[kT][2];  // of the lane's accumulator columns 2 t and 2 t + 1
 #pragma unroll
   for (int h = 0; h < kT; ++h) {
-    qs[h][0] = qsc[8 * h + 2 * t] * (1.4426950408889634f / sqrtf(static_cast<float>(D)));
-    qs[h][1] = qsc[8 * h + 2 * t + 1] * (1.4426950408889634f / sqrtf(static_cast<float>(D)));
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {  // logits in units of log2, from products of 2^-24; all are 0 where the scale is 0
+      const float s = qsc[8 * h + 2 * t + c];
+      qs[h][c] = s == 0.0f ? 1.0f : s * (0x1p24f * 1.4426950408889634f / sqrtf(static_cast<float>(D)));
+    }
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const uint2 w = *reinterpret_cast<const uint2*>(qc + (g + 8 * h) * D + 32 * j + 8 * t);
-      float x[8], even = 0.0f, odd = 0.0f;
+      float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3))));
-        if (i & 1) odd += x[i], x[i] *= 0.0625f;
-        else even += x[i];
+        if (i & 1) x[i] *= 0.0625f;
       }
       qb[j][h][0][0] = f16x2_of(x[0], x[4]);
       qb[j][h][0][1] = f16x2_of(x[2], x[6]);
       qb[j][h][1][0] = f16x2_of(x[1], x[5]);
       qb[j][h][1][1] = f16x2_of(x[3], x[7]);
-      float f = -(1032.0f * even + 72.0f * odd);
-      f += __shfl_xor_sync(0xffffffffu, f, 1);
-      f += __shfl_xor_sync(0xffffffffu, f, 2);
+      int sum = __dp4a(static_cast<int>(w.x), 0x01010101, __dp4a(static_cast<int>(w.y), 0x01010101, 0));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float f = -8.0f * 0x1p-24f * static_cast<float>(sum);
       bias[j][h][0] = __shfl_sync(0xffffffffu, f, 8 * t);
       bias[j][h][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
@@ -304,13 +293,14 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 
   // ------------------------------------------------------------ the tokens
   const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row and matrix that the lane's address is for
-  // columns 2 t and 2 t + 1 of each tile: running maximum, the lazy one's limit, sum over the lane's tokens
-  float m[kT][2], th[kT][2], l[kT][2];
+  // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to (0 before there is a
+  // token), the logit up to which it stays, and the sum over the lane's tokens
+  float ref[kT][2], th[kT][2], l[kT][2];
   float o[D / 16][kT][4];
 #pragma unroll
   for (int h = 0; h < kT; ++h)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) m[h][c] = th[h][c] = -INFINITY, l[h][c] = 0.0f;
+    for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -320,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
                         : kN == 2 ? chunk_off<D>(8 * (lm >> 1) + lr, lm & 1)
                                   : chunk_off<D>(lr, lm);
 
-  // Logits of a unit (log2 units): x[h][0], [1] of token g, [2], [3] of token g + 8.
+  // Logits of a unit before the scale qs: x[h][0], [1] of token g, [2], [3] of token g + 8.
   auto logits = [&](uint32_t base, float (&x)[kT][4]) {
     uint32_t kw[2][kN], s0[(kN + 1) / 2], s1[(kN + 1) / 2];
     if constexpr (kN == 1) {
@@ -337,33 +327,27 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     lds_words<kN>(base + C::kKs + 2 * kN * g, s0);
     lds_words<kN>(base + C::kKs + 2 * kN * (g + 8), s1);
 #pragma unroll
-    for (int h = 0; h < kT; ++h) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.0f;
-#pragma unroll
     for (int j = 0; j < kN; ++j) {
       const uint32_t u0 = kw[0][j], u1 = kw[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
       float acc[kT][4];
 #pragma unroll
       for (int h = 0; h < kT; ++h) {
-        mma_f16_new(acc[h], and_or<0x000f000fu>(u0, k1024), and_or<0x000f000fu>(u1, k1024), and_or<0x000f000fu>(v0, k1024),
-                    and_or<0x000f000fu>(v1, k1024), qb[j][h][0][0], qb[j][h][0][1]);
-        mma_f16_add(acc[h], and_or<0x00f000f0u>(u0, k1024), and_or<0x00f000f0u>(u1, k1024), and_or<0x00f000f0u>(v0, k1024),
-                    and_or<0x00f000f0u>(v1, k1024), qb[j][h][1][0], qb[j][h][1][1]);
+        mma_f16_new(acc[h], u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[j][h][0][0], qb[j][h][0][1]);
+        mma_f16_add(acc[h], u0 & 0x00f000f0u, u1 & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[j][h][1][0], qb[j][h][1][1]);
       }
       const float f0 = __uint_as_float((j & 1) ? s0[j / 2] & 0xffff0000u : s0[j / 2] << 16);
       const float f1 = __uint_as_float((j & 1) ? s1[j / 2] & 0xffff0000u : s1[j / 2] << 16);
 #pragma unroll
       for (int h = 0; h < kT; ++h) {
-        add_scaled(x[h][0], x[h][1], acc[h][0], acc[h][1], bias[j][h][0], bias[j][h][1], f0);
-        add_scaled(x[h][2], x[h][3], acc[h][2], acc[h][3], bias[j][h][0], bias[j][h][1], f1);
+        add_pair(acc[h][0], acc[h][1], bias[j][h][0], bias[j][h][1]);
+        add_pair(acc[h][2], acc[h][3], bias[j][h][0], bias[j][h][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[h][i] = j == 0 ? acc[h][i] * (i < 2 ? f0 : f1) : fmaf(acc[h][i], i < 2 ? f0 : f1, x[h][i]);
       }
     }
-#pragma unroll
-    for (int h = 0; h < kT; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[h][i] *= qs[h][i & 1];
   };
 
-  // Online softmax, lazily rescaled: where a logit passes its column's limit, the maximum moves.
+  // Online softmax, lazily rescaled: where a logit passes its column's limit, the reference moves.
   auto move_maxima = [&](const float (&x)[kT][4]) {
     bool grow = false;
 #pragma unroll
@@ -373,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     for (int h = 0; h < kT; ++h)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float mx = col_max(fmaxf(x[h][c], x[h][2 + c]));
-        if (mx <= th[h][c]) continue;
-        const float f = ex2(m[h][c] - mx);
-        m[h][c] = mx;
-        th[h][c] = mx + kLazy;
+        const float mx = col_max(fmaxf(x[h][c], x[h][2 + c])), y = mx * qs[h][c];
+        if (!(mx > th[h][c]) || isnan(y)) continue;
+        const float f = th[h][c] == -INFINITY ? 0.0f : ex2(ref[h][c] - y);
+        ref[h][c] = y;
+        th[h][c] = (y + kLazy) / qs[h][c];
         l[h][c] *= f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -408,12 +392,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     uint32_t p[kT][kTerms][2];
 #pragma unroll
     for (int h = 0; h < kT; ++h) {
-      const float ra = m[h][0] == -INFINITY ? 0.0f : m[h][0], rb = m[h][1] == -INFINITY ? 0.0f : m[h][1];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        float pa = ex2(x[h][2 * s] - ra), pb = ex2(x[h][2 * s + 1] - rb);
-        l[h][0] += pa;
-        l[h][1] += pb;
+        float pa = ex2(fmaf(x[h][2 * s], qs[h][0], -ref[h][0])), pb = ex2(fmaf(x[h][2 * s + 1], qs[h][1], -ref[h][1]));
+        add_pair(l[h][0], l[h][1], pa, pb);
 #pragma unroll
         for (int e = 0; e < kTerms; ++e) {
           const uint32_t r = bf16x2_of(pa, pb);
@@ -457,8 +439,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
-        const uint32_t a0 = codes_bf16x2(vw[0][j] >> (8 * y)), a1 = codes_bf16x2(vw[0][j] >> (8 * y + 4));
-        const uint32_t a2 = codes_bf16x2(vw[1][j] >> (8 * y)), a3 = codes_bf16x2(vw[1][j] >> (8 * y + 4));
+        const uint32_t u0 = y ? vw[0][j] >> 8 : vw[0][j], u1 = y ? vw[1][j] >> 8 : vw[1][j];
+        const uint32_t a0 = fma_bf16x2(u0 & 0x000f000fu, k2p127, kLow8), a1 = fma_bf16x2(u0 & 0x00f000f0u, k2p127, kHigh8);
+        const uint32_t a2 = fma_bf16x2(u1 & 0x000f000fu, k2p127, kLow8), a3 = fma_bf16x2(u1 & 0x00f000f0u, k2p127, kHigh8);
 #pragma unroll
         for (int h = 0; h < kT; ++h)
 #pragma unroll
@@ -480,14 +463,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   }
   for (int k = 0; k < whole; ++k) {
     move_maxima(x);
-    __syncwarp();
-    issue();  // into the stage that the last iteration read
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
+    cp_async_wait<kStages - 3>();
+    __syncwarp();  // the next unit's bytes are here for all, and the last one's stage is read
+    issue();
     const uint32_t next = next_stage(at);
     float y[kT][4];
-    output(at, x, false, no_mask);
     logits(next, y);  // of the masked unit, or of a stage that holds none: those are not used
+    output(at, x, false, no_mask);
 #pragma unroll
     for (int h = 0; h < kT; ++h)
 #pragma unroll
@@ -531,14 +513,14 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       l[h][c] = col_sum(l[h][c]);
-      m[h][c] = keep_nan(m[h][c], l[h][c]);
+      ref[h][c] = keep_nan(th[h][c] == -INFINITY ? -INFINITY : ref[h][c], l[h][c]);
     }
-    if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(m[h][0], l[h][0], m[h][1], l[h][1]);
+    if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(ref[h][0], l[h][0], ref[h][1], l[h][1]);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
       float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
-      *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0], o[i][h][1]);
-      *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2], o[i][h][3]);
+      *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0] * 64.0f, o[i][h][1] * 64.0f);
+      *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2] * 4.0f, o[i][h][3] * 4.0f);
     }
   }
   __syncthreads();
