@@ -613,8 +613,11 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *   tree_mask     device, nullable, [B][T] uint32.  NULL: query t sees the tokens up to its own
  *                 position.  Else, as in sl8_attn_int8_decode_verify, those below seqlens[b] - T
  *                 and draft u iff bit u is set.
- *   num_splits    parts that each sequence is cut into (0 = automatic; above 1024 counts as
- *                 1024).  Up to 8 are a cluster of CTAs that merges them, more go through the workspace.
+ *   num_splits    parts that a sequence is cut into.  Up to 8: each into so many, a cluster of CTAs that
+ *                 merges them.  More: the work of all sequences, whose lengths only the device knows, is
+ *                 shared out evenly over so many CTAs for each (sequence, kv head, group) (at most 16 an
+ *                 SM), and a second kernel joins what they cut.  0 = automatic: evenly over the CTAs that fit
+ *                 the device where tables are long enough for that to pay, else a cluster.
  *   out           device, [B][T][Hq][d] of out_dtype; a query that sees no token gets 0.
  *   lse_out       device, nullable, [B][T][Hq] fp32 (natural log; -inf for no token), of the stored
  *                 keys: with a k_mean, sum_c q_c k_mean_c / sqrt(d) below that of the keys themselves.

@@ -1211,38 +1211,32 @@ int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t* k_page
 
 // ---------------------------------------------------------------- decode over the paged 4-bit cache
 struct Decode4Plan {
-  int32_t groups, cols, splits;  // splits 0: invalid or unsupported
+  int32_t groups, cols, splits, ctas;  // groups 0: invalid or unsupported
 };
 static Decode4Plan decode4_plan(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks, int32_t page_size,
                                 int32_t d, int32_t num_splits) {
-  Decode4Plan p{0, 0, 0};
+  Decode4Plan p{0, 0, 0, 0};
   if (B <= 0 || T <= 0 || T > 32 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_blocks <= 0 || page_size <= 0 || num_splits < 0)
     return p;
-  if (static_cast<int64_t>(max_blocks) * page_size > kMaxTokens || page_size % 16 || !decode_head_dim_ok(d)) return p;
+  const int64_t tokens = static_cast<int64_t>(max_blocks) * page_size;
+  if (tokens > kMaxTokens || page_size % 16 || !decode_head_dim_ok(d)) return p;
   if (static_cast<int64_t>(B) * T > (int64_t(1) << 27) / Hq) return p;
   const int64_t columns = static_cast<int64_t>(T) * (Hq / Hkv);
   const int64_t most = decode4_max_columns(d);
-  p.groups = static_cast<int32_t>((columns + most - 1) / most);
-  p.cols = static_cast<int32_t>((columns + p.groups - 1) / p.groups);
-  const int64_t items = static_cast<int64_t>(B) * Hkv * p.groups;
-  int64_t n = num_splits;
-  if (n == 0) n = decode4_splits(items, static_cast<int64_t>(max_blocks) * page_size, d);
-  n = std::min<int64_t>(n, 1024);
-  if (items * n < (int64_t(1) << 31)) p.splits = static_cast<int32_t>(n);
+  const int32_t groups = static_cast<int32_t>((columns + most - 1) / most);
+  p.cols = static_cast<int32_t>((columns + groups - 1) / groups);
+  const int64_t items = static_cast<int64_t>(B) * Hkv * groups;
+  decode4_plan_work(items, tokens, d, p.cols, num_splits, &p.splits, &p.ctas);
+  if (items * p.splits < (int64_t(1) << 31)) p.groups = groups;
   return p;
-}
-
-static size_t decode4_ml_offset(int64_t rows, int32_t d, int32_t S) {
-  return align_up(static_cast<size_t>(rows) * S * d * sizeof(float), 256);
 }
 
 size_t sl8_attn_int4_paged_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t max_blocks,
                                                  int32_t page_size, int32_t d, int32_t num_splits) {
   const Decode4Plan p = decode4_plan(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
-  if (p.splits <= 0) return 0;
-  if (p.splits <= decode4_max_cluster()) return 16;  // none is used
-  const int64_t rows = static_cast<int64_t>(B) * T * Hq;
-  return decode4_ml_offset(rows, d, p.splits) + static_cast<size_t>(rows) * p.splits * 2 * sizeof(float);
+  if (p.groups <= 0) return 0;
+  size_t ml, ends;
+  return p.ctas ? decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends) : 16;  // 16: none is used
 }
 
 int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_pages, const void* k_scale_pages,
@@ -1267,7 +1261,7 @@ int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_page
                 aligned16(v_scale_pages),
             SL8_ERR_INVALID_ARG);
   const Decode4Plan p = decode4_plan(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
-  SL8_CHECK(p.splits > 0, SL8_ERR_UNSUPPORTED);
+  SL8_CHECK(p.groups > 0, SL8_ERR_UNSUPPORTED);
   Decode4Args a{};
   a.q = q;
   a.q_dtype = static_cast<sl8_dtype>(q_dtype);
@@ -1291,13 +1285,15 @@ int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_page
   a.out = out;
   a.out_dtype = static_cast<sl8_dtype>(out_dtype);
   a.lse = lse_out;
-  if (p.splits > decode4_max_cluster()) {
-    const size_t need =
-        sl8_attn_int4_paged_decode_workspace_size(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
+  a.ctas = p.ctas;
+  if (p.ctas) {
+    size_t ml, ends;
+    const size_t need = decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends);
     SL8_CHECK(workspace && workspace_bytes >= need && aligned16(workspace), SL8_ERR_WORKSPACE);
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
-                                          decode4_ml_offset(static_cast<int64_t>(B) * T * Hq, d, p.splits));
+    uint8_t* const w = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float2*>(w + ml);
+    a.ends = reinterpret_cast<int32_t*>(w + ends);
   }
   SL8_LAUNCH(launch_decode4(a, d, static_cast<cudaStream_t>(stream)));
   return SL8_OK;

@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kMaxCluster = 8;  // CTAs of a cluster (portable)
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kUnit = 16;  // tokens that a warp takes at a time
 
 // N 16-bit values from shared memory, as words (N = 1: in the low half).
 template <int N, int M>
@@ -128,22 +127,33 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
 
 template <int D, int kCols>
 struct Cfg4 {
-  static constexpr int kN = D / kGroup4;                  // groups (and 16-byte chunks) of a row
-  static constexpr int kK = 0, kV = 8 * D, kKs = 16 * D, kVs = 17 * D, kUnitBytes = 18 * D;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : D == 64 ? 6 : 8;
+  static constexpr int kN = D / kGroup4;  // groups (and 16-byte chunks) of a row
+  static constexpr int kT = (kCols + 7) / 8;  // tiles of eight columns
+  static constexpr int kU = D == 256 ? 1 : 2;  // units of 16 tokens that a warp takes at a time, a step
+  static constexpr int kStep = 16 * kU;
+  static constexpr int kHalf = kU * 9 * D;  // a step's keys, or its values: codes [kU][16][D / 2], scales [kU][16][kN]
+  static constexpr int kScales = kU * 8 * D;
+  static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
   static constexpr int kCtas = D == 256 ? 3 : D == 128 ? (kCols == 8 ? 4 : 3) : D == 64 ? (kCols == 8 ? 5 : 4) : 5;
-  static constexpr int kRing = kWarps * kStages * kUnitBytes;
-  // after the loop the ring holds the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
-  static constexpr int kRed = 0, kPart = kWarps * D * kCols * 4;
-  static_assert(kPart + kCols * D * 4 <= kRing, "the merge fits the ring");
-  static constexpr int kQc = kRing;                       // [kCols][D] query codes
-  static constexpr int kQs = kQc + kCols * D;             // [kCols] scales
-  static constexpr int kStat = kQs + kCols * 4;           // [warp][kCols][2]: max (log2), sum
+  // after the loop the rings hold the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
+  static constexpr int kRed = 0, kPart = kWarps * D * kCols * 4, kMerge = kPart + kCols * D * 4;
+  static constexpr int kQf = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;  // [kN][kT][32] fragments of Q, 16 bytes
+  static constexpr int kBias = kQf + kN * kT * 512;       // [kN][kT][8] 8 sum of q
+  static constexpr int kQs = kBias + kN * kT * 32;        // [kCols] scales
+  static constexpr int kQc = kQs + kCols * 4;             // [kCols][D] query codes
+  static constexpr int kStat = kQc + kCols * D;           // [warp][kCols][2]: max (log2), sum
   static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps
   static constexpr int kMl = kWt + kWarps * kCols * 4;    // [kCols] max, [kCols] sum of the CTA
   static constexpr int kBytes = kMl + kCols * 8;
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "kCtas CTAs fit an SM");
 };
+
+// The work of a balanced launch: the (sequence, kv head, column group)s in a row, each kStart + its steps
+// long, are cut evenly among `ctas` CTAs, but into no less than kLeast.  kStart stands for what a CTA
+// spends on a sequence besides its steps, queries and merge (without it a CTA that had 32 sequences of one token ran five
+// times as long as the others); an empty sequence counts one step.
+constexpr int kStart = 16, kLeast = 4 * kWarps;
+__device__ __forceinline__ int steps_of(int L, int step) { return max(1, (L + step - 1) / step); }
 
 // Byte offset of chunk j of row r: eight rows' chunks j lie in different banks.
 template <int D>
@@ -152,505 +162,662 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int j) {
   return static_cast<uint32_t>(r * (16 * n) + 16 * (j ^ (((r & 7) / m) & (n - 1))));
 }
 
+// Inclusive prefix over the CTA's threads of one value each.
+__device__ __forceinline__ int64_t cta_prefix(int64_t x, int64_t* sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) x += sm[w];
+  return x;
+}
+
 // kCols: 8 or 16 columns.  kTerms: bf16 terms of a weight.
 template <int D, int kCols, int kTerms>
 __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     decode4_kernel(const Decode4Args a, DeviceStatus* st) {
   using C = Cfg4<D, kCols>;
-  constexpr int kN = C::kN, kStages = C::kStages, kT = kCols / 8;  // tiles of eight columns
+  constexpr int kN = C::kN, kT = C::kT, kU = C::kU;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
-  const bool clustered = a.splits <= kMaxCluster;
-  const int S = a.splits;
-  const unsigned item = blockIdx.x / static_cast<unsigned>(S);
-  const int rank = static_cast<int>(blockIdx.x - item * S);
-  const unsigned bh = item / static_cast<unsigned>(a.groups);
-  const int b = static_cast<int>(bh / static_cast<unsigned>(a.Hkv)), head = static_cast<int>(bh - static_cast<unsigned>(b) * a.Hkv);
-  const int G = a.Hq / a.Hkv;
-  const int col0 = static_cast<int>(item - bh * a.groups) * a.cols;  // first of this CTA's columns
-  const int GC = min(a.cols, a.T * G - col0);
+  const int G = a.Hq / a.Hkv, per_seq = a.Hkv * a.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // row of q and out that column c stands for: its draft, its query head
-  auto row_at = [&](int c) {
-    const int dr = (col0 + c) / G;
-    return (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
-  };
-
-  int L = a.seqlens[b];
   const int cap = a.max_blocks * a.page;
-  if (L < 0 || L > cap) {
+  auto length_of = [&](int b) {
+    const int L = a.seqlens[b];
+    if (L >= 0 && L <= cap) return L;
     if (threadIdx.x == 0) record_status(st, kStatusBadArg, 870);
-    L = L < 0 ? 0 : cap;
-  }
-  // this CTA's units of the sequence, [u0, u1); this warp's are u0 + warp, u0 + warp + 4, ...
-  const int n_all = (L + kUnit - 1) / kUnit;  // below 2^27
-  const int u0 = static_cast<int>(static_cast<int64_t>(n_all) * rank / S);
-  const int u1 = static_cast<int>(static_cast<int64_t>(n_all) * (rank + 1) / S);
-  const int n = max(0, (u1 - u0 - warp + kWarps - 1) / kWarps);
-  const int first = u0 + warp;
-
-  // ------------------------------------------------------------ loads
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
-  // the sixteenth of a row index at which unit k + lane lies
-  auto rows_at = [&](int k) -> uint32_t {
-    if (k + lane >= n) return 0;
-    const int tok = (first + (k + lane) * kWarps) * kUnit, blk = tok / a.page;
-    int32_t pg = table[blk];
-    if (pg < 0 || pg >= a.num_pages) {
-      record_status(st, kStatusBadArg, 871);
-      pg = 0;
-    }
-    return (static_cast<uint32_t>(pg) * a.Hkv + head) * (a.page / kUnit) + (tok - blk * a.page) / kUnit;
+    return L < 0 ? 0 : cap;
   };
-  uint32_t rows = rows_at(0), next_rows = n > 32 ? rows_at(32) : 0;
-  // The lane's chunks of a unit: c0, c0 + 32, ... of K's and V's 16 kN, then one of the scales' 2 kN each.
-  // 32 chunks further is 512 bytes further, at d = 256 (four rows) with another swizzle.
+
+  // ------------------------------------------------------------ this CTA's part of the work
+  if (a.ctas) grid_dependents_launch();  // the combine's CTAs may come as this grid's go
+  const int S = a.ctas ? 1 : a.splits;
+  int rank = 0, b, inner;      // inner: kv head * groups + column group
+  int64_t left = 1;            // balanced: what this CTA still has of its share
+  int s0 = 0;                  // first step of the segment in its sequence; below 0: in its kStart
+  if (a.ctas) {
+    int64_t* scan = reinterpret_cast<int64_t*>(smem);
+    int64_t before = 0, x = 0, end = 0;  // a thread's sequence: its length and where it ends
+    auto chunk = [&](int c) {            // kThreads sequences from c on
+      const int i = c + static_cast<int>(threadIdx.x);
+      x = i < a.B ? static_cast<int64_t>(kStart + steps_of(length_of(i), C::kStep)) * per_seq : 0;
+      end = before + cta_prefix(x, scan);
+      if (threadIdx.x == kThreads - 1) scan[kWarps] = end;
+      __syncthreads();
+      before = scan[kWarps];
+    };
+    for (int c = 0; c < a.B; c += kThreads) chunk(c);
+    // CTA i of `used` has [i q + min(i, r), ...) of the total, q r its quotient and remainder
+    const int64_t total = before, used = max(int64_t(1), min(static_cast<int64_t>(a.ctas), total / kLeast));
+    if (blockIdx.x >= used) return;
+    int64_t q, r;
+    if (total < (int64_t(1) << 31)) {
+      q = static_cast<uint32_t>(total) / static_cast<uint32_t>(used);
+      r = total - q * used;
+    } else {
+      q = total / used;
+      r = total - q * used;
+    }
+    const int64_t from = blockIdx.x * q + min(static_cast<int64_t>(blockIdx.x), r);
+    left = q + (blockIdx.x < r ? 1 : 0);
+    // the sequence that `from` lies in
+    auto find = [&](int c) {
+      if (from >= end - x && from < end) scan[kWarps + 1] = c + static_cast<int>(threadIdx.x), scan[kWarps + 2] = end - x;
+    };
+    if (a.B <= kThreads) {
+      find(0);
+    } else {
+      __syncthreads();
+      before = 0;
+      for (int c = 0; c < a.B && before <= from; c += kThreads) {
+        chunk(c);
+        find(c);
+      }
+    }
+    __syncthreads();
+    b = static_cast<int>(scan[kWarps + 1]);
+    const int64_t off = from - scan[kWarps + 2];
+    const int per = kStart + steps_of(length_of(b), C::kStep);
+    inner = static_cast<int>(off < (int64_t(1) << 31) ? static_cast<uint32_t>(off) / static_cast<uint32_t>(per) : off / per);
+    s0 = static_cast<int>(off - static_cast<int64_t>(inner) * per) - kStart;
+    __syncthreads();
+  } else {
+    const unsigned item = blockIdx.x / static_cast<unsigned>(S);
+    rank = static_cast<int>(blockIdx.x - item * S);
+    b = static_cast<int>(item / static_cast<unsigned>(per_seq));
+    inner = static_cast<int>(item - static_cast<unsigned>(b) * per_seq);
+  }
+
+  // ------------------------------------------------------------ what stays from segment to segment
+  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * C::kRing);
+  // a lane's chunks of a unit's 16 kN: c0, c0 + 32, ..., 512 bytes apart (at d = 256, four rows on, with
+  // another swizzle); of its scales' 2 kN: one, the units of a step side by side
   constexpr int kChunks = 16 * kN, kPer = kChunks >= 32 ? kChunks / 32 : 1;
-  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * C::kUnitBytes);
-  const int c0 = kChunks >= 32 ? lane : lane & 15;
-  const uint32_t dst = (kChunks >= 32 || lane < 16 ? C::kK : C::kV) + chunk_off<D>(c0 / kN, c0 % kN);
-  const uint8_t* const src = (kChunks >= 32 || lane < 16 ? a.k_pages : a.v_pages) + 16 * c0;
-  const uint8_t* const src_v = a.v_pages + 16 * lane;
-  const uint8_t* const src_s = reinterpret_cast<const uint8_t*>(lane < 2 * kN ? a.k_scale : a.v_scale) + 16 * (lane % (2 * kN));
-  const uint32_t dst_s = (lane < 2 * kN ? C::kKs : C::kVs) + 16 * (lane % (2 * kN));
-  int issued = 0;
-  uint32_t in = ring;  // the stage that takes the next unit
-  auto issue = [&] {
-    {
-      const bool on = issued < n;
-      if ((issued & 31) == 0 && issued > 0) {
-        rows = next_rows;
-        next_rows = rows_at(issued + 32);
-      }
-      const uint64_t row = __shfl_sync(0xffffffffu, rows, issued & 31);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t to = in + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i;
-        cp_async16_if(on, to, src + row * (8 * D) + 512 * i);
-        if constexpr (kChunks >= 32) cp_async16_if(on, to + (C::kV - C::kK), src_v + row * (8 * D) + 512 * i);
-      }
-      cp_async16_if(on && lane < 4 * kN, in + dst_s, src_s + row * D);
-    }
-    cp_async_commit();
-    ++issued;
-    in += C::kUnitBytes;
-    if (in == ring + kStages * C::kUnitBytes) in = ring;
-  };
-#pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) issue();
-
-  // ------------------------------------------------------------ the query columns: eight lanes a row
-  int8_t* qc = reinterpret_cast<int8_t*>(smem + C::kQc);
-  float* qsc = reinterpret_cast<float*>(smem + C::kQs);
-  if (4 * warp < kCols) {
-    const int c = 4 * warp + (lane >> 3), l8 = lane & 7;
-    float x[D / 32][4] = {}, amax = 0.0f;
-    if (c < GC) load_runs<D / 32>(a.q, a.q_dtype, row_at(c) * D + 4 * l8, 32, x);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[i][e]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const RowScale rs = row_scale(amax);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint32_t*>(qc + c * D + 32 * i + 4 * l8) = quant4(x[i], rs);
-    if (l8 == 0) qsc[c] = rs.s;
-  }
-  __syncthreads();
-  // B fragments of Q^T: word t of a group's chunk holds channels 8 t .. 8 t + 7 of column g, of which
-  // the even ones meet one MMA, the odd ones (whose nibbles stand 16 times as high) another
-  uint32_t qb[kN][kT][2][2];
-  float bias[kN][kT][2], qs[kT][2];  // of the lane's accumulator columns 2 t and 2 t + 1
-#pragma unroll
-  for (int h = 0; h < kT; ++h) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {  // logits in units of log2, from products of 2^-24; all are 0 where the scale is 0
-      const float s = qsc[8 * h + 2 * t + c];
-      qs[h][c] = s == 0.0f ? 1.0f : s * (0x1p24f * 1.4426950408889634f / sqrtf(static_cast<float>(D)));
-    }
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const uint2 w = *reinterpret_cast<const uint2*>(qc + (g + 8 * h) * D + 32 * j + 8 * t);
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3))));
-        if (i & 1) x[i] *= 0.0625f;
-      }
-      qb[j][h][0][0] = f16x2_of(x[0], x[4]);
-      qb[j][h][0][1] = f16x2_of(x[2], x[6]);
-      qb[j][h][1][0] = f16x2_of(x[1], x[5]);
-      qb[j][h][1][1] = f16x2_of(x[3], x[7]);
-      int sum = __dp4a(static_cast<int>(w.x), 0x01010101, __dp4a(static_cast<int>(w.y), 0x01010101, 0));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float f = -8.0f * 0x1p-24f * static_cast<float>(sum);
-      bias[j][h][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-      bias[j][h][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-    }
-  }
-
-  // ------------------------------------------------------------ the tokens
+  const uint32_t dst = chunk_off<D>((lane % kChunks) / kN, lane % kN);
+  const uint32_t dst_s = C::kScales + 16 * lane;
   const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row and matrix that the lane's address is for
-  // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to (0 before there is a
-  // token), the logit up to which it stays, and the sum over the lane's tokens
-  float ref[kT][2], th[kT][2], l[kT][2];
-  float o[D / 16][kT][4];
-#pragma unroll
-  for (int h = 0; h < kT; ++h)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-    for (int h = 0; h < kT; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.0f;
-  const int base_tok = L - a.T;  // position of the first draft
   const uint32_t frag = kN == 1   ? chunk_off<D>(8 * (lm & 1) + lr, 0)
                         : kN == 2 ? chunk_off<D>(8 * (lm >> 1) + lr, lm & 1)
                                   : chunk_off<D>(lr, lm);
+  const uint32_t qf = smem_u32(smem) + C::kQf + 16 * lane, qbias = smem_u32(smem) + C::kBias + 8 * t;
 
-  // Logits of a unit before the scale qs: x[h][0], [1] of token g, [2], [3] of token g + 8.
-  auto logits = [&](uint32_t base, float (&x)[kT][4]) {
-    uint32_t kw[2][kN], s0[(kN + 1) / 2], s1[(kN + 1) / 2];
-    if constexpr (kN == 1) {
-      ldsm2(base + C::kK + frag, kw[0][0], kw[1][0]);
-    } else if constexpr (kN == 2) {
-      ldsm4(base + C::kK + frag, kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
+  for (;;) {
+    const int head = inner / a.groups;
+    const int col0 = (inner - head * a.groups) * a.cols;  // first of this segment's columns
+    const int GC = min(a.cols, a.T * G - col0);
+    // row of q and out that column c stands for: its draft, its query head
+    auto row_at = [&](int c) {
+      const int dr = (col0 + c) / G;
+      return (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
+    };
+    const int L = length_of(b), per = steps_of(L, C::kStep);
+    int s1 = per;
+    if (a.ctas) {
+      s1 = static_cast<int>(min(static_cast<int64_t>(per), s0 + left));
+      left -= s1 - s0;
+      if (s1 <= 0) return;  // the share ends before the first step
+      s0 = max(s0, 0);
     } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < kN; j += 4)
-          ldsm4(base + C::kK + (frag ^ (16 * j)) + 16 * D / 4 * s, kw[s][j], kw[s][j + 1], kw[s][j + 2], kw[s][j + 3]);
+      s0 = static_cast<int>(static_cast<int64_t>(per) * rank / S);
+      s1 = static_cast<int>(static_cast<int64_t>(per) * (rank + 1) / S);
     }
-    lds_words<kN>(base + C::kKs + 2 * kN * g, s0);
-    lds_words<kN>(base + C::kKs + 2 * kN * (g + 8), s1);
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const uint32_t u0 = kw[0][j], u1 = kw[1][j], v0 = u0 >> 8, v1 = u1 >> 8;
-      float acc[kT][4];
-#pragma unroll
-      for (int h = 0; h < kT; ++h) {
-        mma_f16_new(acc[h], u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[j][h][0][0], qb[j][h][0][1]);
-        mma_f16_add(acc[h], u0 & 0x00f000f0u, u1 & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[j][h][1][0], qb[j][h][1][1]);
-      }
-      const float f0 = __uint_as_float((j & 1) ? s0[j / 2] & 0xffff0000u : s0[j / 2] << 16);
-      const float f1 = __uint_as_float((j & 1) ? s1[j / 2] & 0xffff0000u : s1[j / 2] << 16);
-#pragma unroll
-      for (int h = 0; h < kT; ++h) {
-        add_pair(acc[h][0], acc[h][1], bias[j][h][0], bias[j][h][1]);
-        add_pair(acc[h][2], acc[h][3], bias[j][h][0], bias[j][h][1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[h][i] = j == 0 ? acc[h][i] * (i < 2 ? f0 : f1) : fmaf(acc[h][i], i < 2 ? f0 : f1, x[h][i]);
-      }
-    }
-  };
+    // this warp's steps: first, first + kWarps, ...
+    const int first = s0 + warp, n = max(0, (s1 - first + kWarps - 1) / kWarps);
 
-  // Online softmax, lazily rescaled: where a logit passes its column's limit, the reference moves.
-  auto move_maxima = [&](const float (&x)[kT][4]) {
-    bool grow = false;
+    // ---------------------------------------------------------- loads
+    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
+    // the sixteenth of a row index at which a unit lies; lane i looks up unit i % kU of step k + i / kU
+    auto rows_at = [&](int k) -> uint32_t {
+      const int step = k + lane / kU;
+      if (step >= n) return 0xffffffffu;
+      const int tok = (first + step * kWarps) * C::kStep + lane % kU * 16;
+      if (tok >= L) return 0xffffffffu;
+      const int blk = tok / a.page;
+      int32_t pg = table[blk];
+      if (pg < 0 || pg >= a.num_pages) {
+        record_status(st, kStatusBadArg, 871);
+        pg = 0;
+      }
+      return (static_cast<uint32_t>(pg) * a.Hkv + head) * (a.page / 16) + (tok - blk * a.page) / 16;
+    };
+    constexpr int kBatch = 32 / kU;  // steps that a look-up covers
+    uint32_t rows = rows_at(0), next_rows = n > kBatch ? rows_at(kBatch) : 0xffffffffu;
+    uint32_t row[kU];  // of the step whose keys were asked for last
+    int asked = 0;
+    auto ask = [&](uint32_t to, const uint8_t* codes, const uint16_t* scales) {
 #pragma unroll
-    for (int h = 0; h < kT; ++h) grow = grow || fmaxf(x[h][0], x[h][2]) > th[h][0] || fmaxf(x[h][1], x[h][3]) > th[h][1];
-    if (!__any_sync(0xffffffffu, grow)) return;
+      for (int u = 0; u < kU; ++u) {
+        const bool on = row[u] != 0xffffffffu;
+        const uint8_t* src = codes + static_cast<uint64_t>(row[u]) * (8 * D) + 16 * (lane % kChunks);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          cp_async16_if(on && (kChunks >= 32 || lane < kChunks), to + u * 8 * D + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i, src + 512 * i);
+      }
+      const uint32_t r = kU == 2 && lane >= 2 * kN ? row[kU - 1] : row[0];
+      cp_async16_if(lane < 2 * kN * kU && r != 0xffffffffu, to + dst_s,
+                    reinterpret_cast<const uint8_t*>(scales) + static_cast<uint64_t>(r) * D + 16 * (lane % (2 * kN)));
+    };
+    // the keys of the next step and the values of the one before it
+    auto issue = [&](uint32_t to_k, uint32_t to_v) {
+      if (asked > 0) ask(to_v, a.v_pages, a.v_scale);
+      if (asked % kBatch == 0 && asked > 0) {
+        rows = next_rows;
+        next_rows = rows_at(asked + kBatch);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) row[u] = __shfl_sync(0xffffffffu, rows, asked % kBatch * kU + u);
+      ask(to_k, a.k_pages, a.k_scale);
+      cp_async_commit();
+      ++asked;
+    };
+    issue(ring, 0);
+    issue(ring + C::kHalf, ring + 2 * C::kHalf);
+
+    // ---------------------------------------------------------- the query columns: eight lanes a row
+    int8_t* qc = reinterpret_cast<int8_t*>(smem + C::kQc);
+    float* qsc = reinterpret_cast<float*>(smem + C::kQs);
+    if (4 * warp < kCols) {
+      const int c = 4 * warp + (lane >> 3), l8 = lane & 7;
+      float x[D / 32][4] = {}, amax = 0.0f;
+      if (c < GC) load_runs<D / 32>(a.q, a.q_dtype, row_at(c) * D + 4 * l8, 32, x);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[i][e]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const RowScale rs = row_scale(amax);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint32_t*>(qc + c * D + 32 * i + 4 * l8) = quant4(x[i], rs);
+      if (l8 == 0) qsc[c] = rs.s;
+    }
+    __syncthreads();
+    // B fragments of Q^T: word t of a group's chunk holds channels 8 t .. 8 t + 7 of column g, of which
+    // the even ones meet one MMA, the odd ones (whose nibbles stand 16 times as high) another
+    for (int i = warp; i < kN * kT; i += kWarps) {
+      const int j = i / kT, c = g + 8 * (i % kT);
+      const uint2 w = *reinterpret_cast<const uint2*>(qc + c * D + 32 * j + 8 * t);
+      const uint32_t lo = prmt(w.x ^ 0x80808080u, w.y ^ 0x80808080u, 0x5140), hi = prmt(w.x ^ 0x80808080u, w.y ^ 0x80808080u, 0x7362);
+      auto sixteenth = [](uint32_t x) {
+        uint32_t r;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x2c002c00u));
+        return r;
+      };
+      *reinterpret_cast<uint4*>(smem + C::kQf + i * 512 + 16 * lane) =
+          make_uint4(codes_f16x2(lo, 0x4140), codes_f16x2(hi, 0x4140), sixteenth(codes_f16x2(lo, 0x4342)), sixteenth(codes_f16x2(hi, 0x4342)));
+      int sum = __dp4a(static_cast<int>(w.x), 0x01010101, __dp4a(static_cast<int>(w.y), 0x01010101, 0));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0) reinterpret_cast<float*>(smem + C::kBias)[i * 8 + g] = -8.0f * 0x1p-24f * static_cast<float>(sum);
+    }
+    // of the lane's accumulator columns 2 t and 2 t + 1
+    float qs[kT][2];
 #pragma unroll
     for (int h = 0; h < kT; ++h)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float mx = col_max(fmaxf(x[h][c], x[h][2 + c])), y = mx * qs[h][c];
-        if (!(mx > th[h][c]) || isnan(y)) continue;
-        const float f = th[h][c] == -INFINITY ? 0.0f : ex2(ref[h][c] - y);
-        ref[h][c] = y;
-        th[h][c] = (y + kLazy) / qs[h][c];
-        l[h][c] *= f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          o[i][h][c] *= f;
-          o[i][h][2 + c] *= f;
-        }
+      for (int c = 0; c < 2; ++c) {  // logits in units of log2, from products of 2^-24; all are 0 where the scale is 0
+        const float s = qsc[8 * h + 2 * t + c];
+        qs[h][c] = s == 0.0f ? 1.0f : s * (0x1p24f * 1.4426950408889634f / sqrtf(static_cast<float>(D)));
       }
-  };
+    __syncthreads();
 
-  // O += the unit's weighted rows.  vis: masks of the V scales of column g + 8 h's token pairs (masked).
-  auto output = [&](uint32_t base, const float (&x)[kT][4], const bool masked, const uint32_t (&vis)[kT][2]) {
-    uint32_t vw[2][kN], sc[2][kN];
-    if constexpr (kN == 1) {
-      ldsm2_t(base + C::kV + frag, vw[0][0], vw[1][0]);
-    } else if constexpr (kN == 2) {
-      ldsm4_t(base + C::kV + frag, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
-    } else {
+    // ---------------------------------------------------------- the tokens
+    // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to (0 before there is a
+    // token), the logit up to which it stays, and the sum over the lane's tokens
+    float ref[kT][2], th[kT][2], l[kT][2];
+    float o[D / 16][kT][4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+    for (int h = 0; h < kT; ++h)
 #pragma unroll
-        for (int j = 0; j < kN; j += 4)
-          ldsm4_t(base + C::kV + (frag ^ (16 * j)) + 16 * D / 4 * s, vw[s][j], vw[s][j + 1], vw[s][j + 2], vw[s][j + 3]);
-    }
-    // scales of tokens 2 t, 2 t + 1 (and + 8), words of two groups a token; below a word of two tokens a group
-    lds_words<2 * kN>(base + C::kVs + 4 * kN * t, sc[0]);
-    lds_words<2 * kN>(base + C::kVs + 4 * kN * (t + 4), sc[1]);
-    // p as bf16 terms, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
-    uint32_t p[kT][kTerms][2];
+      for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f;
 #pragma unroll
-    for (int h = 0; h < kT; ++h) {
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float pa = ex2(fmaf(x[h][2 * s], qs[h][0], -ref[h][0])), pb = ex2(fmaf(x[h][2 * s + 1], qs[h][1], -ref[h][1]));
-        add_pair(l[h][0], l[h][1], pa, pb);
+      for (int h = 0; h < kT; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.0f;
+    const int base_tok = L - a.T;  // position of the first draft
+
+    // Logits of a step before the scale qs: x[u][h][0], [1] of token g of unit u, [2], [3] of token g + 8.
+    auto logits = [&](uint32_t base, float (&x)[kU][kT][4]) {
+      uint32_t kw[kU][2][kN], sc[kU][2][(kN + 1) / 2];
 #pragma unroll
-        for (int e = 0; e < kTerms; ++e) {
-          const uint32_t r = bf16x2_of(pa, pb);
-          p[h][e][s] = movm_t(r);
-          pa -= __uint_as_float(r << 16);
-          pb -= __uint_as_float(r & 0xffff0000u);
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t p = base + u * 8 * D + frag, q = base + C::kScales + u * D + 2 * kN * g;
+        if constexpr (kN == 1) {
+          ldsm2(p, kw[u][0][0], kw[u][1][0]);
+        } else if constexpr (kN == 2) {
+          ldsm4(p, kw[u][0][0], kw[u][0][1], kw[u][1][0], kw[u][1][1]);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < kN; j += 4)
+              ldsm4((j ? p ^ (16 * j) : p) + 4 * D * s, kw[u][s][j], kw[u][s][j + 1], kw[u][s][j + 2], kw[u][s][j + 3]);
         }
+        lds_words<kN>(q, sc[u][0]);
+        lds_words<kN>(q + 16 * kN, sc[u][1]);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      uint32_t wt[kT][kTerms][2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t pair = kN == 1 ? sc[s][0] : prmt(sc[s][j / 2], sc[s][(kN + j) / 2], (j & 1) ? 0x7632 : 0x5410);
+      for (int j = 0; j < kN; ++j) {
+        uint32_t qb[kT][4];
+        float bias[kT][2];
 #pragma unroll
         for (int h = 0; h < kT; ++h) {
-          const uint32_t f = masked ? pair & vis[h][s] : pair;
-          if constexpr (kTerms == 2) {
-            // p0 s less its rounding is exact in bf16, and p1 s joins it
-            wt[h][0][s] = mul_bf16x2(p[h][0][s], f);
-            wt[h][1][s] = fma_bf16x2(p[h][1][s], f, fma_bf16x2(p[h][0][s], f, mul_bf16x2(p[h][0][s] ^ 0x80008000u, f)));
-          } else {
-            float w0 = 0.0f, w1 = 0.0f;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(qb[h][0]), "=r"(qb[h][1]), "=r"(qb[h][2]), "=r"(qb[h][3]) : "r"(qf + (j * kT + h) * 512));
+          asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(bias[h][0]), "=f"(bias[h][1]) : "r"(qbias + (j * kT + h) * 32));
+        }
 #pragma unroll
-            for (int e = kTerms - 1; e >= 0; --e) {
-              w0 += __uint_as_float(p[h][e][s] << 16);
-              w1 += __uint_as_float(p[h][e][s] & 0xffff0000u);
-            }
-            w0 *= __uint_as_float(f << 16);
-            w1 *= __uint_as_float(f & 0xffff0000u);
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t u0 = kw[u][0][j], u1 = kw[u][1][j], v0 = u0 >> 8, v1 = u1 >> 8;
+          const float f0 = __uint_as_float((j & 1) ? sc[u][0][j / 2] & 0xffff0000u : sc[u][0][j / 2] << 16);
+          const float f1 = __uint_as_float((j & 1) ? sc[u][1][j / 2] & 0xffff0000u : sc[u][1][j / 2] << 16);
 #pragma unroll
-            for (int e = 0; e < kTerms; ++e) {
-              const uint32_t r = bf16x2_of(w0, w1);
-              wt[h][e][s] = r;
-              w0 -= __uint_as_float(r << 16);
-              w1 -= __uint_as_float(r & 0xffff0000u);
-            }
+          for (int h = 0; h < kT; ++h) {
+            float acc[4];
+            mma_f16_new(acc, u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[h][0], qb[h][1]);
+            mma_f16_add(acc, u0 & 0x00f000f0u, u1 & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[h][2], qb[h][3]);
+            add_pair(acc[0], acc[1], bias[h][0], bias[h][1]);
+            add_pair(acc[2], acc[3], bias[h][0], bias[h][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][h][i] = j == 0 ? acc[i] * (i < 2 ? f0 : f1) : fmaf(acc[i], i < 2 ? f0 : f1, x[u][h][i]);
           }
         }
       }
+    };
+
+    // Online softmax, lazily rescaled: where a logit passes its column's limit, the reference moves.
+    auto move_maxima = [&](const float (&x)[kU][kT][4]) {
+      bool grow = false;
+      float mx[kT][2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
-        const uint32_t u0 = y ? vw[0][j] >> 8 : vw[0][j], u1 = y ? vw[1][j] >> 8 : vw[1][j];
-        const uint32_t a0 = fma_bf16x2(u0 & 0x000f000fu, k2p127, kLow8), a1 = fma_bf16x2(u0 & 0x00f000f0u, k2p127, kHigh8);
-        const uint32_t a2 = fma_bf16x2(u1 & 0x000f000fu, k2p127, kLow8), a3 = fma_bf16x2(u1 & 0x00f000f0u, k2p127, kHigh8);
+      for (int h = 0; h < kT; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[h][c] = fmaxf(x[0][h][c], x[0][h][2 + c]);
+          if constexpr (kU == 2) mx[h][c] = fmaxf(mx[h][c], fmaxf(x[kU - 1][h][c], x[kU - 1][h][2 + c]));
+          grow = grow || mx[h][c] > th[h][c];
+        }
+      if (!__any_sync(0xffffffffu, grow)) return;
+#pragma unroll
+      for (int h = 0; h < kT; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float m = col_max(mx[h][c]), y = m * qs[h][c];
+          if (!(m > th[h][c]) || isnan(y)) continue;
+          const float f = th[h][c] == -INFINITY ? 0.0f : ex2(ref[h][c] - y);
+          ref[h][c] = y;
+          th[h][c] = (y + kLazy) / qs[h][c];
+          l[h][c] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][h][c] *= f;
+            o[i][h][2 + c] *= f;
+          }
+        }
+    };
+
+    // O += a step's weighted rows.  vis: masks of the V scales of column g + 8 h's token pairs (masked).
+    auto output = [&](uint32_t base, const float (&x)[kU][kT][4], const bool masked, const uint32_t (&vis)[kU][kT][2]) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t q = base + u * 8 * D + frag, r = base + C::kScales + u * D + 4 * kN * t;
+        uint32_t vw[2][kN], sc[2][kN];
+        if constexpr (kN == 1) {
+          ldsm2_t(q, vw[0][0], vw[1][0]);
+        } else if constexpr (kN == 2) {
+          ldsm4_t(q, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < kN; j += 4)
+              ldsm4_t((j ? q ^ (16 * j) : q) + 4 * D * s, vw[s][j], vw[s][j + 1], vw[s][j + 2], vw[s][j + 3]);
+        }
+        // scales of tokens 2 t, 2 t + 1 (and + 8)
+        lds_words<2 * kN>(r, sc[0]);
+        lds_words<2 * kN>(r + 16 * kN, sc[1]);
+        // p as bf16 terms, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
+        uint32_t p[kT][kTerms][2];
 #pragma unroll
         for (int h = 0; h < kT; ++h)
 #pragma unroll
-          for (int e = 0; e < kTerms; ++e) mma_bf16(o[2 * j + y][h], a0, a1, a2, a3, wt[h][e][0], wt[h][e][1]);
+          for (int s = 0; s < 2; ++s) {
+            float pa = ex2(fmaf(x[u][h][2 * s], qs[h][0], -ref[h][0])), pb = ex2(fmaf(x[u][h][2 * s + 1], qs[h][1], -ref[h][1]));
+            add_pair(l[h][0], l[h][1], pa, pb);
+#pragma unroll
+            for (int e = 0; e < kTerms; ++e) {
+              const uint32_t w = bf16x2_of(pa, pb);
+              p[h][e][s] = movm_t(w);
+              pa -= __uint_as_float(w << 16);
+              pb -= __uint_as_float(w & 0xffff0000u);
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          uint32_t wt[kT][kTerms][2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            // the group's scales of a token pair
+            const uint32_t pair = kN == 1 ? sc[s][0] : prmt(sc[s][j / 2], sc[s][(kN + j) / 2], (j & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int h = 0; h < kT; ++h) {
+              const uint32_t f = masked ? pair & vis[u][h][s] : pair;
+              if constexpr (kTerms == 2) {
+                // p0 s less its rounding is exact in bf16, and p1 s joins it
+                wt[h][0][s] = mul_bf16x2(p[h][0][s], f);
+                wt[h][1][s] = fma_bf16x2(p[h][1][s], f, fma_bf16x2(p[h][0][s], f, mul_bf16x2(p[h][0][s] ^ 0x80008000u, f)));
+              } else {
+                float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll
+                for (int e = kTerms - 1; e >= 0; --e) {
+                  w0 += __uint_as_float(p[h][e][s] << 16);
+                  w1 += __uint_as_float(p[h][e][s] & 0xffff0000u);
+                }
+                w0 *= __uint_as_float(f << 16);
+                w1 *= __uint_as_float(f & 0xffff0000u);
+#pragma unroll
+                for (int e = 0; e < kTerms; ++e) {
+                  const uint32_t w = bf16x2_of(w0, w1);
+                  wt[h][e][s] = w;
+                  w0 -= __uint_as_float(w << 16);
+                  w1 -= __uint_as_float(w & 0xffff0000u);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
+            const uint32_t u0 = y ? vw[0][j] >> 8 : vw[0][j], u1 = y ? vw[1][j] >> 8 : vw[1][j];
+            const uint32_t a0 = fma_bf16x2(u0 & 0x000f000fu, k2p127, kLow8), a1 = fma_bf16x2(u0 & 0x00f000f0u, k2p127, kHigh8);
+            const uint32_t a2 = fma_bf16x2(u1 & 0x000f000fu, k2p127, kLow8), a3 = fma_bf16x2(u1 & 0x00f000f0u, k2p127, kHigh8);
+#pragma unroll
+            for (int h = 0; h < kT; ++h)
+#pragma unroll
+              for (int e = 0; e < kTerms; ++e) mma_bf16(o[2 * j + y][h], a0, a1, a2, a3, wt[h][e][0], wt[h][e][1]);
+          }
+        }
       }
-    }
-  };
-
-  const uint32_t no_mask[kT][2] = {};
-  auto next_stage = [&](uint32_t p) { return p + C::kUnitBytes == ring + kStages * C::kUnitBytes ? ring : p + C::kUnitBytes; };
-  // this warp's last unit can reach past the first draft's position (a sequence has at most three such units)
-  const int whole = n > 0 && (first + (n - 1) * kWarps + 1) * kUnit > base_tok ? n - 1 : n;
-  uint32_t at = ring;
-  float x[kT][4];
-  if (n > 0) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    logits(at, x);
-  }
-  for (int k = 0; k < whole; ++k) {
-    move_maxima(x);
-    cp_async_wait<kStages - 3>();
-    __syncwarp();  // the next unit's bytes are here for all, and the last one's stage is read
-    issue();
-    const uint32_t next = next_stage(at);
-    float y[kT][4];
-    logits(next, y);  // of the masked unit, or of a stage that holds none: those are not used
-    output(at, x, false, no_mask);
-#pragma unroll
-    for (int h = 0; h < kT; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[h][i] = y[h][i];
-    at = next;
-  }
-  if (whole < n) {
-    const int tok = (first + whole * kWarps) * kUnit;
-    // the drafts that column c sees
-    auto seen = [&](int c) {
-      const int dr = c < GC ? (col0 + c) / G : 0;
-      return a.mask ? a.mask[static_cast<int64_t>(b) * a.T + dr] : 0xffffffffu >> (31 - dr);
     };
-    auto visible = [&](uint32_t drafts, int p) { return p < base_tok || (p < L && ((drafts >> (p - base_tok)) & 1u)); };
-    uint32_t vis[kT][2];
+
+    const uint32_t no_mask[kU][kT][2] = {};
+    // this warp's last step can reach past the first draft's position (a sequence has at most three such steps)
+    const int whole = n > 0 && (first + (n - 1) * kWarps + 1) * C::kStep > base_tok ? n - 1 : n;
+    uint32_t now = 0;  // half of the rings that this step's values are in, and its keys were
+    float x[kU][kT][4];
+    cp_async_wait<1>();
+    __syncwarp();
+    logits(ring, x);  // a warp without steps: of stale bytes, not used
+    for (int k = 0; k < whole; ++k) {
+      move_maxima(x);
+      cp_async_wait<0>();
+      __syncwarp();  // this step's values and the next one's keys are here for all, and what they replace is read
+      const uint32_t then = C::kHalf - now;
+      issue(ring + now, ring + 2 * C::kHalf + then);
+      float y[kU][kT][4];
+      logits(ring + then, y);  // of the masked step, or of stale bytes: those are not used
+      output(ring + 2 * C::kHalf + now, x, false, no_mask);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int h = 0; h < kT; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][h][i] = y[u][h][i];
+      now = then;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    if (whole < n) {
+      const int tok = (first + whole * kWarps) * C::kStep;
+      // the drafts that column c sees
+      auto seen = [&](int c) {
+        const int dr = c < GC ? (col0 + c) / G : 0;
+        return a.mask ? a.mask[static_cast<int64_t>(b) * a.T + dr] : 0xffffffffu >> (31 - dr);
+      };
+      auto visible = [&](uint32_t drafts, int p) { return p < base_tok || (p < L && ((drafts >> (p - base_tok)) & 1u)); };
+      uint32_t vis[kU][kT][2];
+#pragma unroll
+      for (int h = 0; h < kT; ++h) {
+        const uint32_t da = seen(8 * h + 2 * t), db = seen(8 * h + 2 * t + 1), dg = seen(8 * h + g);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int p = tok + 16 * u + g + 8 * s, q = tok + 16 * u + 2 * t + 8 * s;
+            if (!visible(da, p)) x[u][h][2 * s] = -INFINITY;
+            if (!visible(db, p)) x[u][h][2 * s + 1] = -INFINITY;
+            vis[u][h][s] = (visible(dg, q) ? 0xffffu : 0u) | (visible(dg, q + 1) ? 0xffff0000u : 0u);
+          }
+      }
+      move_maxima(x);
+      output(ring + 2 * C::kHalf + now, x, true, vis);
+    }
+
+    // ---------------------------------------------------------- the CTA's state from its warps'
+    float* stat = reinterpret_cast<float*>(smem + C::kStat);
+    float* red = reinterpret_cast<float*>(smem + C::kRed);
+    float* wt = reinterpret_cast<float*>(smem + C::kWt);
+    float* ml = reinterpret_cast<float*>(smem + C::kMl);
+    float* part = reinterpret_cast<float*>(smem + C::kPart);
+    __syncthreads();  // the rings are free
 #pragma unroll
     for (int h = 0; h < kT; ++h) {
-      const uint32_t da = seen(8 * h + 2 * t), db = seen(8 * h + 2 * t + 1), dg = seen(8 * h + g);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int p = tok + g + 8 * s, q = tok + 2 * t + 8 * s;
-        if (!visible(da, p)) x[h][2 * s] = -INFINITY;
-        if (!visible(db, p)) x[h][2 * s + 1] = -INFINITY;
-        vis[h][s] = (visible(dg, q) ? 0xffffu : 0u) | (visible(dg, q + 1) ? 0xffff0000u : 0u);
+      for (int c = 0; c < 2; ++c) {
+        l[h][c] = col_sum(l[h][c]);
+        ref[h][c] = keep_nan(th[h][c] == -INFINITY ? -INFINITY : ref[h][c], l[h][c]);
+      }
+      if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(ref[h][0], l[h][0], ref[h][1], l[h][1]);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
+        float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
+        *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0] * 64.0f, o[i][h][1] * 64.0f);
+        *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2] * 4.0f, o[i][h][3] * 4.0f);
       }
     }
-    move_maxima(x);
-    output(at, x, true, vis);
-  }
-  cp_async_wait<0>();
-
-  // ------------------------------------------------------------ the CTA's state from its warps'
-  float* stat = reinterpret_cast<float*>(smem + C::kStat);
-  float* red = reinterpret_cast<float*>(smem + C::kRed);
-  float* wt = reinterpret_cast<float*>(smem + C::kWt);
-  float* ml = reinterpret_cast<float*>(smem + C::kMl);
-  float* part = reinterpret_cast<float*>(smem + C::kPart);
-  __syncthreads();  // the rings are free
-#pragma unroll
-  for (int h = 0; h < kT; ++h) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      l[h][c] = col_sum(l[h][c]);
-      ref[h][c] = keep_nan(th[h][c] == -INFINITY ? -INFINITY : ref[h][c], l[h][c]);
-    }
-    if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(ref[h][0], l[h][0], ref[h][1], l[h][1]);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
-      float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
-      *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0] * 64.0f, o[i][h][1] * 64.0f);
-      *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2] * 4.0f, o[i][h][3] * 4.0f);
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < kCols * kWarps) {  // column c: the weight of warp w's state, and (w = 0) max and sum
-    const int c = threadIdx.x % kCols, w = threadIdx.x / kCols;
-    float M = -INFINITY, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, stat[(i * kCols + c) * 2]);
-    const float mw = stat[(w * kCols + c) * 2];
-    wt[w * kCols + c] = mw == -INFINITY ? 0.0f : ex2(mw - M);
-    if (w == 0) {
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float mi = stat[(i * kCols + c) * 2];
-        if (mi != -INFINITY) sum = fmaf(ex2(mi - M), stat[(i * kCols + c) * 2 + 1], sum);
-      }
-      ml[c] = M;
-      ml[kCols + c] = sum;
-    }
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < D * (kCols / 4); u += kThreads) {  // row u % D, columns 4 (u / D) ..
-    const int r = u % D, q4 = u / D;
-    const int dim = 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1);
-    if (4 * q4 >= GC) continue;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(red + (w * D + r) * kCols + 4 * q4);
-      const float4 f = *reinterpret_cast<const float4*>(wt + w * kCols + 4 * q4);
-      acc.x = fmaf(v.x, f.x, acc.x);
-      acc.y = fmaf(v.y, f.y, acc.y);
-      acc.z = fmaf(v.z, f.z, acc.z);
-      acc.w = fmaf(v.w, f.w, acc.w);
-    }
-    part[(4 * q4 + 0) * D + dim] = acc.x;
-    part[(4 * q4 + 1) * D + dim] = acc.y;
-    part[(4 * q4 + 2) * D + dim] = acc.z;
-    part[(4 * q4 + 3) * D + dim] = acc.w;
-  }
-
-  if (!clustered) {  // to the workspace, for the combine
     __syncthreads();
-    for (int u = threadIdx.x; u < GC * D; u += kThreads) {
-      const int c = u / D;
-      a.part_o[(row_at(c) * S + rank) * D + u % D] = part[u];
-      if (u % D == 0) a.part_ml[row_at(c) * S + rank] = make_float2(ml[c], ml[kCols + c]);
-    }
-    return;
-  }
-  // ------------------------------------------------------------ merge the S parts of the cluster
-  if (S > 1) cluster.sync();
-  else __syncthreads();
-  for (int u = rank * kThreads + threadIdx.x; u < GC * D; u += S * kThreads) {
-    const int c = u / D, dim = u % D;
-    float mr[kMaxCluster], lr2[kMaxCluster], x[kMaxCluster];  // all on their way at once
+    if (threadIdx.x < kCols * kWarps) {  // column c: the weight of warp w's state, and (w = 0) max and sum
+      const int c = threadIdx.x % kCols, w = threadIdx.x / kCols;
+      float M = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      if (r < S) {
-        const float* peer = reinterpret_cast<const float*>(S > 1 ? cluster.map_shared_rank(smem, r) : smem);
-        mr[r] = peer[C::kMl / 4 + c];
-        lr2[r] = peer[C::kMl / 4 + kCols + c];
-        x[r] = peer[C::kPart / 4 + c * D + dim];
+      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, stat[(i * kCols + c) * 2]);
+      const float mw = stat[(w * kCols + c) * 2];
+      wt[w * kCols + c] = mw == -INFINITY ? 0.0f : ex2(mw - M);
+      if (w == 0) {
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float mi = stat[(i * kCols + c) * 2];
+          if (mi != -INFINITY) sum = fmaf(ex2(mi - M), stat[(i * kCols + c) * 2 + 1], sum);
+        }
+        ml[c] = M;
+        ml[kCols + c] = sum;
       }
     }
-    float M = -INFINITY, sum = 0.0f, acc = 0.0f;
+    __syncthreads();
+    for (int u = threadIdx.x; u < D * (kCols / 4); u += kThreads) {  // row u % D, columns 4 (u / D) ..
+      const int r = u % D, q4 = u / D;
+      const int dim = 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1);
+      if (4 * q4 >= GC) continue;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < S) M = fmaxf(M, mr[r]);
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(red + (w * D + r) * kCols + 4 * q4);
+        const float4 f = *reinterpret_cast<const float4*>(wt + w * kCols + 4 * q4);
+        acc.x = fmaf(v.x, f.x, acc.x);
+        acc.y = fmaf(v.y, f.y, acc.y);
+        acc.z = fmaf(v.z, f.z, acc.z);
+        acc.w = fmaf(v.w, f.w, acc.w);
+      }
+      part[(4 * q4 + 0) * D + dim] = acc.x;
+      part[(4 * q4 + 1) * D + dim] = acc.y;
+      part[(4 * q4 + 2) * D + dim] = acc.z;
+      part[(4 * q4 + 3) * D + dim] = acc.w;
+    }
+    if (S > 1) cluster.sync();
+    else __syncthreads();
+
+    if (a.ctas && threadIdx.x == 0) {  // the CTAs that have the first and the last step
+      int32_t* const ends = a.ends + 2 * (static_cast<int64_t>(b) * per_seq + inner);
+      if (s0 == 0) ends[0] = static_cast<int32_t>(blockIdx.x);
+      if (s1 == per) ends[1] = static_cast<int32_t>(blockIdx.x);
+    }
+    if (a.ctas && s1 - s0 < per) {
+      // a part of a sequence, for the combine: slot 0 of this CTA where its work begins, else 1
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0);
+      float* po = a.part_o + slot * (kCols * D);
+      for (int u = threadIdx.x; u < GC * D; u += kThreads) po[u] = part[u];
+      if (threadIdx.x < GC) a.part_ml[slot * kCols + threadIdx.x] = make_float2(ml[threadIdx.x], ml[kCols + threadIdx.x]);
+    } else {
+      // ------------------------------------------------------ merge the S parts of the cluster
+      for (int u = rank * kThreads + threadIdx.x; u < GC * D; u += S * kThreads) {
+        const int c = u / D, dim = u % D;
+        float mr[kMaxCluster], lr2[kMaxCluster], xr[kMaxCluster];  // all on their way at once
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      if (r < S && mr[r] != -INFINITY) {
-        const float f = ex2(mr[r] - M);
-        sum = fmaf(f, lr2[r], sum);
-        acc = fmaf(f, x[r], acc);
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r < S) {
+            const float* peer = reinterpret_cast<const float*>(S > 1 ? cluster.map_shared_rank(smem, r) : smem);
+            mr[r] = peer[C::kMl / 4 + c];
+            lr2[r] = peer[C::kMl / 4 + kCols + c];
+            xr[r] = peer[C::kPart / 4 + c * D + dim];
+          }
+        }
+        float M = -INFINITY, sum = 0.0f, acc = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < S) M = fmaxf(M, mr[r]);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r < S && mr[r] != -INFINITY) {
+            const float f = ex2(mr[r] - M);
+            sum = fmaf(f, lr2[r], sum);
+            acc = fmaf(f, xr[r], acc);
+          }
+        }
+        const int64_t out_row = row_at(c);
+        store_out(a.out, a.out_dtype, out_row * D + dim, sum == 0.0f ? 0.0f : acc / sum);
+        if (a.lse && dim == 0) a.lse[out_row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
       }
     }
-    const int64_t row = row_at(c);
-    store_out(a.out, a.out_dtype, row * D + dim, sum == 0.0f ? 0.0f : acc / sum);
-    if (a.lse && dim == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    if (S > 1) cluster.sync();  // no CTA leaves while another reads its part
+    if (!a.ctas) return;
+    if (left <= 0) return;
+    s0 = -kStart;
+    if (++inner == per_seq) inner = 0, ++b;
+    __syncthreads();  // the parts are read
   }
-  if (S > 1) cluster.sync();  // no CTA leaves while another reads its part
 }
 
-// The S parts of each row from the workspace: one warp a row and 32 channels.
-template <int D>
-__global__ void __launch_bounds__(128) decode4_combine_kernel(const Decode4Args a, int64_t rows) {
+// The parts of each (sequence, kv head, column group) of a balanced launch that was cut, one CTA a
+// column: D / 4 threads take a part, the next ones another.
+constexpr int kJoin = 256;
+template <int D, int kCols>
+__global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Args a) {
+  constexpr int kRow = D / 4, kAtOnce = kJoin / kRow;
+  __shared__ float4 sm[kJoin];
+  __shared__ float red[kJoin / 32], sums[kAtOnce];
+  const int per_seq = a.Hkv * a.groups, G = a.Hq / a.Hkv;
+  const unsigned item = blockIdx.x / static_cast<unsigned>(a.cols);
+  const int c = static_cast<int>(blockIdx.x - item * a.cols);
+  const int b = static_cast<int>(item / static_cast<unsigned>(per_seq));
+  const int inner = static_cast<int>(item - static_cast<unsigned>(b) * per_seq);
+  const int head = inner / a.groups, col0 = (inner - head * a.groups) * a.cols;
+  if (col0 + c >= a.T * G) return;
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t row = w / (D / 32);
-  if (row >= rows) return;
-  const int dim = static_cast<int>(w % (D / 32)) * 32 + lane;
-  const float2* ml = a.part_ml + row * a.splits;
+  const int2 ends = reinterpret_cast<const int2*>(a.ends)[item];
+  const int i0 = ends.x, i1 = ends.y;
+  if (i0 == i1) return;  // written by that CTA
+  auto slot_of = [&](int i) { return static_cast<int64_t>(2 * i + (i == i0 ? 1 : 0)); };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float M = -INFINITY;
-  for (int r = lane; r < a.splits; r += 32) M = fmaxf(M, ml[r].x);
+  for (int i = i0 + static_cast<int>(threadIdx.x); i <= i1; i += kJoin) M = fmaxf(M, a.part_ml[slot_of(i) * kCols + c].x);
   M = warp_max_f(M);
-  float sum = 0.0f, acc = 0.0f;
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoin / 32; ++w) M = fmaxf(M, red[w]);
+  const int q = static_cast<int>(threadIdx.x) % kRow, r = static_cast<int>(threadIdx.x) / kRow;
+  float sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int r = 0; r < a.splits; ++r) {
-    const float2 v = ml[r];
-    const float x = a.part_o[(row * a.splits + r) * D + dim];
+  for (int i = i0 + r; i <= i1; i += kAtOnce) {
+    const int64_t slot = slot_of(i);
+    const float2 v = a.part_ml[slot * kCols + c];
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot * kCols + c) * D + 4 * q);
     if (v.x != -INFINITY) {
       const float f = ex2(v.x - M);
       sum = fmaf(f, v.y, sum);
-      acc = fmaf(f, x, acc);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
     }
   }
-  store_out(a.out, a.out_dtype, row * D + dim, sum == 0.0f ? 0.0f : acc / sum);
-  if (a.lse && dim == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+  sm[threadIdx.x] = acc;
+  if (q == 0) sums[r] = sum;
+  __syncthreads();
+  if (r > 0) return;
+  sum = sums[0];
+  for (int i = 1; i < kAtOnce; ++i) {
+    const float4 x = sm[i * kRow + q];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+    sum += sums[i];
+  }
+  const int dr = (col0 + c) / G;
+  const int64_t row = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
+  const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) store_out(a.out, a.out_dtype, row * D + 4 * q + i, sum == 0.0f ? 0.0f : x[i] / sum);
+  if (a.lse && q == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int kCols, int kTerms>
 cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
   using C = Cfg4<D, kCols>;
   auto kern = decode4_kernel<D, kCols, kTerms>;
-  const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
+  const unsigned items = static_cast<unsigned>(a.B) * a.Hkv * a.groups;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hkv * a.groups * a.splits);
+  cfg.gridDim = dim3(a.ctas ? static_cast<unsigned>(a.ctas) : items * a.splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.splits <= kMaxCluster ? a.splits : 1;
+  attr[0].val.clusterDim.x = a.ctas ? 1 : a.splits;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
+  e = cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
+  if (e != cudaSuccess || !a.ctas) return e;
+  return launch_pdl(decode4_combine_kernel<D, kCols>, dim3(items * a.cols), dim3(kJoin), 0, s, a);
 }
 
 template <int D, int kCols>
@@ -660,27 +827,47 @@ cudaError_t launch_c(const Decode4Args& a, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_d(const Decode4Args& a, cudaStream_t s) {
-  cudaError_t e;
-  if constexpr (D == 256) e = launch_c<D, 8>(a, s);
-  else e = a.cols > 8 ? launch_c<D, 16>(a, s) : launch_c<D, 8>(a, s);
-  if (e != cudaSuccess || a.splits <= kMaxCluster) return e;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  const unsigned grid = static_cast<unsigned>((rows * (D / 32) + 3) / 4);
-  return launch_pdl(decode4_combine_kernel<D>, dim3(grid), dim3(128), 0, s, a, rows);
+  if constexpr (D == 256) return launch_c<D, 8>(a, s);
+  else return a.cols > 8 ? launch_c<D, 16>(a, s) : launch_c<D, 8>(a, s);
+}
+
+// CTAs of the kernel that fit the device at once.
+int slots(int32_t d, int32_t cols) {
+  const int n = d == 256 ? Cfg4<256, 8>::kCtas
+                : d == 128 ? (cols > 8 ? Cfg4<128, 16>::kCtas : Cfg4<128, 8>::kCtas)
+                : d == 64  ? (cols > 8 ? Cfg4<64, 16>::kCtas : Cfg4<64, 8>::kCtas)
+                           : (cols > 8 ? Cfg4<32, 16>::kCtas : Cfg4<32, 8>::kCtas);
+  return n * num_sms();
 }
 
 }  // namespace
 
-int decode4_max_cluster() { return kMaxCluster; }
 int32_t decode4_max_columns(int32_t d) { return d == 256 ? 8 : 16; }
 
-int decode4_splits(int64_t items, int64_t tokens, int32_t d) {
-  const int64_t fit = 4 * static_cast<int64_t>(num_sms());
-  if (items * kMaxCluster < num_sms() && tokens >= 4096 * kMaxCluster)
-    return static_cast<int>(std::max<int64_t>(kMaxCluster + 1, std::min<int64_t>(64, fit / items)));
-  int n = 1;
-  while (n < kMaxCluster && items * (n + 1) <= fit && tokens / (n + 1) >= 128) ++n;
-  return n;
+void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, int32_t num_splits, int32_t* splits,
+                       int32_t* ctas) {
+  const int64_t fit = slots(d, cols), many = 16ll * num_sms();
+  *splits = 1;
+  *ctas = 0;
+  const bool counted = items < (int64_t(1) << 50) / (tokens + 1);  // steps and shares stay within 64 bits
+  if (num_splits > kMaxCluster) {
+    if (counted) *ctas = static_cast<int32_t>(std::min(items * std::min<int64_t>(num_splits, many), many));
+    else *splits = kMaxCluster;
+  } else if (num_splits > 0) {
+    *splits = num_splits;
+  } else if (counted && items * tokens >= fit * 1024) {
+    *ctas = static_cast<int32_t>(fit);
+  } else {
+    // as many CTAs a sequence as fit one wave, of 128 tokens at least
+    while (*splits < kMaxCluster && items * (*splits + 1) <= fit && tokens / (*splits + 1) >= 128) ++*splits;
+  }
+}
+
+size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends) {
+  const size_t slots = 2 * static_cast<size_t>(ctas), c = cols > 8 ? 16 : 8;
+  *ml = slots * c * d * sizeof(float);
+  *ends = *ml + slots * c * sizeof(float2);
+  return *ends + static_cast<size_t>(items) * 2 * sizeof(int32_t);
 }
 
 cudaError_t launch_decode4(const Decode4Args& a, int32_t d, cudaStream_t s) {

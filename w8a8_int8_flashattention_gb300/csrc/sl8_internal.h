@@ -320,8 +320,9 @@ int list_decode_max_splits();
 int list_decode_splits(int64_t lists, int64_t tokens, int32_t d);
 cudaError_t launch_list_decode(const ListDecodeArgs& a, int32_t d, cudaStream_t s);
 // Decode over the paged 4-bit cache (decode4.cu).  The T * Hq / Hkv columns (draft, query head) of a
-// kv head are cut into `groups` of at most `cols`, each of which reads the cache; `splits`
-// CTAs share a sequence: a cluster up to decode4_max_cluster(), more with the combine.
+// kv head are cut into `groups` of at most `cols`, each of which reads the cache.  `splits` CTAs, a
+// cluster, share a sequence, or (ctas > 0) `ctas` CTAs all the work there is, as evenly as its lengths,
+// which only the device knows, allow; a second kernel joins the sequences that they cut.
 struct Decode4Args {
   const void* q;  // [B][T][Hq][d]
   sl8_dtype q_dtype;
@@ -333,17 +334,22 @@ struct Decode4Args {
   const int32_t* seqlens;
   const uint32_t* mask;  // [B][T], nullable: causal
   int32_t B, T, Hq, Hkv;
-  int32_t groups, cols, splits;
+  int32_t groups, cols, splits, ctas;
   void* out;
   sl8_dtype out_dtype;
   float* lse;
-  float* part_o;    // [B * T * Hq][splits][d], not normalised
-  float2* part_ml;  // [B * T * Hq][splits]: max (log2), sum
+  // ctas > 0: two parts a CTA, [2 ctas][8 or 16 columns][d], not normalised, their maxima (log2) and sums,
+  // and the first and last CTA of each (sequence, kv head, column group)
+  float* part_o;
+  float2* part_ml;
+  int32_t* ends;
 };
-int decode4_max_cluster();
 int32_t decode4_max_columns(int32_t d);
-// The splits for `items` (sequence, kv head, column group)s of up to `tokens` tokens.
-int decode4_splits(int64_t items, int64_t tokens, int32_t d);
+// How `items` (sequence, kv head, column group)s of up to `tokens` tokens are shared out: *splits, or *ctas.
+void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, int32_t num_splits, int32_t* splits,
+                       int32_t* ctas);
+// Bytes of part_o, part_ml and ends, at offsets 0, *ml and *ends.
+size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends);
 cudaError_t launch_decode4(const Decode4Args& a, int32_t d, cudaStream_t s);
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, cudaStream_t s);
 
