@@ -838,26 +838,31 @@ def attn_int8_sparse_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, p
 _U8T, _BF16T = torch.uint8, torch.bfloat16
 
 
+def _one(t, dev, dtype, name):
+    """Address of a contiguous tensor of this device and dtype."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _ptrs(dev, dtype, name, t)[0]
+
+
 def _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages):
-    """((num_pages, Hkv, page_size, d), code addresses, scale addresses) of 4-bit pages."""
-    c = _ptrs(dev, _U8T, "k_pages v_pages", k_pages, v_pages)
-    s = _ptrs(dev, _BF16T, "k_scale_pages v_scale_pages", k_scale_pages, v_scale_pages)
-    shape = k_pages.shape
+    """num_pages, Hkv, page_size, d and the addresses of codes and scales of 4-bit pages."""
+    shape, scales = k_pages.shape, k_scale_pages.shape
     if len(shape) != 4:
         raise ValueError("4-bit pages must be [num_pages, Hkv, page_size, d / 2]")
     num_pages, hkv, page_size, half = shape
-    _shaped(v_pages, shape, "v_pages")
-    rows = (num_pages, hkv, page_size, half // 16)
-    _shaped(k_scale_pages, rows, "k_scale_pages")
-    _shaped(v_scale_pages, rows, "v_scale_pages")
-    return (num_pages, hkv, page_size, 2 * half), c, s
+    if v_pages.shape != shape:
+        _shaped(v_pages, shape, "v_pages")
+    if scales != (num_pages, hkv, page_size, half // 16) or v_scale_pages.shape != scales:
+        _shaped(k_scale_pages, (num_pages, hkv, page_size, half // 16), "k_scale_pages")
+        _shaped(v_scale_pages, scales, "v_scale_pages")
+    return (num_pages, hkv, page_size, 2 * half, _one(k_pages, dev, _U8T, "k_pages"), _one(k_scale_pages, dev, _BF16T, "k_scale_pages"),
+            _one(v_pages, dev, _U8T, "v_pages"), _one(v_scale_pages, dev, _BF16T, "v_scale_pages"))
 
 
 def _mean_of(dev, k_mean, hkv, d):
-    if k_mean is None:
-        return None
     _shaped(k_mean, (hkv, d), "k_mean")
-    return _ptrs(dev, _F32T, "k_mean", k_mean)[0]
+    return _one(k_mean, dev, _F32T, "k_mean")
 
 
 def int4_pages(num_pages, Hkv, page_size, d, device=None):
@@ -878,9 +883,10 @@ def rope_append_int4(q, k, v, positions, inv_freq, slot_map, k_pages, k_scale_pa
     k_mean fp32 [Hkv,d] is taken off the rotated keys before they are quantised.  The rest, and what
     is returned, as rope_append."""
     dev = _index(k_pages)
-    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    num_pages, hkv, page_size, d, kc, ks, vc, vs = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
+    mean = None if k_mean is None else _mean_of(dev, k_mean, hkv, d)
     return _append("sl8_rope_append_int4", dev, hkv, d, q, k, v, positions, inv_freq, slot_map, pair_axis, adjacent, q_out,
-                   (_mean_of(dev, k_mean, hkv, d), codes[0], scales[0], codes[1], scales[1], num_pages, page_size))
+                   (mean, kc, ks, vc, vs, num_pages, page_size))
 
 
 def paged_read_int4(k_pages, k_scale_pages, v_pages, v_scale_pages, block_table, seqlens, cu_seqlens=None,
@@ -892,16 +898,17 @@ def paged_read_int4(k_pages, k_scale_pages, v_pages, v_scale_pages, block_table,
     left as they were (zeros where the outputs, of out_dtype, default bfloat16, are made here).
     Returns (k_out, v_out)."""
     dev = _index(k_pages)
-    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
-    table, lens, cu = _ptrs(dev, _I32T, "block_table seqlens cu_seqlens", block_table, seqlens, cu_seqlens)
+    num_pages, hkv, page_size, d, kc, ks, vc, vs = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
     B, max_blocks = block_table.shape
     if seqlens.numel() != B or (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
         raise ValueError("seqlens and cu_seqlens need one entry per row of block_table (and one more)")
     N = max_blocks * page_size if max_seqlen is None else int(max_seqlen)
     given = k_out if k_out is not None else v_out
+    cu, total = None, 0
     if cu_seqlens is None:
-        total, shape = 0, (B, hkv, N, d)
+        shape = (B, hkv, N, d)
     else:
+        cu = _one(cu_seqlens, dev, _I32T, "cu_seqlens")
         if total_tokens is None and given is None:
             raise ValueError("a packed read needs total_tokens or an output")
         total = int(total_tokens) if total_tokens is not None else given.shape[0]
@@ -913,11 +920,12 @@ def paged_read_int4(k_pages, k_scale_pages, v_pages, v_scale_pages, block_table,
         k_out = torch.zeros(shape, dtype=dtype, device=k_pages.device)
     if v_out is None:
         v_out = torch.zeros(shape, dtype=dtype, device=k_pages.device)
-    _shaped(k_out, shape, "k_out")
-    _shaped(v_out, shape, "v_out")
-    o = _ptrs(dev, dtype, "k_out v_out", k_out, v_out)
-    _call("sl8_paged_read_int4", dev, codes[0], scales[0], codes[1], scales[1], num_pages, page_size, table, max_blocks, lens,
-          cu, B, hkv, N, d, total, _mean_of(dev, k_mean, hkv, d), o[0], o[1], _DTYPES[dtype])
+    if k_out.shape != shape or v_out.shape != shape:
+        _shaped(k_out, shape, "k_out")
+        _shaped(v_out, shape, "v_out")
+    _call("sl8_paged_read_int4", dev, kc, ks, vc, vs, num_pages, page_size, _one(block_table, dev, _I32T, "block_table"), max_blocks,
+          _one(seqlens, dev, _I32T, "seqlens"), cu, B, hkv, N, d, total, None if k_mean is None else _mean_of(dev, k_mean, hkv, d),
+          _one(k_out, dev, dtype, "k_out"), _one(v_out, dev, dtype, "v_out"), _DTYPES[dtype])
     return k_out, v_out
 
 
@@ -934,39 +942,43 @@ def attn_int4_paged_decode(q, k_pages, k_scale_pages, v_pages, v_scale_pages, bl
     (dtype q.dtype unless given) and, with return_lse, the fp32 LSE: 0 and -inf for a query that sees no
     token.  workspace: uint8, at least int4_decode_workspace_bytes (16: none is used)."""
     dev = _index(k_pages)
-    (num_pages, hkv, page_size, d), codes, scales = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
-    table, lens, mask = _ptrs(dev, _I32T, "block_table seqlens tree_mask", block_table, seqlens, tree_mask)
+    num_pages, hkv, page_size, d, kc, ks, vc, vs = _pages4_of(dev, k_pages, k_scale_pages, v_pages, v_scale_pages)
     B, max_blocks = block_table.shape
-    shape = q.shape
+    shape, dtype = q.shape, q.dtype
     if len(shape) not in (3, 4):
         raise ValueError("q must be [B, Hq, d] or [B, T, Hq, d]")
     T, hq = (1, shape[1]) if len(shape) == 3 else (shape[1], shape[2])
-    if shape[0] != B or shape[-1] != d or seqlens.numel() != B or (tree_mask is not None and tree_mask.numel() != B * T):
-        raise ValueError("q, block_table, seqlens, tree_mask and the pages do not belong together")
+    if shape[0] != B or shape[-1] != d or seqlens.numel() != B:
+        raise ValueError("q, block_table, seqlens and the pages do not belong together")
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.numel() != B * T:
+            raise ValueError("tree_mask needs one entry per query")
+        mask = _one(tree_mask, dev, _I32T, "tree_mask")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=out_dtype or dtype, device=q.device)
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
-    if q.dtype not in _DTYPES or out.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {q.dtype} or {out.dtype}")
-    qp, = _ptrs(dev, q.dtype, "q", q)
-    op, = _ptrs(dev, out.dtype, "out", out)
+    odt = out.dtype
+    if dtype not in _DTYPES or odt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype} or {odt}")
     lse_p = None
     if return_lse:
         if lse is None:
             lse = torch.empty(shape[:-1], dtype=_F32T, device=q.device)
         elif lse.shape != shape[:-1]:
             raise ValueError("lse must have one entry per query head")
-        lse_p, = _ptrs(dev, _F32T, "lse", lse)
+        lse_p = _one(lse, dev, _F32T, "lse")
     ws, nbytes = None, 0
     if workspace is None:
         need = int4_decode_workspace_bytes(B, T, hq, hkv, max_blocks, page_size, d, num_splits)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 16 else None
     if workspace is not None:
-        ws, = _ptrs(dev, workspace.dtype, "workspace", workspace)
+        ws = _one(workspace, dev, workspace.dtype, "workspace")
         nbytes = workspace.numel() * workspace.element_size()
-    _call("sl8_attn_int4_paged_decode", dev, qp, _DTYPES[q.dtype], codes[0], scales[0], codes[1], scales[1], num_pages,
-          page_size, table, max_blocks, lens, mask, T, B, hq, hkv, d, num_splits, op, _DTYPES[out.dtype], lse_p, ws, nbytes)
+    _call("sl8_attn_int4_paged_decode", dev, _one(q, dev, dtype, "q"), _DTYPES[dtype], kc, ks, vc, vs, num_pages, page_size,
+          _one(block_table, dev, _I32T, "block_table"), max_blocks, _one(seqlens, dev, _I32T, "seqlens"), mask, T, B, hq, hkv, d,
+          num_splits, _one(out, dev, odt, "out"), _DTYPES[odt], lse_p, ws, nbytes)
     return (out, lse) if return_lse else out
 
 

@@ -1028,8 +1028,8 @@ int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_pages, const
   SL8_CHECK(static_cast<int64_t>(page_size) * max_blocks <= kMaxTokens && N <= kMaxTokens, SL8_ERR_UNSUPPORTED);
   SL8_CHECK(static_cast<int64_t>(num_pages) * page_size < (int64_t(1) << 31), SL8_ERR_UNSUPPORTED);
   if (B == 0 || N == 0 || (cu_seqlens && total_tokens == 0)) return SL8_OK;
-  // one CTA per 64 tokens of a sequence's kv head
-  SL8_CHECK((static_cast<int64_t>(N) + 63) / 64 * B < (int64_t(1) << 31) / Hkv, SL8_ERR_UNSUPPORTED);
+  // one CTA per 32 or more tokens of a sequence's kv head
+  SL8_CHECK((static_cast<int64_t>(N) + 31) / 32 * B < (int64_t(1) << 31) / Hkv, SL8_ERR_UNSUPPORTED);
   SL8_CHECK(block_table && seqlens && (k_out || v_out), SL8_ERR_INVALID_ARG);
   SL8_CHECK(!k_out || (k_pages && k_scale_pages), SL8_ERR_INVALID_ARG);
   SL8_CHECK(!v_out || (v_pages && v_scale_pages), SL8_ERR_INVALID_ARG);

@@ -18,24 +18,46 @@ namespace sl8 {
 
 namespace {
 
-constexpr int kReadTok = 64;  // tokens of one (sequence, kv head) per CTA
+// Tokens of one (sequence, kv head) per CTA: a thread takes eight channels of kReadRows rows.
+constexpr int kReadRows = 4;
+constexpr int read_tokens(int d) { return kReadRows * 256 / (d / 8); }
 
 // Eight values as one store, or two of fp32.
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) { return f16x2_of(a, b); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-  store4<T>(p, a);
-  store4<T>(p + 4, b);
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
 }
 
-// out = code * s (+ the mean that the append took off), one rounding.
+// Codes of a word's eight nibbles, exact: the nibble as the low bits of 2^23 + nibble.
+__device__ __forceinline__ void codes8(uint32_t w, float (&x)[8]) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(prmt(even, 0x4b000000u, 0x7440 + i));
+    x[2 * i + 1] = __uint_as_float(prmt(odd, 0x4b000000u, 0x7440 + i));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] -= 8388616.0f;
+}
+
+// out = code * s (+ the mean that the append took off), one rounding.  All of a thread's loads are on
+// their way at once: pages, then codes and scales, keys and values alike.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) read4_kernel(const Read4Args a, DeviceStatus* st) {
-  constexpr int kLanes = D / 8, kRows = 256 / kLanes;  // eight channels a thread
+  constexpr int kLanes = D / 8, kRows = 256 / kLanes, kTok = read_tokens(D);
   const uint32_t u = blockIdx.x / static_cast<uint32_t>(a.Hkv), h = blockIdx.x - u * a.Hkv;
-  const uint32_t chunks = (static_cast<uint32_t>(a.N) + kReadTok - 1) / kReadTok;
+  const uint32_t chunks = (static_cast<uint32_t>(a.N) + kTok - 1) / kTok;
   const uint32_t b = u / chunks;
-  const int first = static_cast<int>(u - b * chunks) * kReadTok;
+  const int first = static_cast<int>(u - b * chunks) * kTok;
   const int l = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int32_t cap = a.max_blocks * a.page;
   int64_t L = a.seqlens[b], room = min(cap, a.N), at = static_cast<int64_t>(b) * a.Hkv * a.N;
@@ -48,7 +70,33 @@ __global__ void __launch_bounds__(256) read4_kernel(const Read4Args a, DeviceSta
   }
   if (L > room) bad = true, L = room;
   if (bad && first == 0 && h == 0 && threadIdx.x == 0) record_status(st, kStatusBadArg, 860);
-  const int n = static_cast<int>(min(L, static_cast<int64_t>(first) + kReadTok));
+  const int n = static_cast<int>(min(L, static_cast<int64_t>(first) + kTok));
+  if (first >= n) return;
+  int32_t pg[kReadRows], off[kReadRows];
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {  // rows past the last one repeat it and store nothing
+    const int tok = min(first + sub + i * kRows, n - 1), blk = tok / a.page;
+    pg[i] = a.table[static_cast<int64_t>(b) * a.max_blocks + blk];
+    off[i] = tok - blk * a.page;
+  }
+  uint32_t w[2][kReadRows];
+  uint16_t s[2][kReadRows];
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    if (pg[i] < 0 || pg[i] >= a.num_pages) {
+      record_status(st, kStatusBadArg, 861);
+      pg[i] = 0;
+    }
+    const int64_t row = (static_cast<int64_t>(pg[i]) * a.Hkv + h) * a.page + off[i];
+    if (a.k_out) {
+      w[0][i] = *reinterpret_cast<const uint32_t*>(a.k_pages + row * (D / 2) + 4 * l);
+      s[0][i] = a.k_scale[row * (D / 32) + l / 4];
+    }
+    if (a.v_out) {
+      w[1][i] = *reinterpret_cast<const uint32_t*>(a.v_pages + row * (D / 2) + 4 * l);
+      s[1][i] = a.v_scale[row * (D / 32) + l / 4];
+    }
+  }
   float mean[8] = {};
   if (a.k_mean) {
     const float4* m = reinterpret_cast<const float4*>(a.k_mean + h * D + 8 * l);
@@ -56,27 +104,21 @@ __global__ void __launch_bounds__(256) read4_kernel(const Read4Args a, DeviceSta
     mean[0] = x.x, mean[1] = x.y, mean[2] = x.z, mean[3] = x.w;
     mean[4] = y.x, mean[5] = y.y, mean[6] = y.z, mean[7] = y.w;
   }
-  for (int t = first + sub; t < n; t += kRows) {
-    int32_t pg = a.table[static_cast<int64_t>(b) * a.max_blocks + t / a.page];
-    if (pg < 0 || pg >= a.num_pages) {
-      record_status(st, kStatusBadArg, 861);
-      pg = 0;
-    }
-    const int64_t row = (static_cast<int64_t>(pg) * a.Hkv + h) * a.page + t % a.page;
-    const int64_t dst = (a.cu_seqlens ? (at + t) * a.Hkv + h : at + static_cast<int64_t>(h) * a.N + t) * D + 8 * l;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      T* const out = static_cast<T*>(kv ? a.v_out : a.k_out);
-      if (!out) continue;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>((kv ? a.v_pages : a.k_pages) + row * (D / 2) + 4 * l);
-      const float s = __uint_as_float(static_cast<uint32_t>((kv ? a.v_scale : a.k_scale)[row * (D / 32) + l / 4]) << 16);
+  for (int kv = 0; kv < 2; ++kv) {
+    T* const out = static_cast<T*>(kv ? a.v_out : a.k_out);
+    if (!out) continue;
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      const int t = first + sub + i * kRows;
+      if (t >= n) break;
+      const int64_t dst = (a.cu_seqlens ? (at + t) * a.Hkv + h : at + static_cast<int64_t>(h) * a.N + t) * D + 8 * l;
+      const float f = __uint_as_float(static_cast<uint32_t>(s[kv][i]) << 16);
       float x[8];
+      codes8(w[kv][i], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float c = static_cast<float>(static_cast<int>((w >> (4 * i)) & 15u) - 8);
-        x[i] = kv == 0 ? fmaf(c, s, mean[i]) : c * s;
-      }
-      store8<T>(out + dst, x);
+      for (int e = 0; e < 8; ++e) x[e] = kv == 0 ? fmaf(x[e], f, mean[e]) : x[e] * f;
+      store8(out + dst, x);
     }
   }
 }
@@ -102,7 +144,7 @@ cudaError_t launch_rope_append_int4(const RopeAppendArgs& r, cudaStream_t s) {
 
 cudaError_t launch_paged_read_int4(const Read4Args& a, int32_t d, cudaStream_t s) {
   TraceScope tr("paged_read_int4", s);
-  const int64_t chunks = (static_cast<int64_t>(a.N) + kReadTok - 1) / kReadTok;
+  const int64_t chunks = (static_cast<int64_t>(a.N) + read_tokens(d) - 1) / read_tokens(d);
   const unsigned grid = static_cast<unsigned>(chunks * a.B * a.Hkv);
   switch (a.out_dtype) {
     case SL8_F16: return launch_read_t<__half>(a, d, grid, s);
