@@ -11,47 +11,72 @@ namespace sl8 {
 
 constexpr int kGroup4 = 32;  // channels that share a scale
 
-// bf16(max|x| / 7) as fp32; a NaN never gets here (maxima drop it), an infinity stays one.
+// bf16(max|x| / 7) as fp32; a NaN never gets here (maxima drop it), an infinity stays one.  The
+// division by a product and a correction by its exact remainder (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990), which for 7 gives the quotient's fp32 rounding
+// for every significand; where the remainder may underflow or the product is infinite, by division.
 __device__ __forceinline__ float group_scale(float amax) {
-  const uint32_t u = __float_as_uint(__fdiv_rn(amax, 7.0f));  // not negative
+  constexpr float kSeventh = 1.0f / 7.0f;
+  const float q = amax * kSeventh;
+  float d = fmaf(fmaf(-7.0f, q, amax), kSeventh, q);
+  if (!(amax > 1e-25f && amax < INFINITY)) d = __fdiv_rn(amax, 7.0f);
+  const uint32_t u = __float_as_uint(d);  // not negative
   return __uint_as_float((u + 0x7fffu + ((u >> 16) & 1u)) & 0xffff0000u);
 }
 
-// The four nibbles c + 8 of x / s, the first lowest.  k = round(x * (1 / s)) is off by one at most,
+__device__ __forceinline__ float max3(float a, float b, float c) {  // of magnitudes; drops NaN
+  asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(fabsf(b)), "f"(fabsf(c)));
+  return a;
+}
+
+// The kN nibbles c + 8 of x / s, the first lowest.  k = round(x * (1 / s)) is off by one at most,
 // next to a border, and x - k s is exact in one fma (k s has 11 bits, and x and k s are within a
 // factor of two of each other for k != 0): where it is below s / 2 in magnitude, k is the nearest
 // integer to x / s; the others are moved by what it says.
-__device__ __forceinline__ uint32_t nibbles4(const float (&x0)[4], float s) {
+template <int kN>
+__device__ __forceinline__ uint32_t nibbles(const float (&x0)[kN], float s) {
   constexpr float kRound = 12582912.0f + 8.0f;  // 1.5 * 2^23 + 8: k + 8 in the low bits of the sum
-  float x[4] = {x0[0], x0[1], x0[2], x0[3]};
+  constexpr uint32_t kBits = 0x4b400000u;       // ... and 1.5 * 2^23 above them
+  float x[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) x[i] = x0[i];
   const bool tiny = s < 1e-30f;  // 1 / s may pass fp32: the same quotient from both times 2^96
   if (tiny) {
     s *= 7.922816251426434e28f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] *= 7.922816251426434e28f;
+    for (int i = 0; i < kN; ++i) x[i] *= 7.922816251426434e28f;
   }
-  if (s == 0.0f || s == INFINITY) return 0x8888u;
+  if (s == 0.0f || s == INFINITY) return 0x88888888u >> (32 - 4 * kN);
   const float r = __frcp_rn(s), h = 0.5f * s;
-  uint32_t w[4];
-  bool sure = !tiny;
+  uint32_t w[kN];
+  float off = 0.0f;  // the largest remainder; NaN if there is one
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float z = fmaf(x[i], r, kRound);
-    sure = sure && fabsf(fmaf(kRound - z, s, x[i])) < h;
-    w[i] = __float_as_uint(z);
+  for (int i = 0; i < kN; i += 2) {
+    const float z0 = fmaf(x[i], r, kRound), z1 = fmaf(x[i + 1], r, kRound);
+    const float e0 = fmaf(kRound - z0, s, x[i]), e1 = fmaf(kRound - z1, s, x[i + 1]);
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(off) : "f"(fabsf(e0)), "f"(fabsf(e1)));
+    w[i] = __float_as_uint(z0);
+    w[i + 1] = __float_as_uint(z1);
   }
-  if (!sure) {
+  if (!(off < h) || tiny) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kN; ++i) {
       const float k = __uint_as_float(w[i]) - kRound;
       const float e = fmaf(-k, s, x[i]);
       int c = static_cast<int>(k);
       if (fabsf(e) > h || (fabsf(e) == h && (c & 1))) c += e > 0.0f ? 1 : -1;
       c = max(-7, min(7, c));  // a scale below 2^-126 can be far below max|x| / 7
-      w[i] = isnan(x[i]) ? 8u : static_cast<uint32_t>(c + 8);
+      w[i] = kBits + (isnan(x[i]) ? 8u : static_cast<uint32_t>(c + 8));
     }
   }
-  return (w[0] & 15u) | ((w[1] & 15u) << 4) | ((w[2] & 15u) << 8) | ((w[3] & 15u) << 12);
+  // sum of (w - kBits) 16^i: what the bits above the nibbles add, mod 2^32, is the same for all
+  uint32_t p = w[kN - 1], extra = kBits;
+#pragma unroll
+  for (int i = kN - 2; i >= 0; --i) {
+    p = p * 16u + w[i];
+    extra = extra * 16u + kBits;
+  }
+  return p - extra;
 }
 
 }  // namespace sl8
