@@ -64,12 +64,13 @@ def visible(L, T, t, mask=None):
 
 def attention(q, kc, ks, vc, vs, tables, lens, masks=None, bounds=False):
     """q [B, T, Hq, d] fp32; packed pages and scales; (out fp64, lse fp64).  bounds: also
-    sum_t p_t |v_t| like out, and the largest sum_c |q_c k_c| / sqrt(d) of each query's tokens."""
+    sum_t p_t |v_t| like out, and of each query's tokens the largest sum_c |q_c k_c| / sqrt(d) and the
+    largest p_t times a V scale."""
     B, T, Hq, d = q.shape
     Hkv = kc.shape[1]
     G = Hq // Hkv
     out, lse = np.zeros(q.shape), np.full(q.shape[:-1], -np.inf)
-    size, reach = np.zeros(q.shape), np.zeros(q.shape[:-1])
+    size, reach, heavy = np.zeros(q.shape), np.zeros(q.shape[:-1]), np.zeros(q.shape[:-1])
     codes, sq = _quant(q)
     for b in range(B):
         n = int(lens[b])
@@ -91,4 +92,5 @@ def attention(q, kc, ks, vc, vs, tables, lens, masks=None, bounds=False):
                 if bounds:
                     size[b, t, h] = e @ np.abs(v[h // G][see]) / e.sum()
                     reach[b, t, h] = (np.abs(k[h // G][see]) @ np.abs(row)).max()
-    return (out, lse, size, reach) if bounds else (out, lse)
+                    heavy[b, t, h] = (e * gather(vs, tables[b], n)[h // G][see].max(-1)).max() / e.sum()
+    return (out, lse, size, reach, heavy) if bounds else (out, lse)

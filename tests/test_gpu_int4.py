@@ -10,10 +10,13 @@ Attention, for n tokens and kN = d / 32 groups (2^-24 is half a step of fp32):
   a logit takes kN fused sums, the scale of q and log2 e, and the reference comes off: (kN + 4) 2^-24 of
   sum |q k| / sqrt(d), in units of log2 1.45 times that; exponentials are good to 2^-22; so each p to
     ep = 1.45 (kN + 4) 2^-24 reach + 2^-22, and the quotient by their sum to twice that;
-  weights are off by 2^-17 of themselves (two bf16 terms, 2^-9 2^-9 and a bit for the product's rounding), 2^-23 for fp32 outputs;
+  weights p s_v of fp32 outputs are off by 2^-23 of themselves (three bf16 terms, the product's rounding); those of
+  16-bit outputs are fp16 numbers of p to two bf16 terms: 2^-11 + 2^-17 of themselves, or half of 2^-24 on a scale on
+  which the largest of the query is at least 1/2: 2^-24 of that one, times |code| <= 8, for each token;
   sums: each MMA's addition may truncate (2^-23 of the partial sum), at most 3 an m16n8k16 step and 16 tokens,
   and some thirty in merges: (3 n / 16 + 32) 2^-23.
-All of these are relative to sum_t p_t |v_t|; then half a step of the output's type.
+All of these are relative to sum_t p_t |v_t|; probabilities below 2^-126 of the largest may be 0; then half a
+step of the output's type.
 """
 import numpy as np
 import pytest
@@ -295,22 +298,23 @@ def test_read_of_infinite_groups_and_what_was_appended():
 
 def _check_attention(out, lse, q, host, tables, lens, masks=None, tag=""):
     """out [B,T,Hq,d], lse [B,T,Hq] against the definition with the bounds above."""
-    want, wlse, size, reach = Q.attention(f32(q), *host, tables, lens, masks, bounds=True)
+    want, wlse, size, reach, heavy = Q.attention(f32(q), *host, tables, lens, masks, bounds=True)
     n, groups = max(int(np.max(lens)), 1), q.shape[-1] // 32
     ep = 1.45 * (groups + 4) * 2.0 ** -24 * reach + 2.0 ** -22
-    ew = 2.0 ** -23 if out.dtype == torch.float32 else 2.0 ** -17
+    ew, floor = (2.0 ** -23, 0.0) if out.dtype == torch.float32 else (2.0 ** -11 + 2.0 ** -17, 2.0 ** -24 * 8 * n)
     rel = 2 * ep[..., None] + ew + (3 * n / 16 + 32) * 2.0 ** -23
     eps = torch.finfo(out.dtype).eps / 2
     got = np64(out)
     assert np.all(np.isfinite(got)), tag
-    tol = size * rel * (1 + eps) + eps * np.abs(want) + (2.0 ** -25 if out.dtype == torch.float16 else 0)
+    gone = 2.0 ** -126 * 8 * n * np.max(np.where(np.isfinite(host[3]), np.abs(host[3]), 0))
+    tol = (size * rel + floor * heavy[..., None] + gone) * (1 + eps) + eps * np.abs(want) + (2.0 ** -25 if out.dtype == torch.float16 else 0)
     worst = np.max((np.abs(got - want) - tol))
     assert worst <= 0, (tag, worst, np.max(np.abs(got - want) / np.maximum(tol, 1e-30)))
     empty = np.isinf(wlse)
     gl = np64(lse)
     assert np.all(np.isneginf(gl[empty])), tag
     tl = 2 * ep + (n / 16 + 32) * 2.0 ** -24 + 2.0 ** -23 * (1 + np.abs(np.where(empty, 0, wlse)))
-    assert np.all(np.abs(gl - wlse)[~empty] <= tl[~empty]), tag
+    assert np.all(np.abs(gl[~empty] - wlse[~empty]) <= tl[~empty]), tag
 
 
 def _attend(B, T, hq, hkv, d, page, lens, qdt, odt, splits=0, tree=False, spread=1.0, seed=0, workspace=None):
@@ -360,10 +364,34 @@ def test_a_long_sequence(splits):
 
 @pytest.mark.parametrize("d,G", [(32, 4), (64, 16), (128, 2), (256, 8)])
 def test_scales_far_apart(d, G):
-    """Groups and rows whose scales are up to 10^12 apart keep their own relative accuracy."""
+    """Groups and rows whose scales are far apart: in fp32 each keeps its own relative accuracy, up to 10^12
+    apart; 16-bit outputs have the weights' accuracy of the largest."""
     for splits in (1, 4, 10):
         _attend(3, 1, G, 1, d, 16, [90, 7, 300], BF16, F32, splits, spread=12.0)
         _attend(3, 1, G, 1, d, 16, [90, 7, 300], BF16, F16, splits, spread=4.0)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 3, 12])
+@pytest.mark.parametrize("odt", [BF16, F32])
+def test_a_huge_value_row_of_no_weight(odt, splits, d):
+    """Rows whose V scales are 2^18 to 2^60 times the others' and whose keys have no probability, first, last and
+    in between, and the reverse, a row that has all of it and the least scale: the other weights keep their bits."""
+    rng = np.random.default_rng(d + splits)
+    L, page, hkv, G = 300, 16, 1, 4
+    for factor, kept in ((2.0 ** 18, False), (2.0 ** 60, False), (2.0 ** -40, True)):
+        pool, (kc, ks, vc, vs) = _filled(rng, 20, hkv, page, d, 0.3)
+        tables = np.arange(20)[None]
+        q = torch.from_numpy(np.abs(rng.standard_normal((1, 1, G, d)).astype(np.float32)) + 0.5).to(DEV)
+        for row in (0, 97, 160, L - 1) if not kept else (150,):
+            at = row // page, 0, row % page
+            kc[at] = 0xff if kept else 0x11  # codes 7 or -7 against positive queries
+            ks[at] = 4.0 if kept else 16.0
+            vs[at] *= factor
+        for i, x in enumerate((kc, ks, vc, vs)):
+            pool[i].copy_(torch.from_numpy(x))
+        out, lse = sl8.attn_int4_paged_decode(q[:, 0], *pool, i32(tables), i32([L]), num_splits=splits, out_dtype=odt, return_lse=True)
+        _check_attention(out[:, None], lse[:, None], q, (kc, ks, vc, vs), tables, [L], tag=(factor, kept))
 
 
 @pytest.mark.parametrize("d", [32, 64, 128, 256])

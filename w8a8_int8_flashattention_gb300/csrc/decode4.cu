@@ -101,25 +101,46 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
 // (x0, x1) += (a0, a1) in fp32, as one instruction.
 __device__ __forceinline__ void add_pair(float& x0, float& x1, float a0, float a1) {
   asm("{\n\t.reg .b64 x, a;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tadd.rn.f32x2 x, x, a;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(x0), "+f"(x1)
       : "f"(a0), "f"(a1));
 }
+// a b + c of two bf16 numbers and an fp32 one, one rounding; at the rate of fp32's own.  kA, kB: the half
+// of the word that a number is in.
+template <int kA, int kB>
+__device__ __forceinline__ float fma_mixed(uint32_t a, uint32_t b, float c) {
+  const uint16_t x = static_cast<uint16_t>(kA ? a >> 16 : a), y = static_cast<uint16_t>(kB ? b >> 16 : b);
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+  return d;
+}
+template <int kA>
+__device__ __forceinline__ float bf16_half(uint32_t a) {  // as fp32
+  const uint16_t x = static_cast<uint16_t>(kA ? a >> 16 : a);
+  float d;
+  asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(d) : "h"(x), "f"(-0.0f));
+  return d;
+}
 // Nibbles where they lie in a 16-bit word are bf16 numbers, n 2^-133 (bits 0..3) and n 2^-129
 // (bits 4..7, since the exponents 0 and 1 have the same step): times 2^127 and less 8 such, codes.
-constexpr uint32_t k2p127 = 0x7f007f00u, kLow8 = 0xbe00be00u, kHigh8 = 0xc000c000u;  // 2^127, -8 2^-6, -8 2^-2
+// As fp16 numbers they are n 2^-24 and n 2^-20, times 2^15 less 8 such.
+template <bool kHalf>
+struct Codes4 {
+  static constexpr uint32_t kUp = kHalf ? 0x78007800u : 0x7f007f00u;     // 2^15, 2^127
+  static constexpr uint32_t kLow8 = kHalf ? 0xa400a400u : 0xbe00be00u;   // -8 2^-9, -8 2^-6
+  static constexpr uint32_t kHigh8 = kHalf ? 0xb400b400u : 0xc000c000u;  // -8 2^-5, -8 2^-2
+  static constexpr float kLow = kHalf ? 512.0f : 64.0f, kHigh = kHalf ? 32.0f : 4.0f;  // what takes codes of them
+  static __device__ __forceinline__ uint32_t low(uint32_t w) { return fma(w & 0x000f000fu, kLow8); }
+  static __device__ __forceinline__ uint32_t high(uint32_t w) { return fma(w & 0x00f000f0u, kHigh8); }
+  static __device__ __forceinline__ uint32_t fma(uint32_t w, uint32_t less) {
+    uint32_t r;
+    if constexpr (kHalf) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(kUp), "r"(less));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(kUp), "r"(less));
+    return r;
+  }
+};
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -177,12 +198,16 @@ __device__ __forceinline__ int64_t cta_prefix(int64_t x, int64_t* sm) {
   return x;
 }
 
-// kCols: 8 or 16 columns.  kTerms: bf16 terms of a weight.
+// kCols: columns of a CTA.  kTerms: 1, weights as one fp16 number; 3, as three bf16 terms.
 template <int D, int kCols, int kTerms>
 __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     decode4_kernel(const Decode4Args a, DeviceStatus* st) {
   using C = Cfg4<D, kCols>;
   constexpr int kN = C::kN, kT = C::kT, kU = C::kU;
+  constexpr bool kHalf = kTerms == 1;           // weights and value codes in fp16, else in bf16
+  constexpr int kParts = kTerms == 1 ? 2 : kTerms;  // bf16 terms of p
+  constexpr uint32_t kMinusOne = 0xbf80u;       // bf16
+  using Codes = Codes4<kHalf>;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int G = a.Hq / a.Hkv, per_seq = a.Hkv * a.groups;
@@ -391,11 +416,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to (0 before there is a
     // token), the logit up to which it stays, and the sum over the lane's tokens
     float ref[kT][2], th[kT][2], l[kT][2];
+    [[maybe_unused]] int down[kT][2];             // fp16 weights: ref is the maximum plus this
+    [[maybe_unused]] uint32_t vlim = 0x7f800000u;  // and the V scale up to which they all fit
     float o[D / 16][kT][4];
 #pragma unroll
     for (int h = 0; h < kT; ++h)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f;
+      for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f, down[h][c] = -126;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -434,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const uint32_t u0 = kw[u][0][j], u1 = kw[u][1][j], v0 = u0 >> 8, v1 = u1 >> 8;
-          const float f0 = __uint_as_float((j & 1) ? sc[u][0][j / 2] & 0xffff0000u : sc[u][0][j / 2] << 16);
-          const float f1 = __uint_as_float((j & 1) ? sc[u][1][j / 2] & 0xffff0000u : sc[u][1][j / 2] << 16);
+          const float f0 = (j & 1) ? bf16_half<1>(sc[u][0][j / 2]) : bf16_half<0>(sc[u][0][j / 2]);
+          const float f1 = (j & 1) ? bf16_half<1>(sc[u][1][j / 2]) : bf16_half<0>(sc[u][1][j / 2]);
 #pragma unroll
           for (int h = 0; h < kT; ++h) {
             float acc[4];
@@ -451,7 +478,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     };
 
     // Online softmax, lazily rescaled: where a logit passes its column's limit, the reference moves.
-    auto move_maxima = [&](const float (&x)[kU][kT][4]) {
+    // fp16 weights w = 2^(y - ref) s_v: with ref the maximum alone a row of a huge scale would not fit, and
+    // with ref following the scales a row of a huge scale and no probability would push the others
+    // below fp16's range.  So ref follows the weights: it is the maximum plus `down`, about log2 of the column's
+    // largest p s_v, and moves where a logit is 2^kLazyLists above the maximum, or a scale 2^10 above that weight.
+    auto move_maxima = [&](const float (&x)[kU][kT][4], uint32_t values) {
       bool grow = false;
       float mx[kT][2];
 #pragma unroll
@@ -462,16 +493,58 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
           if constexpr (kU == 2) mx[h][c] = fmaxf(mx[h][c], fmaxf(x[kU - 1][h][c], x[kU - 1][h][2 + c]));
           grow = grow || mx[h][c] > th[h][c];
         }
+      if constexpr (kHalf) {  // each lane looks at its share of the step's scales
+        constexpr int kMine = kU * D / 64;
+        uint32_t w[(kMine + 1) / 2];
+        lds_words<kMine>(values + C::kScales + 2 * kMine * lane, w);
+        uint32_t s = w[0] << 16;
+        if constexpr (kMine > 1) s = max(s, w[0] & 0xffff0000u);
+        if constexpr (kMine > 2) s = max(s, max(w[(kMine - 1) / 2] << 16, w[(kMine - 1) / 2] & 0xffff0000u));
+        grow = grow || s > vlim;
+      }
       if (!__any_sync(0xffffffffu, grow)) return;
+      [[maybe_unused]] float up[kU][2];  // log2 of the largest scale of tokens g and g + 8, rounded up
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t w[(kN + 1) / 2], most = 0;
+            lds_words<kN>(values + C::kScales + u * D + 2 * kN * (g + 8 * s), w);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) most = max(most, (j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+            up[u][s] = static_cast<float>(static_cast<int>((most >> 7) & 0xffu) - 126);
+          }
+      }
+      auto bounded = [](float v) { return fminf(fmaxf(v, -1048576.0f), 1048576.0f); };
 #pragma unroll
       for (int h = 0; h < kT; ++h)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const float m = col_max(mx[h][c]), y = m * qs[h][c];
-          if (!(m > th[h][c]) || isnan(y)) continue;
-          const float f = th[h][c] == -INFINITY ? 0.0f : ex2(ref[h][c] - y);
-          ref[h][c] = y;
-          th[h][c] = (y + kLazy) / qs[h][c];
+          float heavy = 0.0f;
+          if constexpr (kHalf) {
+            heavy = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) heavy = fmaxf(heavy, bounded(x[u][h][2 * s + c] * qs[h][c]) + up[u][s]);
+            heavy = col_max(heavy);
+          }
+          const bool first = th[h][c] == -INFINITY, higher = m > th[h][c];
+          if ((first && !higher) || isnan(y) || (!kHalf && !higher)) continue;
+          float to = y;
+          if constexpr (kHalf) {
+            const float before = ref[h][c] - static_cast<float>(down[h][c]), now = higher ? y : before;
+            // what the earlier rows' largest weight has become, and this step's, in [2^(e - 1), 2^(e + 1))
+            const int kept = first ? -126 : down[h][c] + __float2int_rd(fmaxf(before - now, -252.0f));
+            const int e = __float2int_ru(heavy - bounded(now)) - 1;
+            down[h][c] = max(-80, min(120, max(kept, e)));
+            to = now + static_cast<float>(down[h][c]);
+          }
+          const float f = first ? 0.0f : ex2(ref[h][c] - to);
+          ref[h][c] = to;
+          if (higher) th[h][c] = (y + static_cast<float>(kHalf ? kLazyLists : static_cast<int>(kLazy))) / qs[h][c];
           l[h][c] *= f;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -479,9 +552,21 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             o[i][h][2 + c] *= f;
           }
         }
+      if constexpr (kHalf) {  // the limit of the column that has the least weights
+        int least = 120;
+#pragma unroll
+        for (int h = 0; h < kT; ++h)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (th[h][c] != -INFINITY) least = min(least, down[h][c]);
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+        vlim = static_cast<uint32_t>(min(127, least + 15 - kLazyLists) + 127) << 23;
+      }
     };
 
-    // O += a step's weighted rows.  vis: masks of the V scales of column g + 8 h's token pairs (masked).
+    // O += a step's weighted rows.  vis (masked): bits of the token pairs that column g + 8 h sees; whatever the
+    // scales of the others hold, they weigh nothing.
     auto output = [&](uint32_t base, const float (&x)[kU][kT][4], const bool masked, const uint32_t (&vis)[kU][kT][2]) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -502,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
         lds_words<2 * kN>(r, sc[0]);
         lds_words<2 * kN>(r + 16 * kN, sc[1]);
         // p as bf16 terms, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
-        uint32_t p[kT][kTerms][2];
+        uint32_t p[kT][kParts][2];
 #pragma unroll
         for (int h = 0; h < kT; ++h)
 #pragma unroll
@@ -510,55 +595,62 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             float pa = ex2(fmaf(x[u][h][2 * s], qs[h][0], -ref[h][0])), pb = ex2(fmaf(x[u][h][2 * s + 1], qs[h][1], -ref[h][1]));
             add_pair(l[h][0], l[h][1], pa, pb);
 #pragma unroll
-            for (int e = 0; e < kTerms; ++e) {
+            for (int e = 0; e < kParts; ++e) {
               const uint32_t w = bf16x2_of(pa, pb);
               p[h][e][s] = movm_t(w);
-              pa -= __uint_as_float(w << 16);
-              pb -= __uint_as_float(w & 0xffff0000u);
+              if (e + 1 < kParts) {
+                pa = fma_mixed<0, 0>(w, kMinusOne, pa);
+                pb = fma_mixed<1, 0>(w, kMinusOne, pb);
+              }
             }
           }
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
           uint32_t wt[kT][kTerms][2];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            // the group's scales of a token pair
-            const uint32_t pair = kN == 1 ? sc[s][0] : prmt(sc[s][j / 2], sc[s][(kN + j) / 2], (j & 1) ? 0x7632 : 0x5410);
+          for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int h = 0; h < kT; ++h) {
-              const uint32_t f = masked ? pair & vis[u][h][s] : pair;
-              if constexpr (kTerms == 2) {
-                // p0 s less its rounding is exact in bf16, and p1 s joins it
-                wt[h][0][s] = mul_bf16x2(p[h][0][s], f);
-                wt[h][1][s] = fma_bf16x2(p[h][1][s], f, fma_bf16x2(p[h][0][s], f, mul_bf16x2(p[h][0][s] ^ 0x80008000u, f)));
-              } else {
-                float w0 = 0.0f, w1 = 0.0f;
+              // the group's scales of the two tokens
+              uint32_t sa = kN == 1 ? sc[s][0] : sc[s][j / 2], sb = kN == 1 ? sc[s][0] : sc[s][(kN + j) / 2];
+              if (masked) {
+                sa = (vis[u][h][s] & 1u) ? sa : 0u;
+                sb = (vis[u][h][s] & 2u) ? sb : 0u;
+              }
+              constexpr int kLo = 0, kHi = 1;
+              float w0 = 0.0f, w1 = 0.0f;
 #pragma unroll
-                for (int e = kTerms - 1; e >= 0; --e) {
-                  w0 += __uint_as_float(p[h][e][s] << 16);
-                  w1 += __uint_as_float(p[h][e][s] & 0xffff0000u);
-                }
-                w0 *= __uint_as_float(f << 16);
-                w1 *= __uint_as_float(f & 0xffff0000u);
+              for (int e = kParts - 1; e >= 0; --e) {
+                w0 = (j & 1) ? fma_mixed<kLo, kHi>(p[h][e][s], sa, w0) : fma_mixed<kLo, kLo>(p[h][e][s], sa, w0);
+                w1 = (j & 1) || kN == 1 ? fma_mixed<kHi, kHi>(p[h][e][s], sb, w1) : fma_mixed<kHi, kLo>(p[h][e][s], sb, w1);
+              }
+              if constexpr (kHalf) {
+                wt[h][0][s] = f16x2_of(w0, w1);
+              } else {
 #pragma unroll
                 for (int e = 0; e < kTerms; ++e) {
                   const uint32_t w = bf16x2_of(w0, w1);
                   wt[h][e][s] = w;
-                  w0 -= __uint_as_float(w << 16);
-                  w1 -= __uint_as_float(w & 0xffff0000u);
+                  if (e + 1 < kTerms) {
+                    w0 = fma_mixed<0, 0>(w, kMinusOne, w0);
+                    w1 = fma_mixed<1, 0>(w, kMinusOne, w1);
+                  }
                 }
               }
             }
-          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
             const uint32_t u0 = y ? vw[0][j] >> 8 : vw[0][j], u1 = y ? vw[1][j] >> 8 : vw[1][j];
-            const uint32_t a0 = fma_bf16x2(u0 & 0x000f000fu, k2p127, kLow8), a1 = fma_bf16x2(u0 & 0x00f000f0u, k2p127, kHigh8);
-            const uint32_t a2 = fma_bf16x2(u1 & 0x000f000fu, k2p127, kLow8), a3 = fma_bf16x2(u1 & 0x00f000f0u, k2p127, kHigh8);
+            const uint32_t a0 = Codes::low(u0), a1 = Codes::high(u0), a2 = Codes::low(u1), a3 = Codes::high(u1);
 #pragma unroll
-            for (int h = 0; h < kT; ++h)
+            for (int h = 0; h < kT; ++h) {
+              if constexpr (kHalf) {
+                mma_f16_add(o[2 * j + y][h], a0, a1, a2, a3, wt[h][0][0], wt[h][0][1]);
+              } else {
 #pragma unroll
-              for (int e = 0; e < kTerms; ++e) mma_bf16(o[2 * j + y][h], a0, a1, a2, a3, wt[h][e][0], wt[h][e][1]);
+                for (int e = 0; e < kTerms; ++e) mma_bf16(o[2 * j + y][h], a0, a1, a2, a3, wt[h][e][0], wt[h][e][1]);
+              }
+            }
           }
         }
       }
@@ -573,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     __syncwarp();
     logits(ring, x);  // a warp without steps: of stale bytes, not used
     for (int k = 0; k < whole; ++k) {
-      move_maxima(x);
       cp_async_wait<0>();
       __syncwarp();  // this step's values and the next one's keys are here for all, and what they replace is read
+      move_maxima(x, ring + 2 * C::kHalf + now);
       const uint32_t then = C::kHalf - now;
       issue(ring + now, ring + 2 * C::kHalf + then);
       float y[kU][kT][4];
@@ -610,10 +702,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             const int p = tok + 16 * u + g + 8 * s, q = tok + 16 * u + 2 * t + 8 * s;
             if (!visible(da, p)) x[u][h][2 * s] = -INFINITY;
             if (!visible(db, p)) x[u][h][2 * s + 1] = -INFINITY;
-            vis[u][h][s] = (visible(dg, q) ? 0xffffu : 0u) | (visible(dg, q + 1) ? 0xffff0000u : 0u);
+            vis[u][h][s] = (visible(dg, q) ? 1u : 0u) | (visible(dg, q + 1) ? 2u : 0u);
           }
       }
-      move_maxima(x);
+      move_maxima(x, ring + 2 * C::kHalf + now);
       output(ring + 2 * C::kHalf + now, x, true, vis);
     }
 
@@ -635,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
         float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
-        *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0] * 64.0f, o[i][h][1] * 64.0f);
-        *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2] * 4.0f, o[i][h][3] * 4.0f);
+        *reinterpret_cast<float2*>(r) = make_float2(o[i][h][0] * Codes::kLow, o[i][h][1] * Codes::kLow);
+        *reinterpret_cast<float2*>(r + 8 * kCols) = make_float2(o[i][h][2] * Codes::kHigh, o[i][h][3] * Codes::kHigh);
       }
     }
     __syncthreads();
@@ -822,7 +914,7 @@ cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
 
 template <int D, int kCols>
 cudaError_t launch_c(const Decode4Args& a, cudaStream_t s) {
-  return a.out_dtype == SL8_F32 ? launch_t<D, kCols, 3>(a, s) : launch_t<D, kCols, 2>(a, s);
+  return a.out_dtype == SL8_F32 ? launch_t<D, kCols, 3>(a, s) : launch_t<D, kCols, 1>(a, s);
 }
 
 template <int D>
