@@ -59,10 +59,8 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[M]) {
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(a + 4 * i) : "memory");
   }
 }
-__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src),
-               "r"(static_cast<uint32_t>(on))
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -285,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   // another swizzle); of its scales' 2 kN: one, the units of a step side by side
   constexpr int kChunks = 16 * kN, kPer = kChunks >= 32 ? kChunks / 32 : 1;
   const uint32_t dst = chunk_off<D>((lane % kChunks) / kN, lane % kN);
-  const uint32_t dst_s = C::kScales + 16 * lane;
+  const uint32_t dst_s = C::kScales + 16 * (lane % (2 * kN * kU));
   const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row and matrix that the lane's address is for
   const uint32_t frag = kN == 1   ? chunk_off<D>(8 * (lm & 1) + lr, 0)
                         : kN == 2 ? chunk_off<D>(8 * (lm >> 1) + lr, lm & 1)
@@ -317,12 +315,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 
     // ---------------------------------------------------------- loads
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_blocks;
-    // the sixteenth of a row index at which a unit lies; lane i looks up unit i % kU of step k + i / kU
+    // the sixteenth of a row index at which a unit lies; lane i looks up unit i % kU of step k + i / kU.
+    // Units past the end are row 0: loaded, and not used.
     auto rows_at = [&](int k) -> uint32_t {
       const int step = k + lane / kU;
-      if (step >= n) return 0xffffffffu;
+      if (step >= n) return 0;
       const int tok = (first + step * kWarps) * C::kStep + lane % kU * 16;
-      if (tok >= L) return 0xffffffffu;
+      if (tok >= L) return 0;
       const int blk = tok / a.page;
       int32_t pg = table[blk];
       if (pg < 0 || pg >= a.num_pages) {
@@ -332,36 +331,46 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       return (static_cast<uint32_t>(pg) * a.Hkv + head) * (a.page / 16) + (tok - blk * a.page) / 16;
     };
     constexpr int kBatch = 32 / kU;  // steps that a look-up covers
-    uint32_t rows = rows_at(0), next_rows = n > kBatch ? rows_at(kBatch) : 0xffffffffu;
+    uint32_t rows = rows_at(0), next_rows = n > kBatch ? rows_at(kBatch) : 0;
     uint32_t row[kU];  // of the step whose keys were asked for last
-    int asked = 0;
+    int looked = 0, at_lane = 0;
+    // Lanes that have no chunk of their own repeat another's.
     auto ask = [&](uint32_t to, const uint8_t* codes, const uint16_t* scales) {
+      if constexpr (kChunks >= 32) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const bool on = row[u] != 0xffffffffu;
-        const uint8_t* src = codes + static_cast<uint64_t>(row[u]) * (8 * D) + 16 * (lane % kChunks);
+        for (int u = 0; u < kU; ++u) {
+          const uint8_t* src = codes + static_cast<uint64_t>(row[u]) * (8 * D) + 16 * lane;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          cp_async16_if(on && (kChunks >= 32 || lane < kChunks), to + u * 8 * D + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i, src + 512 * i);
+          for (int i = 0; i < kPer; ++i) cp_async16(to + u * 8 * D + (kN == 8 ? dst ^ (64 * (i & 1)) : dst) + 512 * i, src + 512 * i);
+        }
+      } else {  // d = 32: half a warp a unit
+        const uint32_t r = lane < 16 ? row[0] : row[kU - 1];
+        cp_async16(to + (lane >> 4) * 8 * D + dst, codes + static_cast<uint64_t>(r) * (8 * D) + 16 * (lane & 15));
       }
-      const uint32_t r = kU == 2 && lane >= 2 * kN ? row[kU - 1] : row[0];
-      cp_async16_if(lane < 2 * kN * kU && r != 0xffffffffu, to + dst_s,
-                    reinterpret_cast<const uint8_t*>(scales) + static_cast<uint64_t>(r) * D + 16 * (lane % (2 * kN)));
+      const uint32_t r = kU == 2 && (lane & (2 * kN)) ? row[kU - 1] : row[0];
+      cp_async16(to + dst_s, reinterpret_cast<const uint8_t*>(scales) + static_cast<uint64_t>(r) * D + 16 * (lane % (2 * kN)));
     };
     // the keys of the next step and the values of the one before it
-    auto issue = [&](uint32_t to_k, uint32_t to_v) {
-      if (asked > 0) ask(to_v, a.v_pages, a.v_scale);
-      if (asked % kBatch == 0 && asked > 0) {
+    auto next_row = [&] {
+      if (at_lane == 32) {
+        looked += kBatch;
         rows = next_rows;
-        next_rows = rows_at(asked + kBatch);
+        next_rows = rows_at(looked + kBatch);
+        at_lane = 0;
       }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) row[u] = __shfl_sync(0xffffffffu, rows, asked % kBatch * kU + u);
+      for (int u = 0; u < kU; ++u) row[u] = __shfl_sync(0xffffffffu, rows, at_lane + u);
+      at_lane += kU;
+    };
+    auto issue = [&](uint32_t to_k, uint32_t to_v) {
+      ask(to_v, a.v_pages, a.v_scale);
+      next_row();
       ask(to_k, a.k_pages, a.k_scale);
       cp_async_commit();
-      ++asked;
     };
-    issue(ring, 0);
+    next_row();
+    ask(ring, a.k_pages, a.k_scale);
+    cp_async_commit();
     issue(ring + C::kHalf, ring + 2 * C::kHalf);
 
     // ---------------------------------------------------------- the query columns: eight lanes a row
@@ -670,15 +679,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       move_maxima(x, ring + 2 * C::kHalf + now);
       const uint32_t then = C::kHalf - now;
       issue(ring + now, ring + 2 * C::kHalf + then);
-      float y[kU][kT][4];
-      logits(ring + then, y);  // of the masked step, or of stale bytes: those are not used
       output(ring + 2 * C::kHalf + now, x, false, no_mask);
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int h = 0; h < kT; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[u][h][i] = y[u][h][i];
+      logits(ring + then, x);  // of the masked step, or of one past the end, which are not used
       now = then;
     }
     cp_async_wait<0>();
