@@ -1235,8 +1235,8 @@ size_t sl8_attn_int4_paged_decode_workspace_size(int32_t B, int32_t T, int32_t H
                                                  int32_t page_size, int32_t d, int32_t num_splits) {
   const Decode4Plan p = decode4_plan(B, T, Hq, Hkv, max_blocks, page_size, d, num_splits);
   if (p.groups <= 0) return 0;
-  size_t ml, ends;
-  return p.ctas ? decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends) : 16;  // 16: none is used
+  size_t ml, ends, starts;
+  return p.ctas ? decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends, &starts) : 16;  // 16: none is used
 }
 
 int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_pages, const void* k_scale_pages,
@@ -1287,13 +1287,14 @@ int sl8_attn_int4_paged_decode(const void* q, int q_dtype, const uint8_t* k_page
   a.lse = lse_out;
   a.ctas = p.ctas;
   if (p.ctas) {
-    size_t ml, ends;
-    const size_t need = decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends);
+    size_t ml, ends, starts;
+    const size_t need = decode4_workspace(static_cast<int64_t>(B) * Hkv * p.groups, d, p.cols, p.ctas, &ml, &ends, &starts);
     SL8_CHECK(workspace && workspace_bytes >= need && aligned16(workspace), SL8_ERR_WORKSPACE);
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(w);
     a.part_ml = reinterpret_cast<float2*>(w + ml);
     a.ends = reinterpret_cast<int32_t*>(w + ends);
+    a.starts = reinterpret_cast<int32_t*>(w + starts);
   }
   SL8_LAUNCH(launch_decode4(a, d, static_cast<cudaStream_t>(stream)));
   return SL8_OK;

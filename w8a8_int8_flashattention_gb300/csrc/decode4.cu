@@ -148,12 +148,14 @@ template <int D, int kCols>
 struct Cfg4 {
   static constexpr int kN = D / kGroup4;  // groups (and 16-byte chunks) of a row
   static constexpr int kT = (kCols + 7) / 8;  // tiles of eight columns
-  static constexpr int kU = D == 256 ? 1 : 2;  // units of 16 tokens that a warp takes at a time, a step
+  static constexpr int kU = D == 256 || (D == 128 && kCols > 16) ? 1 : 2;  // units of 16 tokens that a warp takes at a time, a step
   static constexpr int kStep = 16 * kU;
+  static constexpr int kStart = D == 256 ? 16 : 512 / kStep;  // steps that a sequence's start and end are worth, see below
   static constexpr int kHalf = kU * 9 * D;  // a step's keys, or its values: codes [kU][16][D / 2], scales [kU][16][kN]
   static constexpr int kScales = kU * 8 * D;
   static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
-  static constexpr int kCtas = D == 256 ? 3 : D == 128 ? (kCols == 8 ? 4 : 3) : D == 64 ? (kCols == 8 ? 5 : 4) : 5;
+  // as many CTAs an SM as their registers let: the accumulators are D kT / 4 a thread
+  static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : D == 64 ? 6 - kT : 5;
   // after the loop the rings hold the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
   static constexpr int kRed = 0, kPart = kWarps * D * kCols * 4, kMerge = kPart + kCols * D * 4;
   static constexpr int kQf = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;  // [kN][kT][32] fragments of Q, 16 bytes
@@ -161,17 +163,19 @@ struct Cfg4 {
   static constexpr int kQs = kBias + kN * kT * 32;        // [kCols] scales
   static constexpr int kQc = kQs + kCols * 4;             // [kCols][D] query codes
   static constexpr int kStat = kQc + kCols * D;           // [warp][kCols][2]: max (log2), sum
-  static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps
-  static constexpr int kMl = kWt + kWarps * kCols * 4;    // [kCols] max, [kCols] sum of the CTA
-  static constexpr int kBytes = kMl + kCols * 8;
+  static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps' parts, or of the CTAs'
+  static constexpr int kMl = kWt + kMaxCluster * kCols * 4;  // [kCols][2]: max, sum of the CTA
+  static constexpr int kRows = kMl + kCols * 8;           // [kCols] rows of q and out
+  static constexpr int kBytes = kRows + kCols * 8;
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "kCtas CTAs fit an SM");
 };
 
-// The work of a balanced launch: the (sequence, kv head, column group)s in a row, each kStart + its steps
-// long, are cut evenly among `ctas` CTAs, but into no less than kLeast.  kStart stands for what a CTA
-// spends on a sequence besides its steps, queries and merge (without it a CTA that had 32 sequences of one token ran five
-// times as long as the others); an empty sequence counts one step.
-constexpr int kStart = 16, kLeast = 4 * kWarps;
+// The work of a balanced launch: the (kv head, column group)s, each with all sequences in a row, each
+// sequence kStart and its steps long, are cut evenly among `ctas` CTAs, but into no less than kLeast
+// steps.  kStart stands for what a CTA spends on a sequence besides its steps, queries and merge; an empty
+// sequence counts one step.  (Without kStart a CTA that had 32 sequences of one token ran five times as long as
+// the others; with a sequence's heads in a row, two times with it.)
+constexpr int kLeast = 4 * kWarps;
 __device__ __forceinline__ int steps_of(int L, int step) { return max(1, (L + step - 1) / step); }
 
 // Byte offset of chunk j of row r: eight rows' chunks j lie in different banks.
@@ -219,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   };
 
   // ------------------------------------------------------------ this CTA's part of the work
-  if (a.ctas) grid_dependents_launch();  // the combine's CTAs may come as this grid's go
+  if (a.ctas) {
+    grid_dependents_launch();  // the combine's CTAs may come as this grid's go
+    if (threadIdx.x == 0) a.starts[blockIdx.x] = -1;  // the sequence that this CTA begins and does not end
+  }
   const int S = a.ctas ? 1 : a.splits;
   int rank = 0, b, inner;      // inner: kv head * groups + column group
   int64_t left = 1;            // balanced: what this CTA still has of its share
@@ -229,46 +236,42 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     int64_t before = 0, x = 0, end = 0;  // a thread's sequence: its length and where it ends
     auto chunk = [&](int c) {            // kThreads sequences from c on
       const int i = c + static_cast<int>(threadIdx.x);
-      x = i < a.B ? static_cast<int64_t>(kStart + steps_of(length_of(i), C::kStep)) * per_seq : 0;
+      x = i < a.B ? C::kStart + steps_of(length_of(i), C::kStep) : 0;
       end = before + cta_prefix(x, scan);
       if (threadIdx.x == kThreads - 1) scan[kWarps] = end;
       __syncthreads();
       before = scan[kWarps];
     };
     for (int c = 0; c < a.B; c += kThreads) chunk(c);
+    auto divide = [](int64_t x, int64_t y) {  // of numbers that mostly fit 32 bits
+      return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+    };
     // CTA i of `used` has [i q + min(i, r), ...) of the total, q r its quotient and remainder
-    const int64_t total = before, used = max(int64_t(1), min(static_cast<int64_t>(a.ctas), total / kLeast));
+    const int64_t all = before, total = all * per_seq;
+    const int64_t used = max(int64_t(1), min(static_cast<int64_t>(a.ctas), total / kLeast));
     if (blockIdx.x >= used) return;
-    int64_t q, r;
-    if (total < (int64_t(1) << 31)) {
-      q = static_cast<uint32_t>(total) / static_cast<uint32_t>(used);
-      r = total - q * used;
-    } else {
-      q = total / used;
-      r = total - q * used;
-    }
+    const int64_t q = divide(total, used), r = total - q * used;
     const int64_t from = blockIdx.x * q + min(static_cast<int64_t>(blockIdx.x), r);
     left = q + (blockIdx.x < r ? 1 : 0);
-    // the sequence that `from` lies in
+    inner = static_cast<int>(divide(from, all));
+    const int64_t off = from - inner * all;
+    // the sequence that `off` lies in
     auto find = [&](int c) {
-      if (from >= end - x && from < end) scan[kWarps + 1] = c + static_cast<int>(threadIdx.x), scan[kWarps + 2] = end - x;
+      if (off >= end - x && off < end) scan[kWarps + 1] = c + static_cast<int>(threadIdx.x), scan[kWarps + 2] = end - x;
     };
     if (a.B <= kThreads) {
       find(0);
     } else {
       __syncthreads();
       before = 0;
-      for (int c = 0; c < a.B && before <= from; c += kThreads) {
+      for (int c = 0; c < a.B && before <= off; c += kThreads) {
         chunk(c);
         find(c);
       }
     }
     __syncthreads();
     b = static_cast<int>(scan[kWarps + 1]);
-    const int64_t off = from - scan[kWarps + 2];
-    const int per = kStart + steps_of(length_of(b), C::kStep);
-    inner = static_cast<int>(off < (int64_t(1) << 31) ? static_cast<uint32_t>(off) / static_cast<uint32_t>(per) : off / per);
-    s0 = static_cast<int>(off - static_cast<int64_t>(inner) * per) - kStart;
+    s0 = static_cast<int>(off - scan[kWarps + 2]) - C::kStart;
     __syncthreads();
   } else {
     const unsigned item = blockIdx.x / static_cast<unsigned>(S);
@@ -294,11 +297,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     const int head = inner / a.groups;
     const int col0 = (inner - head * a.groups) * a.cols;  // first of this segment's columns
     const int GC = min(a.cols, a.T * G - col0);
-    // row of q and out that column c stands for: its draft, its query head
-    auto row_at = [&](int c) {
-      const int dr = (col0 + c) / G;
-      return (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
-    };
+    int64_t* const row_of = reinterpret_cast<int64_t*>(smem + C::kRows);  // of q and out, for each column
     const int L = length_of(b), per = steps_of(L, C::kStep);
     int s1 = per;
     if (a.ctas) {
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     };
     constexpr int kBatch = 32 / kU;  // steps that a look-up covers
     uint32_t rows = rows_at(0), next_rows = n > kBatch ? rows_at(kBatch) : 0;
-    uint32_t row[kU];  // of the step whose keys were asked for last
+    uint32_t row[kU] = {};  // of the step whose keys were asked for last
     int looked = 0, at_lane = 0;
     // Lanes that have no chunk of their own repeat another's.
     auto ask = [&](uint32_t to, const uint8_t* codes, const uint16_t* scales) {
@@ -376,10 +375,15 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     // ---------------------------------------------------------- the query columns: eight lanes a row
     int8_t* qc = reinterpret_cast<int8_t*>(smem + C::kQc);
     float* qsc = reinterpret_cast<float*>(smem + C::kQs);
-    if (4 * warp < kCols) {
-      const int c = 4 * warp + (lane >> 3), l8 = lane & 7;
+    for (int c = static_cast<int>(threadIdx.x >> 3); c < kCols; c += kThreads / 8) {
+      const int l8 = lane & 7;
       float x[D / 32][4] = {}, amax = 0.0f;
-      if (c < GC) load_runs<D / 32>(a.q, a.q_dtype, row_at(c) * D + 4 * l8, 32, x);
+      if (c < GC) {
+        const int dr = (col0 + c) / G;  // its draft, its query head
+        const int64_t at = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
+        load_runs<D / 32>(a.q, a.q_dtype, at * D + 4 * l8, 32, x);
+        if (l8 == 0) row_of[c] = at;
+      }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -734,154 +738,186 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       }
     }
     __syncthreads();
-    if (threadIdx.x < kCols * kWarps) {  // column c: the weight of warp w's state, and (w = 0) max and sum
-      const int c = threadIdx.x % kCols, w = threadIdx.x / kCols;
-      float M = -INFINITY, sum = 0.0f;
+    // The parts of a column: weights 2^(m - M) of their sums and outputs, over the whole sum where it is all there is.
+    const bool cut = a.ctas && s1 - s0 < per;  // a part of a sequence, for the combine
+    auto weigh = [&](int c, int n, const auto& v, float& M, float& sum) {
+      constexpr int kMost = sizeof(v) / sizeof(v[0]);
+      M = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, stat[(i * kCols + c) * 2]);
-      const float mw = stat[(w * kCols + c) * 2];
-      wt[w * kCols + c] = mw == -INFINITY ? 0.0f : ex2(mw - M);
-      if (w == 0) {
+      for (int i = 0; i < kMost; ++i)
+        if (i < n) M = fmaxf(M, v[i].x);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float mi = stat[(i * kCols + c) * 2];
-          if (mi != -INFINITY) sum = fmaf(ex2(mi - M), stat[(i * kCols + c) * 2 + 1], sum);
+      for (int i = 0; i < kMost; ++i)
+        if (i < n) {
+          const float f = v[i].x == -INFINITY ? 0.0f : ex2(v[i].x - M);
+          wt[i * kCols + c] = f;
+          if (v[i].x != -INFINITY) sum = fmaf(f, v[i].y, sum);
         }
-        ml[c] = M;
-        ml[kCols + c] = sum;
-      }
-    }
-    __syncthreads();
-    for (int u = threadIdx.x; u < D * (kCols / 4); u += kThreads) {  // row u % D, columns 4 (u / D) ..
-      const int r = u % D, q4 = u / D;
-      const int dim = 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1);
-      if (4 * q4 >= GC) continue;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    auto finish = [&](int c, int n, float M, float sum) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int i = 0; i < n; ++i) wt[i * kCols + c] *= inv;
+      if (a.lse && rank == 0) a.lse[row_of[c]] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    };
+    // slot 0 of a CTA's two parts where its work begins, else 1
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0);
+    if (threadIdx.x < GC) {
+      const int c = threadIdx.x;
+      float M, sum;
+      float2 v[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(red + (w * D + r) * kCols + 4 * q4);
-        const float4 f = *reinterpret_cast<const float4*>(wt + w * kCols + 4 * q4);
-        acc.x = fmaf(v.x, f.x, acc.x);
-        acc.y = fmaf(v.y, f.y, acc.y);
-        acc.z = fmaf(v.z, f.z, acc.z);
-        acc.w = fmaf(v.w, f.w, acc.w);
-      }
-      part[(4 * q4 + 0) * D + dim] = acc.x;
-      part[(4 * q4 + 1) * D + dim] = acc.y;
-      part[(4 * q4 + 2) * D + dim] = acc.z;
-      part[(4 * q4 + 3) * D + dim] = acc.w;
+      for (int i = 0; i < kWarps; ++i) v[i] = *reinterpret_cast<const float2*>(stat + (i * kCols + c) * 2);
+      weigh(c, kWarps, v, M, sum);
+      if (S > 1) *reinterpret_cast<float2*>(ml + 2 * c) = make_float2(M, sum);
+      else if (cut) a.part_ml[slot * kCols + c] = make_float2(M, sum);
+      else finish(c, kWarps, M, sum);
     }
-    if (S > 1) cluster.sync();
-    else __syncthreads();
-
     if (a.ctas && threadIdx.x == 0) {  // the CTAs that have the first and the last step
       int32_t* const ends = a.ends + 2 * (static_cast<int64_t>(b) * per_seq + inner);
       if (s0 == 0) ends[0] = static_cast<int32_t>(blockIdx.x);
       if (s1 == per) ends[1] = static_cast<int32_t>(blockIdx.x);
+      if (s0 == 0 && cut) a.starts[blockIdx.x] = static_cast<int32_t>(b) * per_seq + inner;
     }
-    if (a.ctas && s1 - s0 < per) {
-      // a part of a sequence, for the combine: slot 0 of this CTA where its work begins, else 1
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0);
-      float* po = a.part_o + slot * (kCols * D);
-      for (int u = threadIdx.x; u < GC * D; u += kThreads) po[u] = part[u];
-      if (threadIdx.x < GC) a.part_ml[slot * kCols + threadIdx.x] = make_float2(ml[threadIdx.x], ml[kCols + threadIdx.x]);
-    } else {
-      // ------------------------------------------------------ merge the S parts of the cluster
-      for (int u = rank * kThreads + threadIdx.x; u < GC * D; u += S * kThreads) {
-        const int c = u / D, dim = u % D;
-        float mr[kMaxCluster], lr2[kMaxCluster], xr[kMaxCluster];  // all on their way at once
+    __syncthreads();
+    for (int u = threadIdx.x; u < D * (kCols / 4); u += kThreads) {  // row u % D, columns 4 (u / D) ..
+      const int r = u % D, c = 4 * (u / D);
+      if (c >= GC) break;
+      const int dim = 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1);  // a warp's are 32 in a row
+      float acc[4] = {};
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          if (r < S) {
-            const float* peer = reinterpret_cast<const float*>(S > 1 ? cluster.map_shared_rank(smem, r) : smem);
-            mr[r] = peer[C::kMl / 4 + c];
-            lr2[r] = peer[C::kMl / 4 + kCols + c];
-            xr[r] = peer[C::kPart / 4 + c * D + dim];
-          }
-        }
-        float M = -INFINITY, sum = 0.0f, acc = 0.0f;
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(red + (w * D + r) * kCols + c);
+        const float4 f = *reinterpret_cast<const float4*>(wt + w * kCols + c);
+        acc[0] = fmaf(v.x, f.x, acc[0]);
+        acc[1] = fmaf(v.y, f.y, acc[1]);
+        acc[2] = fmaf(v.z, f.z, acc[2]);
+        acc[3] = fmaf(v.w, f.w, acc[3]);
+      }
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < S) M = fmaxf(M, mr[r]);
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          if (r < S && mr[r] != -INFINITY) {
-            const float f = ex2(mr[r] - M);
-            sum = fmaf(f, lr2[r], sum);
-            acc = fmaf(f, xr[r], acc);
-          }
-        }
-        const int64_t out_row = row_at(c);
-        store_out(a.out, a.out_dtype, out_row * D + dim, sum == 0.0f ? 0.0f : acc / sum);
-        if (a.lse && dim == 0) a.lse[out_row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+      for (int i = 0; i < 4; ++i) {
+        if (c + i >= GC) break;
+        if (S > 1) part[(c + i) * D + dim] = acc[i];
+        else if (cut) a.part_o[(slot * kCols + c + i) * D + dim] = acc[i];
+        else store_out(a.out, a.out_dtype, row_of[c + i] * D + dim, acc[i]);
       }
     }
-    if (S > 1) cluster.sync();  // no CTA leaves while another reads its part
+    if (S > 1) {  // the S CTAs' parts: each takes every S-th run of four channels
+      cluster.sync();
+      if (threadIdx.x < GC) {
+        const int c = threadIdx.x;
+        float M, sum;
+        float2 v[kMaxCluster] = {};
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+          if (i < S) v[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(ml, i) + 2 * c);
+        weigh(c, S, v, M, sum);
+        finish(c, S, M, sum);
+      }
+      __syncthreads();
+      for (int u = rank * kThreads + threadIdx.x; u < GC * (D / 4); u += S * kThreads) {
+        const int c = u / (D / 4), q = u % (D / 4);
+        float4 v[kMaxCluster];
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+          if (i < S) v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, i) + c * D + 4 * q);
+        float acc[4] = {};
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+          if (i < S) {
+            const float f = wt[i * kCols + c];
+            acc[0] = fmaf(v[i].x, f, acc[0]);
+            acc[1] = fmaf(v[i].y, f, acc[1]);
+            acc[2] = fmaf(v[i].z, f, acc[2]);
+            acc[3] = fmaf(v[i].w, f, acc[3]);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_out(a.out, a.out_dtype, row_of[c] * D + 4 * q + i, acc[i]);
+      }
+      cluster.sync();  // no CTA leaves while another reads its part
+    }
     if (!a.ctas) return;
     if (left <= 0) return;
-    s0 = -kStart;
-    if (++inner == per_seq) inner = 0, ++b;
+    s0 = -C::kStart;
+    if (++b == a.B) b = 0, ++inner;
     __syncthreads();  // the parts are read
   }
 }
 
-// The parts of each (sequence, kv head, column group) of a balanced launch that was cut, one CTA a
-// column: D / 4 threads take a part, the next ones another.
+// The parts of each (sequence, kv head, column group) of a balanced launch that was cut: D / 4 threads take
+// a part of a column, the next ones another.  A CTA takes a column of each of them (kEach) or, where there are more than
+// CTAs of the kernel above, of the one that such a CTA began and did not end, if it did.
 constexpr int kJoin = 256;
-template <int D, int kCols>
+template <int D, int kCols, bool kEach>
 __global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Args a) {
   constexpr int kRow = D / 4, kAtOnce = kJoin / kRow;
   __shared__ float4 sm[kJoin];
-  __shared__ float red[kJoin / 32], sums[kAtOnce];
+  __shared__ float2 sums[kAtOnce];
   const int per_seq = a.Hkv * a.groups, G = a.Hq / a.Hkv;
-  const unsigned item = blockIdx.x / static_cast<unsigned>(a.cols);
-  const int c = static_cast<int>(blockIdx.x - item * a.cols);
-  const int b = static_cast<int>(item / static_cast<unsigned>(per_seq));
-  const int inner = static_cast<int>(item - static_cast<unsigned>(b) * per_seq);
-  const int head = inner / a.groups, col0 = (inner - head * a.groups) * a.cols;
-  if (col0 + c >= a.T * G) return;
   grid_dependency_wait();
+  const int which = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.cols));
+  const int c = static_cast<int>(blockIdx.x) - which * a.cols;
+  const int item = kEach ? which : a.starts[which];
+  if (item < 0) return;
   const int2 ends = reinterpret_cast<const int2*>(a.ends)[item];
   const int i0 = ends.x, i1 = ends.y;
   if (i0 == i1) return;  // written by that CTA
+  const int b = item / per_seq, inner = item - b * per_seq;
+  const int head = inner / a.groups, col0 = (inner - head * a.groups) * a.cols, GC = min(a.cols, a.T * G - col0);
   auto slot_of = [&](int i) { return static_cast<int64_t>(2 * i + (i == i0 ? 1 : 0)); };
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float M = -INFINITY;
-  for (int i = i0 + static_cast<int>(threadIdx.x); i <= i1; i += kJoin) M = fmaxf(M, a.part_ml[slot_of(i) * kCols + c].x);
-  M = warp_max_f(M);
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) M = fmaxf(M, red[w]);
+  if (c >= GC) return;
+  // each row of threads joins every kAtOnce-th part, kAhead of them on their way at once
+  constexpr int kAhead = 4;
   const int q = static_cast<int>(threadIdx.x) % kRow, r = static_cast<int>(threadIdx.x) / kRow;
-  float sum = 0.0f;
+  float M = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = i0 + r; i <= i1; i += kAtOnce) {
-    const int64_t slot = slot_of(i);
-    const float2 v = a.part_ml[slot * kCols + c];
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot * kCols + c) * D + 4 * q);
-    if (v.x != -INFINITY) {
-      const float f = ex2(v.x - M);
-      sum = fmaf(f, v.y, sum);
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+  for (int i = i0 + r; i <= i1; i += kAhead * kAtOnce) {
+    float2 v[kAhead];
+    float4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = i + k * kAtOnce;
+      const int64_t slot = slot_of(min(j, i1));
+      v[k] = a.part_ml[slot * kCols + c];
+      x[k] = *reinterpret_cast<const float4*>(a.part_o + (slot * kCols + c) * D + 4 * q);
+      if (j > i1) v[k].x = -INFINITY;
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, v[k].x);
+    if (top == -INFINITY) continue;
+    const float keep = ex2(M - top);
+    M = top;
+    sum *= keep;
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (v[k].x == -INFINITY) continue;
+      const float f = ex2(v[k].x - M);
+      sum = fmaf(f, v[k].y, sum);
+      acc.x = fmaf(f, x[k].x, acc.x);
+      acc.y = fmaf(f, x[k].y, acc.y);
+      acc.z = fmaf(f, x[k].z, acc.z);
+      acc.w = fmaf(f, x[k].w, acc.w);
     }
   }
   sm[threadIdx.x] = acc;
-  if (q == 0) sums[r] = sum;
+  if (q == 0) sums[r] = make_float2(M, sum);
   __syncthreads();
   if (r > 0) return;
-  sum = sums[0];
-  for (int i = 1; i < kAtOnce; ++i) {
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) M = fmaxf(M, sums[i].x);
+  sum = 0.0f;
+  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    if (sums[i].x == -INFINITY) continue;
+    const float f = ex2(sums[i].x - M);
     const float4 x = sm[i * kRow + q];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
-    sum += sums[i];
+    sum = fmaf(f, sums[i].y, sum);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
   }
   const int dr = (col0 + c) / G;
   const int64_t row = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
@@ -911,7 +947,9 @@ cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
   if (e != cudaSuccess || !a.ctas) return e;
-  return launch_pdl(decode4_combine_kernel<D, kCols>, dim3(items * a.cols), dim3(kJoin), 0, s, a);
+  if (items <= static_cast<unsigned>(a.ctas))
+    return launch_pdl(decode4_combine_kernel<D, kCols, true>, dim3(items * a.cols), dim3(kJoin), 0, s, a);
+  return launch_pdl(decode4_combine_kernel<D, kCols, false>, dim3(static_cast<unsigned>(a.ctas) * a.cols), dim3(kJoin), 0, s, a);
 }
 
 template <int D, int kCols>
@@ -922,21 +960,22 @@ cudaError_t launch_c(const Decode4Args& a, cudaStream_t s) {
 template <int D>
 cudaError_t launch_d(const Decode4Args& a, cudaStream_t s) {
   if constexpr (D == 256) return launch_c<D, 8>(a, s);
-  else return a.cols > 8 ? launch_c<D, 16>(a, s) : launch_c<D, 8>(a, s);
+  else return a.cols > 16 ? launch_c<D, 24>(a, s) : a.cols > 8 ? launch_c<D, 16>(a, s) : launch_c<D, 8>(a, s);
 }
 
 // CTAs of the kernel that fit the device at once.
+template <int D>
+int ctas_d(int32_t cols) {
+  if constexpr (D == 256) return Cfg4<D, 8>::kCtas;
+  else return cols > 16 ? Cfg4<D, 24>::kCtas : cols > 8 ? Cfg4<D, 16>::kCtas : Cfg4<D, 8>::kCtas;
+}
 int slots(int32_t d, int32_t cols) {
-  const int n = d == 256 ? Cfg4<256, 8>::kCtas
-                : d == 128 ? (cols > 8 ? Cfg4<128, 16>::kCtas : Cfg4<128, 8>::kCtas)
-                : d == 64  ? (cols > 8 ? Cfg4<64, 16>::kCtas : Cfg4<64, 8>::kCtas)
-                           : (cols > 8 ? Cfg4<32, 16>::kCtas : Cfg4<32, 8>::kCtas);
-  return n * num_sms();
+  return num_sms() * (d == 256 ? ctas_d<256>(cols) : d == 128 ? ctas_d<128>(cols) : d == 64 ? ctas_d<64>(cols) : ctas_d<32>(cols));
 }
 
 }  // namespace
 
-int32_t decode4_max_columns(int32_t d) { return d == 256 ? 8 : 16; }
+int32_t decode4_max_columns(int32_t d) { return d == 256 ? 8 : 24; }
 
 void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, int32_t num_splits, int32_t* splits,
                        int32_t* ctas) {
@@ -957,11 +996,12 @@ void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, i
   }
 }
 
-size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends) {
-  const size_t slots = 2 * static_cast<size_t>(ctas), c = cols > 8 ? 16 : 8;
+size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends, size_t* starts) {
+  const size_t slots = 2 * static_cast<size_t>(ctas), c = (cols + 7) / 8 * 8;
   *ml = slots * c * d * sizeof(float);
   *ends = *ml + slots * c * sizeof(float2);
-  return *ends + static_cast<size_t>(items) * 2 * sizeof(int32_t);
+  *starts = *ends + static_cast<size_t>(items) * 2 * sizeof(int32_t);
+  return *starts + static_cast<size_t>(ctas) * sizeof(int32_t);
 }
 
 cudaError_t launch_decode4(const Decode4Args& a, int32_t d, cudaStream_t s) {

@@ -339,17 +339,18 @@ struct Decode4Args {
   sl8_dtype out_dtype;
   float* lse;
   // ctas > 0: two parts a CTA, [2 ctas][8 or 16 columns][d], not normalised, their maxima (log2) and sums,
-  // and the first and last CTA of each (sequence, kv head, column group)
+  // the first and last CTA of each (sequence, kv head, column group), and for each CTA the one of those
+  // that it begins and does not end, or -1
   float* part_o;
   float2* part_ml;
-  int32_t* ends;
+  int32_t *ends, *starts;
 };
 int32_t decode4_max_columns(int32_t d);
 // How `items` (sequence, kv head, column group)s of up to `tokens` tokens are shared out: *splits, or *ctas.
 void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, int32_t num_splits, int32_t* splits,
                        int32_t* ctas);
-// Bytes of part_o, part_ml and ends, at offsets 0, *ml and *ends.
-size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends);
+// Bytes of part_o, part_ml, ends and starts, at offsets 0, *ml, *ends and *starts.
+size_t decode4_workspace(int64_t items, int32_t d, int32_t cols, int32_t ctas, size_t* ml, size_t* ends, size_t* starts);
 cudaError_t launch_decode4(const Decode4Args& a, int32_t d, cudaStream_t s);
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, cudaStream_t s);
 
