@@ -155,7 +155,7 @@ struct Cfg4 {
   static constexpr int kScales = kU * 8 * D;
   static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
   // as many CTAs an SM as their registers let: the accumulators are D kT / 4 a thread
-  static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : D == 64 ? 6 - kT : 5;
+  static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : 6 - kT;
   // after the loop the rings hold the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
   static constexpr int kRed = 0, kPart = kWarps * D * kCols * 4, kMerge = kPart + kCols * D * 4;
   static constexpr int kQf = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;  // [kN][kT][32] fragments of Q, 16 bytes
@@ -233,21 +233,19 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   int s0 = 0;                  // first step of the segment in its sequence; below 0: in its kStart
   if (a.ctas) {
     int64_t* scan = reinterpret_cast<int64_t*>(smem);
-    int64_t before = 0, x = 0, end = 0;  // a thread's sequence: its length and where it ends
-    auto chunk = [&](int c) {            // kThreads sequences from c on
-      const int i = c + static_cast<int>(threadIdx.x);
-      x = i < a.B ? C::kStart + steps_of(length_of(i), C::kStep) : 0;
-      end = before + cta_prefix(x, scan);
-      if (threadIdx.x == kThreads - 1) scan[kWarps] = end;
-      __syncthreads();
-      before = scan[kWarps];
-    };
-    for (int c = 0; c < a.B; c += kThreads) chunk(c);
+    // a thread's sequences, [i0, i1), and what they and all before them come to
+    const int strip = (a.B + kThreads - 1) / kThreads;
+    const int i0 = min(a.B, static_cast<int>(threadIdx.x) * strip), i1 = min(a.B, i0 + strip);
+    int64_t x = 0;
+    for (int i = i0; i < i1; ++i) x += C::kStart + steps_of(length_of(i), C::kStep);
+    const int64_t end = cta_prefix(x, scan);
+    if (threadIdx.x == kThreads - 1) scan[kWarps] = end;
+    __syncthreads();
+    const int64_t all = scan[kWarps], total = all * per_seq;
     auto divide = [](int64_t x, int64_t y) {  // of numbers that mostly fit 32 bits
       return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
     };
     // CTA i of `used` has [i q + min(i, r), ...) of the total, q r its quotient and remainder
-    const int64_t all = before, total = all * per_seq;
     const int64_t used = max(int64_t(1), min(static_cast<int64_t>(a.ctas), total / kLeast));
     if (blockIdx.x >= used) return;
     const int64_t q = divide(total, used), r = total - q * used;
@@ -255,19 +253,16 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     left = q + (blockIdx.x < r ? 1 : 0);
     inner = static_cast<int>(divide(from, all));
     const int64_t off = from - inner * all;
-    // the sequence that `off` lies in
-    auto find = [&](int c) {
-      if (off >= end - x && off < end) scan[kWarps + 1] = c + static_cast<int>(threadIdx.x), scan[kWarps + 2] = end - x;
-    };
-    if (a.B <= kThreads) {
-      find(0);
-    } else {
-      __syncthreads();
-      before = 0;
-      for (int c = 0; c < a.B && before <= off; c += kThreads) {
-        chunk(c);
-        find(c);
+    if (off >= end - x && off < end) {  // this thread has the sequence that `off` lies in
+      int64_t at = end - x;
+      int i = i0;
+      for (;; ++i) {
+        const int per = C::kStart + steps_of(length_of(i), C::kStep);
+        if (off < at + per) break;
+        at += per;
       }
+      scan[kWarps + 1] = i;
+      scan[kWarps + 2] = at;
     }
     __syncthreads();
     b = static_cast<int>(scan[kWarps + 1]);
