@@ -22,7 +22,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import w8a8_int8_flashattention_gb300 as sl8
+from _parity import check_f32
 from oracle import int4 as Q
 from oracle import serving as S
 
@@ -317,9 +319,9 @@ def _check_attention(out, lse, q, host, tables, lens, masks=None, tag=""):
     assert np.all(np.abs(gl[~empty] - wlse[~empty]) <= tl[~empty]), tag
 
 
-def _attend(B, T, hq, hkv, d, page, lens, qdt, odt, splits=0, tree=False, spread=1.0, seed=0, workspace=None):
+def _attend(B, T, hq, hkv, d, page, lens, qdt, odt, splits=0, tree=False, spread=1.0, seed=0, workspace=None, nb=None):
     rng = np.random.default_rng(seed + d + 7 * T)
-    nb = -(-max(max(lens), 1) // page) + 1
+    nb = nb or -(-max(max(lens), 1) // page) + 1
     num_pages = sum(-(-n // page) for n in lens) + 2
     pool, host = _filled(rng, num_pages, hkv, page, d, spread)
     tables = _tables(rng, lens, nb, page, num_pages)
@@ -483,3 +485,256 @@ def test_the_same_bits_every_time_and_shared_pages():
             b = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32(lens), num_splits=splits, return_lse=True)
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
         _check_attention(a[0][:, None], a[1][:, None], q[:, None], host, tables, lens)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 9])
+@pytest.mark.parametrize("d,cols", [(32, 7), (32, 9), (32, 24), (32, 25), (32, 64), (64, 8), (64, 17), (64, 23), (64, 49), (128, 15), (128, 16),
+                                    (128, 25), (128, 33), (128, 48), (256, 9), (256, 17)])
+def test_columns_of_heads_and_drafts(d, cols, splits):
+    """Drafts times query heads around what a tile and a CTA take, with one draft or one head, or both."""
+    for T, G in ((1, cols), (cols, 1)) + (((cols // 3, 3),) if cols % 3 == 0 else ()) + (((cols // 8, 8),) if cols % 8 == 0 else ()):
+        if T <= 32:
+            _attend(2, T, 2 * G, 2, d, 16, [T + 40, 9], BF16, F32 if cols % 2 else BF16, splits, tree=T > 1, seed=cols)
+
+
+@pytest.mark.parametrize("B,T,G,hkv,d,width,odt", [
+    (64, 1, 4, 2, 128, 16384, BF16), (700, 1, 3, 1, 64, 2048, F32), (5000, 1, 1, 1, 32, 256, F16), (130, 1, 20, 1, 64, 8192, BF16),
+    (257, 4, 2, 1, 128, 4096, F32), (129, 1, 2, 2, 256, 4096, BF16), (40, 32, 1, 1, 32, 32768, BF16)])
+def test_many_sequences_of_uneven_lengths_in_a_wide_table(B, T, G, hkv, d, width, odt):
+    """The work cut evenly among CTAs, where most sequences are empty or short and one is long: shares that hold
+    many sequences, a part of one, the end of one and the start of another; then none with a token."""
+    assert sl8.int4_decode_workspace_bytes(B, T, G * hkv, hkv, width // 16, 16, d) > 16  # the shares' parts
+    rng = np.random.default_rng(B)
+    lens = rng.choice([0, 0, 0, 1, 2, 15, 16, 17, 33, 70], B)
+    lens[rng.integers(0, B, 3)] = 200
+    lens[B // 2] = min(width, 3001)
+    lens[-1] = 5
+    _attend(B, T, G * hkv, hkv, d, 16, lens.tolist(), BF16, odt, nb=width // 16)
+    _attend(B, T, G * hkv, hkv, d, 16, [0] * B, BF16, odt, nb=width // 16)
+    _attend(B, T, G * hkv, hkv, d, 16, [0] * (B - 1) + [width], BF16, odt, nb=width // 16) if width <= 4096 else None
+
+
+def test_rows_and_columns_of_the_workspace_are_not_read_before_they_are_written():
+    """A workspace of NaN, and one that a call of another shape has left: the same bits."""
+    rng = np.random.default_rng(12)
+    pool, host = _filled(rng, 80, 2, 16, 64)
+    tables, lens = i32(rng.permutation(80).reshape(4, 20)), i32([320, 0, 17, 150])
+    q = torch.randn((4, 6, 64), device=DEV).bfloat16()
+    for splits in (9, 40, 1 << 20):
+        n = sl8.int4_decode_workspace_bytes(4, 1, 6, 2, 20, 16, 64, splits)
+        ws = torch.full((n // 4 + 1,), float("nan"), device=DEV).view(torch.uint8)
+        a = sl8.attn_int4_paged_decode(q, *pool, tables, lens, num_splits=splits, return_lse=True, workspace=ws)
+        ws.view(torch.int32).fill_(7)
+        b = sl8.attn_int4_paged_decode(q, *pool, tables, lens, num_splits=splits, return_lse=True, workspace=ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        _check_attention(a[0][:, None], a[1][:, None], q[:, None], host, tables.cpu().numpy(), lens.tolist())
+
+
+def test_offsets_past_32_bits():
+    """A pool whose codes pass 2^32 bytes many times, and whose scales do too: its last pages through every operator."""
+    hq, hkv, d, page = 8, 8, 128, 64
+    num_pages = (1 << 32) // (hkv * page * (d // 32) * 2) + 9
+    codes, scales = (num_pages, hkv, page, d // 2), (num_pages, hkv, page, d // 32)
+    pool = [torch.empty(s, dtype=t, device=DEV) for _ in range(2) for s, t in ((codes, torch.uint8), (scales, torch.bfloat16))]
+    assert pool[1].numel() * 2 > 1 << 32
+    ids, n = np.array([num_pages - 1, 3, num_pages - 2, num_pages // 2]), 3 * page + 21
+    slots = (ids[:, None] * page + np.arange(page)).reshape(-1)[:n]
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((n, 2 * hkv, d), generator=g).bfloat16()
+    xd = x.to(DEV)
+    sl8.rope_append_int4(None, xd[:, :hkv], xd[:, hkv:], None, None, i32(slots), *pool)
+    small = [np.zeros((4, hkv, page, c), t) for _ in range(2) for c, t in ((d // 2, np.uint8), (d // 32, np.float32))]
+    c, s = Q.quant4(x.float().numpy())
+    for t in range(n):
+        for i in range(2):
+            small[2 * i][t // page, :, t % page], small[2 * i + 1][t // page, :, t % page] = Q.pack(c[t, i * hkv:(i + 1) * hkv]), s[t, i * hkv:(i + 1) * hkv]
+    k, v = sl8.paged_read_int4(*pool, i32(ids[None]), i32([n]), max_seqlen=n, out_dtype=F32)
+    for got, i in ((k, 0), (v, 2)):
+        np.testing.assert_array_equal(f32(got[0]), Q.values(Q.gather(small[i], range(4), n), Q.gather(small[i + 1], range(4), n)).astype(np.float32))
+    q = torch.randn((1, 1, hq, d), generator=g).bfloat16()
+    for splits in (1, 9):
+        out, lse = sl8.attn_int4_paged_decode(q.to(DEV), *pool, i32(ids[None]), i32([n]), num_splits=splits, out_dtype=F32, return_lse=True)
+        _check_attention(out, lse, q, small, [range(4)], [n])
+
+
+# ------------------------------------------------------------------ one step
+
+def _state(B, hq, hkv, d, page, nb, num_pages, T, mean):
+    z = lambda *n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    return dict(seq=z(B), new=z(B), release=z(B), table=z(B, nb) - 1, free=torch.arange(num_pages, dtype=torch.int32, device=DEV),
+                count=i32([num_pages]), pool=sl8.int4_pages(num_pages, hkv, page, d, DEV), mean=mean,
+                qkv=torch.zeros((T, (hq + 2 * hkv) * d), dtype=BF16, device=DEV), dims=(B, hq, hkv, d, page, T))
+
+
+def _step(s, inv, new, splits=0, plan=None, out=None, workspace=None):
+    """One step of one layer: plan, rotary append, attention; with `new` tokens of every sequence as drafts, or, new = 0,
+    of its last token."""
+    B, hq, hkv, d, page, T = s["dims"]
+    plan = sl8.paged_assign(s["seq"], s["new"], s["table"], s["free"], s["count"], page, T, release=s["release"], out=plan)
+    s["seq"].copy_(plan["seqlens"])
+    s["count"].copy_(plan["free_count"])
+    q, k, v = (x.unflatten(1, (-1, d)) for x in s["qkv"].split([hq * d, hkv * d, hkv * d], 1))
+    q = sl8.rope_append_int4(q, k, v, plan["token_pos"], inv, plan["slot_map"], *s["pool"], k_mean=s["mean"])
+    q = q[:B * new].view(B, new, hq, d) if new else q[(plan["cu_new"][1:] - 1).clamp(min=0).long()][:, None]
+    out = sl8.attn_int4_paged_decode(q, *s["pool"], s["table"], s["seq"], num_splits=splits, return_lse=True, workspace=workspace,
+                                     out=out and out[0], lse=out and out[1])
+    return plan, q, out
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,splits,with_mean", [(8, 2, 64, 16, 0, True), (12, 2, 128, 32, 9, False), (3, 1, 256, 16, 3, True),
+                                                            (25, 1, 32, 48, 0, False)])
+def test_a_serving_loop(hq, hkv, d, page, splits, with_mean):
+    """Prompts, decode steps, drafts, a release and a new request in its slot.  Each step's attention is the definition's over
+    the cache as it stands; what is read back is the tokens' keys and values to half a step of 4 bits; and a prompt's chunk
+    and a ragged batch attend over it."""
+    B, nb, T = 5, 200 // page + 1, 256
+    rng = np.random.default_rng(d)
+    mean = rng.standard_normal((hkv, d)).astype(np.float32) if with_mean else np.zeros((hkv, d), np.float32)
+    s = _state(B, hq, hkv, d, page, nb, B * nb, T, torch.from_numpy(mean).to(DEV) if with_mean else None)
+    freq = (10000.0 ** (-np.arange(0, d, 2) / d)).astype(np.float32)
+    inv = torch.from_numpy(freq).to(DEV)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    rows = [[] for _ in range(B)]  # of each sequence: exact keys, their error, values
+    steps = [([60, 33, 1, 100, 0], [0] * 5, 0)] + [([1, 1, 1, 1, 0], [0] * 5, 0)] * 5 + [([1, 20, 1, 1, 16], [0, 1, 0, 0, 0], 0)] + \
+            [([1] * 5, [0] * 5, 1)] * 3 + [([4] * 5, [0] * 5, 4)] * 2
+    for new, release, drafts in steps:
+        s["new"].copy_(i32(new)), s["release"].copy_(i32(release))
+        s["qkv"].copy_(torch.randn(s["qkv"].shape, generator=g, device=DEV))
+        plan, q, out = _step(s, inv, drafts, splits)
+        kv = np64(s["qkv"])[:, hq * d:].reshape(T, 2 * hkv, d)
+        at = 0
+        for b in range(B):
+            if release[b]:
+                rows[b] = []
+            for _ in range(new[b]):
+                x = kv[at:at + 1, :hkv]
+                k = S.rope(x, np.array([[len(rows[b])]]), freq)
+                err = 2e-6 * _pair_length(x, d, False) + (2.0 ** -24 * (np.abs(k) + np.abs(mean)) if with_mean else 0)
+                rows[b].append((k[0], err[0], kv[at, hkv:]))
+                at += 1
+        lens = s["seq"].tolist()
+        assert lens == [len(r) for r in rows]
+        host = [s["pool"][0].cpu().numpy(), f32(s["pool"][1]), s["pool"][2].cpu().numpy(), f32(s["pool"][3])]
+        _check_attention(*out, q, host, s["table"].cpu().numpy(), lens, tag=lens)
+    keys, values = sl8.paged_read_int4(*s["pool"], s["table"], s["seq"], k_mean=s["mean"], out_dtype=F32)
+    for b in range(B):
+        k, err, v = (np.stack([r[i] for r in rows[b]], 1) for i in range(3))
+        for got, want, off, tol in ((keys, k, mean[:, None], err), (values, v, 0.0, np.zeros_like(err))):
+            most = (np.abs(want - off) + tol).reshape(*want.shape[:-1], -1, 32).max(-1)
+            half = np.repeat(most / 7 * (1 + 2.0 ** -8) * (1 + 2.0 ** -22), 32, -1) / 2
+            x = np64(got[b, :, :lens[b]])
+            assert np.all(np.abs(x - want) <= half + tol + 2.0 ** -24 * np.abs(x)), b
+    # the last 7 tokens of a sequence as a prompt's chunk
+    b, n = 3, lens[3]
+    k, v = sl8.paged_read_int4(*s["pool"], s["table"][b:b + 1], s["seq"][b:b + 1], max_seqlen=n, k_mean=s["mean"])
+    qc = torch.randn((1, hq, 7, d), generator=g, device=DEV).bfloat16()
+    o = sl8.attn_int8_fwd_chunk(qc, k, v, out_dtype=F32)
+    check_f32(f32(o), oracle.attn_prefill(f32(qc), f32(k), f32(v), causal=True, smooth_k=True)["out"], "chunk")
+    # the sequences side by side
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    k, v = sl8.paged_read_int4(*s["pool"], s["table"], s["seq"], cu_seqlens=i32(cu), max_seqlen=max(lens), total_tokens=int(cu[-1]),
+                               k_mean=s["mean"])
+    qp = torch.randn((int(cu[-1]), hq, d), generator=g, device=DEV).bfloat16()
+    o = sl8.attn_int8_fwd(qp, k, v, cu_seqlens=i32(cu), max_seqlen=max(lens), out_dtype=F32)
+    for b in range(B):
+        part = [f32(x[cu[b]:cu[b + 1]].transpose(0, 1)[None]) for x in (qp, k, v, o)]
+        check_f32(part[3], oracle.attn_prefill(*part[:3], causal=True, smooth_k=True)["out"], "ragged")
+
+
+@pytest.mark.parametrize("splits", [0, 4, 12])
+def test_two_captured_steps_and_an_eager_one(splits):
+    """Two graphs of a step, each with its state and workspace, replayed at the same time on two streams, do what eager
+    calls do."""
+    B, hq, hkv, d, page, nb, T = 3, 8, 2, 64, 16, 20, 8
+    inv = (10000.0 ** (-torch.arange(0, d, 2, device=DEV) / d)).float()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for seed in (1, 2, 3):
+        s = _state(B, hq, hkv, d, page, nb, 60, T, torch.ones((hkv, d), device=DEV))
+        s["new"].fill_(2)
+        _step(s, inv, 2, splits)  # warms up what a capture may not do
+        sl8.paged_read_int4(*s["pool"], s["table"], s["seq"], out_dtype=BF16)
+        torch.cuda.synchronize()
+        s["seq"].zero_(), s["table"].fill_(-1), s["count"].fill_(60)
+        s["free"].copy_(torch.arange(60)), s["pool"][0].fill_(0x88), s["pool"][2].fill_(0x88), s["pool"][1].zero_(), s["pool"][3].zero_()
+        ws = torch.empty(max(16, sl8.int4_decode_workspace_bytes(B, 2, hq, hkv, nb, page, d, splits)), dtype=torch.uint8, device=DEV)
+        dense = [torch.zeros((B, hkv, nb * page, d), dtype=BF16, device=DEV) for _ in range(2)]
+
+        def step(s=s, ws=ws, dense=dense):
+            res = _step(s, inv, 2, splits, workspace=ws)
+            sl8.paged_read_int4(*s["pool"], s["table"], s["seq"], k_mean=s["mean"], k_out=dense[0], v_out=dense[1])
+            return res[2] + tuple(dense) + s["pool"]
+        g, res = torch.cuda.CUDAGraph(), None
+        if seed < 3:
+            with torch.cuda.graph(g):
+                res = step()
+        runs.append([s, g, res, step])
+    for n in range(40):
+        x = torch.randn(runs[0][0]["qkv"].shape, generator=torch.Generator(device=DEV).manual_seed(n), device=DEV)
+        for run in runs:
+            run[0]["qkv"].copy_(x)
+        for st in (side, other):
+            st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            runs[0][1].replay()
+        with torch.cuda.stream(other):
+            runs[1][1].replay()
+        want = runs[2][3]()
+        for st in (side, other):
+            torch.cuda.current_stream().wait_stream(st)
+        for run in runs[:2]:
+            for a, b in zip(run[2], want):
+                assert torch.equal(a, b), n
+    assert runs[0][0]["seq"].tolist() == [80] * 3
+
+
+def test_side_stream_and_refusals():
+    rng = np.random.default_rng(2)
+    pool, _ = _filled(rng, 6, 2, 16, 64)
+    table, lens = i32([[0, 1, 2], [3, 4, 5]]), i32([40, 20])
+    q = torch.randn((2, 4, 64), device=DEV).half()
+    want = sl8.attn_int4_paged_decode(q, *pool, table, lens, num_splits=12), *sl8.paged_read_int4(*pool, table, lens)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        got = sl8.attn_int4_paged_decode(q, *pool, table, lens, num_splits=12), *sl8.paged_read_int4(*pool, table, lens)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # out, lse and workspace of the caller's
+    out, lse = torch.empty((2, 4, 64), device=DEV), torch.empty((2, 4), device=DEV)
+    a, b = sl8.attn_int4_paged_decode(q, *pool, table, lens, return_lse=True, out=out, lse=lse,
+                                      workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    assert a is out and b is lse
+    decode = lambda *x, **kw: sl8.attn_int4_paged_decode(*x, **kw)  # noqa: E731
+    bad = [(ValueError, lambda: decode(q.transpose(0, 1), *pool, table, lens)), (ValueError, lambda: decode(q[:1], *pool, table, lens)),
+           (TypeError, lambda: decode(q, *pool, table.long(), lens)), (ValueError, lambda: decode(q, *pool, table, lens[:1])),
+           (ValueError, lambda: decode(q, *pool, table.t().contiguous().t(), lens)), (TypeError, lambda: decode(q.double(), *pool, table, lens)),
+           (ValueError, lambda: decode(q, *pool, table, lens, tree_mask=i32([1]))), (ValueError, lambda: decode(q, *pool, table, lens, out=out[:1])),
+           (ValueError, lambda: decode(q, *pool, table, lens, return_lse=True, lse=lse[:1])), (ValueError, lambda: decode(q[0], *pool, table, lens)),
+           (TypeError, lambda: decode(q, pool[0].view(torch.int8), *pool[1:], table, lens)),
+           (TypeError, lambda: decode(q, pool[0], pool[1].half(), *pool[2:], table, lens)),
+           (ValueError, lambda: decode(q, pool[0], pool[1][:5], *pool[2:], table, lens)),
+           (ValueError, lambda: decode(q, *pool[:2], pool[2][:5], pool[3], table, lens)),
+           (sl8.SL8Error, lambda: decode(q, *pool, table, lens, num_splits=12, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))),
+           (ValueError, lambda: decode(q.cpu(), *pool, table, lens))]
+    k = torch.randn((4, 2, 64), device=DEV).half()
+    slots = i32([0, 1, 2, 3])
+    append = sl8.rope_append_int4
+    bad += [(ValueError, lambda: append(None, k[..., ::2], k[..., ::2], None, None, slots, *pool)),
+            (TypeError, lambda: append(None, k, k.float(), None, None, slots, *pool)),
+            (ValueError, lambda: append(None, k, k, slots, None, slots, *pool)), (ValueError, lambda: append(None, k, k, None, None, slots[:3], *pool)),
+            (ValueError, lambda: append(None, k, k, None, None, slots, *pool, k_mean=torch.zeros(64, device=DEV))),
+            (TypeError, lambda: append(None, k, k, None, None, slots, *pool, k_mean=torch.zeros((2, 64), device=DEV).half()))]
+    read = sl8.paged_read_int4
+    bad += [(ValueError, lambda: read(*pool, table, lens[:1])), (ValueError, lambda: read(*pool, table, lens, cu_seqlens=i32([0, 40, 60]))),
+            (ValueError, lambda: read(*pool, table, lens, cu_seqlens=i32([0, 40]), total_tokens=60)),
+            (TypeError, lambda: read(*pool, table, lens, out_dtype=torch.float64)),
+            (ValueError, lambda: read(*pool, table, lens, max_seqlen=40, k_out=torch.empty((2, 2, 39, 64), device=DEV))),
+            (TypeError, lambda: read(*pool, table, lens, max_seqlen=8, k_out=torch.empty((2, 2, 8, 64), device=DEV), out_dtype=BF16)),
+            (ValueError, lambda: read(*pool, table, lens, k_mean=torch.zeros((1, 64), device=DEV)))]
+    for i, (error, call) in enumerate(bad):
+        try:
+            call()
+        except error:
+            continue
+        pytest.fail(f"call {i} was not refused with {error}")
