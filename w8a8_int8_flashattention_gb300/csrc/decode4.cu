@@ -156,17 +156,20 @@ struct Cfg4 {
   static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
   // as many CTAs an SM as their registers let: the accumulators are D kT / 4 a thread
   static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : 6 - kT;
-  // after the loop the rings hold the warps' O^T [warp][D][kCols] and the CTA's [kCols][D], fp32
-  static constexpr int kRed = 0, kPart = kWarps * D * kCols * 4, kMerge = kPart + kCols * D * 4;
+  // after the loop the rings hold the warps' O^T [warp][D][kCols], fp32
+  static constexpr int kRed = 0, kMerge = kWarps * D * kCols * 4;
   static constexpr int kQf = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;  // [kN][kT][32] fragments of Q, 16 bytes
   static constexpr int kBias = kQf + kN * kT * 512;       // [kN][kT][8] 8 sum of q
   static constexpr int kQs = kBias + kN * kT * 32;        // [kCols] scales
   static constexpr int kQc = kQs + kCols * 4;             // [kCols][D] query codes
   static constexpr int kStat = kQc + kCols * D;           // [warp][kCols][2]: max (log2), sum
   static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps' parts, or of the CTAs'
-  static constexpr int kMl = kWt + kMaxCluster * kCols * 4;  // [kCols][2]: max, sum of the CTA
-  static constexpr int kRows = kMl + kCols * 8;           // [kCols] rows of q and out
-  static constexpr int kBytes = kRows + kCols * 8;
+  static constexpr int kRows = kWt + kMaxCluster * kCols * 4;  // [kCols] rows of q and out
+  // what a cluster's CTAs send: [CTA][kCols][2] max and sum, and of each CTA its runs [CTA][run][32], four columns each
+  static constexpr int kMl = kRows + kCols * 8;
+  static constexpr int kIn = kMl + kMaxCluster * kCols * 8;
+  static constexpr int kRuns = D * kCols / 128;  // of 32 rows of O^T and four columns
+  static constexpr int kBytes = kIn + (kRuns + kMaxCluster - 1) * 512;
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "kCtas CTAs fit an SM");
 };
 
@@ -184,6 +187,10 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int j) {
   constexpr int n = D / kGroup4, m = 8 / n;  // chunks of a row, rows in 128 bytes
   return static_cast<uint32_t>(r * (16 * n) + 16 * (j ^ (((r & 7) / m) & (n - 1))));
 }
+
+// A cluster's barrier: what a thread has written before it arrives is there for those that have waited.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Inclusive prefix over the CTA's threads of one value each.
 __device__ __forceinline__ int64_t cta_prefix(int64_t x, int64_t* sm) {
@@ -215,8 +222,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   const int G = a.Hq / a.Hkv, per_seq = a.Hkv * a.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cap = a.max_blocks * a.page;
-  auto length_of = [&](int b) {
-    const int L = a.seqlens[b];
+  auto checked = [&](int L) {
     if (L >= 0 && L <= cap) return L;
     if (threadIdx.x == 0) record_status(st, kStatusBadArg, 870);
     return L < 0 ? 0 : cap;
@@ -228,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     if (threadIdx.x == 0) a.starts[blockIdx.x] = -1;  // the sequence that this CTA begins and does not end
   }
   const int S = a.ctas ? 1 : a.splits;
+  if (S > 1) cluster_arrive();
   int rank = 0, b, inner;      // inner: kv head * groups + column group
   int64_t left = 1;            // balanced: what this CTA still has of its share
   int s0 = 0;                  // first step of the segment in its sequence; below 0: in its kStart
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     const int strip = (a.B + kThreads - 1) / kThreads;
     const int i0 = min(a.B, static_cast<int>(threadIdx.x) * strip), i1 = min(a.B, i0 + strip);
     int64_t x = 0;
-    for (int i = i0; i < i1; ++i) x += C::kStart + steps_of(length_of(i), C::kStep);
+    for (int i = i0; i < i1; ++i) x += C::kStart + steps_of(checked(a.seqlens[i]), C::kStep);
     const int64_t end = cta_prefix(x, scan);
     if (threadIdx.x == kThreads - 1) scan[kWarps] = end;
     __syncthreads();
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       int64_t at = end - x;
       int i = i0;
       for (;; ++i) {
-        const int per = C::kStart + steps_of(length_of(i), C::kStep);
+        const int per = C::kStart + steps_of(checked(a.seqlens[i]), C::kStep);
         if (off < at + per) break;
         at += per;
       }
@@ -293,7 +300,22 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     const int col0 = (inner - head * a.groups) * a.cols;  // first of this segment's columns
     const int GC = min(a.cols, a.T * G - col0);
     int64_t* const row_of = reinterpret_cast<int64_t*>(smem + C::kRows);  // of q and out, for each column
-    const int L = length_of(b), per = steps_of(L, C::kStep);
+    // The query columns, eight lanes a row, are asked for beside the length, and quantised while the first rows' pages
+    // are looked up: a segment starts with a chain of loads that wait for one another.
+    const int len = a.seqlens[b];
+    constexpr int kPass = (8 * kCols + kThreads - 1) / kThreads;
+    float qx[kPass][D / 32][4] = {};
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+      const int c = static_cast<int>(threadIdx.x >> 3) + i * (kThreads / 8);
+      if (c < GC) {
+        const int dr = (col0 + c) / G;  // its draft, its query head
+        const int64_t at = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
+        load_runs<D / 32>(a.q, a.q_dtype, at * D + 4 * (lane & 7), 32, qx[i]);
+        if ((lane & 7) == 0) row_of[c] = at;
+      }
+    }
+    const int L = checked(len), per = steps_of(L, C::kStep);
     int s1 = per;
     if (a.ctas) {
       s1 = static_cast<int>(min(static_cast<int64_t>(per), s0 + left));
@@ -362,34 +384,29 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       ask(to_k, a.k_pages, a.k_scale);
       cp_async_commit();
     };
-    next_row();
-    ask(ring, a.k_pages, a.k_scale);
-    cp_async_commit();
-    issue(ring + C::kHalf, ring + 2 * C::kHalf);
-
-    // ---------------------------------------------------------- the query columns: eight lanes a row
+    // ---------------------------------------------------------- the query columns
     int8_t* qc = reinterpret_cast<int8_t*>(smem + C::kQc);
     float* qsc = reinterpret_cast<float*>(smem + C::kQs);
-    for (int c = static_cast<int>(threadIdx.x >> 3); c < kCols; c += kThreads / 8) {
-      const int l8 = lane & 7;
-      float x[D / 32][4] = {}, amax = 0.0f;
-      if (c < GC) {
-        const int dr = (col0 + c) / G;  // its draft, its query head
-        const int64_t at = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
-        load_runs<D / 32>(a.q, a.q_dtype, at * D + 4 * l8, 32, x);
-        if (l8 == 0) row_of[c] = at;
-      }
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int c = static_cast<int>(threadIdx.x >> 3) + p * (kThreads / 8), l8 = lane & 7;
+      if (c >= kCols) break;
+      float amax = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[i][e]));
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(qx[p][i][e]));
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const RowScale rs = row_scale(amax);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint32_t*>(qc + c * D + 32 * i + 4 * l8) = quant4(x[i], rs);
+      for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint32_t*>(qc + c * D + 32 * i + 4 * l8) = quant4(qx[p][i], rs);
       if (l8 == 0) qsc[c] = rs.s;
     }
+    next_row();
+    ask(ring, a.k_pages, a.k_scale);
+    cp_async_commit();
+    issue(ring + C::kHalf, ring + 2 * C::kHalf);
     __syncthreads();
     // B fragments of Q^T: word t of a group's chunk holds channels 8 t .. 8 t + 7 of column g, of which
     // the even ones meet one MMA, the odd ones (whose nibbles stand 16 times as high) another
@@ -714,8 +731,6 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     float* stat = reinterpret_cast<float*>(smem + C::kStat);
     float* red = reinterpret_cast<float*>(smem + C::kRed);
     float* wt = reinterpret_cast<float*>(smem + C::kWt);
-    float* ml = reinterpret_cast<float*>(smem + C::kMl);
-    float* part = reinterpret_cast<float*>(smem + C::kPart);
     __syncthreads();  // the rings are free
 #pragma unroll
     for (int h = 0; h < kT; ++h) {
@@ -756,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     };
     // slot 0 of a CTA's two parts where its work begins, else 1
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0);
+    if (S > 1) cluster_wait();  // all of the cluster have started
     if (threadIdx.x < GC) {
       const int c = threadIdx.x;
       float M, sum;
@@ -763,8 +779,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) v[i] = *reinterpret_cast<const float2*>(stat + (i * kCols + c) * 2);
       weigh(c, kWarps, v, M, sum);
-      if (S > 1) *reinterpret_cast<float2*>(ml + 2 * c) = make_float2(M, sum);
-      else if (cut) a.part_ml[slot * kCols + c] = make_float2(M, sum);
+      if (S > 1) {
+        for (int i = 0; i < S; ++i) *cluster.map_shared_rank(reinterpret_cast<float2*>(smem + C::kMl) + rank * kCols + c, i) = make_float2(M, sum);
+      } else if (cut) a.part_ml[slot * kCols + c] = make_float2(M, sum);
       else finish(c, kWarps, M, sum);
     }
     if (a.ctas && threadIdx.x == 0) {  // the CTAs that have the first and the last step
@@ -774,10 +791,12 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       if (s0 == 0 && cut) a.starts[blockIdx.x] = static_cast<int32_t>(b) * per_seq + inner;
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < D * (kCols / 4); u += kThreads) {  // row u % D, columns 4 (u / D) ..
-      const int r = u % D, c = 4 * (u / D);
-      if (c >= GC) break;
-      const int dim = 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1);  // a warp's are 32 in a row
+    // O^T in runs of 32 rows (a warp's, of channels that lie in a row) and four columns
+    const int runs = D / 32 * ((GC + 3) / 4), slots = (runs + S - 1) / S;
+    auto dim_of = [](int r) { return 32 * (r >> 5) + 4 * (r & 7) + 2 * ((r >> 4) & 1) + ((r >> 3) & 1); };
+    float4* const in = reinterpret_cast<float4*>(smem + C::kIn);
+    for (int run = warp; run < runs; run += kWarps) {
+      const int r = 32 * (run % (D / 32)) + lane, c = 4 * (run / (D / 32)), dim = dim_of(r);
       float acc[4] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -788,47 +807,48 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
         acc[2] = fmaf(v.z, f.z, acc[2]);
         acc[3] = fmaf(v.w, f.w, acc[3]);
       }
+      if (S > 1) {  // run i is joined by CTA i % S of the cluster
+        const int to = run % S;
+        cluster.map_shared_rank(in, to)[(rank * slots + run / S) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (c + i >= GC) break;
-        if (S > 1) part[(c + i) * D + dim] = acc[i];
-        else if (cut) a.part_o[(slot * kCols + c + i) * D + dim] = acc[i];
+        if (cut) a.part_o[(slot * kCols + c + i) * D + dim] = acc[i];
         else store_out(a.out, a.out_dtype, row_of[c + i] * D + dim, acc[i]);
       }
     }
-    if (S > 1) {  // the S CTAs' parts: each takes every S-th run of four channels
-      cluster.sync();
+    if (S > 1) {  // what the cluster's CTAs have sent
+      cluster_arrive();
+      cluster_wait();
       if (threadIdx.x < GC) {
         const int c = threadIdx.x;
         float M, sum;
         float2 v[kMaxCluster] = {};
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i)
-          if (i < S) v[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(ml, i) + 2 * c);
+          if (i < S) v[i] = reinterpret_cast<const float2*>(smem + C::kMl)[i * kCols + c];
         weigh(c, S, v, M, sum);
         finish(c, S, M, sum);
       }
       __syncthreads();
-      for (int u = rank * kThreads + threadIdx.x; u < GC * (D / 4); u += S * kThreads) {
-        const int c = u / (D / 4), q = u % (D / 4);
-        float4 v[kMaxCluster];
-#pragma unroll
-        for (int i = 0; i < kMaxCluster; ++i)
-          if (i < S) v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, i) + c * D + 4 * q);
+      for (int n = warp; n * S + rank < runs; n += kWarps) {
+        const int run = n * S + rank, r = 32 * (run % (D / 32)) + lane, c = 4 * (run / (D / 32)), dim = dim_of(r);
         float acc[4] = {};
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i)
           if (i < S) {
-            const float f = wt[i * kCols + c];
-            acc[0] = fmaf(v[i].x, f, acc[0]);
-            acc[1] = fmaf(v[i].y, f, acc[1]);
-            acc[2] = fmaf(v[i].z, f, acc[2]);
-            acc[3] = fmaf(v[i].w, f, acc[3]);
+            const float4 v = in[(i * slots + n) * 32 + lane], f = *reinterpret_cast<const float4*>(wt + i * kCols + c);
+            acc[0] = fmaf(v.x, f.x, acc[0]);
+            acc[1] = fmaf(v.y, f.y, acc[1]);
+            acc[2] = fmaf(v.z, f.z, acc[2]);
+            acc[3] = fmaf(v.w, f.w, acc[3]);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_out(a.out, a.out_dtype, row_of[c] * D + 4 * q + i, acc[i]);
+        for (int i = 0; i < 4; ++i)
+          if (c + i < GC) store_out(a.out, a.out_dtype, row_of[c + i] * D + dim, acc[i]);
       }
-      cluster.sync();  // no CTA leaves while another reads its part
     }
     if (!a.ctas) return;
     if (left <= 0) return;
