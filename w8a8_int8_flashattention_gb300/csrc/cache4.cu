@@ -55,9 +55,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) read4_kernel(const Read4Args a, DeviceStatus* st) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes, kTok = read_tokens(D);
   const uint32_t u = blockIdx.x / static_cast<uint32_t>(a.Hkv), h = blockIdx.x - u * a.Hkv;
-  const uint32_t chunks = (static_cast<uint32_t>(a.N) + kTok - 1) / kTok;
-  const uint32_t b = u / chunks;
-  const int first = static_cast<int>(u - b * chunks) * kTok;
+  const uint32_t chunk = u / static_cast<uint32_t>(a.B), b = u - chunk * a.B;
+  const int first = static_cast<int>(chunk) * kTok;
   const int l = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int32_t cap = a.max_blocks * a.page;
   int64_t L = a.seqlens[b], room = min(cap, a.N), at = static_cast<int64_t>(b) * a.Hkv * a.N;
