@@ -437,6 +437,41 @@ def test_infinite_value_groups_reach_their_channels():
     assert torch.isnan(out2[0, 1]).all() and torch.isnan(lse2[0, 1]) and torch.equal(out2[0, 0], out[0, 0])
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3, 8, 9, 40])
+@pytest.mark.parametrize("d,odt", [(32, F32), (64, BF16), (128, F16), (256, F32)])
+def test_nan_logits_reach_the_output(d, odt, splits):
+    """A query row with an infinity, whose logits are all NaN, and keys whose scales are NaN in every row, in all but
+    the first, or in the last alone: NaN for the queries that see them; the others as ever (not to the bit: 16-bit outputs' columns
+    that share a warp move their references together)."""
+    rng = np.random.default_rng(d)
+    for L in (30, 2000):
+        nb = -(-L // 16)
+        pool, host = _filled(rng, 2 * nb, 2, 16, d)
+        tables, lens = i32(rng.permutation(2 * nb).reshape(2, nb)), i32([L, L - 3])
+        q = torch.randn((2, 6, d), device=DEV)
+        call = lambda: sl8.attn_int4_paged_decode(q, *pool, tables, lens, num_splits=splits, out_dtype=odt, return_lse=True)  # noqa: E731
+        want, wl = call()
+        assert torch.isfinite(want).all() and torch.isfinite(wl).all()
+        kept = q[0, 4].clone()
+        q[0, 4, d // 2] = float("-inf")
+        out, lse = call()
+        q[0, 4] = kept
+        hit = torch.zeros((2, 6), dtype=torch.bool, device=DEV)
+        hit[0, 4] = True
+        for rows in (None, slice(None), slice(1, None), slice(L - 4, L - 3)):
+            if rows is not None:  # head 1 of the second sequence
+                at = torch.arange(nb * 16, device=DEV)[rows]
+                scales = pool[1].clone()
+                pool[1][tables[1][at // 16].long(), 1, at % 16, -1] = float("nan")
+                out, lse = call()
+                pool[1].copy_(scales)
+                hit = torch.zeros((2, 6), dtype=torch.bool, device=DEV)
+                hit[1, 3:] = True
+            assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all(), (L, rows)
+            rest = torch.where(hit[..., None], want, out), torch.where(hit, wl, lse)
+            _check_attention(rest[0][:, None], rest[1][:, None], q[:, None], host, tables.cpu().numpy(), lens.tolist(), tag=(L, rows))
+
+
 @pytest.mark.parametrize("d,splits", [(32, 1), (64, 0), (128, 1), (128, 8), (256, 2), (128, 12)])
 def test_every_row_and_channel_counts(d, splits):
     """Value rows one by one: with the others zero, a row's weight comes out of each of its channels;

@@ -763,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
           wt[i * kCols + c] = f;
           if (v[i].x != -INFINITY) sum = fmaf(f, v[i].y, sum);
         }
+      M = keep_nan(M, sum);  // which stays beside the others' maxima
     };
     auto finish = [&](int c, int n, float M, float sum) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -858,49 +859,48 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   }
 }
 
-// The parts of each (sequence, kv head, column group) of a balanced launch that was cut: D / 4 threads take
-// a part of a column, the next ones another.  A CTA takes a column of each of them (kEach) or, where there are more than
-// CTAs of the kernel above, of the one that such a CTA began and did not end, if it did.
-constexpr int kJoin = 256;
-template <int D, int kCols, bool kEach>
-__global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Args a) {
-  constexpr int kRow = D / 4, kAtOnce = kJoin / kRow;
+// The parts of each (sequence, kv head, column group) of a balanced launch that was cut.  D / 4 threads, a row, hold a
+// column; `stripes` rows share its parts, each taking kAhead of them at once, and a CTA has kRows / stripes columns
+// of one item: each of them in turn (kEach) or, where there are more than CTAs of the kernel above, of the one that such
+// a CTA began and did not end, if it did.
+constexpr int kJoin = 256, kAhead = 4;
+template <int D, bool kEach>
+__global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Args a, int pad, int stripes) {
+  constexpr int kRow = D / 4;
   __shared__ float4 sm[kJoin];
-  __shared__ float2 sums[kAtOnce];
+  __shared__ float2 sums[kJoin / kRow];
   const int per_seq = a.Hkv * a.groups, G = a.Hq / a.Hkv;
+  const int q = static_cast<int>(threadIdx.x) % kRow, r = static_cast<int>(threadIdx.x) / kRow;
+  const int columns = kJoin / kRow / stripes, ctas = (a.cols + columns - 1) / columns;  // of a CTA, of an item
+  const int which = static_cast<int>(blockIdx.x) / ctas;
+  const int c = (static_cast<int>(blockIdx.x) - which * ctas) * columns + r / stripes, stripe = r % stripes;
   grid_dependency_wait();
-  const int which = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.cols));
-  const int c = static_cast<int>(blockIdx.x) - which * a.cols;
   const int item = kEach ? which : a.starts[which];
   if (item < 0) return;
   const int2 ends = reinterpret_cast<const int2*>(a.ends)[item];
   const int i0 = ends.x, i1 = ends.y;
   if (i0 == i1) return;  // written by that CTA
   const int b = item / per_seq, inner = item - b * per_seq;
-  const int head = inner / a.groups, col0 = (inner - head * a.groups) * a.cols, GC = min(a.cols, a.T * G - col0);
+  const int head = inner / a.groups, col0 = (inner - head * a.groups) * a.cols;
+  const bool mine = c < min(a.cols, a.T * G - col0);
   auto slot_of = [&](int i) { return static_cast<int64_t>(2 * i + (i == i0 ? 1 : 0)); };
-  if (c >= GC) return;
-  // each row of threads joins every kAtOnce-th part, kAhead of them on their way at once
-  constexpr int kAhead = 4;
-  const int q = static_cast<int>(threadIdx.x) % kRow, r = static_cast<int>(threadIdx.x) / kRow;
   float M = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = i0 + r; i <= i1; i += kAhead * kAtOnce) {
+  for (int i = i0 + stripe; mine && i <= i1; i += kAhead * stripes) {
     float2 v[kAhead];
     float4 x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int j = i + k * kAtOnce;
+      const int j = i + k * stripes;
       const int64_t slot = slot_of(min(j, i1));
-      v[k] = a.part_ml[slot * kCols + c];
-      x[k] = *reinterpret_cast<const float4*>(a.part_o + (slot * kCols + c) * D + 4 * q);
+      v[k] = a.part_ml[slot * pad + c];
+      x[k] = *reinterpret_cast<const float4*>(a.part_o + (slot * pad + c) * D + 4 * q);
       if (j > i1) v[k].x = -INFINITY;
     }
     float top = M;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) top = fmaxf(top, v[k].x);
-    if (top == -INFINITY) continue;
-    const float keep = ex2(M - top);
+    const float keep = M == -INFINITY ? 0.0f : ex2(M - top);
     M = top;
     sum *= keep;
     acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
@@ -915,25 +915,28 @@ __global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Arg
       acc.w = fmaf(f, x[k].w, acc.w);
     }
   }
-  sm[threadIdx.x] = acc;
-  if (q == 0) sums[r] = make_float2(M, sum);
-  __syncthreads();
-  if (r > 0) return;
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) M = fmaxf(M, sums[i].x);
-  sum = 0.0f;
-  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    if (sums[i].x == -INFINITY) continue;
-    const float f = ex2(sums[i].x - M);
-    const float4 x = sm[i * kRow + q];
-    sum = fmaf(f, sums[i].y, sum);
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
+  if (stripes > 1) {
+    sm[threadIdx.x] = acc;
+    if (q == 0) sums[r] = make_float2(keep_nan(M, sum), sum);
+    __syncthreads();
+    if (stripe == 0) {
+      for (int i = 1; i < stripes; ++i) M = fmaxf(M, sums[r + i].x);
+      sum = 0.0f;
+      acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < stripes; ++i) {
+        const float2 v = sums[r + i];
+        if (v.x == -INFINITY) continue;
+        const float f = ex2(v.x - M);
+        const float4 x = sm[threadIdx.x + i * kRow];
+        sum = fmaf(f, v.y, sum);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+    }
   }
+  if (!mine || stripe > 0) return;
   const int dr = (col0 + c) / G;
   const int64_t row = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
   const float x[4] = {acc.x, acc.y, acc.z, acc.w};
@@ -962,9 +965,14 @@ cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
   if (e != cudaSuccess || !a.ctas) return e;
-  if (items <= static_cast<unsigned>(a.ctas))
-    return launch_pdl(decode4_combine_kernel<D, kCols, true>, dim3(items * a.cols), dim3(kJoin), 0, s, a);
-  return launch_pdl(decode4_combine_kernel<D, kCols, false>, dim3(static_cast<unsigned>(a.ctas) * a.cols), dim3(kJoin), 0, s, a);
+  // rows of the combine that share a column's parts: as many as take them kMany times over at once, since lengths differ
+  constexpr int kRows = kJoin / (D / 4), kMany = 2;
+  const unsigned ctas = static_cast<unsigned>(a.ctas);
+  int stripes = 1;
+  while (stripes < kRows && stripes * kAhead < kMany * static_cast<int>(ctas / items + 2)) stripes *= 2;
+  const unsigned each = (a.cols + kRows / stripes - 1) / (kRows / stripes);
+  if (items <= ctas) return launch_pdl(decode4_combine_kernel<D, true>, dim3(items * each), dim3(kJoin), 0, s, a, kCols, stripes);
+  return launch_pdl(decode4_combine_kernel<D, false>, dim3(ctas * each), dim3(kJoin), 0, s, a, kCols, stripes);
 }
 
 template <int D, int kCols>
