@@ -79,12 +79,12 @@ __device__ __forceinline__ void ldsm2(uint32_t a, uint32_t& r0, uint32_t& r1) {
 __device__ __forceinline__ void ldsm2_t(uint32_t a, uint32_t& r0, uint32_t& r1) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(a) : "memory");
 }
-// d = a b in fp16 with fp32 sums, and d += a b.
-__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                            uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+// d = c + a b in fp16 with fp32 sums, and d += a b.
+__device__ __forceinline__ void mma_f16_on(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
@@ -159,8 +159,8 @@ struct Cfg4 {
   // after the loop the rings hold the warps' O^T [warp][D][kCols], fp32
   static constexpr int kRed = 0, kMerge = kWarps * D * kCols * 4;
   static constexpr int kQf = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;  // [kN][kT][32] fragments of Q, 16 bytes
-  static constexpr int kBias = kQf + kN * kT * 512;       // [kN][kT][8] 8 sum of q
-  static constexpr int kQs = kBias + kN * kT * 32;        // [kCols] scales
+  static constexpr int kBias = kQf + kN * kT * 512;       // [kN][kT][4][4] -8 sum of q of columns 2 t, 2 t + 1, twice
+  static constexpr int kQs = kBias + kN * kT * 64;        // [kCols] scales
   static constexpr int kQc = kQs + kCols * 4;             // [kCols][D] query codes
   static constexpr int kStat = kQc + kCols * D;           // [warp][kCols][2]: max (log2), sum
   static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps' parts, or of the CTAs'
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   const uint32_t frag = kN == 1   ? chunk_off<D>(8 * (lm & 1) + lr, 0)
                         : kN == 2 ? chunk_off<D>(8 * (lm >> 1) + lr, lm & 1)
                                   : chunk_off<D>(lr, lm);
-  const uint32_t qf = smem_u32(smem) + C::kQf + 16 * lane, qbias = smem_u32(smem) + C::kBias + 8 * t;
+  const uint32_t qf = smem_u32(smem) + C::kQf + 16 * lane, qbias = smem_u32(smem) + C::kBias + 16 * t;
 
   for (;;) {
     const int head = inner / a.groups;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       int sum = __dp4a(static_cast<int>(w.x), 0x01010101, __dp4a(static_cast<int>(w.y), 0x01010101, 0));
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) reinterpret_cast<float*>(smem + C::kBias)[i * 8 + g] = -8.0f * 0x1p-24f * static_cast<float>(sum);
+      if (t < 2) reinterpret_cast<float*>(smem + C::kBias)[i * 16 + 4 * (g >> 1) + 2 * t + (g & 1)] = -8.0f * 0x1p-24f * static_cast<float>(sum);
     }
     // of the lane's accumulator columns 2 t and 2 t + 1
     float qs[kT][2];
@@ -477,11 +477,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         uint32_t qb[kT][4];
-        float bias[kT][2];
+        float bias[kT][4];
 #pragma unroll
         for (int h = 0; h < kT; ++h) {
           asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(qb[h][0]), "=r"(qb[h][1]), "=r"(qb[h][2]), "=r"(qb[h][3]) : "r"(qf + (j * kT + h) * 512));
-          asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(bias[h][0]), "=f"(bias[h][1]) : "r"(qbias + (j * kT + h) * 32));
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(bias[h][0]), "=f"(bias[h][1]), "=f"(bias[h][2]), "=f"(bias[h][3]) : "r"(qbias + (j * kT + h) * 64));
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -491,10 +491,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
           for (int h = 0; h < kT; ++h) {
             float acc[4];
-            mma_f16_new(acc, u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[h][0], qb[h][1]);
+            mma_f16_on(acc, u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[h][0], qb[h][1], bias[h]);
             mma_f16_add(acc, u0 & 0x00f000f0u, u1 & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[h][2], qb[h][3]);
-            add_pair(acc[0], acc[1], bias[h][0], bias[h][1]);
-            add_pair(acc[2], acc[3], bias[h][0], bias[h][1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[u][h][i] = j == 0 ? acc[i] * (i < 2 ? f0 : f1) : fmaf(acc[i], i < 2 ? f0 : f1, x[u][h][i]);
           }
