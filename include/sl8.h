@@ -630,7 +630,7 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *                 unsupported shape; 16: none is used and it may be null), 16-byte aligned; launches
  *                 that run at the same time need their own.
  * Any Hq that is a multiple of Hkv.  The T * Hq / Hkv (query, head) columns of a kv head are taken in
- * the fewest groups of at most 16 (8 at d = 256), each of which reads the cache.  page_size a multiple of 16,
+ * the fewest groups of at most 24 (8 at d = 256), each of which reads the cache.  page_size a multiple of 16,
  * page_size * max_blocks <= 2^31 - 256.  A page or a length out of range is recorded
  * (SL8_ERR_DEVICE_ARG), and page 0 read or the length clamped.
  */

@@ -533,8 +533,8 @@ def test_columns_of_heads_and_drafts(d, cols, splits):
 
 
 @pytest.mark.parametrize("B,T,G,hkv,d,width,odt", [
-    (64, 1, 4, 2, 128, 16384, BF16), (700, 1, 3, 1, 64, 2048, F32), (5000, 1, 1, 1, 32, 256, F16), (130, 1, 20, 1, 64, 8192, BF16),
-    (257, 4, 2, 1, 128, 4096, F32), (129, 1, 2, 2, 256, 4096, BF16), (40, 32, 1, 1, 32, 32768, BF16)])
+    (64, 1, 4, 2, 128, 16384, BF16), (700, 1, 3, 1, 64, 8192, F32), (5000, 1, 1, 1, 32, 1024, F16), (130, 1, 20, 1, 64, 8192, BF16),
+    (257, 4, 2, 1, 128, 8192, F32), (129, 1, 2, 2, 256, 4096, BF16), (40, 32, 1, 1, 32, 32768, BF16)])
 def test_many_sequences_of_uneven_lengths_in_a_wide_table(B, T, G, hkv, d, width, odt):
     """The work cut evenly among CTAs, where most sequences are empty or short and one is long: shares that hold
     many sequences, a part of one, the end of one and the start of another; then none with a token."""

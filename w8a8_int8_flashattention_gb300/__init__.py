@@ -14,7 +14,8 @@ varlen ("Attention kernels" table, attn_int8_fwd / attn_varlen_fwd; "Quick start
 layouts) and split-KV decode over an int8 KV cache ("Attention kernels" table,
 attn_decode, int8-V variant); and what serving from the paged int8 cache takes ("Engine"
 table, "Paged KV cache" row): the page plan of a step, the rotary append, page bounds,
-page selection and decode over page lists.
+page selection and decode over page lists; and that cache in 4 bits: the rotary append to it,
+reading it back as dense keys and values, and decode attention over it.
 """
 from __future__ import annotations
 

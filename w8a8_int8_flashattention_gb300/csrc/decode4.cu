@@ -4,24 +4,31 @@
 //   O   = sum_t p_t * s_v[t, g] * c_v[t]
 // over the tokens t that the query sees, g the groups of 32 channels.
 //
-// GB300 design.  A column is one query row of a kv head: a draft and a query head.  A CTA takes
-// up to 16 columns of one (sequence, kv head) and a contiguous run of its tokens; a cluster of S
-// CTAs, or more with a combine, share a sequence.
-//  * Four warps, each on its own: units of 16 tokens, taken in turn, arrive by 16-byte cp.async in a ring of
-//    the warp's own, so that no warp waits for another before the end.  Page ids are read 32 units ahead.
+// GB300 design.  A column is one query row of a kv head: a draft and a query head.  A CTA takes up to 24 columns
+// (8 at d = 256, whose outputs fill the registers) of one (sequence, kv head) and a run of its tokens.
+//  * Four warps, each on its own: steps of 32 tokens (16 at d = 256, and at d = 128 with 24 columns), every fourth of
+//    the run, arrive by 16-byte cp.async in a ring of the warp's own, the keys of the next step and the values of this one,
+//    so that no warp waits for another before the end.  Page ids are read 32 units of 16 tokens ahead.
 //  * S[16 tokens x 8 columns] = K Q^T as fp16 m16n8k16 MMAs on the nibbles where they lie, which are
-//    fp16 subnormals, n 2^-24 (or, four bits higher, 16 times that, against q / 16); 8 times the sum of the
-//    q's comes off again.  All partial sums are whole multiples of 2^-24 below 2^17 of them, so that a
+//    fp16 subnormals, n 2^-24 (or, four bits higher, 16 times that, against q / 16); their sums start at -8 times the sum of the
+//    q's, which is what the stored offset of 8 adds.  All partial sums are whole multiples of 2^-24 below 2^17 of them, so that a
 //    group's integer product is exact.  It meets its scale in fp32.  (The int8 MMA that would take the codes as
 //    they are takes 17 cycles an SM on this part, where the fp16 one takes 2 and does half; e4m3
 //    operands, in which nibbles are numbers too, are converted to fp16 one by one.)
-//  * O^T[d x 8 columns] += V^T P^T as bf16 MMAs: ldmatrix.trans hands each lane the four nibbles of
-//    two tokens' channels; where they lie they are bf16 numbers too, and one fma makes codes of them.  The
-//    weights p * s_v of a group are sums of bf16 terms, two (2^-17 of themselves left over; 16-bit
-//    outputs) or three (fp32).  They have fp32's range, so that no scale, however far from the
-//    others, costs another one its bits.
-//  * The logits of the next unit are computed beside the output of this one, so that neither
-//    chain waits alone; the units that end behind the first draft, at most one a warp, come last, with masks.
+//  * O^T[d x 8 columns] += V^T P^T as MMAs: ldmatrix.trans hands each lane the four nibbles of two tokens' channels; where
+//    they lie they are numbers too, and one fma makes codes of them.  The weight of a row in a group is p * s_v, p to 17 bits
+//    (two bf16 terms; mixed-precision fmas take bf16 scales as they are).  16-bit outputs take it as one fp16 number, relative
+//    to a reference that follows the largest weight so far, 2^-11 of itself; fp32 outputs as three bf16 terms, which have
+//    fp32's range, so that no scale, however far from the others, costs another one its bits.
+//  * The logits of the next step are computed beside the output of this one, so that neither
+//    chain waits alone; the steps that end behind the first draft, at most one a warp, come last, with masks.
+//  * Few tokens: a cluster of up to 8 CTAs a sequence, which send their parts to one another's shared memory.  Many: all
+//    sequences' steps are shared out evenly over the CTAs that fit the device, and a second kernel joins what the
+//    shares cut (64 sequences of 1,024 to 8,192 tokens, 8 x 4 heads, d = 128: 74 us, and 92 with a cluster of 2 each).
+// Bound by instruction issue, not by HBM: a step's masks, codes, scales and weights take as long as its MMAs and
+// loads together.  76 sequences of 8,192 tokens, 8 kv heads: 132 us at d = 128 with up to 8 columns, 0.80 of the copy rate
+// for codes and scales; 204 with 16 and 280 with 24, where 8 at a time would take 264 and 396; 180 with fp32 outputs.
+// d = 64: 97 us, 117, 166; d = 32: 70, 83, 114; d = 256: 253, 0.83 of the copy rate, and 338 with fp32 outputs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1009,11 +1016,19 @@ void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, i
     else *splits = kMaxCluster;
   } else if (num_splits > 0) {
     *splits = num_splits;
-  } else if (counted && items * tokens >= fit * 1024) {
-    *ctas = static_cast<int32_t>(fit);
   } else {
-    // as many CTAs a sequence as fit one wave, of 128 tokens at least
-    while (*splits < kMaxCluster && items * (*splits + 1) <= fit && tokens / (*splits + 1) >= 128) ++*splits;
+    // A cluster for each item, of as many CTAs as fit one wave and have 128 tokens each, 1,024 where they are more than
+    // two an SM, whose starts hold one another up (64 items of 1,024 tokens: 9.6 us with 4 CTAs each, 11.7 with 8); or even shares, if the table's
+    // width says that a CTA's longest run could be longer than a share (of lengths that are five eighths of the width) by
+    // what the second kernel and the ends of the shares cost: 1,000 tokens' time, 750 at d = 256.
+    // One sequence, 8 heads: 8,192 tokens 14.1 us in clusters and 13.7 in shares, 65,536 54 and 27; 512 tokens a CTA 10.7
+    // and 12.8.  64 sequences of 256 to 2,048: 30.1 and 34.1, of 512 to 4,096: 52.7 and 48.0.
+    while (*splits < kMaxCluster && items * (*splits + 1) <= fit && tokens / (*splits + 1) >= (items * (*splits + 1) <= 2 * num_sms() ? 128 : 1024))
+      ++*splits;
+    if (counted) {
+      const int64_t share = items * tokens / fit, run = std::max(tokens / *splits, share);
+      if (run - share * 5 / 8 >= (d == 256 ? 750 : 1000)) *splits = 1, *ctas = static_cast<int32_t>(fit);
+    }
   }
 }
 
