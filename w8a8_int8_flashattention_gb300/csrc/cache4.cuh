@@ -79,4 +79,14 @@ __device__ __forceinline__ uint32_t nibbles(const float (&x0)[kN], float s) {
   return p - extra;
 }
 
+// a b + c of two bf16 numbers and an fp32 one, one rounding; at the rate of fp32's own.  kA, kB: the half
+// of the word that a number is in.
+template <int kA, int kB>
+__device__ __forceinline__ float fma_mixed(uint32_t a, uint32_t b, float c) {
+  const uint16_t x = static_cast<uint16_t>(kA ? a >> 16 : a), y = static_cast<uint16_t>(kB ? b >> 16 : b);
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+  return d;
+}
+
 }  // namespace sl8

@@ -112,15 +112,6 @@ __device__ __forceinline__ void add_pair(float& x0, float& x1, float a0, float a
       : "+f"(x0), "+f"(x1)
       : "f"(a0), "f"(a1));
 }
-// a b + c of two bf16 numbers and an fp32 one, one rounding; at the rate of fp32's own.  kA, kB: the half
-// of the word that a number is in.
-template <int kA, int kB>
-__device__ __forceinline__ float fma_mixed(uint32_t a, uint32_t b, float c) {
-  const uint16_t x = static_cast<uint16_t>(kA ? a >> 16 : a), y = static_cast<uint16_t>(kB ? b >> 16 : b);
-  float d;
-  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
-  return d;
-}
 template <int kA>
 __device__ __forceinline__ float bf16_half(uint32_t a) {  // as fp32
   const uint16_t x = static_cast<uint16_t>(kA ? a >> 16 : a);
