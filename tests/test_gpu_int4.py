@@ -773,3 +773,49 @@ def test_side_stream_and_refusals():
         except error:
             continue
         pytest.fail(f"call {i} was not refused with {error}")
+
+
+def test_a_sequence_of_almost_2_31_tokens():
+    """Positions, steps and block numbers near their limits: one token outweighs all others by 2^80 (they come to 2^-49 of it),
+    and the output is its value row, wherever it lies."""
+    d, page = 32, 1 << 20
+    nb = (1 << 31) // page - 1
+    pool = sl8.int4_pages(2, 1, page, d, DEV)  # page 0: keys and values of 0
+    row = page - 1
+    pool[0][1, 0, row], pool[1][1, 0, row] = 0xff, 1.0  # codes 7
+    c = torch.arange(16, dtype=torch.uint8) * 17
+    pool[2][1, 0, row], pool[3][1, 0, row] = c.to(DEV), 0.5
+    want = Q.values(c.numpy()[None], np.array([[0.5]]))[0]
+    q = torch.ones((1, 2, d), device=DEV)
+    q *= 80 * np.log(2) * np.sqrt(d) / (7 * d)  # codes 127 of the scale's own: a logit of 80 log 2
+    for block in (0, 1024, nb - 1):
+        table = torch.zeros((1, nb), dtype=torch.int32, device=DEV)
+        table[0, block] = 1
+        for splits, odt in ((0, F32), (1 << 20, F16)):
+            out, lse = sl8.attn_int4_paged_decode(q, *pool, table, i32([nb * page]), num_splits=splits, out_dtype=odt, return_lse=True)
+            # the weight's roundings (2^-23, or 2^-11 + 2^-17), those of the merges and the output's
+            tol = np.abs(want) * (2.0 ** -18 if odt == F32 else 2.0 ** -11 + 2.0 ** -16 + 2.0 ** -11)
+            assert np.all(np.abs(np64(out[0]) - want) <= tol), (block, splits)
+            assert np.all(np.abs(np64(lse[0]) - 80 * np.log(2)) <= 80 * 2.0 ** -20)
+        # cut before that token, all logits are 0: the mean of values of 0; each lane's sum of ones is whole, and a few dozen merges
+        # of 4 x 2,432 parts at most round by 2^-24 each
+        if block == nb - 1:
+            out, lse = sl8.attn_int4_paged_decode(q, *pool, table, i32([nb * page - 1]), return_lse=True)
+            assert not out.any() and np.all(np.abs(np64(lse) - np.log(nb * page - 1)) <= 2.0 ** -10)
+
+
+def test_nothing_to_do():
+    """No sequences, no tokens, no room: nothing is written and nothing refused."""
+    pool = sl8.int4_pages(2, 2, 16, 64, DEV)
+    before = [x.clone() for x in pool]
+    k = torch.zeros((0, 2, 64), device=DEV)
+    assert sl8.rope_append_int4(k, k, k, i32([]), torch.ones(32, device=DEV), i32([]), *pool).shape == (0, 2, 64)
+    out = sl8.attn_int4_paged_decode(torch.zeros((0, 4, 64), device=DEV), *pool, i32(np.zeros((0, 3))), i32([]))
+    assert out.shape == (0, 4, 64)
+    k, v = sl8.paged_read_int4(*pool, i32(np.zeros((0, 3))), i32([]))
+    assert k.shape == v.shape == (0, 2, 48, 64)
+    k, v = sl8.paged_read_int4(*pool, i32([[0, 1]]), i32([0]), max_seqlen=0)
+    assert k.shape == (1, 2, 0, 64)
+    k, v = sl8.paged_read_int4(*pool, i32([[0, 1]]), i32([0]), cu_seqlens=i32([0, 0]), total_tokens=0)
+    assert k.shape == (0, 2, 64)
+    assert all(torch.equal(a, b) for a, b in zip(pool, before))
