@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
   using C = Cfg4<D, kCols>;
   constexpr int kN = C::kN, kT = C::kT, kU = C::kU;
   constexpr bool kHalf = kTerms == 1;           // weights and value codes in fp16, else in bf16
-  constexpr int kParts = kTerms == 1 ? 2 : kTerms;  // bf16 terms of p
   constexpr uint32_t kMinusOne = 0xbf80u;       // bf16
   using Codes = Codes4<kHalf>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -586,13 +585,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       }
     };
 
-    // O += a step's weighted rows.  vis (masked): bits of the token pairs that column g + 8 h sees; whatever the
+    // O += a step's weighted rows.  vis (masked): which of the columns 2 t and 2 t + 1 see tokens g and g + 8; whatever the
     // scales of the others hold, they weigh nothing.
     auto output = [&](uint32_t base, const float (&x)[kU][kT][4], const bool masked, const uint32_t (&vis)[kU][kT][2]) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const uint32_t q = base + u * 8 * D + frag, r = base + C::kScales + u * D + 4 * kN * t;
-        uint32_t vw[2][kN], sc[2][kN];
+        const uint32_t q = base + u * 8 * D + frag, r = base + C::kScales + u * D + 2 * kN * g;
+        uint32_t vw[2][kN], sc[2][(kN + 1) / 2];
         if constexpr (kN == 1) {
           ldsm2_t(q, vw[0][0], vw[1][0]);
         } else if constexpr (kN == 2) {
@@ -604,54 +603,37 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             for (int j = 0; j < kN; j += 4)
               ldsm4_t((j ? q ^ (16 * j) : q) + 4 * D * s, vw[s][j], vw[s][j + 1], vw[s][j + 2], vw[s][j + 3]);
         }
-        // scales of tokens 2 t, 2 t + 1 (and + 8)
-        lds_words<2 * kN>(r, sc[0]);
-        lds_words<2 * kN>(r + 16 * kN, sc[1]);
-        // p as bf16 terms, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
-        uint32_t p[kT][kParts][2];
+        lds_words<kN>(r, sc[0]);
+        lds_words<kN>(r + 16 * kN, sc[1]);
+        float p[kT][2][2];  // of tokens g and g + 8 and columns 2 t and 2 t + 1
 #pragma unroll
         for (int h = 0; h < kT; ++h)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            float pa = ex2(fmaf(x[u][h][2 * s], qs[h][0], -ref[h][0])), pb = ex2(fmaf(x[u][h][2 * s + 1], qs[h][1], -ref[h][1]));
-            add_pair(l[h][0], l[h][1], pa, pb);
-#pragma unroll
-            for (int e = 0; e < kParts; ++e) {
-              const uint32_t w = bf16x2_of(pa, pb);
-              p[h][e][s] = movm_t(w);
-              if (e + 1 < kParts) {
-                pa = fma_mixed<0, 0>(w, kMinusOne, pa);
-                pb = fma_mixed<1, 0>(w, kMinusOne, pb);
-              }
-            }
+            p[h][s][0] = ex2(fmaf(x[u][h][2 * s], qs[h][0], -ref[h][0]));
+            p[h][s][1] = ex2(fmaf(x[u][h][2 * s + 1], qs[h][1], -ref[h][1]));
+            add_pair(l[h][0], l[h][1], p[h][s][0], p[h][s][1]);
           }
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          uint32_t wt[kT][kTerms][2];
+          uint32_t wt[kT][kTerms][2];  // p s_v, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int s = 0; s < 2; ++s) {
+            const float f = (j & 1) ? bf16_half<1>(sc[s][j / 2]) : bf16_half<0>(sc[s][j / 2]);
 #pragma unroll
             for (int h = 0; h < kT; ++h) {
-              // the group's scales of the two tokens
-              uint32_t sa = kN == 1 ? sc[s][0] : sc[s][j / 2], sb = kN == 1 ? sc[s][0] : sc[s][(kN + j) / 2];
+              float w0 = p[h][s][0] * f, w1 = p[h][s][1] * f;
               if (masked) {
-                sa = (vis[u][h][s] & 1u) ? sa : 0u;
-                sb = (vis[u][h][s] & 2u) ? sb : 0u;
-              }
-              constexpr int kLo = 0, kHi = 1;
-              float w0 = 0.0f, w1 = 0.0f;
-#pragma unroll
-              for (int e = kParts - 1; e >= 0; --e) {
-                w0 = (j & 1) ? fma_mixed<kLo, kHi>(p[h][e][s], sa, w0) : fma_mixed<kLo, kLo>(p[h][e][s], sa, w0);
-                w1 = (j & 1) || kN == 1 ? fma_mixed<kHi, kHi>(p[h][e][s], sb, w1) : fma_mixed<kHi, kLo>(p[h][e][s], sb, w1);
+                w0 = (vis[u][h][s] & 1u) ? w0 : 0.0f;
+                w1 = (vis[u][h][s] & 2u) ? w1 : 0.0f;
               }
               if constexpr (kHalf) {
-                wt[h][0][s] = f16x2_of(w0, w1);
+                wt[h][0][s] = movm_t(f16x2_of(w0, w1));
               } else {
 #pragma unroll
                 for (int e = 0; e < kTerms; ++e) {
                   const uint32_t w = bf16x2_of(w0, w1);
-                  wt[h][e][s] = w;
+                  wt[h][e][s] = movm_t(w);
                   if (e + 1 < kTerms) {
                     w0 = fma_mixed<0, 0>(w, kMinusOne, w0);
                     w1 = fma_mixed<1, 0>(w, kMinusOne, w1);
@@ -659,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
                 }
               }
             }
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {  // channels 32 j + 4 g + 2 y and + 1
             const uint32_t u0 = y ? vw[0][j] >> 8 : vw[0][j], u1 = y ? vw[1][j] >> 8 : vw[1][j];
@@ -708,15 +691,16 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       uint32_t vis[kU][kT][2];
 #pragma unroll
       for (int h = 0; h < kT; ++h) {
-        const uint32_t da = seen(8 * h + 2 * t), db = seen(8 * h + 2 * t + 1), dg = seen(8 * h + g);
+        const uint32_t da = seen(8 * h + 2 * t), db = seen(8 * h + 2 * t + 1);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const int p = tok + 16 * u + g + 8 * s, q = tok + 16 * u + 2 * t + 8 * s;
-            if (!visible(da, p)) x[u][h][2 * s] = -INFINITY;
-            if (!visible(db, p)) x[u][h][2 * s + 1] = -INFINITY;
-            vis[u][h][s] = (visible(dg, q) ? 1u : 0u) | (visible(dg, q + 1) ? 2u : 0u);
+            const int p = tok + 16 * u + g + 8 * s;
+            const bool va = visible(da, p), vb = visible(db, p);
+            if (!va) x[u][h][2 * s] = -INFINITY;
+            if (!vb) x[u][h][2 * s + 1] = -INFINITY;
+            vis[u][h][s] = (va ? 1u : 0u) | (vb ? 2u : 0u);
           }
       }
       move_maxima(x, ring + 2 * C::kHalf + now);
