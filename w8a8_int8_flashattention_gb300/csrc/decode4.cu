@@ -119,6 +119,17 @@ __device__ __forceinline__ float bf16_half(uint32_t a) {  // as fp32
   asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(d) : "h"(x), "f"(-0.0f));
   return d;
 }
+// (x0, x1) = (a0, a1) f, and (x0, x1) += (a0, a1) f.
+__device__ __forceinline__ void mul_pair(float& x0, float& x1, float a0, float a1, float f) {
+  asm("{\n\t.reg .b64 x, a, f;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tmul.rn.f32x2 x, a, f;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(f));
+}
+__device__ __forceinline__ void fma_pair(float& x0, float& x1, float a0, float a1, float f) {
+  asm("{\n\t.reg .b64 x, a, f;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tfma.rn.f32x2 x, a, f, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1), "f"(f));
+}
 // Nibbles where they lie in a 16-bit word are bf16 numbers, n 2^-133 (bits 0..3) and n 2^-129
 // (bits 4..7, since the exponents 0 and 1 have the same step): times 2^127 and less 8 such, codes.
 // As fp16 numbers they are n 2^-24 and n 2^-20, times 2^15 less 8 such.
@@ -491,7 +502,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             mma_f16_on(acc, u0 & 0x000f000fu, u1 & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu, qb[h][0], qb[h][1], bias[h]);
             mma_f16_add(acc, u0 & 0x00f000f0u, u1 & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[h][2], qb[h][3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[u][h][i] = j == 0 ? acc[i] * (i < 2 ? f0 : f1) : fmaf(acc[i], i < 2 ? f0 : f1, x[u][h][i]);
+            for (int i = 0; i < 4; i += 2) {
+              const float f = i < 2 ? f0 : f1;
+              if (j == 0) mul_pair(x[u][h][i], x[u][h][i + 1], acc[i], acc[i + 1], f);
+              else fma_pair(x[u][h][i], x[u][h][i + 1], acc[i], acc[i + 1], f);
+            }
           }
         }
       }
@@ -622,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             const float f = (j & 1) ? bf16_half<1>(sc[s][j / 2]) : bf16_half<0>(sc[s][j / 2]);
 #pragma unroll
             for (int h = 0; h < kT; ++h) {
-              float w0 = p[h][s][0] * f, w1 = p[h][s][1] * f;
+              float w0, w1;
+              mul_pair(w0, w1, p[h][s][0], p[h][s][1], f);
               if (masked) {
                 w0 = (vis[u][h][s] & 1u) ? w0 : 0.0f;
                 w1 = (vis[u][h][s] & 2u) ? w1 : 0.0f;
