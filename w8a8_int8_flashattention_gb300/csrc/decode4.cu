@@ -16,19 +16,19 @@
 //    they are takes 17 cycles an SM on this part, where the fp16 one takes 2 and does half; e4m3
 //    operands, in which nibbles are numbers too, are converted to fp16 one by one.)
 //  * O^T[d x 8 columns] += V^T P^T as MMAs: ldmatrix.trans hands each lane the four nibbles of two tokens' channels; where
-//    they lie they are numbers too, and one fma makes codes of them.  The weight of a row in a group is p * s_v, p to 17 bits
-//    (two bf16 terms; mixed-precision fmas take bf16 scales as they are).  16-bit outputs take it as one fp16 number, relative
+//    they lie they are numbers too, and one fma makes codes of them.  The weight of a row in a group is p * s_v, formed in fp32,
+//    two columns at a time, and transposed between lanes in 16 bits.  16-bit outputs take it as one fp16 number, relative
 //    to a reference that follows the largest weight so far, 2^-11 of itself; fp32 outputs as three bf16 terms, which have
 //    fp32's range, so that no scale, however far from the others, costs another one its bits.
 //  * The logits of the next step are computed beside the output of this one, so that neither
 //    chain waits alone; the steps that end behind the first draft, at most one a warp, come last, with masks.
 //  * Few tokens: a cluster of up to 8 CTAs a sequence, which send their parts to one another's shared memory.  Many: all
 //    sequences' steps are shared out evenly over the CTAs that fit the device, and a second kernel joins what the
-//    shares cut (64 sequences of 1,024 to 8,192 tokens, 8 x 4 heads, d = 128: 74 us, and 92 with a cluster of 2 each).
+//    shares cut (64 sequences of 1,024 to 8,192 tokens, 8 x 4 heads, d = 128: 70 us, and 81 with a cluster of 2 each).
 // Bound by instruction issue, not by HBM: a step's masks, codes, scales and weights take as long as its MMAs and
-// loads together.  76 sequences of 8,192 tokens, 8 kv heads: 132 us at d = 128 with up to 8 columns, 0.80 of the copy rate
-// for codes and scales; 204 with 16 and 280 with 24, where 8 at a time would take 264 and 396; 180 with fp32 outputs.
-// d = 64: 97 us, 117, 166; d = 32: 70, 83, 114; d = 256: 253, 0.83 of the copy rate, and 338 with fp32 outputs.
+// loads together.  76 sequences of 8,192 tokens, 8 kv heads: 124 us at d = 128 with up to 8 columns, 0.85 of the copy rate
+// for codes and scales; 186 with 16 and 259 with 24, where 8 at a time would take 248 and 372; 165 with fp32 outputs.
+// d = 64: 89 us, 107, 149; d = 32: 66, 71, 100; d = 256: 236, 0.89 of the copy rate, and 316 with fp32 outputs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -157,13 +157,16 @@ template <int D, int kCols>
 struct Cfg4 {
   static constexpr int kN = D / kGroup4;  // groups (and 16-byte chunks) of a row
   static constexpr int kT = (kCols + 7) / 8;  // tiles of eight columns
-  static constexpr int kU = D == 256 || (D == 128 && kCols > 16) ? 1 : 2;  // units of 16 tokens that a warp takes at a time, a step
+  // Units of 16 tokens that a warp takes at a time, a step: two where the registers hold them (64 sequences of up to 8,192
+  // tokens 70 us, and 76 with one; 24 columns at d = 128 46 with one and 50 with two).
+  static constexpr int kU = D == 256 || (D == 128 && kCols > 16) ? 1 : 2;
   static constexpr int kStep = 16 * kU;
   static constexpr int kStart = D == 256 ? 16 : 512 / kStep;  // steps that a sequence's start and end are worth, see below
   static constexpr int kHalf = kU * 9 * D;  // a step's keys, or its values: codes [kU][16][D / 2], scales [kU][16][kN]
   static constexpr int kScales = kU * 8 * D;
   static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
-  // as many CTAs an SM as their registers let: the accumulators are D kT / 4 a thread
+  // as many CTAs an SM as their registers let, the accumulators being D kT / 4 a thread (d = 64: with one more 39 us for
+  // 35, with one less 37; d = 128 with one less 74.4 for 73.8)
   static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : 6 - kT;
   // after the loop the rings hold the warps' O^T [warp][D][kCols], fp32
   static constexpr int kRed = 0, kMerge = kWarps * D * kCols * 4;
@@ -962,6 +965,7 @@ cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
   if (e != cudaSuccess || !a.ctas) return e;
   // rows of the combine that share a column's parts: as many as take them kMany times over at once, since lengths differ
+  // (kMany 1, 2, 4, 8 on sequences of up to 8,192 tokens: 75.2 us, 75.9, 77.8, 80.2; a CTA for each column 77.3)
   constexpr int kRows = kJoin / (D / 4), kMany = 2;
   const unsigned ctas = static_cast<unsigned>(a.ctas);
   int stripes = 1;
@@ -1009,11 +1013,11 @@ void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, i
     *splits = num_splits;
   } else {
     // A cluster for each item, of as many CTAs as fit one wave and have 128 tokens each, 1,024 where they are more than
-    // two an SM, whose starts hold one another up (64 items of 1,024 tokens: 9.6 us with 4 CTAs each, 11.7 with 8); or even shares, if the table's
+    // two an SM, whose starts hold one another up (64 items of up to 1,024 tokens: 9.3 us with 4 CTAs each, 11.3 with 8); or even shares, if the table's
     // width says that a CTA's longest run could be longer than a share (of lengths that are five eighths of the width) by
     // what the second kernel and the ends of the shares cost: 1,000 tokens' time, 750 at d = 256.
-    // One sequence, 8 heads: 8,192 tokens 14.1 us in clusters and 13.7 in shares, 65,536 54 and 27; 512 tokens a CTA 10.7
-    // and 12.8.  64 sequences of 256 to 2,048: 30.1 and 34.1, of 512 to 4,096: 52.7 and 48.0.
+    // One sequence, 8 heads: 8,192 tokens 13.5 us in clusters and 13.2 in shares, 65,536 51 and 26; 512 tokens a CTA 10.5
+    // and 12.3.  64 sequences of 256 to 2,048: 30.1 and 34.1, of 512 to 4,096: 52.7 and 48.0.
     while (*splits < kMaxCluster && items * (*splits + 1) <= fit && tokens / (*splits + 1) >= (items * (*splits + 1) <= 2 * num_sms() ? 128 : 1024))
       ++*splits;
     if (counted) {
