@@ -11,7 +11,7 @@ Attention, for n tokens and kN = d / 32 groups (2^-24 is half a step of fp32):
   sum |q k| / sqrt(d), in units of log2 1.45 times that; exponentials are good to 2^-22; so each p to
     ep = 1.45 (kN + 4) 2^-24 reach + 2^-22, and the quotient by their sum to twice that;
   weights p s_v of fp32 outputs are off by 2^-23 of themselves (three bf16 terms, the product's rounding); those of
-  16-bit outputs are fp16 numbers of p to two bf16 terms: 2^-11 + 2^-17 of themselves, or half of 2^-24 on a scale on
+  16-bit outputs are fp16 numbers of the product in fp32: 2^-11 + 2^-23 of themselves, or half of 2^-24 on a scale on
   which the largest of the query is at least 1/2: 2^-24 of that one, times |code| <= 8, for each token;
   sums: each MMA's addition may truncate (2^-23 of the partial sum), at most 3 an m16n8k16 step and 16 tokens,
   and some thirty in merges: (3 n / 16 + 32) 2^-23.
@@ -303,7 +303,7 @@ def _check_attention(out, lse, q, host, tables, lens, masks=None, tag=""):
     want, wlse, size, reach, heavy = Q.attention(f32(q), *host, tables, lens, masks, bounds=True)
     n, groups = max(int(np.max(lens)), 1), q.shape[-1] // 32
     ep = 1.45 * (groups + 4) * 2.0 ** -24 * reach + 2.0 ** -22
-    ew, floor = (2.0 ** -23, 0.0) if out.dtype == torch.float32 else (2.0 ** -11 + 2.0 ** -17, 2.0 ** -24 * 8 * n)
+    ew, floor = (2.0 ** -23, 0.0) if out.dtype == torch.float32 else (2.0 ** -11 + 2.0 ** -23, 2.0 ** -24 * 8 * n)
     rel = 2 * ep[..., None] + ew + (3 * n / 16 + 32) * 2.0 ** -23
     eps = torch.finfo(out.dtype).eps / 2
     got = np64(out)
