@@ -562,9 +562,10 @@ SL8_API int sl8_attn_int8_sparse_decode(const void* q, int q_dtype, const int8_t
  *                                 the low half of byte i, of channel 2 i + 1 in its high half;
  *   k_scale_pages, v_scale_pages  [num_pages][Hkv][page_size][d / 32] bf16;
  * 18 bytes for 32 values.  A half of 0 (which no append writes) is the code -8.  A group with an
- * infinity has the scale inf and codes 0, which stand for NaN; a NaN has the code 0.  Scales below
- * 2^-126 hold fewer than 8 bits, and codes stay within +-7 all the same.  All four
- * arrays are 16-byte aligned.  Slots, block tables and the page plan are those of the int8 pages.
+ * infinity has the scale inf and codes 0, which stand for NaN; a NaN has the code 0, and a group of
+ * NaN alone the scale 0.  Scales below 2^-126 hold fewer than 8 bits, and codes stay within +-7 all
+ * the same.  All four arrays are 16-byte aligned.  Slots, block tables and the page plan are those of
+ * the int8 pages.
  *
  * Rotary positions and the 4-bit append: sl8_rope_append (all of its arguments, checks and
  * guarantees) with these pages, and

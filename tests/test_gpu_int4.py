@@ -819,3 +819,37 @@ def test_nothing_to_do():
     k, v = sl8.paged_read_int4(*pool, i32([[0, 1]]), i32([0]), cu_seqlens=i32([0, 0]), total_tokens=0)
     assert k.shape == (0, 2, 64)
     assert all(torch.equal(a, b) for a, b in zip(pool, before))
+
+
+# ------------------------------------------------------------------ groups and rows that are not numbers, scales far apart
+
+def test_groups_of_nan_alone_are_zeros():
+    """A group whose 32 values are all NaN has the codes 0 and the scale +0, bit for bit, where pairs turn (halves or adjacent)
+    and where they do not; what its row's other groups hold comes out of a 16-bit attention, alone or with most of the weight."""
+    T, hkv, d = 9, 2, 64
+    for dtype in (F32, F16, BF16):
+        for adjacent, rot in ((False, 0), (True, 32), (False, 32)):
+            x = torch.randn((T, hkv, d), device=DEV).to(dtype)
+            x[2, 0, :32], x[5, 1], x[7, :, 32:] = float("nan"), float("nan"), float("nan")
+            pool = _pool(1, hkv, 16, d)
+            pos, inv = (torch.arange(T, dtype=torch.int32, device=DEV), torch.rand(rot // 2, device=DEV)) if rot else (None, None)
+            sl8.rope_append_int4(None, x, x, pos, inv, i32(np.arange(T)), *pool, adjacent=adjacent)
+            for i in (0, 2):
+                bits = pool[i + 1][0].transpose(0, 1)[:T].view(torch.int16)  # [T, hkv, 2]
+                nan = torch.isnan(x).unflatten(-1, (2, 32)).all(-1)
+                assert bool((bits[nan] == 0).all()) and bool((bits[~nan] > 0).all()), (dtype, adjacent, rot, i)
+                assert bool((pool[i][0].transpose(0, 1)[:T].unflatten(-1, (2, 16))[nan] == 0x88).all())
+    for d, odt in ((64, F16), (128, BF16), (256, F16), (32, BF16)):
+        d2 = max(d, 64)
+        for L in (1, 40):
+            k = torch.zeros((L, 1, d2), device=DEV)
+            v = torch.randn((L, 1, d2), device=DEV)
+            k[L // 2], v[L // 2, :, 32:] = 30.0, float("nan")  # almost all of the weight
+            v[L // 2, :, :32] = torch.linspace(-3.5, 3.5, 32, device=DEV)
+            q = torch.ones((1, 1, 4, d2), device=DEV)
+            pool = sl8.int4_pages(3, 1, 16, d2, DEV)
+            sl8.rope_append_int4(None, k, v, None, None, i32(np.arange(L)), *pool)
+            host = [x.float().cpu().numpy() if x.dtype == BF16 else x.cpu().numpy() for x in pool]
+            for splits in (1, 3, 12):
+                out, lse = sl8.attn_int4_paged_decode(q, *pool, i32([[0, 1, 2]]), i32([L]), num_splits=splits, out_dtype=odt, return_lse=True)
+                _check_attention(out, lse, q, host, [[0, 1, 2]], [L], tag=(d2, L, splits))

@@ -11,11 +11,13 @@ namespace sl8 {
 
 constexpr int kGroup4 = 32;  // channels that share a scale
 
-// bf16(max|x| / 7) as fp32; a NaN never gets here (maxima drop it), an infinity stays one.  The
-// division by a product and a correction by its exact remainder (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990), which for 7 gives the quotient's fp32 rounding
-// for every significand; where the remainder may underflow or the product is infinite, by division.
+// bf16(max|x| / 7) as fp32; an infinity stays one.  Maxima drop a NaN, but that of NaNs alone is one, whose bits
+// the rounding below would wrap to those of -0: it counts as 0.  The division by a product and a correction by its
+// exact remainder (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), which for 7 gives the quotient's fp32 rounding for every significand; where the remainder may underflow
+// or the product is infinite, by division.
 __device__ __forceinline__ float group_scale(float amax) {
+  amax = fmaxf(amax, 0.0f);
   constexpr float kSeventh = 1.0f / 7.0f;
   const float q = amax * kSeventh;
   float d = fmaf(fmaf(-7.0f, q, amax), kSeventh, q);
