@@ -853,3 +853,34 @@ def test_groups_of_nan_alone_are_zeros():
             for splits in (1, 3, 12):
                 out, lse = sl8.attn_int4_paged_decode(q, *pool, i32([[0, 1, 2]]), i32([L]), num_splits=splits, out_dtype=odt, return_lse=True)
                 _check_attention(out, lse, q, host, [[0, 1, 2]], [L], tag=(d2, L, splits))
+
+
+@pytest.mark.parametrize("splits", [1, 3, 12])
+@pytest.mark.parametrize("d,odt", [(64, F16), (64, BF16), (128, F16), (128, BF16), (256, BF16), (128, F32)])
+def test_infinite_value_groups_leave_the_others_their_values(d, odt, splits):
+    """An infinite V scale (codes 0, as the append stores it), a NaN one, and scales of -0 and below, in rows of ordinary, most and
+    hardly any weight: the group's own channels are NaN where the scale is, all others and the lse the definition's."""
+    rng = np.random.default_rng(d + splits)
+    hkv, G, page, L = 1, 3, 16, 300
+    q = torch.from_numpy(np.abs(rng.standard_normal((1, 1, G, d)).astype(np.float32)) + 0.5).to(DEV)
+    for value in (float("inf"), float("nan"), -0.0, -0.5):
+        for row, key in ((0, None), (19, None), (L - 1, None), (131, 0xff), (44, 0x11)):
+            for n in (L, row + 1) if row == 0 else (L,):
+                pool, (kc, ks, vc, vs) = _filled(rng, 20, hkv, page, d, 0.5)
+                at = row // page, 0, row % page
+                if key is not None:  # codes 7 or -7 against positive queries
+                    kc[at], ks[at] = key, 2.0
+                if not np.isfinite(value):
+                    vc[at][16:32] = 0x88
+                vs[at][1] = value
+                for i, x in enumerate((kc, ks, vc, vs)):
+                    pool[i].copy_(torch.from_numpy(x))
+                out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(np.arange(20)[None]), i32([n]), num_splits=splits, out_dtype=odt,
+                                                      return_lse=True)
+                if not np.isfinite(value):
+                    assert torch.isnan(out[..., 32:64]).all(), (value, row)
+                    vs[at][1] = 0
+                    want = Q.attention(f32(q), kc, ks, vc, vs, [np.arange(20)], [n])[0]
+                    out[..., 32:64] = torch.from_numpy(want[..., 32:64]).to(out)
+                _check_attention(out, lse, q, (kc, ks, vc, np.abs(vs)) if value != -0.5 else (kc, ks, vc, vs), [np.arange(20)], [n],
+                                 tag=(value, row, n))

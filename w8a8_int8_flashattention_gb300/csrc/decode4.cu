@@ -148,6 +148,12 @@ struct Codes4 {
     return r;
   }
 };
+// The magnitude's bits of the bf16 number in the low half of a word; 0 for infinities and NaN, which make their
+// group's channels NaN whatever the others' weights are relative to.
+__device__ __forceinline__ uint32_t finite_scale(uint32_t w) {
+  const uint32_t s = w & 0x7fffu;
+  return s < 0x7f80u ? s : 0u;
+}
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -538,10 +544,15 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
         uint32_t s = w[0] << 16;
         if constexpr (kMine > 1) s = max(s, w[0] & 0xffff0000u);
         if constexpr (kMine > 2) s = max(s, max(w[(kMine - 1) / 2] << 16, w[(kMine - 1) / 2] & 0xffff0000u));
-        grow = grow || s > vlim;
+        if (!__any_sync(0xffffffffu, grow || s > vlim)) return;
+        // The bits of an infinity, a NaN or a negative scale lie above any limit; here they count as below.
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) most = max(most, finite_scale((i & 1) ? w[i / 2] >> 16 : w[i / 2]));
+        grow = grow || (most << 16) > vlim;
       }
       if (!__any_sync(0xffffffffu, grow)) return;
-      [[maybe_unused]] float up[kU][2];  // log2 of the largest scale of tokens g and g + 8, rounded up
+      [[maybe_unused]] float up[kU][2];  // log2 of the largest finite scale of tokens g and g + 8, rounded up
       if constexpr (kHalf) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -550,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             uint32_t w[(kN + 1) / 2], most = 0;
             lds_words<kN>(values + C::kScales + u * D + 2 * kN * (g + 8 * s), w);
 #pragma unroll
-            for (int j = 0; j < kN; ++j) most = max(most, (j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
-            up[u][s] = static_cast<float>(static_cast<int>((most >> 7) & 0xffu) - 126);
+            for (int j = 0; j < kN; ++j) most = max(most, finite_scale((j & 1) ? w[j / 2] >> 16 : w[j / 2]));
+            up[u][s] = static_cast<float>(static_cast<int>(most >> 7) - 126);
           }
       }
       auto bounded = [](float v) { return fminf(fmaxf(v, -1048576.0f), 1048576.0f); };
