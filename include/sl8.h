@@ -624,9 +624,12 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *                 keys: with a k_mean, sum_c q_c k_mean_c / sqrt(d) below that of the keys themselves.
  *                 A NaN logit (a group with an infinite k scale, or such a query row) makes out and
  *                 lse_out of its query NaN, an infinite v scale the group's channels of out.
- *                 Each weight p * s_v is off by 2^-11 of itself before it meets its row, or by 2^-24
- *                 of the query's largest weight (an fp32 out: 2^-23 of itself).  V scales are 0, or between 2^-94
- *                 and 2^112: smaller ones keep fewer bits in 16-bit outputs, larger ones may overflow.
+ *                 The sum of the p, and with it lse_out, does not depend on the values; a p below 2^-126 of the
+ *                 largest may count as 0.  Each weight p * s_v is off by 2^-11 of itself before it meets its row,
+ *                 or by 2^-24 of the query's largest weight (an fp32 out: 2^-23 of itself).  V scales are, in
+ *                 magnitude, 0 or between 2^-94 and 2^124 (for an fp32 out, also at most 2^117 over the
+ *                 sequence's length): smaller ones keep fewer bits in 16-bit outputs, larger ones may
+ *                 overflow.
  *   workspace     at least sl8_attn_int4_paged_decode_workspace_size() bytes (0: invalid or
  *                 unsupported shape; 16: none is used and it may be null), 16-byte aligned; launches
  *                 that run at the same time need their own.

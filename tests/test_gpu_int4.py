@@ -884,3 +884,65 @@ def test_infinite_value_groups_leave_the_others_their_values(d, odt, splits):
                     out[..., 32:64] = torch.from_numpy(want[..., 32:64]).to(out)
                 _check_attention(out, lse, q, (kc, ks, vc, np.abs(vs)) if value != -0.5 else (kc, ks, vc, vs), [np.arange(20)], [n],
                                  tag=(value, row, n))
+
+
+@pytest.mark.parametrize("splits", [1, 3, 12])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+def test_probabilities_do_not_depend_on_value_scales(d, splits):
+    """The sum of the probabilities, and with it out and lse, whatever the V scales: rows of zero or the least scale beside one
+    of a large one, equal logits or far apart, in one warp, in several and in several parts; scales of both ends of the stated range."""
+    rng = np.random.default_rng(d)
+    hkv, G, page, L = 1, 4, 16, 300
+    tables = [np.arange(20)]
+    q = torch.ones((1, 1, G, d), device=DEV)
+    unit = 7 * np.sqrt(d)  # the logit of a row of codes 7 and the scale 1
+    for most, least, row, x in ((60, None, 150, 0.0), (60, None, 299, 0.0), (60, None, 1, 0.0), (47, None, 131, 0.0), (112, -94, 40, 0.0),
+                                (112, -94, 200, -50.0), (112, -94, 3, -20.0), (100, None, 257, -50.0), (0, 112, 64, 17.0), (112, 0, 5, 17.0),
+                                (-94, None, 290, 3.0), (20, -20, 33, 30.0), (124, -94, 77, 30.0), (124, -94, 77, 0.0), (-94, 124, 291, 9.0)):
+        pool, (kc, ks, vc, vs) = _filled(rng, 20, hkv, page, d)
+        kc[:], ks[:] = 0x88, 1.0
+        vs[:] = 0.0 if least is None else 2.0 ** least
+        at = row // page, 0, row % page
+        kc[at] = 0xff if x >= 0 else 0x11
+        ks[at] = Q.to_bf16(np.float32(abs(x) * np.log(2) / unit))
+        vs[at] = 2.0 ** most
+        for i, a in enumerate((kc, ks, vc, vs)):
+            pool[i].copy_(torch.from_numpy(a))
+        for odt in (BF16, F32) if 124 not in (most, least) else (BF16,):  # fp32 outputs take up to 2^117 over the length
+            out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), num_splits=splits, out_dtype=odt, return_lse=True)
+            _check_attention(out, lse, q, (kc, ks, vc, vs), tables, [L], tag=(most, least, row, x, odt))
+
+
+@pytest.mark.parametrize("splits", [1, 8, 40])
+def test_many_small_probabilities_beside_a_large_scale(splits):
+    """20,000 tokens of 2^-17 of the largest probability each come to 15 % of the sum, beside a row of the scale 2^110."""
+    d, page, L = 64, 16, 20001
+    nb = -(-L // page)
+    tables = [np.arange(nb)]
+    kc, ks = np.full((nb, 1, page, d // 2), 0x88, np.uint8), np.ones((nb, 1, page, d // 32), np.float32)
+    vc, vs = np.full((nb, 1, page, d // 2), 0x9d, np.uint8), np.ones((nb, 1, page, d // 32), np.float32)
+    at = 700, 0, 3
+    kc[at], ks[at], vs[at] = 0xff, Q.to_bf16(np.float32(17 * np.log(2) / (7 * np.sqrt(d)))), 2.0 ** 110
+    pool = sl8.int4_pages(nb, 1, page, d, DEV)
+    for i, x in enumerate((kc, ks, vc, vs)):
+        pool[i].copy_(torch.from_numpy(x))
+    q = torch.ones((1, 1, 2, d), device=DEV)
+    out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32([L]), num_splits=splits, out_dtype=BF16, return_lse=True)
+    _check_attention(out, lse, q, (kc, ks, vc, vs), tables, [L])
+
+
+@pytest.mark.parametrize("d,T,G", [(32, 1, 3), (64, 1, 16), (128, 2, 4), (128, 1, 24), (256, 1, 8)])
+def test_the_lse_has_the_same_bits_for_any_values(d, T, G):
+    rng = np.random.default_rng(d + G)
+    lens = [700, 33, 1, 260]
+    pool, host = _filled(rng, 80, 1, 16, d)
+    tables = _tables(rng, lens, 44, 16, 80)
+    q = torch.from_numpy(rng.standard_normal((4, T, G, d)).astype(np.float32) * 3).to(DEV)
+    for splits in (0, 1, 4, 12):
+        call = lambda odt: sl8.attn_int4_paged_decode(q, *pool, i32(tables), i32(lens), num_splits=splits, out_dtype=odt, return_lse=True)  # noqa: E731
+        for odt in (F16, BF16):
+            pool[3].copy_(torch.from_numpy(host[3]))
+            _, want = call(odt)
+            for make in (lambda s: s * 0, lambda s: 10.0 ** rng.uniform(-28, 33, s.shape), lambda s: np.where(rng.random(s.shape) < 0.1, np.inf, s)):
+                pool[3].copy_(torch.from_numpy(make(host[3]).astype(np.float32)))
+                assert torch.equal(call(odt)[1], want), (splits, odt)

@@ -18,7 +18,7 @@
 //  * O^T[d x 8 columns] += V^T P^T as MMAs: ldmatrix.trans hands each lane the four nibbles of two tokens' channels; where
 //    they lie they are numbers too, and one fma makes codes of them.  The weight of a row in a group is p * s_v, formed in fp32,
 //    two columns at a time, and transposed between lanes in 16 bits.  16-bit outputs take it as one fp16 number, relative
-//    to a reference that follows the largest weight so far, 2^-11 of itself; fp32 outputs as three bf16 terms, which have
+//    to a power of two that follows the largest weight so far, 2^-11 of itself; fp32 outputs as three bf16 terms, which have
 //    fp32's range, so that no scale, however far from the others, costs another one its bits.
 //  * The logits of the next step are computed beside the output of this one, so that neither
 //    chain waits alone; the steps that end behind the first draft, at most one a warp, come last, with masks.
@@ -119,6 +119,12 @@ __device__ __forceinline__ float bf16_half(uint32_t a) {  // as fp32
   asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(d) : "h"(x), "f"(-0.0f));
   return d;
 }
+// (x0, x1) *= (f0, f1).
+__device__ __forceinline__ void scale_pair(float& x0, float& x1, float f0, float f1) {
+  asm("{\n\t.reg .b64 x, f;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmul.rn.f32x2 x, x, f;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(f0), "f"(f1));
+}
 // (x0, x1) = (a0, a1) f, and (x0, x1) += (a0, a1) f.
 __device__ __forceinline__ void mul_pair(float& x0, float& x1, float a0, float a1, float f) {
   asm("{\n\t.reg .b64 x, a, f;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tmul.rn.f32x2 x, a, f;\n\tmov.b64 {%0, %1}, x;\n\t}"
@@ -181,7 +187,8 @@ struct Cfg4 {
   static constexpr int kQs = kBias + kN * kT * 64;        // [kCols] scales
   static constexpr int kQc = kQs + kCols * 4;             // [kCols][D] query codes
   static constexpr int kStat = kQc + kCols * D;           // [warp][kCols][2]: max (log2), sum
-  static constexpr int kWt = kStat + kWarps * kCols * 8;  // [warp][kCols] weights of the warps' parts, or of the CTAs'
+  // [warp][kCols] exponents of the warps' fp16 weights, then weights of the warps' parts, or of the CTAs'
+  static constexpr int kWt = kStat + kWarps * kCols * 8;
   static constexpr int kRows = kWt + kMaxCluster * kCols * 4;  // [kCols] rows of q and out
   // what a cluster's CTAs send: [CTA][kCols][2] max and sum, and of each CTA its runs [CTA][run][32], four columns each
   static constexpr int kMl = kRows + kCols * 8;
@@ -455,16 +462,16 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     __syncthreads();
 
     // ---------------------------------------------------------- the tokens
-    // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to (0 before there is a
+    // columns 2 t and 2 t + 1 of each tile: what the exponents are relative to, the maximum (0 before there is a
     // token), the logit up to which it stays, and the sum over the lane's tokens
     float ref[kT][2], th[kT][2], l[kT][2];
-    [[maybe_unused]] int down[kT][2];             // fp16 weights: ref is the maximum plus this
+    [[maybe_unused]] float inv[kT][2];             // fp16 weights are p s_v 2^-E: 2^-E
     [[maybe_unused]] uint32_t vlim = 0x7f800000u;  // and the V scale up to which they all fit
     float o[D / 16][kT][4];
 #pragma unroll
     for (int h = 0; h < kT; ++h)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f, down[h][c] = -126;
+      for (int c = 0; c < 2; ++c) th[h][c] = -INFINITY, ref[h][c] = l[h][c] = 0.0f, inv[h][c] = 1.0f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -522,10 +529,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
     };
 
     // Online softmax, lazily rescaled: where a logit passes its column's limit, the reference moves.
-    // fp16 weights w = 2^(y - ref) s_v: with ref the maximum alone a row of a huge scale would not fit, and
-    // with ref following the scales a row of a huge scale and no probability would push the others
-    // below fp16's range.  So ref follows the weights: it is the maximum plus `down`, about log2 of the column's
-    // largest p s_v, and moves where a logit is 2^kLazyLists above the maximum, or a scale 2^10 above that weight.
+    // fp16 weights w = p s_v 2^-E: without E a row of a huge scale would not fit, and with E following the scales
+    // alone a row of a huge scale and no probability would push the others below fp16's range.  So E follows the
+    // weights: it is about log2 of the column's largest p s_v, and moves where a logit is 2^kLazyLists above the
+    // maximum, or a scale 2^10 above that weight.  The sum of the p knows nothing of it.
     auto move_maxima = [&](const float (&x)[kU][kT][4], uint32_t values) {
       bool grow = false;
       float mx[kT][2];
@@ -582,23 +589,24 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
           }
           const bool first = th[h][c] == -INFINITY, higher = m > th[h][c];
           if ((first && !higher) || isnan(y) || (!kHalf && !higher)) continue;
-          float to = y;
+          const float to = higher ? y : ref[h][c], shift = ref[h][c] - to, f = first ? 0.0f : ex2(shift);
+          float fo = f;
           if constexpr (kHalf) {
-            const float before = ref[h][c] - static_cast<float>(down[h][c]), now = higher ? y : before;
             // what the earlier rows' largest weight has become, and this step's, in [2^(e - 1), 2^(e + 1))
-            const int kept = first ? -126 : down[h][c] + __float2int_rd(fmaxf(before - now, -252.0f));
-            const int e = __float2int_ru(heavy - bounded(now)) - 1;
-            down[h][c] = max(-80, min(120, max(kept, e)));
-            to = now + static_cast<float>(down[h][c]);
+            const int before = 127 - static_cast<int>(__float_as_uint(inv[h][c]) >> 23);
+            const int kept = first ? -120 : before + __float2int_rd(fmaxf(shift, -252.0f));
+            const int e = __float2int_ru(heavy - bounded(to)) - 1;
+            const int E = max(-120, min(120, max(kept, e)));
+            inv[h][c] = pow2i(-E);
+            fo = f * pow2i(min(127, before - E));  // at most 2: f is 0 where before - E is above
           }
-          const float f = first ? 0.0f : ex2(ref[h][c] - to);
           ref[h][c] = to;
           if (higher) th[h][c] = (y + static_cast<float>(kHalf ? kLazyLists : static_cast<int>(kLazy))) / qs[h][c];
           l[h][c] *= f;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            o[i][h][c] *= f;
-            o[i][h][2 + c] *= f;
+            o[i][h][c] *= fo;
+            o[i][h][2 + c] *= fo;
           }
         }
       if constexpr (kHalf) {  // the limit of the column that has the least weights
@@ -607,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
         for (int h = 0; h < kT; ++h)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            if (th[h][c] != -INFINITY) least = min(least, down[h][c]);
+            if (th[h][c] != -INFINITY) least = min(least, 127 - static_cast<int>(__float_as_uint(inv[h][c]) >> 23));
         least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
         least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
         vlim = static_cast<uint32_t>(min(127, least + 15 - kLazyLists) + 127) << 23;
@@ -642,10 +650,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
             p[h][s][0] = ex2(fmaf(x[u][h][2 * s], qs[h][0], -ref[h][0]));
             p[h][s][1] = ex2(fmaf(x[u][h][2 * s + 1], qs[h][1], -ref[h][1]));
             add_pair(l[h][0], l[h][1], p[h][s][0], p[h][s][1]);
+            if constexpr (kHalf) scale_pair(p[h][s][0], p[h][s][1], inv[h][0], inv[h][1]);
           }
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          uint32_t wt[kT][kTerms][2];  // p s_v, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
+          uint32_t wt[kT][kTerms][2];  // the weights, transposed: column g, tokens 2 t and 2 t + 1 (and + 8)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const float f = (j & 1) ? bf16_half<1>(sc[s][j / 2]) : bf16_half<0>(sc[s][j / 2]);
@@ -750,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
         ref[h][c] = keep_nan(th[h][c] == -INFINITY ? -INFINITY : ref[h][c], l[h][c]);
       }
       if (g == 0) *reinterpret_cast<float4*>(stat + (warp * kCols + 8 * h + 2 * t) * 2) = make_float4(ref[h][0], l[h][0], ref[h][1], l[h][1]);
+      if (kHalf && g == 0) *reinterpret_cast<float2*>(wt + warp * kCols + 8 * h + 2 * t) = make_float2(pow2_inverse(inv[h][0]), pow2_inverse(inv[h][1]));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {  // rows g and g + 8 of tile i
         float* r = red + (warp * D + 16 * i + g) * kCols + 8 * h + 2 * t;
@@ -758,9 +768,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       }
     }
     __syncthreads();
-    // The parts of a column: weights 2^(m - M) of their sums and outputs, over the whole sum where it is all there is.
     const bool cut = a.ctas && s1 - s0 < per;  // a part of a sequence, for the combine
-    auto weigh = [&](int c, int n, const auto& v, float& M, float& sum) {
+    // The parts of a column, of maxima v.x and sums v.y: the joined ones, and weights of the parts' outputs.  A warp's
+    // output is relative to 2^E (in wt) and not divided by anything yet, a CTA's is divided by its sum, so that
+    // neither passes fp32 where the joined output does not.
+    auto weigh = [&](int c, int n, const auto& v, bool ctas, float& M, float& sum) {
       constexpr int kMost = sizeof(v) / sizeof(v[0]);
       M = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -770,14 +782,16 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       for (int i = 0; i < kMost; ++i)
         if (i < n) {
           const float f = v[i].x == -INFINITY ? 0.0f : ex2(v[i].x - M);
-          wt[i * kCols + c] = f;
           if (v[i].x != -INFINITY) sum = fmaf(f, v[i].y, sum);
+          wt[i * kCols + c] = f * (ctas ? v[i].y : kHalf ? wt[i * kCols + c] : 1.0f);
         }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < n) wt[i * kCols + c] *= inv;
       M = keep_nan(M, sum);  // which stays beside the others' maxima
     };
-    auto finish = [&](int c, int n, float M, float sum) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      for (int i = 0; i < n; ++i) wt[i * kCols + c] *= inv;
+    auto store_lse = [&](int c, float M, float sum) {
       if (a.lse && rank == 0) a.lse[row_of[c]] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
     };
     // slot 0 of a CTA's two parts where its work begins, else 1
@@ -789,11 +803,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
       float2 v[kWarps];
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) v[i] = *reinterpret_cast<const float2*>(stat + (i * kCols + c) * 2);
-      weigh(c, kWarps, v, M, sum);
+      weigh(c, kWarps, v, false, M, sum);
       if (S > 1) {
         for (int i = 0; i < S; ++i) *cluster.map_shared_rank(reinterpret_cast<float2*>(smem + C::kMl) + rank * kCols + c, i) = make_float2(M, sum);
       } else if (cut) a.part_ml[slot * kCols + c] = make_float2(M, sum);
-      else finish(c, kWarps, M, sum);
+      else store_lse(c, M, sum);
     }
     if (a.ctas && threadIdx.x == 0) {  // the CTAs that have the first and the last step
       int32_t* const ends = a.ends + 2 * (static_cast<int64_t>(b) * per_seq + inner);
@@ -840,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i)
           if (i < S) v[i] = reinterpret_cast<const float2*>(smem + C::kMl)[i * kCols + c];
-        weigh(c, S, v, M, sum);
-        finish(c, S, M, sum);
+        weigh(c, S, v, true, M, sum);
+        store_lse(c, M, sum);
       }
       __syncthreads();
       for (int n = warp; n * S + rank < runs; n += kWarps) {
@@ -874,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, kCols>::kCtas)
 // of one item: each of them in turn (kEach) or, where there are more than CTAs of the kernel above, of the one that such
 // a CTA began and did not end, if it did.
 constexpr int kJoin = 256, kAhead = 4;
+constexpr float kJoinScale = 0x1p-32f;  // of the outputs' sums over parts, which may otherwise pass fp32 where the outputs do not
 template <int D, bool kEach>
 __global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Args a, int pad, int stripes) {
   constexpr int kRow = D / 4;
@@ -917,8 +932,8 @@ __global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Arg
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (v[k].x == -INFINITY) continue;
-      const float f = ex2(v[k].x - M);
-      sum = fmaf(f, v[k].y, sum);
+      const float w = ex2(v[k].x - M) * v[k].y, f = w * kJoinScale;
+      sum += w;
       acc.x = fmaf(f, x[k].x, acc.x);
       acc.y = fmaf(f, x[k].y, acc.y);
       acc.z = fmaf(f, x[k].z, acc.z);
@@ -951,7 +966,7 @@ __global__ void __launch_bounds__(kJoin) decode4_combine_kernel(const Decode4Arg
   const int64_t row = (static_cast<int64_t>(b) * a.T + dr) * a.Hq + head * G + (col0 + c - dr * G);
   const float x[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store_out(a.out, a.out_dtype, row * D + 4 * q + i, sum == 0.0f ? 0.0f : x[i] / sum);
+  for (int i = 0; i < 4; ++i) store_out(a.out, a.out_dtype, row * D + 4 * q + i, sum == 0.0f ? 0.0f : x[i] / (sum * kJoinScale));
   if (a.lse && q == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 

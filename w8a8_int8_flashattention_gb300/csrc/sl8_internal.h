@@ -338,7 +338,7 @@ struct Decode4Args {
   void* out;
   sl8_dtype out_dtype;
   float* lse;
-  // ctas > 0: two parts a CTA, [2 ctas][8 or 16 columns][d], not normalised, their maxima (log2) and sums,
+  // ctas > 0: two parts a CTA, [2 ctas][8, 16 or 24 columns][d], outputs of their tokens alone, their maxima (log2) and sums,
   // the first and last CTA of each (sequence, kv head, column group), and for each CTA the one of those
   // that it begins and does not end, or -1
   float* part_o;
