@@ -629,7 +629,7 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *                 or by 2^-24 of the query's largest weight (an fp32 out: 2^-23 of itself).  V scales are, in
  *                 magnitude, 0 or between 2^-94 and 2^124 (for an fp32 out, also at most 2^117 over the
  *                 sequence's length): smaller ones keep fewer bits in 16-bit outputs, larger ones may
- *                 overflow.
+ *                 overflow.  A query's values are below 2^106 in magnitude: larger ones may make it NaN.
  *   workspace     at least sl8_attn_int4_paged_decode_workspace_size() bytes (0: invalid or
  *                 unsupported shape; 16: none is used and it may be null), 16-byte aligned; launches
  *                 that run at the same time need their own.

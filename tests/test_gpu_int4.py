@@ -946,3 +946,18 @@ def test_the_lse_has_the_same_bits_for_any_values(d, T, G):
             for make in (lambda s: s * 0, lambda s: 10.0 ** rng.uniform(-28, 33, s.shape), lambda s: np.where(rng.random(s.shape) < 0.1, np.inf, s)):
                 pool[3].copy_(torch.from_numpy(make(host[3]).astype(np.float32)))
                 assert torch.equal(call(odt)[1], want), (splits, odt)
+
+
+@pytest.mark.parametrize("d,splits", [(32, 1), (64, 3), (128, 12), (256, 1)])
+def test_large_queries_meet_small_keys(d, splits):
+    """Queries just below 2^106 and key scales that make ordinary logits of them."""
+    rng = np.random.default_rng(d)
+    pool, (kc, ks, vc, vs) = _filled(rng, 10, 1, 16, d)
+    ks = ks * np.float32(2.0 ** -104)
+    pool[1].copy_(torch.from_numpy(ks))
+    x = rng.standard_normal((1, 1, 5, d)).clip(-4, 4).astype(np.float32) * np.float32(2.0 ** 103)
+    x[0, 0, 0, 0] = 2.0 ** 106 * (1 - 2.0 ** -24)
+    q = torch.from_numpy(x).to(DEV)
+    for odt in (F32, F16):
+        out, lse = sl8.attn_int4_paged_decode(q, *pool, i32(np.arange(10)[None]), i32([150]), num_splits=splits, out_dtype=odt, return_lse=True)
+        _check_attention(out, lse, q, (kc, ks, vc, vs), [np.arange(10)], [150], tag=odt)
