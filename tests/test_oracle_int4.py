@@ -88,3 +88,25 @@ def test_drafts_are_single_queries_of_shorter_sequences():
     full = [[0b111] * T]
     every, _ = Q.attention(q, kc, ks, vc, vs, [[2, 0, 3]], [37], full)
     np.testing.assert_allclose(every[:, 2], out[:, 2], rtol=1e-12)
+
+
+def test_the_scale_s_quotient_without_a_division():
+    """group_scale of csrc/cache4.cuh forms m / 7 as q + (m - 7 q) c, q = RN(m c) and c = RN(1 / 7), each sum fused: the quotient's
+    own rounding for every significand m of 24 bits, in whole numbers.  A power of two scales all of it alike."""
+    c = int(np.float32(1 / 7) * 2.0 ** 26)  # of 2^-26
+    assert 1 << 23 <= c < 1 << 24 and c == float(np.float32(1) / np.float32(7)) * 2.0 ** 26
+
+    def rounded(x):  # to 24 significant bits, ties to even; frexp is exact for x < 2^53
+        drop = np.frexp(x.astype(np.float64))[1] - 24
+        low, half, kept = x & ((1 << drop) - 1), np.int64(1) << (drop - 1), x >> drop
+        return (kept + ((low > half) | ((low == half) & (kept & 1 == 1)))) << drop
+
+    for first in range(1 << 23, 1 << 24, 1 << 20):
+        m = np.arange(first, first + (1 << 20), dtype=np.int64)
+        q = rounded(m * c)  # of 2^-26
+        rest = (m << 26) - 7 * q
+        assert np.all(rest % (1 << 22) == 0) and np.all(np.abs(rest) >> 22 < 1 << 24)  # exact in fp32
+        got = rounded((q << 4) + (rest >> 22) * c)  # of 2^-30
+        whole, left = np.divmod(m << 30, 7)
+        want = rounded(2 * whole + (left > 0)) >> 1  # the last bit says that something is left
+        np.testing.assert_array_equal(got, want)
