@@ -582,8 +582,8 @@ SL8_API int sl8_rope_append_int4(const void* q, const void* k, const void* v, in
                                  void* stream);
 
 /*
- * The first seqlens[b] tokens of each sequence as dense keys and values (code * s, + k_mean; rounded
- * once to out_dtype), for a prefill that continues from them.
+ * The first seqlens[b] tokens of each sequence as dense keys and values (code * s, + k_mean; rounded to
+ * fp32 and to out_dtype), for a prefill that continues from them.
  *   block_table   device, [B][max_blocks] int32; seqlens device, [B] int32.
  *   cu_seqlens    device, nullable.  NULL: k_out, v_out are [B][Hkv][N][d] and every length is
  *                 at most N.  Else [B + 1] int32, and they are [total_tokens][Hkv][d]: token i of
@@ -626,10 +626,11 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *                 lse_out of its query NaN, an infinite v scale the group's channels of out.
  *                 The sum of the p, and with it lse_out, does not depend on the values; a p below 2^-126 of the
  *                 largest may count as 0.  Each weight p * s_v is off by 2^-11 of itself before it meets its row,
- *                 or by 2^-24 of the query's largest weight (an fp32 out: 2^-23 of itself).  V scales are, in
- *                 magnitude, 0 or between 2^-94 and 2^124 (for an fp32 out, also at most 2^117 over the
- *                 sequence's length): smaller ones keep fewer bits in 16-bit outputs, larger ones may
- *                 overflow.  A query's values are below 2^106 in magnitude: larger ones may make it NaN.
+ *                 or by 2^-24 of the query's largest weight (an fp32 out: 2^-23 of itself).  Sums are fp32: those
+ *                 of n tokens in one CTA's part are off by up to 3 n 2^-29 of what their magnitudes come to.
+ *                 V scales are, in magnitude, 0 or between 2^-94 and 2^124 (for an fp32 out, also at most 2^117
+ *                 over the sequence's length): smaller ones keep fewer bits in 16-bit outputs, larger ones
+ *                 may overflow.  A query's values are below 2^106 in magnitude: larger ones may make it NaN.
  *   workspace     at least sl8_attn_int4_paged_decode_workspace_size() bytes (0: invalid or
  *                 unsupported shape; 16: none is used and it may be null), 16-byte aligned; launches
  *                 that run at the same time need their own.
