@@ -617,8 +617,9 @@ SL8_API int sl8_paged_read_int4(const uint8_t* k_pages, const void* k_scale_page
  *   num_splits    parts that a sequence is cut into.  Up to 8: each into so many, a cluster of CTAs that
  *                 merges them.  More: the work of all sequences, whose lengths only the device knows, is
  *                 shared out evenly over so many CTAs for each (sequence, kv head, group) (at most 16 an
- *                 SM), and a second kernel joins what they cut.  0 = automatic: evenly over the CTAs that fit
- *                 the device where tables are long enough for that to pay, else a cluster.
+ *                 SM), and a second kernel joins what they cut.  0 = automatic, by the table's width alone: evenly
+ *                 over the CTAs that fit the device where tables are long enough for that to pay, else a cluster
+ *                 (a caller that knows its sequences to be far shorter gains by asking for 1 to 8).
  *   out           device, [B][T][Hq][d] of out_dtype; a query that sees no token gets 0.
  *   lse_out       device, nullable, [B][T][Hq] fp32 (natural log; -inf for no token), of the stored
  *                 keys: with a k_mean, sum_c q_c k_mean_c / sqrt(d) below that of the keys themselves.

@@ -24,11 +24,13 @@
 //    chain waits alone; the steps that end behind the first draft, at most one a warp, come last, with masks.
 //  * Few tokens: a cluster of up to 8 CTAs a sequence, which send their parts to one another's shared memory.  Many: all
 //    sequences' steps are shared out evenly over the CTAs that fit the device, and a second kernel joins what the
-//    shares cut (64 sequences of 1,024 to 8,192 tokens, 8 x 4 heads, d = 128: 70 us, and 81 with a cluster of 2 each).
-// Bound by instruction issue, not by HBM: a step's masks, codes, scales and weights take as long as its MMAs and
-// loads together.  76 sequences of 8,192 tokens, 8 kv heads: 124 us at d = 128 with up to 8 columns, 0.85 of the copy rate
-// for codes and scales; 186 with 16 and 259 with 24, where 8 at a time would take 248 and 372; 165 with fp32 outputs.
-// d = 64: 89 us, 107, 149; d = 32: 66, 71, 100; d = 256: 236, 0.89 of the copy rate, and 316 with fp32 outputs.
+//    shares cut (64 sequences of 1,024 to 8,192 tokens, 8 x 4 heads, d = 128: 72 us, and 87 with a cluster of 2 each).
+// Bound by the warps' own latency, not by HBM: the accumulators leave 2 to 3.6 warps a scheduler, which wait for the last
+// instruction's result or for a turn at a pipe.  At 8 columns and d = 128 issue is at 61 %, the busiest pipe (logic, shifts,
+// conversions) at 54 %, the tensor cores at 28 %; at 24 columns at 41, 27 and 29 %.
+// 76 sequences of 8,192 tokens, 8 kv heads: 126 us at d = 128 with up to 8 columns, 0.84 of the copy rate
+// for codes and scales; 192 with 16 and 257 with 24, where 8 at a time would take 251 and 377; 165 with fp32 outputs.
+// d = 64: 91 us, 110, 155; d = 32: 67, 73, 101; d = 256: 241, 0.87 of the copy rate, and 318 with fp32 outputs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -170,15 +172,15 @@ struct Cfg4 {
   static constexpr int kN = D / kGroup4;  // groups (and 16-byte chunks) of a row
   static constexpr int kT = (kCols + 7) / 8;  // tiles of eight columns
   // Units of 16 tokens that a warp takes at a time, a step: two where the registers hold them (64 sequences of up to 8,192
-  // tokens 70 us, and 76 with one; 24 columns at d = 128 46 with one and 50 with two).
+  // tokens 71 us, and 77 with one; 16 x 5 drafts of 4 heads, 20 columns, at d = 128 46 with one and 51 with two).
   static constexpr int kU = D == 256 || (D == 128 && kCols > 16) ? 1 : 2;
   static constexpr int kStep = 16 * kU;
   static constexpr int kStart = D == 256 ? 16 : 512 / kStep;  // steps that a sequence's start and end are worth, see below
   static constexpr int kHalf = kU * 9 * D;  // a step's keys, or its values: codes [kU][16][D / 2], scales [kU][16][kN]
   static constexpr int kScales = kU * 8 * D;
   static constexpr int kRing = 4 * kHalf;  // of a warp: two steps' keys, two steps' values
-  // as many CTAs an SM as their registers let, the accumulators being D kT / 4 a thread (d = 64: with one more 39 us for
-  // 35, with one less 37; d = 128 with one less 74.4 for 73.8)
+  // as many CTAs an SM as their registers let, the accumulators being D kT / 4 a thread (48 sequences, 16 columns at
+  // d = 64: with one more 37.0 us for 33.8, with one less 34.1; 64 at d = 128 with one less 71.8 for 71.3)
   static constexpr int kCtas = D == 256 ? 3 : D == 128 ? 5 - kT : 6 - kT;
   // after the loop the rings hold the warps' O^T [warp][D][kCols], fp32
   static constexpr int kRed = 0, kMerge = kWarps * D * kCols * 4;
@@ -991,7 +993,7 @@ cudaError_t launch_t(const Decode4Args& a, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, kern, a, device_status_ptr());
   if (e != cudaSuccess || !a.ctas) return e;
   // rows of the combine that share a column's parts: as many as take them kMany times over at once, since lengths differ
-  // (kMany 1, 2, 4, 8 on sequences of up to 8,192 tokens: 75.2 us, 75.9, 77.8, 80.2; a CTA for each column 77.3)
+  // (kMany 1, 2, 4, 8: 64 sequences of up to 8,192 tokens 70.6 us, 71.3, 73.2, 75.6; 48 of up to 16,384, d = 64, 34.4, 33.8, 34.1, 37.0)
   constexpr int kRows = kJoin / (D / 4), kMany = 2;
   const unsigned ctas = static_cast<unsigned>(a.ctas);
   int stripes = 1;
@@ -1039,11 +1041,13 @@ void decode4_plan_work(int64_t items, int64_t tokens, int32_t d, int32_t cols, i
     *splits = num_splits;
   } else {
     // A cluster for each item, of as many CTAs as fit one wave and have 128 tokens each, 1,024 where they are more than
-    // two an SM, whose starts hold one another up (64 items of up to 1,024 tokens: 9.3 us with 4 CTAs each, 11.3 with 8); or even shares, if the table's
+    // two an SM, whose starts hold one another up (64 items of up to 1,024 tokens: 9.2 us with 4 CTAs each, 11.4 with 8); or even shares, if the table's
     // width says that a CTA's longest run could be longer than a share (of lengths that are five eighths of the width) by
     // what the second kernel and the ends of the shares cost: 1,000 tokens' time, 750 at d = 256.
-    // One sequence, 8 heads: 8,192 tokens 13.5 us in clusters and 13.2 in shares, 65,536 51 and 26; 512 tokens a CTA 10.5
-    // and 12.3.  64 sequences of 256 to 2,048: 30.1 and 34.1, of 512 to 4,096: 52.7 and 48.0.
+    // One sequence, 8 heads: 8,192 tokens 13.8 us in clusters and 13.7 in shares, 65,536 53 and 27; 4,096 (512 a CTA) 10.3
+    // and 12.8.  64 sequences of 256 to 2,048: 29.0 and 32.8, of 512 to 4,096: 50.7 and 47.4.  Only the device knows the
+    // lengths: where tables are far wider, shares are taken that a cluster would beat (4 sequences of up to 2,048 tokens
+    // 13.1 for 9.7 us, 64 of up to 512 22 for 14).
     while (*splits < kMaxCluster && items * (*splits + 1) <= fit && tokens / (*splits + 1) >= (items * (*splits + 1) <= 2 * num_sms() ? 128 : 1024))
       ++*splits;
     if (counted) {
